@@ -312,6 +312,62 @@ sq_status sq_f32_decode_step(float *state_pool, int32_t n_slots, int32_t n_heads
                              const void *g, sq_dtype in_dtype, void *y, sq_dtype y_dtype,
                              hipStream_t stream);
 
+/* Whole sequences: the same recurrence over many tokens (prefill of a prompt
+ * into a state, the layer of a training step), on fp32 states that
+ * sq_quant_state then brings into a pool.  Tokens of all sequences lie one
+ * after another:
+ *   q, k: [n_tokens, n_key_heads, d_k]   v: [n_tokens, n_heads, d_v]
+ *   beta: [n_tokens, n_heads]            y: [n_tokens, n_heads, d_v]
+ *   g (log-gate): [n_tokens, n_heads] for GDN, [n_tokens, n_heads, d_k] for KDA
+ * Head h reads the key head h / (n_heads / n_key_heads).  q, k and v may be
+ * parts of one wider tensor: q_stride, k_stride and v_stride are the elements
+ * from one token to the next (0: dense), a multiple of 16 bytes; everything
+ * else is dense. */
+typedef struct {
+    int32_t n_seq;        /* sequences, >= 0 */
+    int32_t n_heads;      /* heads of v, >= 1 */
+    int32_t n_key_heads;  /* heads of q and k, a divisor of n_heads */
+    int32_t d_k, d_v;     /* equal, 64 or 128 */
+    int64_t n_tokens;     /* tokens of all sequences, < 2^31 */
+    sq_gate gate;
+    sq_dtype in_dtype;    /* q, k, v, beta, g, and every gradient but dS0's */
+    sq_dtype y_dtype;
+    int64_t q_stride, k_stride, v_stride;
+} sq_seq_desc;
+
+/* Bytes that sq_chunk_forward needs as `work`.  Grows with
+ * n_tokens and n_seq alone, so one buffer of the largest batch serves all
+ * smaller ones; its contents between calls are of no concern.  Errors:
+ * SQ_EINVAL for a NULL or inconsistent descriptor, SQ_EUNSUPPORTED for shapes
+ * outside the supported set. */
+sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work);
+
+/* The recurrence of sq_decode_step, unquantized, over whole sequences
+ * ("Paper Explained: STEPQuant" (ta-paperlens), section "The mechanism:
+ * rewriting state with the delta rule"), in chunks of 64 tokens.
+ *   cu:    DEVICE int32 [n_seq + 1]: sequence s is the tokens cu[s] .. cu[s+1] - 1;
+ *          non-decreasing, within [0, n_tokens].  Lengths of 0 are fine
+ *          (S_out is then the initial state).  Tokens that no sequence has are
+ *          neither read nor written.  With SQ_DEBUG set the list is checked first
+ *          (which synchronises the stream); otherwise a wrong list gives
+ *          undefined (but memory-safe) results.
+ *   S0:    initial states fp32 [n_seq, n_heads, d_k, d_v], or NULL for zeros.
+ *   y:     output, y_dtype.
+ *   S_out: final states, as S0; may be S0 itself, or NULL.
+ *   work:  DEVICE scratch of sq_chunk_bytes, 256-byte aligned; calls that may
+ *          overlap need one each.
+ * Arithmetic: states, sums and decays in fp32; matrix products on operands
+ * split into bf16 terms so that S_out (and an fp32 y) has fp32 accuracy, a
+ * bf16 y 16 bits before its rounding.  Log-gates below -150 act as -150 (their
+ * gate is 0 in fp32), so a gate of exactly 0, g = -inf, resets the state.
+ * n_seq = 0 is a no-op.  Errors: SQ_EINVAL for a NULL or misaligned pointer, a
+ * bad stride or head count, SQ_ENOMEM if work_bytes is too small,
+ * SQ_EUNSUPPORTED as sq_chunk_bytes. */
+sq_status sq_chunk_forward(const sq_seq_desc *desc, const int32_t *cu, const void *q,
+                           const void *k, const void *v, const void *beta, const void *g,
+                           const float *S0, void *y, float *S_out, void *work, size_t work_bytes,
+                           hipStream_t stream);
+
 /* Debug check: copy slot_idx[0..n) (device) to the host, synchronising the
  * stream, and verify every entry is in [0, n_slots) and distinct.  Returns
  * SQ_EINVAL with the first offending index in sq_last_error() otherwise. */

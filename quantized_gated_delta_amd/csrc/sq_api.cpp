@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "sq_internal.h"
+#include "sq_seq.h"
 
 struct sq_pool {
     sq_pool_desc desc;          // head_bits points at bits below
@@ -158,6 +159,90 @@ sq_status check_step_io(const void *q, const void *k, const void *v, const void 
     if ((st = check_io("q", q, true)) || (st = check_io("k", k, true)) ||
         (st = check_io("v", v, true)) || (st = check_io("beta", beta, true)) ||
         (st = check_io("g", g, true)) || (st = check_io("y", y, true)))
+        return st;
+    return SQ_OK;
+}
+
+sq_status check_seq(const sq_seq_desc *d) {
+    if (!d) return fail(SQ_EINVAL, "desc is NULL");
+    if (d->n_seq < 0) return fail(SQ_EINVAL, "n_seq must be >= 0 (got %d)", d->n_seq);
+    if (d->n_tokens < 0) return fail(SQ_EINVAL, "n_tokens must be >= 0 (got %lld)", (long long)d->n_tokens);
+    if (d->n_heads < 1) return fail(SQ_EINVAL, "n_heads must be >= 1 (got %d)", d->n_heads);
+    if (d->n_key_heads < 1 || d->n_heads % d->n_key_heads != 0)
+        return fail(SQ_EINVAL, "n_key_heads = %d is not a divisor of n_heads = %d", d->n_key_heads, d->n_heads);
+    if (d->d_k != d->d_v) return fail(SQ_EUNSUPPORTED, "d_k must equal d_v (got %d, %d)", d->d_k, d->d_v);
+    if (d->d_k != 64 && d->d_k != 128)
+        return fail(SQ_EUNSUPPORTED, "d_k = d_v must be 64 or 128 (got %d)", d->d_k);
+    if (d->gate != SQ_GATE_GDN && d->gate != SQ_GATE_KDA)
+        return fail(SQ_EINVAL, "gate must be SQ_GATE_GDN or SQ_GATE_KDA (got %d)", (int)d->gate);
+    if (d->in_dtype != SQ_F32 && d->in_dtype != SQ_BF16)
+        return fail(SQ_EINVAL, "in_dtype must be SQ_F32 or SQ_BF16 (got %d)", (int)d->in_dtype);
+    if (d->y_dtype != SQ_F32 && d->y_dtype != SQ_BF16)
+        return fail(SQ_EINVAL, "y_dtype must be SQ_F32 or SQ_BF16 (got %d)", (int)d->y_dtype);
+    if (d->n_tokens > 0x7FFFFFFFll - 64) return fail(SQ_EUNSUPPORTED, "n_tokens exceeds 2^31 - 65");
+    // grids: one workgroup per (chunk slot, head) and per (sequence, head, 16 columns)
+    const int64_t slots = sqk::chunk_slots(d->n_tokens, d->n_seq);
+    if (slots * d->n_heads > 0x7FFFFFFFll || (int64_t)d->n_seq * d->n_heads > 0x7FFFFFFFll / 8 - 8)
+        return fail(SQ_EUNSUPPORTED, "n_tokens or n_seq times n_heads exceeds the grid limit");
+    const int64_t per16 = d->in_dtype == SQ_BF16 ? 8 : 4, dense_k = (int64_t)d->n_key_heads * d->d_k,
+                  dense_v = (int64_t)d->n_heads * d->d_v;
+    const struct { const char *name; int64_t stride, dense; } st[3] = {
+        {"q_stride", d->q_stride, dense_k}, {"k_stride", d->k_stride, dense_k}, {"v_stride", d->v_stride, dense_v}};
+    for (const auto &s : st)
+        if (s.stride != 0 && (s.stride < s.dense || s.stride % per16 != 0 || s.stride > INT64_MAX / 16 / (d->n_tokens + 1)))
+            return fail(SQ_EINVAL, "%s = %lld must be 0 or a multiple of %lld, at least %lld", s.name,
+                        (long long)s.stride, (long long)per16, (long long)s.dense);
+    return SQ_OK;
+}
+
+// With SQ_DEBUG: the sequence list on the host (synchronises the stream).
+sq_status check_cu(const sq_seq_desc *d, const int32_t *cu, hipStream_t stream) {
+    std::vector<int32_t> host((size_t)d->n_seq + 1);
+    hipError_t e = hipStreamSynchronize(stream);
+    if (e != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
+    e = hipMemcpy(host.data(), cu, sizeof(int32_t) * host.size(), hipMemcpyDeviceToHost);
+    if (e != hipSuccess) return hip_fail(e, "hipMemcpy(cu)");
+    for (int32_t i = 0; i <= d->n_seq; ++i)
+        if (host[(size_t)i] < (i ? host[(size_t)i - 1] : 0) || host[(size_t)i] > d->n_tokens)
+            return fail(SQ_EINVAL, "cu[%d] = %d must be non-decreasing within [0, %lld]", i, host[(size_t)i],
+                        (long long)d->n_tokens);
+    return SQ_OK;
+}
+
+sqk::SeqArgs seq_args(const sq_seq_desc *d, const int32_t *cu, const void *q, const void *k, const void *v,
+                      const void *beta, const void *g, const float *S0, void *work) {
+    sqk::SeqArgs a{};
+    a.q = q; a.k = k; a.v = v; a.beta = beta; a.g = g;
+    a.q_stride = d->q_stride ? d->q_stride : (int64_t)d->n_key_heads * d->d_k;
+    a.k_stride = d->k_stride ? d->k_stride : (int64_t)d->n_key_heads * d->d_k;
+    a.v_stride = d->v_stride ? d->v_stride : (int64_t)d->n_heads * d->d_v;
+    a.cu = cu;
+    a.n_seq = d->n_seq;
+    a.n_heads = d->n_heads;
+    a.n_key_heads = d->n_key_heads;
+    a.n_tokens = d->n_tokens;
+    a.S0 = S0;
+    a.work = static_cast<uint8_t *>(work);
+    return a;
+}
+
+sq_status check_work(const char *name, const void *p, size_t have, size_t need) {
+    if (need == 0) return SQ_OK;
+    if (!p) return fail(SQ_EINVAL, "%s is NULL", name);
+    if (!aligned(p, 256)) return fail(SQ_EINVAL, "%s is not 256-byte aligned", name);
+    if (have < need) return fail(SQ_ENOMEM, "%s has %zu bytes, %zu are needed", name, have, need);
+    return SQ_OK;
+}
+
+// Pointers that every sequence call takes.
+sq_status check_seq_io(const sq_seq_desc *d, const int32_t *cu, const void *q, const void *k, const void *v,
+                       const void *beta, const void *g, const float *S0) {
+    sq_status st;
+    const bool any = d->n_tokens > 0;
+    if (!cu) return fail(SQ_EINVAL, "cu is NULL");
+    if (!aligned(cu, 4)) return fail(SQ_EINVAL, "cu is not 4-byte aligned");
+    if ((st = check_io("q", q, any)) || (st = check_io("k", k, any)) || (st = check_io("v", v, any)) ||
+        (st = check_io("beta", beta, any)) || (st = check_io("g", g, any)) || (st = check_io("S0", S0, S0 != nullptr)))
         return st;
     return SQ_OK;
 }
@@ -394,6 +479,36 @@ sq_status sq_check_slots(const sq_pool *pool, const int32_t *slot_idx, int32_t n
         seen[(size_t)s] = 1;
     }
     return SQ_OK;
+}
+
+sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work) {
+    sq_status st = check_seq(desc);
+    if (st) return st;
+    if (!work) return fail(SQ_EINVAL, "work is NULL");
+    const bool y_f32 = desc->y_dtype == SQ_F32;
+    const int64_t blocks = sqk::chunk_slots(desc->n_tokens, desc->n_seq) * desc->n_heads;
+    *work = (size_t)(blocks * sqk::forward_layout(desc->d_k, desc->gate == SQ_GATE_KDA, desc->in_dtype == SQ_F32,
+                                                  y_f32 ? 3 : 2).block);
+    return SQ_OK;
+}
+
+sq_status sq_chunk_forward(const sq_seq_desc *desc, const int32_t *cu, const void *q, const void *k, const void *v,
+                           const void *beta, const void *g, const float *S0, void *y, float *S_out, void *work,
+                           size_t work_bytes, hipStream_t stream) {
+    size_t need = 0;
+    sq_status st = sq_chunk_bytes(desc, &need);
+    if (st) return st;
+    if (desc->n_seq == 0) return SQ_OK;
+    if ((st = check_seq_io(desc, cu, q, k, v, beta, g, S0)) || (st = check_io("y", y, desc->n_tokens > 0)) ||
+        (st = check_io("S_out", S_out, S_out != nullptr)) || (st = check_work("work", work, work_bytes, need)))
+        return st;
+    if (debug_slots() && (st = check_cu(desc, cu, stream))) return st;
+    sqk::SeqArgs a = seq_args(desc, cu, q, k, v, beta, g, S0, work);
+    a.y = y;
+    a.S_out = S_out;
+    const hipError_t e = sqk::launch_chunk_forward(a, desc->d_k, desc->gate == SQ_GATE_KDA, desc->in_dtype == SQ_F32,
+                                                   desc->y_dtype == SQ_F32, stream);
+    return e == hipSuccess ? SQ_OK : hip_fail(e, "chunk_forward launch");
 }
 
 sq_status sq_device_copy(const void *src, void *dst, size_t bytes, hipStream_t stream) {

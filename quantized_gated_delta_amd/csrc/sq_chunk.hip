@@ -1,0 +1,353 @@
+// The gated Delta rule over whole sequences, forward, in chunks of 64 tokens.
+//
+// Within a chunk that starts at state S0 (ta-paperlens page, mechanism section,
+// for the recurrence), with the notation of sq_prep.h,
+//   R' = V - (K e^G) S0        X = diag(beta) R'
+//   E  = R' + M X              U = diag(beta) E
+//   y  = (Q e^G) S0 + P U      S_C = diag(e^{G_C}) S0 + (K e^{G_C - G})^T U
+// Two kernels: prep (sq_prep.h: M, P and the decayed keys and queries, every chunk
+// in parallel) and scan, which walks the chunks of one (sequence, head).
+//
+// The scan is bound by its chain of dependent products (three per chunk) when
+// there are few (sequence, head) pairs, so a workgroup holds only 16 NCT columns
+// of the state (columns never interact) and splits every product's rows over
+// its four waves: wave w owns tokens 16 w .. 16 w + 15 of each chunk and rows
+// w d / 4 .. of the state.  The state stays in registers as fp32 accumulators.  What
+// another wave needs next (S, X, U) goes through LDS in the layout that is both the
+// result's and the next operand's; the left operands come from HBM
+// straight into fragments, the next chunk's issued right after their last use.
+#include "sq_prep.h"
+
+namespace sqk {
+namespace {
+
+template <int D, bool F32, int NTP>
+__global__ __launch_bounds__(256) void prep_gdn_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr ChunkLayout lay = forward_layout(D, false, F32, NTP);
+    constexpr int TROW = D + 16 / (int)sizeof(E);
+    __shared__ union { struct { float B[kChunk * kBRow], P[kChunk * kBRow]; }; E tok[kChunk * TROW]; } s;
+    __shared__ float sInv[4 * 16 * 20], sBeta[kChunk];
+    __shared__ double sG[kChunk];
+    const int t = threadIdx.x, w = t >> 6, l = t & 63;
+    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
+    const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+    uint8_t *out = a.work + (x * a.n_heads + h) * lay.block;
+
+    gates_gdn<F32>(a, t0, rows, h, sG, sBeta, t);
+    // the keys by channel serve every value head that shares them: the first one's block holds them
+    if (h == hk * share) write_transposed<D, F32>(a.k, a.k_stride, t0, rows, hk, s.tok, reinterpret_cast<E *>(out + lay.KT), t);
+    else __syncthreads();
+    if (t < kChunk) {
+        float *gt = reinterpret_cast<float *>(out + lay.gates);
+        gt[t] = exp_of((float)sG[t]);
+        gt[kChunk + t] = exp_of((float)(sG[kChunk - 1] - sG[t]));
+        gt[2 * kChunk + t] = sBeta[t];
+    }
+    pairs_gdn<D, F32>(a, t0, rows, hk, sG, s.B, s.P, w, l);
+    __syncthreads();
+    write_square<F32, NTP, false>(s.P, reinterpret_cast<E *>(out + lay.P), t);
+    invert_block(s.B, sBeta, sInv + w * 320, w, l);
+    __syncthreads();
+    f4 m[4];
+    solve_column(s.B, sBeta, sInv, w, l, m);
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.P[(16 * I + (l >> 4) * 4 + i) * kBRow + 16 * w + (l & 15)] = m[I][i];
+    __syncthreads();
+    write_square<F32, 3, false>(s.P, reinterpret_cast<E *>(out + lay.M), t);
+}
+
+template <int D, bool F32, int NTP>
+__global__ __launch_bounds__(256) void prep_kda_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr ChunkLayout lay = forward_layout(D, true, F32, NTP);
+    __shared__ KdaLds<D, F32> s;
+    __shared__ float sInv[4 * 16 * 20];
+    const int t = threadIdx.x, w = t >> 6, l = t & 63;
+    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
+    const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+    uint8_t *out = a.work + (x * a.n_heads + h) * lay.block;
+
+    load_kda<D, F32>(a, t0, rows, h, hk, s, t);
+    for (int u = t; u < kChunk * D / 8; u += 256) {
+        const int row = u / (D / 8), c8 = u % (D / 8) * 8;
+        float v[8];
+        decayed8<D, F32, 1>(s, s.k, row, c8, 0, v);
+        store8<F32, 3>(reinterpret_cast<E *>(out + lay.K) + row * D + c8, kChunk * D, v);
+        decayed8<D, F32, 1>(s, s.q, row, c8, 0, v);
+        store8<F32, NTP>(reinterpret_cast<E *>(out + lay.Q) + row * D + c8, kChunk * D, v);
+    }
+    for (int u = t; u < kChunk * D / 8; u += 256) {
+        // eight tokens of a channel; consecutive lanes take consecutive channels
+        const int ch = u % D, k8 = u / D * 8;
+        constexpr int GROW = KdaLds<D, F32>::GROW, ROW = KdaLds<D, F32>::ROW;
+        float after = 0.f, v[8];
+        for (int b = (k8 >> 4) + 1; b < 4; ++b) after += s.L[(16 * b + 15) * GROW + ch];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ld_elem<F32>(s.k, (k8 + i) * ROW + ch) * exp_of(s.R[(k8 + i) * GROW + ch] + after);
+        store8<F32, 3>(reinterpret_cast<E *>(out + lay.KT) + ch * kChunk + k8, D * kChunk, v);
+    }
+    float *gt = reinterpret_cast<float *>(out + lay.gates);
+    if (t < kChunk) gt[t] = s.beta[t];
+    if (t < D) {
+        float e = 0.f;
+        for (int b = 0; b < 4; ++b) e += s.L[(16 * b + 15) * KdaLds<D, F32>::GROW + t];
+        gt[kChunk + t] = exp_of(e);
+    }
+    pairs_kda<D, F32, NTP>(a, t0, rows, h, s, w, l);
+    __syncthreads();
+    write_square<F32, NTP, false>(s.P, reinterpret_cast<E *>(out + lay.P), t);
+    invert_block(s.B, s.beta, sInv + w * 320, w, l);
+    __syncthreads();
+    f4 m[4];
+    solve_column(s.B, s.beta, sInv, w, l, m);
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.P[(16 * I + (l >> 4) * 4 + i) * kBRow + 16 * w + (l & 15)] = m[I][i];
+    __syncthreads();
+    write_square<F32, 3, false>(s.P, reinterpret_cast<E *>(out + lay.M), t);
+}
+
+// One (sequence, head), 16 NCT columns of its state, all chunks.  NTY: terms
+// that y is accurate to.
+template <int D, bool KDA, bool F32, int NTY, bool YF32, int NCT>
+__global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr ChunkLayout lay = forward_layout(D, KDA, F32, NTY);
+    constexpr int MT = D / 64, KB = D / 32, COLS = 16 * NCT, SLICES = D / COLS;
+    constexpr int KN = KDA ? 3 : 1, QN = KDA ? NTY : 1;
+    typedef LdsMat<F32, 3, D, COLS> SMat;
+    typedef LdsMat<F32, 3, kChunk, COLS> XMat;
+    typedef LdsMat<F32, NTY, kChunk, COLS> YMat;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[SMat::BYTES + 2 * XMat::BYTES + (KDA ? 0 : YMat::BYTES)];
+    E *sS = reinterpret_cast<E *>(lds), *sX = reinterpret_cast<E *>(lds + SMat::BYTES);
+    E *sU = reinterpret_cast<E *>(lds + SMat::BYTES + XMat::BYTES);
+    E *sY = KDA ? sU : reinterpret_cast<E *>(lds + SMat::BYTES + 2 * XMat::BYTES);
+
+    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    // the slices of one (sequence, head) read the same operands: workgroups go
+    // to the 8 XCDs in turn, so they are 8 apart to share an L2
+    const uint32_t pairs = (uint32_t)a.n_seq * a.n_heads, j = blockIdx.x >> 3;
+    const uint32_t pair = j / SLICES * 8 + (blockIdx.x & 7);
+    if (pair >= pairs) return;
+    const int c0 = (int)(j % SLICES) * COLS;
+    const int h = pair % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
+    const SeqSpan sp = seq_span(a, pair / (uint32_t)a.n_heads);
+    const int n_chunks = (sp.len + kChunk - 1) / kChunk;
+    const int64_t state = (int64_t)pair * D * D;
+
+    f4 S[MT][NCT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NCT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                S[m][n][i] = a.S0 ? a.S0[state + (int64_t)((w * MT + m) * 16 + g4 + i) * D + c0 + 16 * n + r] : 0.f;
+
+    Frag<F32, KN> fK[KB], fKT[MT][2];
+    Frag<F32, QN> fQ[KB];
+    Frag<F32, 3> fM[2];
+    Frag<F32, NTY> fP[2];
+    f4 v[NCT], eg{}, ec{}, beta{}, fade[MT];
+    float fade1 = 1.f, eq = 1.f;
+
+    auto block_of = [&](int c, int head) { return a.work + ((sp.slot0 + c) * a.n_heads + head) * lay.block; };
+    auto rows_of = [&](int c) { return min(kChunk, sp.len - c * kChunk); };
+    auto load_kq = [&](int c) {
+        if constexpr (KDA) {
+            const uint8_t *b = block_of(c, h);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const int at = (16 * w + r) * D + kb * 32 + g8;
+                fK[kb] = load_frag<F32, KN>(reinterpret_cast<const E *>(b + lay.K) + at, kChunk * D);
+                fQ[kb] = load_frag<F32, QN>(reinterpret_cast<const E *>(b + lay.Q) + at, kChunk * D);
+            }
+        } else {
+            // past the end: the last token again; its beta is 0 there and its y is not stored
+            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + r, rows_of(c) - 1);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const int64_t at = (int64_t)hk * D + kb * 32 + g8;
+                fK[kb] = load_frag<F32, KN>(static_cast<const E *>(a.k) + tok * a.k_stride + at, 0);
+                fQ[kb] = load_frag<F32, QN>(static_cast<const E *>(a.q) + tok * a.q_stride + at, 0);
+            }
+        }
+    };
+    auto load_v = [&](int c) {
+        const int last = rows_of(c) - 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + g4 + i, last);
+#pragma unroll
+            for (int n = 0; n < NCT; ++n) v[n][i] = ld_elem<F32>(a.v, tok * a.v_stride + (int64_t)h * D + c0 + 16 * n + r);
+        }
+    };
+    auto load_gates = [&](int c) {
+        const float *gt = reinterpret_cast<const float *>(block_of(c, h) + lay.gates);
+        if constexpr (KDA) {
+            beta = *reinterpret_cast<const f4 *>(gt + 16 * w + g4);
+        } else {
+            eg = *reinterpret_cast<const f4 *>(gt + 16 * w + g4);
+            ec = *reinterpret_cast<const f4 *>(gt + kChunk + 16 * w + g4);
+            beta = *reinterpret_cast<const f4 *>(gt + 2 * kChunk + 16 * w + g4);
+            eq = gt[16 * w + r];
+            fade1 = gt[kChunk - 1];
+        }
+    };
+    auto load_m = [&](int c) {
+        const E *b = reinterpret_cast<const E *>(block_of(c, h) + lay.M);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb == 0 || w >= 2) fM[kb] = load_frag<F32, 3>(b + (16 * w + r) * kChunk + kb * 32 + g8, kChunk * kChunk);
+    };
+    auto load_p = [&](int c) {
+        const E *b = reinterpret_cast<const E *>(block_of(c, h) + lay.P);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb == 0 || w >= 2) fP[kb] = load_frag<F32, NTY>(b + (16 * w + r) * kChunk + kb * 32 + g8, kChunk * kChunk);
+    };
+    auto load_kt = [&](int c) {
+        const E *b = reinterpret_cast<const E *>(block_of(c, KDA ? h : hk * share) + lay.KT);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                fKT[m][kb] = load_frag<F32, KN>(b + ((w * MT + m) * 16 + r) * kChunk + kb * 32 + g8, D * kChunk);
+        if constexpr (KDA) {
+            const float *gt = reinterpret_cast<const float *>(block_of(c, h) + lay.gates) + kChunk;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) fade[m] = *reinterpret_cast<const f4 *>(gt + (w * MT + m) * 16 + g4);
+        }
+    };
+    if (n_chunks > 0) load_kq(0), load_v(0), load_gates(0), load_m(0), load_p(0), load_kt(0);
+
+    for (int c = 0; c < n_chunks; ++c) {
+        const int next = min(c + 1, n_chunks - 1), rows = rows_of(c);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NCT; ++n) SMat::put4(sS, 16 * n + r, (w * MT + m) * 16 + g4, S[m][n]);
+        __syncthreads();
+        // y is formed with its columns as the result's rows: a lane then holds four neighbours of one token
+        f4 ks[NCT], y[NCT];
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) ks[n] = y[n] = f4{};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int n = 0; n < NCT; ++n) {
+                const Frag<F32, 3> fs = SMat::get(sS, 16 * n + r, kb * 32 + g8);
+                ks[n] = mma<3>(fK[kb], fs, ks[n]);
+                y[n] = mma<NTY>(fs, fQ[kb], y[n]);
+            }
+        load_kq(next);
+        f4 e[NCT];
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[n][i] = v[n][i] - (KDA ? ks[n][i] : eg[i] * ks[n][i]);
+            XMat::put4(sX, 16 * n + r, 16 * w + g4, e[n] * beta);
+        }
+        __syncthreads();
+        load_v(next);
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (kb == 0 || w >= 2) e[n] = mma<3>(fM[kb], XMat::get(sX, 16 * n + r, kb * 32 + g8), e[n]);
+            const f4 u = e[n] * beta;
+            if constexpr (KDA) {
+                XMat::put4(sU, 16 * n + r, 16 * w + g4, u);
+            } else {
+                XMat::put4(sU, 16 * n + r, 16 * w + g4, u * ec);
+                YMat::put4(sY, 16 * n + r, 16 * w + g4, u);
+            }
+        }
+        load_m(next);
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NCT; ++n) {
+                S[m][n] = KDA ? S[m][n] * fade[m] : S[m][n] * fade1;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+                    S[m][n] = mma<3>(fKT[m][kb], XMat::get(sU, 16 * n + r, kb * 32 + g8), S[m][n]);
+            }
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) {
+            if (!KDA) y[n] *= eq;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (kb == 0 || w >= 2) {
+                    if constexpr (KDA)
+                        y[n] = mma<NTY>(XMat::get(sU, 16 * n + r, kb * 32 + g8), fP[kb], y[n]);
+                    else
+                        y[n] = mma<NTY>(YMat::get(sY, 16 * n + r, kb * 32 + g8), fP[kb], y[n]);
+                }
+            if (16 * w + r < rows)
+                st_elem4<YF32>(a.y, ((sp.t0 + (int64_t)c * kChunk + 16 * w + r) * a.n_heads + h) * D + c0 + 16 * n + g4, y[n]);
+        }
+        load_kt(next);
+        load_p(next);
+        load_gates(next);
+    }
+    if (a.S_out)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NCT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a.S_out[state + (int64_t)((w * MT + m) * 16 + g4 + i) * D + c0 + 16 * n + r] = S[m][n][i];
+}
+
+template <int D, bool KDA, bool F32, int NTY, bool YF32, int NCT>
+void launch_scan(const SeqArgs &a, hipStream_t stream) {
+    const uint32_t pairs = (uint32_t)a.n_seq * a.n_heads;
+    const uint32_t grid = (pairs + 7) / 8 * 8 * (D / (16 * NCT));
+    hipLaunchKernelGGL((scan_kernel<D, KDA, F32, NTY, YF32, NCT>), dim3(grid), dim3(256), 0, stream, a);
+}
+
+template <int D, bool KDA, bool F32, bool YF32> hipError_t forward(const SeqArgs &a, hipStream_t stream) {
+    constexpr int NTY = YF32 ? 3 : 2;
+    const uint32_t blocks = (uint32_t)(chunk_slots(a.n_tokens, a.n_seq) * a.n_heads);
+    if (a.n_tokens > 0) {
+        if constexpr (KDA)
+            hipLaunchKernelGGL((prep_kda_kernel<D, F32, NTY>), dim3(blocks), dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((prep_gdn_kernel<D, F32, NTY>), dim3(blocks), dim3(256), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    launch_scan<D, KDA, F32, NTY, YF32, 1>(a, stream);
+    return hipGetLastError();
+}
+
+template <int D, bool KDA> hipError_t forward_types(const SeqArgs &a, bool f32, bool y_f32, hipStream_t stream) {
+    if (f32) return y_f32 ? forward<D, KDA, true, true>(a, stream) : forward<D, KDA, true, false>(a, stream);
+    return y_f32 ? forward<D, KDA, false, true>(a, stream) : forward<D, KDA, false, false>(a, stream);
+}
+
+} // namespace
+
+hipError_t launch_chunk_forward(const SeqArgs &a, int d, bool kda, bool f32, bool y_f32, hipStream_t stream) {
+    if (d == 128) return kda ? forward_types<128, true>(a, f32, y_f32, stream) : forward_types<128, false>(a, f32, y_f32, stream);
+    return kda ? forward_types<64, true>(a, f32, y_f32, stream) : forward_types<64, false>(a, f32, y_f32, stream);
+}
+
+} // namespace sqk

@@ -42,6 +42,15 @@ class _Desc(ctypes.Structure):
                 ("head_bits", ctypes.POINTER(ctypes.c_uint8)), ("gate", ctypes.c_int)]
 
 
+class _SeqDesc(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("n_key_heads", ctypes.c_int32), ("d_k", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("n_tokens", ctypes.c_int64), ("gate", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
 def lib():
     """Load libsq.so (built in-tree).  Raises if it is missing: no fallback."""
     global _lib
@@ -92,6 +101,11 @@ def lib():
         L.sq_device_copy.argtypes = [vp, vp, ctypes.c_size_t, vp]
         L.sq_issue_probe.restype = st
         L.sq_issue_probe.argtypes = [ctypes.c_int, vp, vp]
+        pseq, psize = ctypes.POINTER(_SeqDesc), ctypes.POINTER(ctypes.c_size_t)
+        L.sq_chunk_bytes.restype = st
+        L.sq_chunk_bytes.argtypes = [pseq, psize]
+        L.sq_chunk_forward.restype = st
+        L.sq_chunk_forward.argtypes = [pseq] + [vp] * 10 + [ctypes.c_size_t, vp]
         L.sq_last_error.restype = ctypes.c_char_p
         L.sq_last_error.argtypes = []
         L.sq_version.restype = ctypes.c_char_p
@@ -300,6 +314,99 @@ def sq_issue_probe(op: int, sink, stream=None) -> None:
 def sq_arith_selfcheck(counts, stream=None) -> None:
     """counts: a device tensor of 4 int64 that receives the mismatch counts."""
     _check(lib().sq_arith_selfcheck(_ptr(counts), _stream(stream)), "sq_arith_selfcheck")
+
+
+def seq_desc(n_seq, n_tokens, n_heads, d, gate, in_dtype, y_dtype, n_key_heads=None, q_stride=0,
+             k_stride=0, v_stride=0) -> _SeqDesc:
+    """The descriptor of the sequence calls (gate and dtypes: the ABI's codes)."""
+    return _SeqDesc(int(n_seq), int(n_heads), int(n_key_heads or n_heads), int(d), int(d),
+                    int(n_tokens), int(gate), int(in_dtype), int(y_dtype), int(q_stride),
+                    int(k_stride), int(v_stride))
+
+
+def sq_chunk_bytes(desc) -> int:
+    """Bytes of `work` for sq_chunk_forward."""
+    work = ctypes.c_size_t(0)
+    _check(lib().sq_chunk_bytes(ctypes.byref(desc), ctypes.byref(work)), "sq_chunk_bytes")
+    return work.value
+
+
+def sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, work, work_bytes=None,
+                     stream=None) -> None:
+    """q, k, v: pointers, or tensors whose token strides the descriptor holds."""
+    if work_bytes is None:
+        work_bytes = work.numel() * work.element_size()
+    _check(lib().sq_chunk_forward(ctypes.byref(desc), _ptr(cu), _data(q), _data(k), _data(v),
+                                  _ptr(beta), _ptr(g), _ptr(S0), _ptr(y), _ptr(S_out), _ptr(work),
+                                  int(work_bytes), _stream(stream)), "sq_chunk_forward")
+
+
+def _data(x) -> Optional[int]:
+    """Raw pointer of an int or of a tensor of any strides."""
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+class ChunkedDelta:
+    """The gated Delta rule over whole sequences, with its workspace.
+
+    Holds a workspace for batches of up to n_seq sequences and n_tokens tokens
+    in all; a call may bring fewer.  Calls that may overlap (on several
+    streams) need an object each.  q, k: [tokens, n_key_heads, d] and
+    v: [tokens, n_heads, d] may be parts of one wider tensor; every other tensor
+    is contiguous."""
+
+    def __init__(self, n_seq: int, n_tokens: int, n_heads: int, d: int, gate: str = "gdn",
+                 n_key_heads=None, dtype=None, y_dtype=None, device="cuda", train=False):
+        import torch
+        codes = {torch.float32: SQ_F32, torch.bfloat16: SQ_BF16}
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        self.y_dtype = self.dtype if y_dtype is None else y_dtype
+        if self.dtype not in codes or self.y_dtype not in codes:
+            raise TypeError("dtype and y_dtype must be float32 or bfloat16")
+        self.n_seq, self.n_tokens = int(n_seq), int(n_tokens)
+        self.n_heads, self.d = int(n_heads), int(d)
+        self.n_key_heads = int(n_key_heads or n_heads)
+        self.gate = SQ_GATE_KDA if gate == "kda" else SQ_GATE_GDN
+        self._codes = (codes[self.dtype], codes[self.y_dtype])
+        work = sq_chunk_bytes(self._desc(n_seq, n_tokens))
+        self.work = torch.empty(max(256, work), dtype=torch.uint8, device=device)
+
+    def _desc(self, n_seq, n_tokens, qs=0, ks=0, vs=0):
+        return seq_desc(n_seq, n_tokens, self.n_heads, self.d, self.gate, self._codes[0],
+                        self._codes[1], self.n_key_heads, qs, ks, vs)
+
+    def _tokens(self, name, t, n, heads):
+        """Token stride of q, k or v: [n, heads, d] with dense heads."""
+        if t.shape != (n, heads, self.d) or not t.is_cuda or t.dtype != self.dtype:
+            raise ValueError("%s must be a %s device tensor of shape %s, got %s %s" % (
+                name, self.dtype, (n, heads, self.d), t.dtype, tuple(t.shape)))
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.d):
+            raise ValueError("the heads of %s must be dense" % name)
+        return t.stride(0) if n > 1 else 0
+
+    def _args(self, q, k, v, beta, g, cu, S0):
+        import torch
+        n_seq, n, H, d = cu.numel() - 1, q.shape[0], self.n_heads, self.d
+        if n_seq < 0:
+            raise ValueError("cu needs one entry more than there are sequences")
+        desc = self._desc(n_seq, n, self._tokens("q", q, n, self.n_key_heads),
+                          self._tokens("k", k, n, self.n_key_heads), self._tokens("v", v, n, H))
+        _need(cu, "cu", n_seq + 1, (torch.int32,))
+        _need(beta, "beta", n * H, (self.dtype,))
+        _need(g, "g", n * H * (d if self.gate == SQ_GATE_KDA else 1), (self.dtype,))
+        if S0 is not None:
+            _need(S0, "S0", n_seq * H * d * d, (torch.float32,))
+        return desc, n_seq, n
+
+    def forward(self, q, k, v, beta, g, cu, y, S0=None, S_out=None, stream=None):
+        """y and, where given, the final states S_out [n_seq, n_heads, d, d]; cu: int32
+        [n_seq + 1] on the device, the tokens at which the sequences begin and end."""
+        import torch
+        desc, n_seq, n = self._args(q, k, v, beta, g, cu, S0)
+        _need(y, "y", n * self.n_heads * self.d, (self.y_dtype,))
+        if S_out is not None:
+            _need(S_out, "S_out", n_seq * self.n_heads * self.d * self.d, (torch.float32,))
+        sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, self.work, stream=stream)
 
 
 class StatePool:
