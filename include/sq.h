@@ -368,6 +368,46 @@ sq_status sq_chunk_forward(const sq_seq_desc *desc, const int32_t *cu, const voi
                            const float *S0, void *y, float *S_out, void *work, size_t work_bytes,
                            hipStream_t stream);
 
+/* Tokens of the longest window. */
+#define SQ_WINDOW_MAX 16
+
+/* A window of tokens per request, read against the pool without changing it
+ * (the recurrence of sq_decode_step over `length` tokens; the pages describe
+ * one token at a time, "Paper Explained: STEPQuant" (ta-paperlens), section "The
+ * mechanism: rewriting state with the delta rule"): for drafted tokens, which the
+ * target model reads all at once and of which it then keeps some.
+ *   length: tokens per request, 1 .. SQ_WINDOW_MAX;
+ *   lens:   DEVICE int32 [n], or NULL for `length` everywhere: how many of a
+ *           request's tokens count (held to [0, length]); the others write
+ *           nothing and their y is 0.
+ *   q, k: [n, length, n_key_heads, d_k]   v: [n, length, n_heads, d_v]
+ *   beta: [n, length, n_heads]            y: [n, length, n_heads, d_v]
+ *   g: [n, length, n_heads] for GDN, [n, length, n_heads, d_k] for KDA
+ *   y:      output, or NULL (q may then be NULL too);
+ *   S_out:  fp32 [n, n_heads, d_k, d_v], the state after a request's last
+ *           token that counts, or NULL.  sq_quant_state(pool, slot_idx, n, S_out,
+ *           ...) stores it: one requantization for the whole window.
+ * A speculative step is: one call for y; sq_verify_draft; one call with lens =
+ * the accepted tokens, y = NULL and S_out; sq_quant_state.
+ * Head h reads the key head h / (n_heads / n_key_heads) of q and k.
+ * Arithmetic: as sq_chunk_forward; the state is exactly what the record
+ * stands for.  Errors: as sq_decode_step, and SQ_EINVAL for a length or key head
+ * count outside its range or if y and S_out are both NULL. */
+sq_status sq_window_update(const sq_pool *pool, const int32_t *slot_idx, int32_t n, int32_t length,
+                           const int32_t *lens, int32_t n_key_heads, const void *q, const void *k,
+                           const void *v, const void *beta, const void *g, sq_dtype in_dtype,
+                           void *y, sq_dtype y_dtype, float *S_out, hipStream_t stream);
+
+/* The same on an fp32 state pool state_pool [n_slots, n_heads, d_k, d_v]
+ * (bayesiansapien page, TL;DR: the state is kept per request in FP32), which
+ * is only read.  Errors: as sq_f32_decode_step and sq_window_update. */
+sq_status sq_f32_window_update(const float *state_pool, int32_t n_slots, int32_t n_heads,
+                               int32_t n_key_heads, int32_t d_k, int32_t d_v, sq_gate gate,
+                               const int32_t *slot_idx, int32_t n, int32_t length,
+                               const int32_t *lens, const void *q, const void *k, const void *v,
+                               const void *beta, const void *g, sq_dtype in_dtype, void *y,
+                               sq_dtype y_dtype, float *S_out, hipStream_t stream);
+
 /* Debug check: copy slot_idx[0..n) (device) to the host, synchronising the
  * stream, and verify every entry is in [0, n_slots) and distinct.  Returns
  * SQ_EINVAL with the first offending index in sq_last_error() otherwise. */

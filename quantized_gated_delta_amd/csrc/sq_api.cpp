@@ -16,6 +16,7 @@
 
 #include "sq_internal.h"
 #include "sq_seq.h"
+#include "sq_window.h"
 
 struct sq_pool {
     sq_pool_desc desc;          // head_bits points at bits below
@@ -245,6 +246,41 @@ sq_status check_seq_io(const sq_seq_desc *d, const int32_t *cu, const void *q, c
         (st = check_io("beta", beta, any)) || (st = check_io("g", g, any)) || (st = check_io("S0", S0, S0 != nullptr)))
         return st;
     return SQ_OK;
+}
+
+// What both window calls check besides the pool.
+sq_status check_window(int32_t length, const int32_t *lens, int32_t n_heads, int32_t n_key_heads, const void *q,
+                       const void *k, const void *v, const void *beta, const void *g, sq_dtype in_dtype,
+                       const void *y, sq_dtype y_dtype, const float *S_out) {
+    if (length < 1 || length > SQ_WINDOW_MAX)
+        return fail(SQ_EINVAL, "length must be in [1, %d] (got %d)", SQ_WINDOW_MAX, length);
+    if (n_key_heads < 1 || n_heads % n_key_heads != 0)
+        return fail(SQ_EINVAL, "n_key_heads = %d is not a divisor of n_heads = %d", n_key_heads, n_heads);
+    if (in_dtype != SQ_F32 && in_dtype != SQ_BF16)
+        return fail(SQ_EINVAL, "in_dtype must be SQ_F32 or SQ_BF16 (got %d)", (int)in_dtype);
+    if (y_dtype != SQ_F32 && y_dtype != SQ_BF16)
+        return fail(SQ_EINVAL, "y_dtype must be SQ_F32 or SQ_BF16 (got %d)", (int)y_dtype);
+    if (!y && !S_out) return fail(SQ_EINVAL, "y and S_out are both NULL");
+    if (lens && !aligned(lens, 4)) return fail(SQ_EINVAL, "lens is not 4-byte aligned");
+    sq_status st;
+    if ((st = check_io("q", q, y != nullptr)) || (st = check_io("k", k, true)) || (st = check_io("v", v, true)) ||
+        (st = check_io("beta", beta, true)) || (st = check_io("g", g, true)) || (st = check_io("y", y, y != nullptr)) ||
+        (st = check_io("S_out", S_out, S_out != nullptr)))
+        return st;
+    return SQ_OK;
+}
+
+sqk::WindowArgs window_args(const void *base, int64_t slot_stride, const int32_t *slot_idx, int32_t n, int32_t length,
+                            const int32_t *lens, int32_t n_heads, int32_t n_key_heads, const void *q, const void *k,
+                            const void *v, const void *beta, const void *g, void *y, float *S_out) {
+    sqk::WindowArgs a;
+    a.base = static_cast<const uint8_t *>(base);
+    a.slot_stride = slot_stride;
+    a.slot = slot_idx; a.lens = lens;
+    a.n = n; a.length = length; a.n_heads = n_heads; a.n_key_heads = n_key_heads;
+    a.q = q; a.k = k; a.v = v; a.beta = beta; a.g = g;
+    a.y = y; a.S_out = S_out;
+    return a;
 }
 
 } // namespace
@@ -509,6 +545,50 @@ sq_status sq_chunk_forward(const sq_seq_desc *desc, const int32_t *cu, const voi
     const hipError_t e = sqk::launch_chunk_forward(a, desc->d_k, desc->gate == SQ_GATE_KDA, desc->in_dtype == SQ_F32,
                                                    desc->y_dtype == SQ_F32, stream);
     return e == hipSuccess ? SQ_OK : hip_fail(e, "chunk_forward launch");
+}
+
+sq_status sq_window_update(const sq_pool *pool, const int32_t *slot_idx, int32_t n, int32_t length,
+                           const int32_t *lens, int32_t n_key_heads, const void *q, const void *k, const void *v,
+                           const void *beta, const void *g, sq_dtype in_dtype, void *y, sq_dtype y_dtype,
+                           float *S_out, hipStream_t stream) {
+    sq_status st = check_rows(pool, slot_idx, n);
+    if (st) return st;
+    if (n == 0) return SQ_OK;
+    if ((st = check_window(length, lens, pool->desc.n_heads, n_key_heads, q, k, v, beta, g, in_dtype, y, y_dtype, S_out)))
+        return st;
+    if (debug_slots() && (st = sq_check_slots(pool, slot_idx, n, stream))) return st;
+    const sqk::WindowArgs a = window_args(pool->view.base, pool->view.slot_stride, slot_idx, n, length, lens,
+                                          pool->desc.n_heads, n_key_heads, q, k, v, beta, g, y, S_out);
+    const hipError_t e = sqk::launch_window(a, &pool->tab, pool->desc.d_k, pool->desc.gate == SQ_GATE_KDA,
+                                            in_dtype == SQ_F32, y_dtype == SQ_F32, stream);
+    return e == hipSuccess ? SQ_OK : hip_fail(e, "window_update launch");
+}
+
+sq_status sq_f32_window_update(const float *state_pool, int32_t n_slots, int32_t n_heads, int32_t n_key_heads,
+                               int32_t d_k, int32_t d_v, sq_gate gate, const int32_t *slot_idx, int32_t n,
+                               int32_t length, const int32_t *lens, const void *q, const void *k, const void *v,
+                               const void *beta, const void *g, sq_dtype in_dtype, void *y, sq_dtype y_dtype,
+                               float *S_out, hipStream_t stream) {
+    if (n_slots < 1) return fail(SQ_EINVAL, "n_slots must be >= 1 (got %d)", n_slots);
+    if (n_heads < 1) return fail(SQ_EINVAL, "n_heads must be >= 1 (got %d)", n_heads);
+    if (d_k != d_v) return fail(SQ_EUNSUPPORTED, "d_k must equal d_v (got %d, %d)", d_k, d_v);
+    if (d_k != 64 && d_k != 128) return fail(SQ_EUNSUPPORTED, "d must be 64 or 128 (got %d)", d_k);
+    if (gate != SQ_GATE_GDN && gate != SQ_GATE_KDA)
+        return fail(SQ_EINVAL, "gate must be SQ_GATE_GDN or SQ_GATE_KDA (got %d)", (int)gate);
+    if (n < 0) return fail(SQ_EINVAL, "n must be >= 0 (got %d)", n);
+    if (n > n_slots) return fail(SQ_EINVAL, "n = %d exceeds n_slots = %d", n, n_slots);
+    if ((int64_t)n * n_heads > 0x7FFFFFFFll) return fail(SQ_EUNSUPPORTED, "grid too large");
+    if (n == 0) return SQ_OK;
+    if (!slot_idx) return fail(SQ_EINVAL, "slot_idx is NULL");
+    sq_status st;
+    if ((st = check_io("state_pool", state_pool, true)) ||
+        (st = check_window(length, lens, n_heads, n_key_heads, q, k, v, beta, g, in_dtype, y, y_dtype, S_out)))
+        return st;
+    const sqk::WindowArgs a = window_args(state_pool, (int64_t)n_heads * d_k * d_v, slot_idx, n, length, lens, n_heads,
+                                          n_key_heads, q, k, v, beta, g, y, S_out);
+    const hipError_t e = sqk::launch_window(a, nullptr, d_k, gate == SQ_GATE_KDA, in_dtype == SQ_F32,
+                                            y_dtype == SQ_F32, stream);
+    return e == hipSuccess ? SQ_OK : hip_fail(e, "f32_window_update launch");
 }
 
 sq_status sq_device_copy(const void *src, void *dst, size_t bytes, hipStream_t stream) {

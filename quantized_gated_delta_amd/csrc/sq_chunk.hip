@@ -82,22 +82,21 @@ __global__ __launch_bounds__(256) void prep_kda_kernel(SeqArgs a) {
 
     load_kda<D, F32>(a, t0, rows, h, hk, s, t);
     for (int u = t; u < kChunk * D / 8; u += 256) {
-        const int row = u / (D / 8), c8 = u % (D / 8) * 8;
+        const int row = u / (2 * D) * 16 + (u & 15), c8 = u % (2 * D) / 16 * 8;
         float v[8];
         decayed8<D, F32, 1>(s, s.k, row, c8, 0, v);
-        store8<F32, 3>(reinterpret_cast<E *>(out + lay.K) + row * D + c8, kChunk * D, v);
+        Operand<F32, 3, D / 32>::put8(reinterpret_cast<E *>(out + lay.K), row, c8, v);
         decayed8<D, F32, 1>(s, s.q, row, c8, 0, v);
-        store8<F32, NTP>(reinterpret_cast<E *>(out + lay.Q) + row * D + c8, kChunk * D, v);
+        Operand<F32, NTP, D / 32>::put8(reinterpret_cast<E *>(out + lay.Q), row, c8, v);
     }
     for (int u = t; u < kChunk * D / 8; u += 256) {
-        // eight tokens of a channel; consecutive lanes take consecutive channels
-        const int ch = u % D, k8 = u / D * 8;
+        const int ch = (u >> 7) * 16 + (u & 15), k8 = (u >> 4 & 7) * 8;  // eight tokens of a channel
         constexpr int GROW = KdaLds<D, F32>::GROW, ROW = KdaLds<D, F32>::ROW;
         float after = 0.f, v[8];
         for (int b = (k8 >> 4) + 1; b < 4; ++b) after += s.L[(16 * b + 15) * GROW + ch];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = ld_elem<F32>(s.k, (k8 + i) * ROW + ch) * exp_of(s.R[(k8 + i) * GROW + ch] + after);
-        store8<F32, 3>(reinterpret_cast<E *>(out + lay.KT) + ch * kChunk + k8, D * kChunk, v);
+        Operand<F32, 3, 2>::put8(reinterpret_cast<E *>(out + lay.KT), ch, k8, v);
     }
     float *gt = reinterpret_cast<float *>(out + lay.gates);
     if (t < kChunk) gt[t] = s.beta[t];
@@ -162,8 +161,9 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
     Frag<F32, QN> fQ[KB];
     Frag<F32, 3> fM[2];
     Frag<F32, NTY> fP[2];
-    f4 v[NCT], eg{}, ec{}, beta{}, fade[MT];
-    float fade1 = 1.f, eq = 1.f;
+    f4 v[NCT];
+    // the gates' factors are needed early in a chunk: they are fetched a whole chunk ahead
+    struct Gates { f4 eg, ec, beta, fade[MT]; float fade1, eq; } gt{}, gt_next{};
 
     auto block_of = [&](int c, int head) { return a.work + ((sp.slot0 + c) * a.n_heads + head) * lay.block; };
     auto rows_of = [&](int c) { return min(kChunk, sp.len - c * kChunk); };
@@ -172,9 +172,8 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
             const uint8_t *b = block_of(c, h);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const int at = (16 * w + r) * D + kb * 32 + g8;
-                fK[kb] = load_frag<F32, KN>(reinterpret_cast<const E *>(b + lay.K) + at, kChunk * D);
-                fQ[kb] = load_frag<F32, QN>(reinterpret_cast<const E *>(b + lay.Q) + at, kChunk * D);
+                fK[kb] = Operand<F32, KN, KB>::get(reinterpret_cast<const E *>(b + lay.K), w, kb, l);
+                fQ[kb] = Operand<F32, QN, KB>::get(reinterpret_cast<const E *>(b + lay.Q), w, kb, l);
             }
         } else {
             // past the end: the last token again; its beta is 0 there and its y is not stored
@@ -197,28 +196,32 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         }
     };
     auto load_gates = [&](int c) {
-        const float *gt = reinterpret_cast<const float *>(block_of(c, h) + lay.gates);
+        const float *p = reinterpret_cast<const float *>(block_of(c, h) + lay.gates);
+        Gates x{};
         if constexpr (KDA) {
-            beta = *reinterpret_cast<const f4 *>(gt + 16 * w + g4);
+            x.beta = *reinterpret_cast<const f4 *>(p + 16 * w + g4);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) x.fade[m] = *reinterpret_cast<const f4 *>(p + kChunk + (w * MT + m) * 16 + g4);
         } else {
-            eg = *reinterpret_cast<const f4 *>(gt + 16 * w + g4);
-            ec = *reinterpret_cast<const f4 *>(gt + kChunk + 16 * w + g4);
-            beta = *reinterpret_cast<const f4 *>(gt + 2 * kChunk + 16 * w + g4);
-            eq = gt[16 * w + r];
-            fade1 = gt[kChunk - 1];
+            x.eg = *reinterpret_cast<const f4 *>(p + 16 * w + g4);
+            x.ec = *reinterpret_cast<const f4 *>(p + kChunk + 16 * w + g4);
+            x.beta = *reinterpret_cast<const f4 *>(p + 2 * kChunk + 16 * w + g4);
+            x.eq = p[16 * w + r];
+            x.fade1 = p[kChunk - 1];
         }
+        return x;
     };
     auto load_m = [&](int c) {
         const E *b = reinterpret_cast<const E *>(block_of(c, h) + lay.M);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
-            if (kb == 0 || w >= 2) fM[kb] = load_frag<F32, 3>(b + (16 * w + r) * kChunk + kb * 32 + g8, kChunk * kChunk);
+            if (kb == 0 || w >= 2) fM[kb] = Operand<F32, 3, 2>::get(b, w, kb, l);
     };
     auto load_p = [&](int c) {
         const E *b = reinterpret_cast<const E *>(block_of(c, h) + lay.P);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
-            if (kb == 0 || w >= 2) fP[kb] = load_frag<F32, NTY>(b + (16 * w + r) * kChunk + kb * 32 + g8, kChunk * kChunk);
+            if (kb == 0 || w >= 2) fP[kb] = Operand<F32, NTY, 2>::get(b, w, kb, l);
     };
     auto load_kt = [&](int c) {
         const E *b = reinterpret_cast<const E *>(block_of(c, KDA ? h : hk * share) + lay.KT);
@@ -226,17 +229,13 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
-                fKT[m][kb] = load_frag<F32, KN>(b + ((w * MT + m) * 16 + r) * kChunk + kb * 32 + g8, D * kChunk);
-        if constexpr (KDA) {
-            const float *gt = reinterpret_cast<const float *>(block_of(c, h) + lay.gates) + kChunk;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) fade[m] = *reinterpret_cast<const f4 *>(gt + (w * MT + m) * 16 + g4);
-        }
+                fKT[m][kb] = Operand<F32, KN, 2>::get(b, w * MT + m, kb, l);
     };
-    if (n_chunks > 0) load_kq(0), load_v(0), load_gates(0), load_m(0), load_p(0), load_kt(0);
+    if (n_chunks > 0) gt = load_gates(0), load_kq(0), load_v(0), load_m(0), load_p(0), load_kt(0);
 
     for (int c = 0; c < n_chunks; ++c) {
         const int next = min(c + 1, n_chunks - 1), rows = rows_of(c);
+        gt_next = load_gates(next);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -259,8 +258,8 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[n][i] = v[n][i] - (KDA ? ks[n][i] : eg[i] * ks[n][i]);
-            XMat::put4(sX, 16 * n + r, 16 * w + g4, e[n] * beta);
+            for (int i = 0; i < 4; ++i) e[n][i] = v[n][i] - (KDA ? ks[n][i] : gt.eg[i] * ks[n][i]);
+            XMat::put4(sX, 16 * n + r, 16 * w + g4, e[n] * gt.beta);
         }
         __syncthreads();
         load_v(next);
@@ -269,11 +268,11 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
                 if (kb == 0 || w >= 2) e[n] = mma<3>(fM[kb], XMat::get(sX, 16 * n + r, kb * 32 + g8), e[n]);
-            const f4 u = e[n] * beta;
+            const f4 u = e[n] * gt.beta;
             if constexpr (KDA) {
                 XMat::put4(sU, 16 * n + r, 16 * w + g4, u);
             } else {
-                XMat::put4(sU, 16 * n + r, 16 * w + g4, u * ec);
+                XMat::put4(sU, 16 * n + r, 16 * w + g4, u * gt.ec);
                 YMat::put4(sY, 16 * n + r, 16 * w + g4, u);
             }
         }
@@ -283,14 +282,14 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NCT; ++n) {
-                S[m][n] = KDA ? S[m][n] * fade[m] : S[m][n] * fade1;
+                S[m][n] = KDA ? S[m][n] * gt.fade[m] : S[m][n] * gt.fade1;
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
                     S[m][n] = mma<3>(fKT[m][kb], XMat::get(sU, 16 * n + r, kb * 32 + g8), S[m][n]);
             }
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
-            if (!KDA) y[n] *= eq;
+            if (!KDA) y[n] *= gt.eq;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
                 if (kb == 0 || w >= 2) {
@@ -304,7 +303,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         }
         load_kt(next);
         load_p(next);
-        load_gates(next);
+        gt = gt_next;
     }
     if (a.S_out)
 #pragma unroll

@@ -72,19 +72,16 @@ __device__ __forceinline__ void solve_column(const float *sB, const float *sBeta
     }
 }
 
-// Planes of a 64 x 64 matrix in LDS; TRANS: of its transpose.
+// A 64 x 64 matrix in LDS as an operand; TRANS: its transpose.
 template <bool F32, int N, bool TRANS>
 __device__ __forceinline__ void write_square(const float *s, Elem<F32> *out, int t) {
-    const int row = t >> 2, c0 = (t & 3) * 16;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int n = 0; n < 2; ++n) {
+        const int u = t + 256 * n, row = (u >> 7) * 16 + (u & 15), k = (u >> 4 & 7) * 8;
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + 8 * half + i;
-            x[i] = TRANS ? s[c * kBRow + row] : s[row * kBRow + c];
-        }
-        store8<F32, N>(out + row * kChunk + c0 + 8 * half, kChunk * kChunk, x);
+        for (int i = 0; i < 8; ++i) x[i] = TRANS ? s[(k + i) * kBRow + row] : s[row * kBRow + k + i];
+        Operand<F32, N, 2>::put8(out, row, k, x);
     }
 }
 
@@ -118,19 +115,11 @@ __device__ __forceinline__ void write_transposed(const void *base, int64_t strid
     }
     __syncthreads();
     for (int u = t; u < D * 8; u += 256) {
-        const int ch = u >> 3, k = (u & 7) * 8;
-        if constexpr (F32) {
-            float x[8];
+        const int ch = (u >> 7) * 16 + (u & 15), k = (u >> 4 & 7) * 8;
+        float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = s[(k + i) * ROW + ch];
-            store8<true, 1>(out + ch * kChunk + k, 0, x);
-        } else {
-            uint32_t x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = (uint32_t)s[(k + 2 * i) * ROW + ch] | (uint32_t)s[(k + 2 * i + 1) * ROW + ch] << 16;
-            *reinterpret_cast<uint4 *>(out + ch * kChunk + k) = make_uint4(x[0], x[1], x[2], x[3]);
-        }
+        for (int i = 0; i < 8; ++i) x[i] = ld_elem<F32>(s, (k + i) * ROW + ch);
+        Operand<F32, 1, 2>::put8(out, ch, k, x);
     }
     __syncthreads();
 }

@@ -182,17 +182,39 @@ template <bool F32> __device__ __forceinline__ void st_elem4(void *p, int64_t i,
     }
 }
 
-// N terms (or the fp32 value) of eight consecutive elements at p, 16-byte aligned.
-template <bool F32, int N> __device__ __forceinline__ void store8(Elem<F32> *p, int64_t plane, const float (&x)[8]) {
-    if constexpr (F32) {
-        *reinterpret_cast<f4 *>(p) = f4{x[0], x[1], x[2], x[3]};
-        *reinterpret_cast<f4 *>(p + 4) = f4{x[4], x[5], x[6], x[7]};
-    } else {
-        const Frag<false, N> f = make_frag<false, N>(x);
+// Operands in the workspace lie as the fragments are read: for every 16 rows
+// and 32 contracted elements, the terms one after another, each 64 lanes of
+// 16 bytes (fp32: two halves of 64 lanes of 16 bytes).  A wave's load is then 1 KB
+// of consecutive bytes; rows in memory order would make it 16 half cache lines.
+// KB: fragments along the contracted axis.
+template <bool F32, int N, int KB> struct Operand {
+    static constexpr int SIZE = F32 ? 512 : 512 * N;  // elements of a fragment
+    __device__ __forceinline__ static Frag<F32, N> get(const Elem<F32> *m, int tile, int kb, int lane) {
+        Frag<F32, N> f;
+        const Elem<F32> *p = m + (tile * KB + kb) * SIZE;
+        if constexpr (F32) {
+            f.v[0] = *reinterpret_cast<const f4 *>(p + 4 * lane);
+            f.v[1] = *reinterpret_cast<const f4 *>(p + 256 + 4 * lane);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<bf8 *>(p + i * plane) = f.t[i];
+            for (int i = 0; i < N; ++i) f.t[i] = *reinterpret_cast<const bf8 *>(p + 512 * i + 8 * lane);
+        }
+        return f;
     }
-}
+    // row `row`, contracted elements k .. k + 7 (k a multiple of 8)
+    __device__ __forceinline__ static void put8(Elem<F32> *m, int row, int k, const float (&x)[8]) {
+        const int lane = (k & 31) / 8 * 16 + (row & 15);
+        Elem<F32> *p = m + ((row >> 4) * KB + (k >> 5)) * SIZE;
+        if constexpr (F32) {
+            *reinterpret_cast<f4 *>(p + 4 * lane) = f4{x[0], x[1], x[2], x[3]};
+            *reinterpret_cast<f4 *>(p + 256 + 4 * lane) = f4{x[4], x[5], x[6], x[7]};
+        } else {
+            const Frag<false, N> f = make_frag<false, N>(x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) *reinterpret_cast<bf8 *>(p + 512 * i + 8 * lane) = f.t[i];
+        }
+    }
+};
 
 // exp(x) for x <= 0 (or moderate x > 0): the hardware exponential of x log2(e)
 // with the rounding error of that product put back; relative error about 2^-22.

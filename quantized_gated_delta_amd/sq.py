@@ -106,6 +106,13 @@ def lib():
         L.sq_chunk_bytes.argtypes = [pseq, psize]
         L.sq_chunk_forward.restype = st
         L.sq_chunk_forward.argtypes = [pseq] + [vp] * 10 + [ctypes.c_size_t, vp]
+        L.sq_window_update.restype = st
+        L.sq_window_update.argtypes = [vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp,
+                                       ctypes.c_int, vp, ctypes.c_int, vp, vp]
+        L.sq_f32_window_update.restype = st
+        L.sq_f32_window_update.argtypes = [vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, i32,
+                                           i32, vp, vp, vp, vp, vp, vp, ctypes.c_int, vp,
+                                           ctypes.c_int, vp, vp]
         L.sq_last_error.restype = ctypes.c_char_p
         L.sq_last_error.argtypes = []
         L.sq_version.restype = ctypes.c_char_p
@@ -346,6 +353,67 @@ def _data(x) -> Optional[int]:
     return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
+def sq_window_update(handle, slot_idx, n: int, length: int, lens, n_key_heads: int, q, k, v, beta,
+                     g, y, S_out, in_dtype=None, y_dtype=None, stream=None) -> None:
+    in_dtype = _dtype_code(k) if in_dtype is None else in_dtype
+    y_dtype = (in_dtype if y is None else _dtype_code(y)) if y_dtype is None else y_dtype
+    _check(lib().sq_window_update(handle, _ptr(slot_idx), int(n), int(length), _ptr(lens),
+                                  int(n_key_heads), _ptr(q), _ptr(k), _ptr(v), _ptr(beta),
+                                  _ptr(g), in_dtype, _ptr(y), y_dtype, _ptr(S_out),
+                                  _stream(stream)), "sq_window_update")
+
+
+def sq_f32_window_update(state, n_slots, n_heads, n_key_heads, d_k, d_v, gate, slot_idx, n, length,
+                         lens, q, k, v, beta, g, y, S_out, in_dtype=None, y_dtype=None,
+                         stream=None) -> None:
+    in_dtype = _dtype_code(k) if in_dtype is None else in_dtype
+    y_dtype = (in_dtype if y is None else _dtype_code(y)) if y_dtype is None else y_dtype
+    _check(lib().sq_f32_window_update(_ptr(state), int(n_slots), int(n_heads), int(n_key_heads),
+                                      int(d_k), int(d_v), int(gate), _ptr(slot_idx), int(n),
+                                      int(length), _ptr(lens), _ptr(q), _ptr(k), _ptr(v),
+                                      _ptr(beta), _ptr(g), in_dtype, _ptr(y), y_dtype,
+                                      _ptr(S_out), _stream(stream)), "sq_f32_window_update")
+
+
+SQ_WINDOW_MAX = 16
+
+
+def _window_need(slot_idx, q, k, v, beta, g, y, S_out, lens, H, d, kda):
+    """Shapes of a window's tensors; returns n, length and the key heads."""
+    import torch
+    n = slot_idx.numel()
+    if k.dim() != 4 or k.shape[0] != n:
+        raise ValueError("k must be [n, length, n_key_heads, d]")
+    length, hk, dt = k.shape[1], k.shape[2], (k.dtype,)
+    if k.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("k must be float32 or bfloat16")
+    _need(slot_idx, "slot_idx", n, (torch.int32,))
+    _need(k, "k", n * length * hk * d, dt)
+    if y is not None:
+        _need(q, "q", n * length * hk * d, dt)
+        _need(y, "y", n * length * H * d, (torch.float32, torch.bfloat16))
+    _need(v, "v", n * length * H * d, dt)
+    _need(beta, "beta", n * length * H, dt)
+    _need(g, "g", n * length * H * (d if kda else 1), dt)
+    if S_out is not None:
+        _need(S_out, "S_out", n * H * d * d, (torch.float32,))
+    if lens is not None:
+        _need(lens, "lens", n, (torch.int32,))
+    return n, length, hk
+
+
+def f32_window_update(state, slot_idx, q, k, v, beta, g, y=None, S_out=None, lens=None, gate="gdn",
+                      stream=None) -> None:
+    """A window of tokens per request on an fp32 state pool [n_slots, n_heads, d, d], which is
+    only read; see StatePool.window_update."""
+    import torch
+    n_slots, H, d, _ = state.shape
+    _need(state, "state", n_slots * H * d * d, (torch.float32,))
+    n, length, hk = _window_need(slot_idx, q, k, v, beta, g, y, S_out, lens, H, d, gate == "kda")
+    sq_f32_window_update(state, n_slots, H, hk, d, d, SQ_GATE_KDA if gate == "kda" else SQ_GATE_GDN,
+                         slot_idx, n, length, lens, q, k, v, beta, g, y, S_out, stream=stream)
+
+
 class ChunkedDelta:
     """The gated Delta rule over whole sequences, with its workspace.
 
@@ -488,6 +556,19 @@ class StatePool:
         self._step_args(slot_idx, q, k, v, beta, g, y)
         sq_split_step_noalloc(self.handle, slot_idx, slot_idx.numel(), q, k, v, beta, g, y,
                               stream=stream)
+
+    def window_update(self, slot_idx, q, k, v, beta, g, y=None, S_out=None, lens=None,
+                      stream=None):
+        """A window of up to SQ_WINDOW_MAX tokens per request, the pool only read.
+
+        q, k: [n, length, n_key_heads, d], v: [n, length, H, d]; y: the read-outs, S_out: the
+        fp32 states after each request's first lens tokens (all of them where lens is None);
+        store them with quant_state(slot_idx, S_out).  Either of y and S_out may be None (q too
+        where y is)."""
+        n, length, hk = _window_need(slot_idx, q, k, v, beta, g, y, S_out, lens, self.n_heads,
+                                     self.d, self.gate == SQ_GATE_KDA)
+        sq_window_update(self.handle, slot_idx, n, length, lens, hk, q, k, v, beta, g, y, S_out,
+                         stream=stream)
 
     def check_slots(self, slot_idx, stream=None):
         sq_check_slots(self.handle, slot_idx, slot_idx.numel(), stream)
