@@ -408,6 +408,49 @@ sq_status sq_f32_window_update(const float *state_pool, int32_t n_slots, int32_t
                                const void *beta, const void *g, sq_dtype in_dtype, void *y,
                                sq_dtype y_dtype, float *S_out, hipStream_t stream);
 
+/* Most drafted tokens per request of sq_verify_draft. */
+#define SQ_DRAFT_MAX 32
+
+/* Bytes that sq_verify_draft needs as `work` for n requests of up to m drafted
+ * tokens.  Errors: SQ_EINVAL for negative n or m outside [1, SQ_DRAFT_MAX]. */
+sq_status sq_verify_bytes(int32_t n, int32_t m, size_t *bytes);
+
+/* How many drafted tokens of each request stand against the target's
+ * probabilities, and the token after them, from given random numbers (the step
+ * that turns the read-outs of sq_window_update, through the model's output
+ * layer, into tokens; the pages describe no drafting).
+ *   target: logits [n, m + 1, vocab], in logits_dtype; row i judges drafted token i,
+ *           the row after a request's last one gives the token after them;
+ *   draft:  the draft model's logits [n, m, vocab], or NULL where the draft was
+ *           certain of its tokens (looked up, or greedy);
+ *   target_stride, draft_stride: elements from one row to the next (0: vocab);
+ *   tokens: int32 [n, m], the drafts; lens: int32 [n] how many of them count
+ *           (held to [0, m]), or NULL for m;
+ *   accept_u: fp32 [n, m] uniform in [0, 1); sample_e: fp32 [n, vocab] positive,
+ *           exponentially distributed; both may be NULL at temperature 0;
+ *   accepted, next: int32 [n], outputs.
+ * With p, q the softmax of target / temperature and draft / temperature (fp32;
+ * q = 1 at the drafted token without draft logits): drafted token x_i stands if all before it
+ * do and accept_u_i * q_i(x_i) < p_i(x_i).  next is the argmax of r / sample_e, where
+ * r = max(p - q, 0) in the first rejected row and p in the row after the last
+ * draft where all stood; r = p if that leaves nothing.  temperature = 0: a token
+ * stands if it is the argmax of its target row; next is the argmax.  Ties go
+ * to the lower token.  A NaN logit counts as minus infinity; a row without any
+ * logit above minus infinity accepts nothing and gives next = -1; drafted tokens
+ * outside [0, vocab) are rejected.  n = 0 is a no-op.
+ *   work: DEVICE scratch of sq_verify_bytes, 256-byte aligned; calls that may
+ *         overlap need one each.
+ * Errors: SQ_EINVAL for NULL or misaligned pointers (4 bytes; logits the size
+ * of their type), m, vocab or a stride out of range, a negative or non-finite
+ * temperature; SQ_ENOMEM if work_bytes is too small; SQ_EUNSUPPORTED if
+ * n * (2 m + 1) exceeds the grid limit of 65535 rows. */
+sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *target,
+                          int64_t target_stride, const void *draft, int64_t draft_stride,
+                          sq_dtype logits_dtype, const int32_t *tokens, const int32_t *lens,
+                          const float *accept_u, const float *sample_e, float temperature,
+                          int32_t *accepted, int32_t *next, void *work, size_t work_bytes,
+                          hipStream_t stream);
+
 /* Debug check: copy slot_idx[0..n) (device) to the host, synchronising the
  * stream, and verify every entry is in [0, n_slots) and distinct.  Returns
  * SQ_EINVAL with the first offending index in sq_last_error() otherwise. */

@@ -7,6 +7,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -16,6 +17,7 @@
 
 #include "sq_internal.h"
 #include "sq_seq.h"
+#include "sq_verify.h"
 #include "sq_window.h"
 
 struct sq_pool {
@@ -589,6 +591,58 @@ sq_status sq_f32_window_update(const float *state_pool, int32_t n_slots, int32_t
     const hipError_t e = sqk::launch_window(a, nullptr, d_k, gate == SQ_GATE_KDA, in_dtype == SQ_F32,
                                             y_dtype == SQ_F32, stream);
     return e == hipSuccess ? SQ_OK : hip_fail(e, "f32_window_update launch");
+}
+
+sq_status sq_verify_bytes(int32_t n, int32_t m, size_t *bytes) {
+    if (n < 0) return fail(SQ_EINVAL, "n must be >= 0 (got %d)", n);
+    if (m < 1 || m > SQ_DRAFT_MAX) return fail(SQ_EINVAL, "m must be in [1, %d] (got %d)", SQ_DRAFT_MAX, m);
+    if (!bytes) return fail(SQ_EINVAL, "bytes is NULL");
+    *bytes = sqk::verify_layout(n, m).bytes;
+    return SQ_OK;
+}
+
+sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *target, int64_t target_stride,
+                          const void *draft, int64_t draft_stride, sq_dtype logits_dtype, const int32_t *tokens,
+                          const int32_t *lens, const float *accept_u, const float *sample_e, float temperature,
+                          int32_t *accepted, int32_t *next, void *work, size_t work_bytes, hipStream_t stream) {
+    size_t need = 0;
+    sq_status st = sq_verify_bytes(n, m, &need);
+    if (st) return st;
+    if (vocab < 1 || vocab > 0x7FFFFFFF - 65536) return fail(SQ_EINVAL, "vocab = %d is out of range", vocab);
+    if (logits_dtype != SQ_F32 && logits_dtype != SQ_BF16)
+        return fail(SQ_EINVAL, "logits_dtype must be SQ_F32 or SQ_BF16 (got %d)", (int)logits_dtype);
+    if (!(temperature >= 0.f) || std::isinf(temperature) || (temperature > 0.f && std::isinf(1.f / temperature)))
+        return fail(SQ_EINVAL, "temperature = %g must be 0 or a positive number", (double)temperature);
+    if ((target_stride && target_stride < vocab) || (draft && draft_stride && draft_stride < vocab) ||
+        target_stride > INT64_MAX / 16 / 65536 || draft_stride > INT64_MAX / 16 / 65536)
+        return fail(SQ_EINVAL, "a row stride must be 0 or at least vocab = %d", vocab);
+    if (n == 0) return SQ_OK;
+    if ((int64_t)n * (2 * m + 1) > 65535) return fail(SQ_EUNSUPPORTED, "n * (2 m + 1) exceeds 65535 rows");
+    const bool greedy = temperature == 0.f;
+    const uintptr_t e = logits_dtype == SQ_F32 ? 4 : 2;
+    const struct { const char *name; const void *p; bool need; uintptr_t align; } io[8] = {
+        {"target", target, true, e}, {"draft", draft, false, e}, {"tokens", tokens, true, 4}, {"lens", lens, false, 4},
+        {"accept_u", accept_u, !greedy, 4}, {"sample_e", sample_e, !greedy, 4}, {"accepted", accepted, true, 4}, {"next", next, true, 4}};
+    for (const auto &x : io) {
+        if (x.need && !x.p) return fail(SQ_EINVAL, "%s is NULL", x.name);
+        if (x.p && !aligned(x.p, x.align)) return fail(SQ_EINVAL, "%s is not %d-byte aligned", x.name, (int)x.align);
+    }
+    if ((st = check_work("work", work, work_bytes, need))) return st;
+    const sqk::VerifyLayout lay = sqk::verify_layout(n, m);
+    uint8_t *base = static_cast<uint8_t *>(work);
+    sqk::VerifyArgs a{};
+    a.target = target; a.draft = greedy ? nullptr : draft;
+    a.target_stride = target_stride ? target_stride : vocab;
+    a.draft_stride = draft_stride ? draft_stride : vocab;
+    a.tokens = tokens; a.lens = lens; a.accept_u = accept_u; a.sample_e = sample_e;
+    a.n = n; a.m = m; a.vocab = vocab;
+    a.inv_temperature = greedy ? 1.f : 1.f / temperature;
+    a.accepted = accepted; a.next = next;
+    a.stats = reinterpret_cast<float2 *>(base + lay.stats);
+    a.best = reinterpret_cast<uint64_t *>(base + lay.best);
+    a.done = reinterpret_cast<int32_t *>(base + lay.done);
+    const hipError_t err = sqk::launch_verify(a, logits_dtype == SQ_F32, greedy, stream);
+    return err == hipSuccess ? SQ_OK : hip_fail(err, "verify_draft launch");
 }
 
 sq_status sq_device_copy(const void *src, void *dst, size_t bytes, hipStream_t stream) {

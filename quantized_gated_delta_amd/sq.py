@@ -113,6 +113,11 @@ def lib():
         L.sq_f32_window_update.argtypes = [vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, i32,
                                            i32, vp, vp, vp, vp, vp, vp, ctypes.c_int, vp,
                                            ctypes.c_int, vp, vp]
+        L.sq_verify_bytes.restype = st
+        L.sq_verify_bytes.argtypes = [i32, i32, psize]
+        L.sq_verify_draft.restype = st
+        L.sq_verify_draft.argtypes = [i32, i32, i32, vp, i64, vp, i64, ctypes.c_int, vp, vp, vp, vp,
+                                      ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
         L.sq_last_error.restype = ctypes.c_char_p
         L.sq_last_error.argtypes = []
         L.sq_version.restype = ctypes.c_char_p
@@ -475,6 +480,71 @@ class ChunkedDelta:
         if S_out is not None:
             _need(S_out, "S_out", n_seq * self.n_heads * self.d * self.d, (torch.float32,))
         sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, self.work, stream=stream)
+
+
+SQ_DRAFT_MAX = 32
+
+
+def sq_verify_bytes(n: int, m: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().sq_verify_bytes(int(n), int(m), ctypes.byref(out)), "sq_verify_bytes")
+    return out.value
+
+
+def sq_verify_draft(n, m, vocab, target, target_stride, draft, draft_stride, tokens, lens, accept_u,
+                    sample_e, temperature, accepted, next_token, work, work_bytes=None,
+                    logits_dtype=None, stream=None) -> None:
+    """target, draft: pointers, or tensors whose row strides the arguments hold."""
+    logits_dtype = _dtype_code(target) if logits_dtype is None else logits_dtype
+    if work_bytes is None:
+        work_bytes = work.numel() * work.element_size()
+    _check(lib().sq_verify_draft(int(n), int(m), int(vocab), _data(target), int(target_stride),
+                                 _data(draft), int(draft_stride), logits_dtype, _ptr(tokens),
+                                 _ptr(lens), _ptr(accept_u), _ptr(sample_e), float(temperature),
+                                 _ptr(accepted), _ptr(next_token), _ptr(work), int(work_bytes),
+                                 _stream(stream)), "sq_verify_draft")
+
+
+class DraftVerifier:
+    """sq_verify_draft with its workspace, for up to n requests of up to m drafted tokens.
+    Calls that may overlap (on several streams) need an object each."""
+
+    def __init__(self, n: int, m: int, vocab: int, device="cuda"):
+        import torch
+        self.n, self.m, self.vocab = int(n), int(m), int(vocab)
+        self.work = torch.empty(max(256, sq_verify_bytes(n, m)), dtype=torch.uint8, device=device)
+
+    def _rows(self, name, t, n, m, dtype):
+        """Stride of the rows of logits [n, m, vocab], whose rows may be padded."""
+        if t.shape != (n, m, self.vocab) or not t.is_cuda or t.dtype != dtype:
+            raise ValueError("%s must be a %s device tensor of shape %s, got %s %s" % (
+                name, dtype, (n, m, self.vocab), t.dtype, tuple(t.shape)))
+        stride = t.stride(1) if m > 1 else t.stride(0)
+        if (self.vocab > 1 and t.stride(2) != 1) or (n > 1 and m > 1 and t.stride(0) != m * stride):
+            raise ValueError("the rows of %s must be evenly spaced and dense" % name)
+        return stride if n * m > 1 else 0
+
+    def verify(self, target, tokens, accepted, next_token, draft=None, accept_u=None,
+               sample_e=None, lens=None, temperature=1.0, stream=None):
+        """target: logits [n, m + 1, vocab]; tokens: int32 [n, m]; accepted, next_token: int32 [n],
+        the outputs; the rest as sq_verify_draft."""
+        import torch
+        f32, i32 = (torch.float32,), (torch.int32,)
+        if target.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("target must be float32 or bfloat16")
+        n, m = target.shape[0], target.shape[1] - 1
+        ts = self._rows("target", target, n, m + 1, target.dtype)
+        ds = 0 if draft is None else self._rows("draft", draft, n, m, target.dtype)
+        _need(tokens, "tokens", n * m, i32)
+        _need(accepted, "accepted", n, i32)
+        _need(next_token, "next_token", n, i32)
+        if lens is not None:
+            _need(lens, "lens", n, i32)
+        if temperature:
+            _need(accept_u, "accept_u", n * m, f32)
+            _need(sample_e, "sample_e", n * self.vocab, f32)
+        sq_verify_draft(n, m, self.vocab, target, ts, draft, ds, tokens, lens, accept_u, sample_e,
+                        temperature, accepted, next_token, self.work, stream=stream)
 
 
 class StatePool:
