@@ -335,12 +335,13 @@ typedef struct {
     int64_t q_stride, k_stride, v_stride;
 } sq_seq_desc;
 
-/* Bytes that sq_chunk_forward needs as `work`.  Grows with
- * n_tokens and n_seq alone, so one buffer of the largest batch serves all
- * smaller ones; its contents between calls are of no concern.  Errors:
- * SQ_EINVAL for a NULL or inconsistent descriptor, SQ_EUNSUPPORTED for shapes
- * outside the supported set. */
-sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work);
+/* Bytes that sq_chunk_forward needs as `work`; with save not NULL, *save is
+ * what it needs as `save` for a backward pass, and *work covers
+ * sq_chunk_backward too.  Both grow with n_tokens and n_seq alone, so buffers of
+ * the largest batch serve all smaller ones.  Errors: SQ_EINVAL for a NULL or
+ * inconsistent descriptor, SQ_EUNSUPPORTED for shapes outside the supported
+ * set. */
+sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work, size_t *save);
 
 /* The recurrence of sq_decode_step, unquantized, over whole sequences
  * ("Paper Explained: STEPQuant" (ta-paperlens), section "The mechanism:
@@ -354,19 +355,41 @@ sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work);
  *   S0:    initial states fp32 [n_seq, n_heads, d_k, d_v], or NULL for zeros.
  *   y:     output, y_dtype.
  *   S_out: final states, as S0; may be S0 itself, or NULL.
- *   work:  DEVICE scratch of sq_chunk_bytes, 256-byte aligned; calls that may
- *          overlap need one each.
+ *   save:  DEVICE buffer of sq_chunk_bytes for sq_chunk_backward, or NULL: each
+ *          chunk's initial state and differences to v.
+ *   work:  DEVICE scratch of sq_chunk_bytes; its contents between calls are of no
+ *          concern.  save and work are 256-byte aligned; calls that may overlap
+ *          need one each.
  * Arithmetic: states, sums and decays in fp32; matrix products on operands
  * split into bf16 terms so that S_out (and an fp32 y) has fp32 accuracy, a
  * bf16 y 16 bits before its rounding.  Log-gates below -150 act as -150 (their
  * gate is 0 in fp32), so a gate of exactly 0, g = -inf, resets the state.
  * n_seq = 0 is a no-op.  Errors: SQ_EINVAL for a NULL or misaligned pointer, a
- * bad stride or head count, SQ_ENOMEM if work_bytes is too small,
+ * bad stride or head count, SQ_ENOMEM if a buffer is too small,
  * SQ_EUNSUPPORTED as sq_chunk_bytes. */
 sq_status sq_chunk_forward(const sq_seq_desc *desc, const int32_t *cu, const void *q,
                            const void *k, const void *v, const void *beta, const void *g,
-                           const float *S0, void *y, float *S_out, void *work, size_t work_bytes,
-                           hipStream_t stream);
+                           const float *S0, void *y, float *S_out, void *save, size_t save_bytes,
+                           void *work, size_t work_bytes, hipStream_t stream);
+
+/* Gradients of sq_chunk_forward (of the recurrence on the same page), from
+ * the `save` that it filled for the same inputs.
+ *   dy:     gradient of y, in in_dtype, dense like y;
+ *   dS_out: gradient of S_out, fp32, or NULL for zeros;
+ *   dq, dk: [n_tokens, n_key_heads, d_k], summed over the heads that share a key
+ *           head; dv, dbeta, dg: as v (dense), beta, g; all in in_dtype and
+ *           required;
+ *   dS0:    gradient of S0, fp32, or NULL; may be dS_out itself.
+ * Nothing is written for tokens that no sequence has.  A log-gate below -150
+ * gets the gradient of -150 (0 but for rounding).  Arithmetic: dS0 and fp32
+ * gradients have fp32 accuracy, bf16 gradients 16 bits before their
+ * rounding; sums go in a fixed order, so equal inputs give equal bits.
+ * Overwrites work, leaves save as it is.  Errors as sq_chunk_forward. */
+sq_status sq_chunk_backward(const sq_seq_desc *desc, const int32_t *cu, const void *q,
+                            const void *k, const void *v, const void *beta, const void *g,
+                            const void *dy, const float *dS_out, const void *save,
+                            size_t save_bytes, void *dq, void *dk, void *dv, void *dbeta, void *dg,
+                            float *dS0, void *work, size_t work_bytes, hipStream_t stream);
 
 /* Tokens of the longest window. */
 #define SQ_WINDOW_MAX 16

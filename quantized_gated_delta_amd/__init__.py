@@ -7,6 +7,7 @@ from .sq import (SQ_BF16, SQ_EHIP, SQ_EINVAL, SQ_ENOMEM, SQ_EUNSUPPORTED, SQ_F32
                  SQ_GATE_KDA, SQ_OK, SQError, ChunkedDelta, DraftVerifier, StatePool, header_symbols, lib, sq_arith_selfcheck,
                  SQ_WINDOW_MAX, f32_window_update, sq_f32_window_update, sq_window_update,
                  SQ_DRAFT_MAX, sq_verify_bytes, sq_verify_draft, seq_desc, sq_check_slots, sq_chunk_bytes, sq_chunk_forward,
+                 sq_chunk_backward,
                  sq_decode_step, sq_decode_update, sq_dequant_state, sq_device_copy,
                  sq_f32_decode_step, sq_issue_probe, SQ_PROBE_OPS_PER_LAUNCH, SQ_PROBE_COUNT,
                  SQ_PROBE_FMA_F32, SQ_PROBE_MUL_F32, SQ_PROBE_MAX3_F32, SQ_PROBE_CVT_BYTE,

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libsq.so")
 LIB_TIMELINE = os.path.join(HERE, "libsq_timeline.so")
 ARCH = "gfx950"
 
-SOURCES = ["sq_kernels.hip", "sq_probe.hip", "sq_chunk.hip", "sq_window.hip", "sq_verify.hip", "sq_api.cpp"]
+SOURCES = ["sq_kernels.hip", "sq_probe.hip", "sq_chunk.hip", "sq_chunk_bwd.hip",
+           "sq_window.hip", "sq_verify.hip", "sq_api.cpp"]
 
 HIP_FLAGS = [
     "--offload-arch=" + ARCH,

@@ -519,34 +519,66 @@ sq_status sq_check_slots(const sq_pool *pool, const int32_t *slot_idx, int32_t n
     return SQ_OK;
 }
 
-sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work) {
+sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work, size_t *save) {
     sq_status st = check_seq(desc);
     if (st) return st;
     if (!work) return fail(SQ_EINVAL, "work is NULL");
-    const bool y_f32 = desc->y_dtype == SQ_F32;
+    const bool kda = desc->gate == SQ_GATE_KDA, f32 = desc->in_dtype == SQ_F32;
     const int64_t blocks = sqk::chunk_slots(desc->n_tokens, desc->n_seq) * desc->n_heads;
-    *work = (size_t)(blocks * sqk::forward_layout(desc->d_k, desc->gate == SQ_GATE_KDA, desc->in_dtype == SQ_F32,
-                                                  y_f32 ? 3 : 2).block);
+    int64_t block = sqk::forward_layout(desc->d_k, kda, f32, desc->y_dtype == SQ_F32 ? 3 : 2).block;
+    if (save) {
+        const int64_t back = sqk::backward_layout(desc->d_k, kda, f32).block;
+        block = back > block ? back : block;
+        *save = (size_t)(blocks * sqk::save_layout(desc->d_k).block);
+    }
+    *work = (size_t)(blocks * block);
     return SQ_OK;
 }
 
 sq_status sq_chunk_forward(const sq_seq_desc *desc, const int32_t *cu, const void *q, const void *k, const void *v,
-                           const void *beta, const void *g, const float *S0, void *y, float *S_out, void *work,
-                           size_t work_bytes, hipStream_t stream) {
-    size_t need = 0;
-    sq_status st = sq_chunk_bytes(desc, &need);
-    if (st) return st;
+                           const void *beta, const void *g, const float *S0, void *y, float *S_out, void *save,
+                           size_t save_bytes, void *work, size_t work_bytes, hipStream_t stream) {
+    size_t need = 0, both = 0, keep = 0;
+    sq_status st = sq_chunk_bytes(desc, &need, nullptr);
+    if (st || (st = sq_chunk_bytes(desc, &both, &keep))) return st;
     if (desc->n_seq == 0) return SQ_OK;
     if ((st = check_seq_io(desc, cu, q, k, v, beta, g, S0)) || (st = check_io("y", y, desc->n_tokens > 0)) ||
-        (st = check_io("S_out", S_out, S_out != nullptr)) || (st = check_work("work", work, work_bytes, need)))
+        (st = check_io("S_out", S_out, S_out != nullptr)) || (st = check_work("work", work, work_bytes, need)) ||
+        (save && (st = check_work("save", save, save_bytes, keep))))
         return st;
     if (debug_slots() && (st = check_cu(desc, cu, stream))) return st;
     sqk::SeqArgs a = seq_args(desc, cu, q, k, v, beta, g, S0, work);
     a.y = y;
     a.S_out = S_out;
+    a.save = static_cast<uint8_t *>(save);
     const hipError_t e = sqk::launch_chunk_forward(a, desc->d_k, desc->gate == SQ_GATE_KDA, desc->in_dtype == SQ_F32,
                                                    desc->y_dtype == SQ_F32, stream);
     return e == hipSuccess ? SQ_OK : hip_fail(e, "chunk_forward launch");
+}
+
+sq_status sq_chunk_backward(const sq_seq_desc *desc, const int32_t *cu, const void *q, const void *k, const void *v,
+                            const void *beta, const void *g, const void *dy, const float *dS_out, const void *save,
+                            size_t save_bytes, void *dq, void *dk, void *dv, void *dbeta, void *dg, float *dS0,
+                            void *work, size_t work_bytes, hipStream_t stream) {
+    size_t need = 0, keep = 0;
+    sq_status st = sq_chunk_bytes(desc, &need, &keep);
+    if (st) return st;
+    if (desc->n_seq == 0) return SQ_OK;
+    const bool any = desc->n_tokens > 0;
+    if ((st = check_seq_io(desc, cu, q, k, v, beta, g, nullptr)) || (st = check_io("dy", dy, any)) ||
+        (st = check_io("dS_out", dS_out, dS_out != nullptr)) || (st = check_io("dq", dq, any)) ||
+        (st = check_io("dk", dk, any)) || (st = check_io("dv", dv, any)) || (st = check_io("dbeta", dbeta, any)) ||
+        (st = check_io("dg", dg, any)) || (st = check_io("dS0", dS0, dS0 != nullptr)) ||
+        (st = check_work("save", save, save_bytes, keep)) || (st = check_work("work", work, work_bytes, need)))
+        return st;
+    if (debug_slots() && (st = check_cu(desc, cu, stream))) return st;
+    sqk::SeqArgs a = seq_args(desc, cu, q, k, v, beta, g, nullptr, work);
+    a.save = static_cast<uint8_t *>(const_cast<void *>(save));
+    a.dy = dy; a.dS_out = dS_out;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dbeta = dbeta; a.dg = dg; a.dS0 = dS0;
+    const hipError_t e = sqk::launch_chunk_backward(a, desc->d_k, desc->gate == SQ_GATE_KDA,
+                                                    desc->in_dtype == SQ_F32, stream);
+    return e == hipSuccess ? SQ_OK : hip_fail(e, "chunk_backward launch");
 }
 
 sq_status sq_window_update(const sq_pool *pool, const int32_t *slot_idx, int32_t n, int32_t length,

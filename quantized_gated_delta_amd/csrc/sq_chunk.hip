@@ -126,12 +126,14 @@ template <int D, bool KDA, bool F32, int NTY, bool YF32, int NCT>
 __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
     typedef Elem<F32> E;
     constexpr ChunkLayout lay = forward_layout(D, KDA, F32, NTY);
+    constexpr SaveLayout save = save_layout(D);
     constexpr int MT = D / 64, KB = D / 32, COLS = 16 * NCT, SLICES = D / COLS;
     constexpr int KN = KDA ? 3 : 1, QN = KDA ? NTY : 1;
     typedef LdsMat<F32, 3, D, COLS> SMat;
     typedef LdsMat<F32, 3, kChunk, COLS> XMat;
     typedef LdsMat<F32, NTY, kChunk, COLS> YMat;
     __shared__ __attribute__((aligned(16))) uint8_t lds[SMat::BYTES + 2 * XMat::BYTES + (KDA ? 0 : YMat::BYTES)];
+    __shared__ __attribute__((aligned(16))) float sTurn[4 * 320];
     E *sS = reinterpret_cast<E *>(lds), *sX = reinterpret_cast<E *>(lds + SMat::BYTES);
     E *sU = reinterpret_cast<E *>(lds + SMat::BYTES + XMat::BYTES);
     E *sY = KDA ? sU : reinterpret_cast<E *>(lds + SMat::BYTES + 2 * XMat::BYTES);
@@ -240,6 +242,14 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NCT; ++n) SMat::put4(sS, 16 * n + r, (w * MT + m) * 16 + g4, S[m][n]);
+        uint8_t *keep = a.save + ((sp.slot0 + c) * a.n_heads + h) * save.block;
+        if (a.save)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NCT; ++n)
+                    put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(keep + save.S), (w * MT + m) * 16 + r, c0 + 16 * n + g4,
+                                                      turn(sTurn + w * 320, S[m][n], l));
         __syncthreads();
         // y is formed with its columns as the result's rows: a lane then holds four neighbours of one token
         f4 ks[NCT], y[NCT];
@@ -268,6 +278,9 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
                 if (kb == 0 || w >= 2) e[n] = mma<3>(fM[kb], XMat::get(sX, 16 * n + r, kb * 32 + g8), e[n]);
+            if (a.save)
+                put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(keep + save.E), 16 * w + r, c0 + 16 * n + g4,
+                                                  turn(sTurn + w * 320, e[n], l));
             const f4 u = e[n] * gt.beta;
             if constexpr (KDA) {
                 XMat::put4(sU, 16 * n + r, 16 * w + g4, u);

@@ -1,0 +1,676 @@
+// Gradients of the chunked gated Delta rule (sq_chunk.hip, sq_prep.h for the notation).
+//
+// With dY the gradient of y and dS_C that of a chunk's final state,
+//   dU  = P^T dY + (K e^{G_C - G}) dS_C
+//   dF  = dU + M^T diag(beta) dU            dV = diag(beta) dF     dbeta_i = E_i . dF_i
+//   dS0 = diag(e^{G_C}) dS_C + (Q e^G)^T dY - (K e^G)^T dV
+//   dP  = dY U^T (j <= i)                   dB = -dV U^T (j < i)
+//   dq_i = e^{G_i} dY_i S0^T + sum_j dP_ij k_j e^{G_i - G_j}
+//   dk   = row + col,  row_i = -e^{G_i} dV_i S0^T + sum_{j<i} dB_ij k_j e^{G_i - G_j}
+//                      col_j = e^{G_C - G_j} U_j dS_C^T + sum_{i>j} dB_ij k_i e^{G_i - G_j}
+//                                                        + sum_{i>=j} dP_ij q_i e^{G_i - G_j}
+//   dG_i = q_i dq_i + k_i (row_i - col_i)   (GDN: summed over channels)
+//   dG_C += sum_j k_j (e^{G_C - G_j} U_j dS_C^T) + e^{G_C} rowsum(S0 dS_C),   dg_t = sum_{i >= t} dG_i
+// dF needs no division by beta: M has no beta on its left.
+//
+// Three kernels: the operands (prep, all chunks in parallel), a scan from the last
+// chunk to the first that carries dS and leaves dV and each chunk's dS, shaped like the forward
+// scan (16 columns of the state per workgroup, rows over its four waves), and
+// the gradients of q, k, beta and g (all chunks in parallel), which read the states that
+// the forward pass saved.  The heads that share a key head are added up in the
+// registers of one workgroup: in a fixed order, without another pass.
+#include "sq_prep.h"
+
+namespace sqk {
+namespace {
+
+template <int D, bool F32> __global__ __launch_bounds__(256) void prep_gdn_bwd_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr BackwardLayout lay = backward_layout(D, false, F32);
+    constexpr int TROW = D + 16 / (int)sizeof(E);
+    __shared__ union { struct { float B[kChunk * kBRow], P[kChunk * kBRow]; }; E tok[kChunk * TROW]; } s;
+    __shared__ float sInv[4 * 16 * 20], sBeta[kChunk];
+    __shared__ double sG[kChunk];
+    const int t = threadIdx.x, w = t >> 6, l = t & 63;
+    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
+    const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+    uint8_t *out = a.work + (x * a.n_heads + h) * lay.block;
+
+    gates_gdn<F32>(a, t0, rows, h, sG, sBeta, t);
+    if (h == hk * share) {
+        write_transposed<D, F32>(a.k, a.k_stride, t0, rows, hk, s.tok, reinterpret_cast<E *>(out + lay.KT), t);
+        write_transposed<D, F32>(a.q, a.q_stride, t0, rows, hk, s.tok, reinterpret_cast<E *>(out + lay.QT), t);
+    } else {
+        __syncthreads();
+    }
+    if (t < kChunk) {
+        float *gt = reinterpret_cast<float *>(out + lay.gates);
+        gt[t] = exp_of((float)sG[t]);
+        gt[kChunk + t] = exp_of((float)(sG[kChunk - 1] - sG[t]));
+        gt[2 * kChunk + t] = sBeta[t];
+    }
+    pairs_gdn<D, F32>(a, t0, rows, hk, sG, s.B, s.P, w, l);
+    __syncthreads();
+    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.PT), t);
+    invert_block(s.B, sBeta, sInv + w * 320, w, l);
+    __syncthreads();
+    f4 m[4];
+    solve_column(s.B, sBeta, sInv, w, l, m);
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.P[(16 * I + (l >> 4) * 4 + i) * kBRow + 16 * w + (l & 15)] = m[I][i];
+    __syncthreads();
+    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.MT), t);
+}
+
+template <int D, bool F32> __global__ __launch_bounds__(256) void prep_kda_bwd_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr BackwardLayout lay = backward_layout(D, true, F32);
+    constexpr int GROW = KdaLds<D, F32>::GROW, ROW = KdaLds<D, F32>::ROW;
+    __shared__ KdaLds<D, F32> s;
+    __shared__ float sInv[4 * 16 * 20];
+    const int t = threadIdx.x, w = t >> 6, l = t & 63;
+    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
+    const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+    uint8_t *out = a.work + (x * a.n_heads + h) * lay.block;
+
+    load_kda<D, F32>(a, t0, rows, h, hk, s, t);
+    for (int u = t; u < kChunk * D / 8; u += 256) {
+        const int row = u / (2 * D) * 16 + (u & 15), c8 = u % (2 * D) / 16 * 8;
+        float v[8];
+        decayed8<D, F32, 2>(s, s.k, row, c8, 0, v);
+        Operand<F32, 3, D / 32>::put8(reinterpret_cast<E *>(out + lay.K), row, c8, v);
+    }
+    for (int u = t; u < kChunk * D / 8; u += 256) {
+        const int ch = (u >> 7) * 16 + (u & 15), k8 = (u >> 4 & 7) * 8;  // eight tokens of a channel
+        float before = 0.f, vk[8], vq[8];
+        for (int b = 0; b < k8 >> 4; ++b) before += s.L[(16 * b + 15) * GROW + ch];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float e = exp_of(s.L[(k8 + i) * GROW + ch] + before);
+            vk[i] = ld_elem<F32>(s.k, (k8 + i) * ROW + ch) * e;
+            vq[i] = ld_elem<F32>(s.q, (k8 + i) * ROW + ch) * e;
+        }
+        Operand<F32, 3, 2>::put8(reinterpret_cast<E *>(out + lay.KT), ch, k8, vk);
+        Operand<F32, 3, 2>::put8(reinterpret_cast<E *>(out + lay.QT), ch, k8, vq);
+    }
+    float *gt = reinterpret_cast<float *>(out + lay.gates);
+    if (t < kChunk) gt[t] = s.beta[t];
+    if (t < D) {
+        float e = 0.f;
+        for (int b = 0; b < 4; ++b) e += s.L[(16 * b + 15) * GROW + t];
+        gt[kChunk + t] = exp_of(e);
+    }
+    pairs_kda<D, F32, 3>(a, t0, rows, h, s, w, l);
+    __syncthreads();
+    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.PT), t);
+    invert_block(s.B, s.beta, sInv + w * 320, w, l);
+    __syncthreads();
+    f4 m[4];
+    solve_column(s.B, s.beta, sInv, w, l, m);
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.P[(16 * I + (l >> 4) * 4 + i) * kBRow + 16 * w + (l & 15)] = m[I][i];
+    __syncthreads();
+    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.MT), t);
+}
+
+// One (sequence, head), 16 NCT columns of the state's gradient, all chunks backwards.
+template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) void scan_bwd_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr BackwardLayout lay = backward_layout(D, KDA, F32);
+    constexpr SaveLayout save = save_layout(D);
+    constexpr int MT = D / 64, KB = D / 32, COLS = 16 * NCT, SLICES = D / COLS, KN = KDA ? 3 : 1;
+    typedef LdsMat<F32, 3, D, COLS> SMat;
+    typedef LdsMat<F32, 3, kChunk, COLS> XMat;
+    typedef LdsMat<F32, 1, kChunk, COLS> YMat;
+    constexpr int GY = KDA ? 0 : XMat::BYTES;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[SMat::BYTES + 2 * XMat::BYTES + 2 * YMat::BYTES + GY];
+    __shared__ __attribute__((aligned(16))) float sTurn[4 * 320];
+    E *sS = reinterpret_cast<E *>(lds), *sX = reinterpret_cast<E *>(lds + SMat::BYTES);
+    E *sU = reinterpret_cast<E *>(lds + SMat::BYTES + XMat::BYTES);
+    E *sYg = reinterpret_cast<E *>(lds + SMat::BYTES + 2 * XMat::BYTES + 2 * YMat::BYTES);
+
+    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    float *tile = sTurn + w * 320;
+    const uint32_t pairs = (uint32_t)a.n_seq * a.n_heads, j = blockIdx.x >> 3;
+    const uint32_t pair = j / SLICES * 8 + (blockIdx.x & 7);
+    if (pair >= pairs) return;
+    const int c0 = (int)(j % SLICES) * COLS;
+    const int h = pair % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
+    const SeqSpan sp = seq_span(a, pair / (uint32_t)a.n_heads);
+    const int n_chunks = (sp.len + kChunk - 1) / kChunk;
+    const int64_t state = (int64_t)pair * D * D;
+
+    f4 S[MT][NCT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NCT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                S[m][n][i] = a.dS_out ? a.dS_out[state + (int64_t)((w * MT + m) * 16 + g4 + i) * D + c0 + 16 * n + r] : 0.f;
+
+    Frag<F32, KN> fK[KB], fKT[MT][2], fQT[MT][2];
+    Frag<F32, 3> fM[2], fP[2];
+    f4 dy[NCT], fe[NCT];
+    struct Gates { f4 eg, ec, beta, fade[MT]; float fade1; } gt{}, gt_next{};
+
+    auto block_of = [&](int c, int head) { return a.work + ((sp.slot0 + c) * a.n_heads + head) * lay.block; };
+    auto rows_of = [&](int c) { return min(kChunk, sp.len - c * kChunk); };
+    auto load_k = [&](int c) {
+        if constexpr (KDA) {
+            const E *b = reinterpret_cast<const E *>(block_of(c, h) + lay.K);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) fK[kb] = Operand<F32, KN, KB>::get(b, w, kb, l);
+        } else {
+            // past the end: the last token again; its beta is 0, so its dV is 0 too
+            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + r, rows_of(c) - 1);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                fK[kb] = load_frag<F32, KN>(static_cast<const E *>(a.k) + tok * a.k_stride + (int64_t)hk * D + kb * 32 + g8, 0);
+        }
+    };
+    auto load_dy = [&](int c) {
+        const int rows = rows_of(c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 16 * w + g4 + i;
+            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(row, rows - 1);
+#pragma unroll
+            for (int n = 0; n < NCT; ++n) {
+                const float x = ld_elem<F32>(a.dy, (tok * a.n_heads + h) * D + c0 + 16 * n + r);
+                dy[n][i] = row < rows ? x : 0.f;
+            }
+        }
+    };
+    auto load_e = [&](int c) {
+        const E *b = reinterpret_cast<const E *>(a.save + ((sp.slot0 + c) * a.n_heads + h) * save.block + save.E);
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) fe[n] = get_operand4<F32, kSaveTerms, KB>(b, 16 * w + r, c0 + 16 * n + g4);
+    };
+    auto load_gates = [&](int c) {
+        const float *p = reinterpret_cast<const float *>(block_of(c, h) + lay.gates);
+        Gates x{};
+        if constexpr (KDA) {
+            x.beta = *reinterpret_cast<const f4 *>(p + 16 * w + g4);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) x.fade[m] = *reinterpret_cast<const f4 *>(p + kChunk + (w * MT + m) * 16 + g4);
+        } else {
+            x.eg = *reinterpret_cast<const f4 *>(p + 16 * w + g4);
+            x.ec = *reinterpret_cast<const f4 *>(p + kChunk + 16 * w + g4);
+            x.beta = *reinterpret_cast<const f4 *>(p + 2 * kChunk + 16 * w + g4);
+            x.fade1 = p[kChunk - 1];
+        }
+        return x;
+    };
+    // M^T and P^T: nothing left of the diagonal
+    auto load_m = [&](int c) {
+        const E *b = reinterpret_cast<const E *>(block_of(c, h) + lay.MT);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb == 1 || w < 2) fM[kb] = Operand<F32, 3, 2>::get(b, w, kb, l);
+    };
+    auto load_p = [&](int c) {
+        const E *b = reinterpret_cast<const E *>(block_of(c, h) + lay.PT);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb == 1 || w < 2) fP[kb] = Operand<F32, 3, 2>::get(b, w, kb, l);
+    };
+    auto load_t = [&](int c) {
+        const uint8_t *b = block_of(c, KDA ? h : hk * share);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                fKT[m][kb] = Operand<F32, KN, 2>::get(reinterpret_cast<const E *>(b + lay.KT), w * MT + m, kb, l);
+                fQT[m][kb] = Operand<F32, KN, 2>::get(reinterpret_cast<const E *>(b + lay.QT), w * MT + m, kb, l);
+            }
+    };
+    const int last = n_chunks - 1;
+    if (n_chunks > 0) gt = load_gates(last), load_dy(last), load_k(last), load_p(last), load_m(last), load_e(last), load_t(last);
+
+    for (int c = last; c >= 0; --c) {
+        const int next = max(c - 1, 0), rows = rows_of(c);
+        uint8_t *blk = block_of(c, h);
+        // two places in turn: the last chunk's may still be read
+        E *sY = reinterpret_cast<E *>(lds + SMat::BYTES + 2 * XMat::BYTES + (c & 1) * YMat::BYTES);
+        gt_next = load_gates(next);
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                SMat::put4(sS, 16 * n + r, (w * MT + m) * 16 + g4, S[m][n]);
+                put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(blk + lay.dS), (w * MT + m) * 16 + r, c0 + 16 * n + g4, turn(tile, S[m][n], l));
+            }
+            YMat::put4(sY, 16 * n + r, 16 * w + g4, dy[n]);
+        }
+        __syncthreads();
+        f4 du[NCT];
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) {
+            du[n] = f4{};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) du[n] = mma<3>(fK[kb], SMat::get(sS, 16 * n + r, kb * 32 + g8), du[n]);
+            if (!KDA) du[n] *= gt.ec;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (kb == 1 || w < 2) du[n] = mma<3>(fP[kb], YMat::get(sY, 16 * n + r, kb * 32 + g8), du[n]);
+            XMat::put4(sX, 16 * n + r, 16 * w + g4, du[n] * gt.beta);
+            if constexpr (!KDA) XMat::put4(sYg, 16 * n + r, 16 * w + g4, dy[n] * gt.eg);
+        }
+        load_k(next);
+        load_p(next);
+        load_dy(next);
+        __syncthreads();
+        float db = 0.f;
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (kb == 1 || w < 2) du[n] = mma<3>(fM[kb], XMat::get(sX, 16 * n + r, kb * 32 + g8), du[n]);  // dF
+            const f4 dv = du[n] * gt.beta;
+            XMat::put4(sU, 16 * n + r, 16 * w + g4, KDA ? -dv : -(dv * gt.eg));
+            const f4 df = turn(tile, du[n], l), tv = turn(tile, dv, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) db = fmaf(df[i], fe[n][i], db);
+            put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(blk + lay.dV), 16 * w + r, c0 + 16 * n + g4, tv);
+            if (16 * w + r < rows)
+                st_elem4<F32>(a.dv, ((sp.t0 + (int64_t)c * kChunk + 16 * w + r) * a.n_heads + h) * D + c0 + 16 * n + g4, tv);
+        }
+        db += __shfl_xor(db, 16);
+        db += __shfl_xor(db, 32);
+        if (l < 16) reinterpret_cast<float *>(blk + lay.dbeta)[c0 / COLS * kChunk + 16 * w + r] = db;
+        load_m(next);
+        load_e(next);
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NCT; ++n) {
+                S[m][n] = KDA ? S[m][n] * gt.fade[m] : S[m][n] * gt.fade1;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    if constexpr (KDA) S[m][n] = mma<3>(fQT[m][kb], YMat::get(sY, 16 * n + r, kb * 32 + g8), S[m][n]);
+                    else S[m][n] = mma<3>(fQT[m][kb], XMat::get(sYg, 16 * n + r, kb * 32 + g8), S[m][n]);
+                    S[m][n] = mma<3>(fKT[m][kb], XMat::get(sU, 16 * n + r, kb * 32 + g8), S[m][n]);
+                }
+            }
+        load_t(next);
+        gt = gt_next;
+    }
+    if (a.dS0)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NCT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a.dS0[state + (int64_t)((w * MT + m) * 16 + g4 + i) * D + c0 + 16 * n + r] = S[m][n][i];
+}
+
+// Gradients of q, k, beta and g of one chunk and key head.  Wave w: tokens 16 w .. + 15.
+// SLICES: the parts of beta's gradient that the scan left.
+template <int D, bool KDA, bool F32> struct GradLds {
+    static constexpr bool KQ = !(F32 && KDA && D == 128);  // keys and queries fit beside the rest
+    static constexpr int ROW = D + 16 / (int)sizeof(Elem<F32>), GROW = D + 4;
+    float dP[kChunk * kBRow], dB[kChunk * kBRow];
+    Elem<F32> k[KQ ? kChunk * ROW : 1], q[KQ ? kChunk * ROW : 1];
+    float L[KDA ? kChunk * GROW : 1], R[KDA ? kChunk * GROW : 1];
+    __attribute__((aligned(16))) float turn[4][320];
+    double G[kChunk];
+    float beta[kChunk], dG[kChunk], end[KDA ? 5 * D : 8], range[4];
+};
+
+template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(256) void grad_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr BackwardLayout lay = backward_layout(D, KDA, F32);
+    constexpr SaveLayout save = save_layout(D);
+    typedef GradLds<D, KDA, F32> Lds;
+    constexpr int KB = D / 32, NT = D / 16, ROW = Lds::ROW, GROW = Lds::GROW, N2 = kSaveTerms;
+    __shared__ Lds s;
+    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    const int64_t x = blockIdx.x / (uint32_t)a.n_key_heads;
+    const int hk = blockIdx.x % (uint32_t)a.n_key_heads, share = a.n_heads / a.n_key_heads;
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+
+    if constexpr (Lds::KQ) {
+        for (int u = t; u < kChunk * D / 8; u += 256) {
+            const int row = u / (D / 8), ch = u % (D / 8) * 8;
+            const Frag<F32, 1> fk = token_frag<F32>(a.k, a.k_stride, t0, rows, row, (int64_t)hk * D + ch);
+            const Frag<F32, 1> fq = token_frag<F32>(a.q, a.q_stride, t0, rows, row, (int64_t)hk * D + ch);
+            if constexpr (F32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    *reinterpret_cast<f4 *>(s.k + row * ROW + ch + 4 * i) = fk.v[i];
+                    *reinterpret_cast<f4 *>(s.q + row * ROW + ch + 4 * i) = fq.v[i];
+                }
+            } else {
+                *reinterpret_cast<bf8 *>(s.k + row * ROW + ch) = fk.t[0];
+                *reinterpret_cast<bf8 *>(s.q + row * ROW + ch) = fq.t[0];
+            }
+        }
+    }
+    auto key = [&](int tok, int ch) {
+        if constexpr (Lds::KQ) return ld_elem<F32>(s.k, tok * ROW + ch);
+        else return tok < rows ? ld_elem<F32>(a.k, (t0 + tok) * a.k_stride + (int64_t)hk * D + ch) : 0.f;
+    };
+    auto query = [&](int tok, int ch) {
+        if constexpr (Lds::KQ) return ld_elem<F32>(s.q, tok * ROW + ch);
+        else return tok < rows ? ld_elem<F32>(a.q, (t0 + tok) * a.q_stride + (int64_t)hk * D + ch) : 0.f;
+    };
+
+    // the sums over the heads that share the key head, in the place of operands that
+    // only the scans read; every lane adds to what it wrote itself
+    f4 *sums = reinterpret_cast<f4 *>(a.work + (x * a.n_heads + hk * share) * lay.block) + t;
+
+    for (int h = hk * share; h < (hk + 1) * share; ++h) {
+        const uint8_t *blk = a.work + (x * a.n_heads + h) * lay.block, *sv = a.save + (x * a.n_heads + h) * save.block;
+        const E *pS = reinterpret_cast<const E *>(sv + save.S), *pE = reinterpret_cast<const E *>(sv + save.E);
+        const E *pdS = reinterpret_cast<const E *>(blk + lay.dS), *pdV = reinterpret_cast<const E *>(blk + lay.dV);
+        __syncthreads();  // the last head's LDS is done with
+        if constexpr (KDA) {
+            for (int u = t; u < kChunk * D; u += 256) {
+                const int row = u / D, ch = u % D;
+                s.L[row * GROW + ch] = row < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + row) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
+            }
+            if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
+            if (t < 4) s.range[t] = 0.f;
+            __syncthreads();
+            for (int u = t; u < 4 * D; u += 256) {
+                const int b = u / D, ch = u % D;
+                float *L = s.L + b * 16 * GROW + ch, *R = s.R + b * 16 * GROW + ch, g[16], up = 0.f, down = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] = L[i * GROW];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) up += g[i], L[i * GROW] = up;
+#pragma unroll
+                for (int i = 15; i >= 0; --i) R[i * GROW] = down, down += g[i];
+                atomicMax(reinterpret_cast<int *>(&s.range[b]), __float_as_int(fmaxf(-up, 0.f)));
+            }
+        } else {
+            gates_gdn<F32>(a, t0, rows, h, s.G, s.beta, t);
+        }
+        // ---- the pairs' gradients, rows of this wave: dP and dB (GDN: with the decay)
+        Frag<F32, 1> fy[KB];
+        Frag<F32, N2> fv[KB], fe[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            fy[kb] = token_frag<F32>(a.dy, (int64_t)a.n_heads * D, t0, rows, 16 * w + r, (int64_t)h * D + kb * 32 + g8);
+            fv[kb] = Operand<F32, N2, KB>::get(pdV, w, kb, l);
+            fe[kb] = Operand<F32, N2, KB>::get(pE, w, kb, l);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f4 p{}, b{};
+            if (j <= w) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const Frag<F32, N2> f = j == w ? fe[kb] : Operand<F32, N2, KB>::get(pE, j, kb, l);
+                    p = mma<N2>(fy[kb], f, p);
+                    b = mma<N2>(fv[kb], f, b);
+                }
+            }
+            const int col = 16 * j + r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 16 * w + g4 + i;
+                float e = col <= row ? s.beta[col] : 0.f;
+                if (!KDA && col <= row) e *= exp_of((float)(s.G[row] - s.G[col]));
+                s.dP[row * kBRow + col] = p[i] * e;
+                s.dB[row * kBRow + col] = col < row ? -b[i] * e : 0.f;
+            }
+        }
+        __syncthreads();
+        const bool fast = !KDA || s.range[w] <= kBlockRange;
+        f4 dg{};      // GDN: sum over channels of dG, this wave's tokens
+        float tail = 0.f;  // GDN: what the chunk's end adds to every dg
+#pragma unroll 1
+        for (int n = 0; n < NT; ++n) {
+            const int ch = 16 * n + r;
+            // ---- through the states
+            f4 dq{}, row{}, col{};
+            float dot = 0.f;  // S0 . dS of one channel, this lane's columns
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const Frag<F32, N2> f0 = Operand<F32, N2, KB>::get(pS, n, kb, l), f1 = Operand<F32, N2, KB>::get(pdS, n, kb, l);
+                dq = mma<N2>(fy[kb], f0, dq);
+                row = mma<N2>(fv[kb], f0, row);
+                col = mma<N2>(fe[kb], f1, col);
+                if (n % 4 == w) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if constexpr (F32) dot = fmaf(f0.v[i / 4][i % 4], f1.v[i / 4][i % 4], dot);
+                        else dot = fmaf((float)f0.t[0][i] + (float)f0.t[1][i], (float)f1.t[0][i] + (float)f1.t[1][i], dot);
+                    }
+                }
+            }
+            f4 eL, eR;  // decay to the token from its block's start, and from it to the block's end
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = 16 * w + g4 + i;
+                float in, out;
+                if constexpr (KDA) {
+                    float lo = s.L[tok * GROW + ch], hi = s.R[tok * GROW + ch];
+                    eL[i] = exp_of(lo), eR[i] = exp_of(hi);
+                    for (int b = 0; b < w; ++b) lo += s.L[(16 * b + 15) * GROW + ch];
+                    for (int b = w + 1; b < 4; ++b) hi += s.L[(16 * b + 15) * GROW + ch];
+                    in = exp_of(lo), out = exp_of(hi);
+                } else {
+                    in = exp_of((float)s.G[tok]), out = exp_of((float)(s.G[kChunk - 1] - s.G[tok]));
+                }
+                dq[i] *= in;
+                row[i] *= -in;
+                col[i] *= out * s.beta[tok];
+            }
+            f4 kt, qt;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kt[i] = key(16 * w + g4 + i, ch), qt[i] = query(16 * w + g4 + i, ch);
+            float end = kt[0] * col[0] + kt[1] * col[1] + kt[2] * col[2] + kt[3] * col[3];
+            if (n % 4 == w) {  // the channel's lanes r, r + 16, ..: rows of the operand, not columns of the result
+                dot += __shfl_xor(dot, 16);
+                dot += __shfl_xor(dot, 32);
+                if constexpr (KDA) {
+                    float e = 0.f;
+                    for (int b = 0; b < 4; ++b) e += s.L[(16 * b + 15) * GROW + ch];
+                    if (l < 16) s.end[4 * D + ch] = dot * exp_of(e);
+                } else if (l < 16) {
+                    tail = fmaf(dot, exp_of((float)s.G[kChunk - 1]), tail);
+                }
+            }
+            if constexpr (KDA) {
+                end += __shfl_xor(end, 16);
+                end += __shfl_xor(end, 32);
+                if (l < 16) s.end[w * D + ch] = end;
+            } else {
+                tail += end;
+            }
+            // ---- between the chunk's tokens, 16 by 16
+#pragma unroll
+            for (int J = 0; J < 4; ++J) {  // rows of this wave against keys of block J
+                if (J > w || (J == w && !fast)) continue;
+                f4 kj;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 16 * J + g4 + i;
+                    kj[i] = key(tok, ch);
+                    if constexpr (KDA) {
+                        float e = J == w ? -s.L[tok * GROW + ch] : s.R[tok * GROW + ch];
+                        for (int b = J + 1; b < w; ++b) e += s.L[(16 * b + 15) * GROW + ch];
+                        kj[i] *= exp_of(e);
+                    }
+                }
+                const f4 p = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
+                const f4 b = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
+                if constexpr (KDA) {
+                    dq += eL * mma16(p, kj, f4{});
+                    row += eL * mma16(b, kj, f4{});
+                } else {
+                    dq = mma16(p, kj, dq);
+                    row = mma16(b, kj, row);
+                }
+            }
+#pragma unroll
+            for (int I = 0; I < 4; ++I) {  // keys of this wave against rows of block I
+                if (I < w || (I == w && !fast)) continue;
+                f4 ki, qi, p, b;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 16 * I + g4 + i;
+                    ki[i] = key(tok, ch), qi[i] = query(tok, ch);
+                    if constexpr (KDA) {
+                        const float e = exp_of(s.L[tok * GROW + ch]);
+                        ki[i] *= e, qi[i] *= e;
+                    }
+                    p[i] = s.dP[tok * kBRow + 16 * w + r];
+                    b[i] = s.dB[tok * kBRow + 16 * w + r];
+                }
+                if constexpr (KDA) {
+                    f4 o = mma16(b, ki, f4{});
+                    o = mma16(p, qi, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 16 * w + g4 + i;
+                        float e = I == w ? -s.L[tok * GROW + ch] : s.R[tok * GROW + ch];
+                        for (int k = w + 1; k < I; ++k) e += s.L[(16 * k + 15) * GROW + ch];
+                        col[i] = fmaf(exp_of(e), o[i], col[i]);
+                    }
+                } else {
+                    col = mma16(b, ki, col);
+                    col = mma16(p, qi, col);
+                }
+            }
+            if (!fast) {  // strong gates: the block's pairs one by one, each by its own sum of log-gates
+                float gs[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int tok = 16 * w + i;
+                    gs[i] = KDA && tok < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
+                }
+#pragma unroll 1
+                for (int j = 0; j < 16; ++j) {
+                    float e = 0.f;
+                    const float kj = key(16 * w + j, ch);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (i < j) continue;
+                        if (i > j) e += gs[i];
+                        const float d = exp_of(e), p = s.dP[(16 * w + i) * kBRow + 16 * w + j], b = s.dB[(16 * w + i) * kBRow + 16 * w + j];
+                        const float k = d * (b * key(16 * w + i, ch) + p * query(16 * w + i, ch));
+                        if (i / 4 == l >> 4) dq[i % 4] = fmaf(p * d, kj, dq[i % 4]), row[i % 4] = fmaf(b * d, kj, row[i % 4]);
+                        if (j >> 2 == l >> 4) {
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) col[m] += (j & 3) == m ? k : 0.f;
+                        }
+                    }
+                }
+            }
+            const f4 G = qt * dq + kt * (row - col);
+            f4 dk = row + col;
+            if (share > 1) {
+                if (h > hk * share) dq += sums[512 * n], dk += sums[512 * n + 256];
+                if (h + 1 < (hk + 1) * share) sums[512 * n] = dq, sums[512 * n + 256] = dk;
+            }
+            if (h + 1 == (hk + 1) * share) {
+                const f4 oq = turn(s.turn[w], dq, l), ok = turn(s.turn[w], dk, l);
+                if (16 * w + r < rows) {
+                    const int64_t at = ((t0 + 16 * w + r) * a.n_key_heads + hk) * D + 16 * n + g4;
+                    st_elem4<F32>(a.dq, at, oq);
+                    st_elem4<F32>(a.dk, at, ok);
+                }
+            }
+            if constexpr (KDA) {
+                // into dG's place once every wave has read L and R of these channels
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s.L[(16 * w + g4 + i) * GROW + ch] = G[i];
+            } else {
+                dg += G;
+            }
+        }
+        if constexpr (KDA) {
+            __syncthreads();
+            if (t < D) {
+                float sum = s.end[t] + s.end[D + t] + s.end[2 * D + t] + s.end[3 * D + t] + s.end[4 * D + t];
+                for (int i = kChunk - 1; i >= 0; --i) {
+                    sum += s.L[i * GROW + t];
+                    if (i < rows) st_elem<F32>(a.dg, ((t0 + i) * a.n_heads + h) * D + t, sum);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dg[i] += __shfl_xor(dg[i], off);
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) tail += __shfl_xor(tail, off);
+            if (r == 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s.dG[16 * w + g4 + i] = dg[i];
+            if (l == 0) s.end[w] = tail;
+            __syncthreads();
+            if (t < kChunk) {
+                float sum = s.dG[t];  // over the tokens from this one on
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const float up = __shfl_down(sum, off);
+                    if (t + off < 64) sum += up;
+                }
+                sum += s.end[0] + s.end[1] + s.end[2] + s.end[3];
+                if (t < rows) st_elem<F32>(a.dg, (t0 + t) * a.n_heads + h, sum);
+            }
+        }
+        if (t < rows) {
+            float sum = 0.f;
+            for (int i = 0; i < SLICES; ++i) sum += reinterpret_cast<const float *>(blk + lay.dbeta)[i * kChunk + t];
+            st_elem<F32>(a.dbeta, (t0 + t) * a.n_heads + h, sum);
+        }
+    }
+}
+
+template <int D, bool KDA, bool F32> hipError_t backward(const SeqArgs &a, hipStream_t stream) {
+    constexpr int NCT = 1;
+    const int64_t slots = chunk_slots(a.n_tokens, a.n_seq);
+    hipError_t e = hipSuccess;
+    if (a.n_tokens > 0) {
+        const dim3 grid((uint32_t)(slots * a.n_heads));
+        if constexpr (KDA) hipLaunchKernelGGL((prep_kda_bwd_kernel<D, F32>), grid, dim3(256), 0, stream, a);
+        else hipLaunchKernelGGL((prep_gdn_bwd_kernel<D, F32>), grid, dim3(256), 0, stream, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const uint32_t pairs = (uint32_t)a.n_seq * a.n_heads;
+    hipLaunchKernelGGL((scan_bwd_kernel<D, KDA, F32, NCT>), dim3((pairs + 7) / 8 * 8 * (D / (16 * NCT))), dim3(256), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess || a.n_tokens == 0) return e;
+    hipLaunchKernelGGL((grad_kernel<D, KDA, F32, D / (16 * NCT)>), dim3((uint32_t)(slots * a.n_key_heads)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_chunk_backward(const SeqArgs &a, int d, bool kda, bool f32, hipStream_t stream) {
+    if (d == 128) {
+        if (kda) return f32 ? backward<128, true, true>(a, stream) : backward<128, true, false>(a, stream);
+        return f32 ? backward<128, false, true>(a, stream) : backward<128, false, false>(a, stream);
+    }
+    if (kda) return f32 ? backward<64, true, true>(a, stream) : backward<64, true, false>(a, stream);
+    return f32 ? backward<64, false, true>(a, stream) : backward<64, false, false>(a, stream);
+}
+
+} // namespace sqk

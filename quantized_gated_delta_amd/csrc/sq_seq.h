@@ -216,6 +216,60 @@ template <bool F32, int N, int KB> struct Operand {
     }
 };
 
+// Four consecutive contracted elements k .. k + 3 of one row, N terms: what a lane
+// of a transposed 16 x 16 result tile holds.
+template <bool F32, int N, int KB>
+__device__ __forceinline__ Elem<F32> *operand4(Elem<F32> *m, int row, int k) {
+    const int lane = (k & 31) / 8 * 16 + (row & 15), half = k >> 2 & 1;
+    Elem<F32> *p = m + ((row >> 4) * KB + (k >> 5)) * Operand<F32, N, KB>::SIZE;
+    return F32 ? p + 256 * half + 4 * lane : p + 8 * lane + 4 * half;
+}
+template <bool F32, int N, int KB> __device__ __forceinline__ void put_operand4(Elem<F32> *m, int row, int k, f4 x) {
+    Elem<F32> *p = operand4<F32, N, KB>(m, row, k);
+    if constexpr (F32) {
+        *reinterpret_cast<f4 *>(p) = x;
+    } else {
+        bf4 v[N];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __bf16 t[N];
+            split<N>(x[i], t);
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n][i] = t[n];
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) *reinterpret_cast<bf4 *>(p + 512 * n) = v[n];
+    }
+}
+template <bool F32, int N, int KB> __device__ __forceinline__ f4 get_operand4(const Elem<F32> *m, int row, int k) {
+    const Elem<F32> *p = operand4<F32, N, KB>(const_cast<Elem<F32> *>(m), row, k);
+    if constexpr (F32) {
+        return *reinterpret_cast<const f4 *>(p);
+    } else {
+        f4 x{};
+#pragma unroll
+        for (int n = N - 1; n >= 0; --n) {
+            const bf4 v = *reinterpret_cast<const bf4 *>(p + 512 * n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += (float)v[i];
+        }
+        return x;
+    }
+}
+
+// A 16 x 16 result tile turned around through a wave's own LDS (16 x 20
+// floats): in, column l % 16 and rows 4 (l / 16) .. + 3; out, row l % 16 and
+// columns 4 (l / 16) .. + 3.
+__device__ __forceinline__ f4 turn(float *s, f4 x, int l) {
+    const int r = l & 15, g4 = (l >> 4) * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[(g4 + i) * 20 + r] = x[i];
+    __builtin_amdgcn_wave_barrier();
+    const f4 y = *reinterpret_cast<const f4 *>(s + r * 20 + g4);
+    __builtin_amdgcn_wave_barrier();
+    return y;
+}
+
 // exp(x) for x <= 0 (or moderate x > 0): the hardware exponential of x log2(e)
 // with the rounding error of that product put back; relative error about 2^-22.
 __device__ __forceinline__ float exp_of(float x) {
@@ -313,8 +367,46 @@ __host__ __device__ constexpr ChunkLayout forward_layout(int d, bool kda, bool f
     return l;
 }
 
+// What the forward pass leaves for the backward, per (chunk slot, head): the
+// state at the chunk's start as an operand [channel][column] and E as
+// [token][column], two terms each (as many bytes as fp32).
+constexpr int kSaveTerms = 2;
+struct SaveLayout { int64_t S, E, block; };
+__host__ __device__ constexpr SaveLayout save_layout(int d) {
+    SaveLayout l{};
+    l.S = 0;
+    l.E = (int64_t)d * d * 4;
+    l.block = l.E + (int64_t)kChunk * d * 4;
+    return l;
+}
+
+// Backward operands, per (chunk slot, head): M and P transposed, keys and
+// queries as [channel][token] (KDA: decayed from the chunk's start), KDA's keys
+// decayed to the chunk's end, the gates' factors as forward, and what the
+// backward scan leaves for the gradients: the state's gradient at the chunk's end
+// and v's, two terms each, and the parts of beta's gradient per 16 columns.
+struct BackwardLayout {
+    int64_t MT, PT, KT, QT, K, gates, dS, dV, dbeta, block;
+};
+__host__ __device__ constexpr BackwardLayout backward_layout(int d, bool kda, bool f32) {
+    BackwardLayout l{};
+    int64_t at = 0;
+    l.MT = at, at += plane_bytes(f32, 3, kChunk, kChunk);
+    l.PT = at, at += plane_bytes(f32, 3, kChunk, kChunk);
+    l.KT = at, at += plane_bytes(f32, kda ? 3 : 1, d, kChunk);
+    l.QT = at, at += plane_bytes(f32, kda ? 3 : 1, d, kChunk);
+    if (kda) l.K = at, at += plane_bytes(f32, 3, kChunk, d);
+    l.dS = at, at += plane_bytes(f32, kSaveTerms, d, d);
+    l.dV = at, at += plane_bytes(f32, kSaveTerms, kChunk, d);
+    l.gates = at, at += 4 * (3 * kChunk + d);
+    l.dbeta = at, at += 4 * kChunk * (d / 16);
+    l.block = (at + 255) / 256 * 256;
+    return l;
+}
+
 inline int64_t chunk_slots(int64_t n_tokens, int32_t n_seq) { return n_tokens / kChunk + n_seq; }
 
 hipError_t launch_chunk_forward(const SeqArgs &a, int d, bool kda, bool f32, bool y_f32, hipStream_t stream);
+hipError_t launch_chunk_backward(const SeqArgs &a, int d, bool kda, bool f32, hipStream_t stream);
 
 } // namespace sqk

@@ -103,9 +103,12 @@ def lib():
         L.sq_issue_probe.argtypes = [ctypes.c_int, vp, vp]
         pseq, psize = ctypes.POINTER(_SeqDesc), ctypes.POINTER(ctypes.c_size_t)
         L.sq_chunk_bytes.restype = st
-        L.sq_chunk_bytes.argtypes = [pseq, psize]
+        sz = ctypes.c_size_t
+        L.sq_chunk_bytes.argtypes = [pseq, psize, psize]
         L.sq_chunk_forward.restype = st
-        L.sq_chunk_forward.argtypes = [pseq] + [vp] * 10 + [ctypes.c_size_t, vp]
+        L.sq_chunk_forward.argtypes = [pseq] + [vp] * 10 + [sz, vp, sz, vp]
+        L.sq_chunk_backward.restype = st
+        L.sq_chunk_backward.argtypes = [pseq] + [vp] * 9 + [sz] + [vp] * 7 + [sz, vp]
         L.sq_window_update.restype = st
         L.sq_window_update.argtypes = [vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp,
                                        ctypes.c_int, vp, ctypes.c_int, vp, vp]
@@ -336,21 +339,35 @@ def seq_desc(n_seq, n_tokens, n_heads, d, gate, in_dtype, y_dtype, n_key_heads=N
                     int(k_stride), int(v_stride))
 
 
-def sq_chunk_bytes(desc) -> int:
-    """Bytes of `work` for sq_chunk_forward."""
-    work = ctypes.c_size_t(0)
-    _check(lib().sq_chunk_bytes(ctypes.byref(desc), ctypes.byref(work)), "sq_chunk_bytes")
-    return work.value
+def sq_chunk_bytes(desc, train: bool = False):
+    """Bytes of `work` for sq_chunk_forward; train: (work, save), for the backward pass too."""
+    work, save = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().sq_chunk_bytes(ctypes.byref(desc), ctypes.byref(work),
+                                ctypes.byref(save) if train else None), "sq_chunk_bytes")
+    return (work.value, save.value) if train else work.value
 
 
-def sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, work, work_bytes=None,
-                     stream=None) -> None:
+def _bytes(x, given) -> int:
+    return int(given) if given is not None else 0 if x is None else x.numel() * x.element_size()
+
+
+def sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, save, work, save_bytes=None,
+                     work_bytes=None, stream=None) -> None:
     """q, k, v: pointers, or tensors whose token strides the descriptor holds."""
-    if work_bytes is None:
-        work_bytes = work.numel() * work.element_size()
     _check(lib().sq_chunk_forward(ctypes.byref(desc), _ptr(cu), _data(q), _data(k), _data(v),
-                                  _ptr(beta), _ptr(g), _ptr(S0), _ptr(y), _ptr(S_out), _ptr(work),
-                                  int(work_bytes), _stream(stream)), "sq_chunk_forward")
+                                  _ptr(beta), _ptr(g), _ptr(S0), _ptr(y), _ptr(S_out), _ptr(save),
+                                  _bytes(save, save_bytes), _ptr(work), _bytes(work, work_bytes),
+                                  _stream(stream)), "sq_chunk_forward")
+
+
+def sq_chunk_backward(desc, cu, q, k, v, beta, g, dy, dS_out, save, dq, dk, dv, dbeta, dg, dS0,
+                      work, save_bytes=None, work_bytes=None, stream=None) -> None:
+    _check(lib().sq_chunk_backward(ctypes.byref(desc), _ptr(cu), _data(q), _data(k), _data(v),
+                                   _ptr(beta), _ptr(g), _ptr(dy), _ptr(dS_out), _ptr(save),
+                                   _bytes(save, save_bytes), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(dbeta), _ptr(dg), _ptr(dS0), _ptr(work),
+                                   _bytes(work, work_bytes), _stream(stream)),
+           "sq_chunk_backward")
 
 
 def _data(x) -> Optional[int]:
@@ -423,8 +440,9 @@ class ChunkedDelta:
     """The gated Delta rule over whole sequences, with its workspace.
 
     Holds a workspace for batches of up to n_seq sequences and n_tokens tokens
-    in all; a call may bring fewer.  Calls that may overlap (on several
-    streams) need an object each.  q, k: [tokens, n_key_heads, d] and
+    in all; a call may bring fewer.  With train=True, also what backward needs
+    of the last forward call, which it belongs to.  Calls that may overlap (on
+    several streams) need an object each.  q, k: [tokens, n_key_heads, d] and
     v: [tokens, n_heads, d] may be parts of one wider tensor; every other tensor
     is contiguous."""
 
@@ -441,8 +459,12 @@ class ChunkedDelta:
         self.n_key_heads = int(n_key_heads or n_heads)
         self.gate = SQ_GATE_KDA if gate == "kda" else SQ_GATE_GDN
         self._codes = (codes[self.dtype], codes[self.y_dtype])
-        work = sq_chunk_bytes(self._desc(n_seq, n_tokens))
+        work, save = sq_chunk_bytes(self._desc(n_seq, n_tokens), train=True)
+        if not train:
+            work, save = sq_chunk_bytes(self._desc(n_seq, n_tokens)), None
         self.work = torch.empty(max(256, work), dtype=torch.uint8, device=device)
+        self.save = None if save is None else torch.empty(max(256, save), dtype=torch.uint8,
+                                                          device=device)
 
     def _desc(self, n_seq, n_tokens, qs=0, ks=0, vs=0):
         return seq_desc(n_seq, n_tokens, self.n_heads, self.d, self.gate, self._codes[0],
@@ -479,7 +501,27 @@ class ChunkedDelta:
         _need(y, "y", n * self.n_heads * self.d, (self.y_dtype,))
         if S_out is not None:
             _need(S_out, "S_out", n_seq * self.n_heads * self.d * self.d, (torch.float32,))
-        sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, self.work, stream=stream)
+        sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, self.save, self.work,
+                         stream=stream)
+
+    def backward(self, q, k, v, beta, g, cu, dy, dq, dk, dv, dbeta, dg, S0=None, dS_out=None,
+                 dS0=None, stream=None):
+        """Gradients of the last forward call, which had the same inputs; dy and every gradient in
+        `dtype` and contiguous, dS_out and dS0 [n_seq, n_heads, d, d] fp32 or None."""
+        import torch
+        if self.save is None:
+            raise ValueError("backward needs train=True")
+        desc, n_seq, n = self._args(q, k, v, beta, g, cu, S0)
+        H, hk, d, dt = self.n_heads, self.n_key_heads, self.d, (self.dtype,)
+        for name, t, numel in (("dy", dy, n * H * d), ("dq", dq, n * hk * d), ("dk", dk, n * hk * d),
+                               ("dv", dv, n * H * d), ("dbeta", dbeta, n * H),
+                               ("dg", dg, n * H * (d if self.gate == SQ_GATE_KDA else 1))):
+            _need(t, name, numel, dt)
+        for name, t in (("dS_out", dS_out), ("dS0", dS0)):
+            if t is not None:
+                _need(t, name, n_seq * H * d * d, (torch.float32,))
+        sq_chunk_backward(desc, cu, q, k, v, beta, g, dy, dS_out, self.save, dq, dk, dv, dbeta, dg,
+                          dS0, self.work, stream=stream)
 
 
 SQ_DRAFT_MAX = 32
