@@ -10,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -48,7 +49,7 @@ def hipcc() -> str:
 def build(verbose: bool = False, extra=(), timeline: bool = False) -> str:
     """Compile every source and link libsq.so (always rebuilds); timeline:
     the instrumented build libsq_timeline.so instead."""
-    objs = []
+    objs, jobs = [], []
     build_dir = os.path.join(HERE, "_build_timeline" if timeline else "_build")
     os.makedirs(build_dir, exist_ok=True)
     flags = HIP_FLAGS + (["-DSQ_TIMELINE"] if timeline else [])
@@ -59,8 +60,10 @@ def build(verbose: bool = False, extra=(), timeline: bool = False) -> str:
         cmd = [hipcc()] + flags + list(extra) + lang + ["-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.check_call(cmd)
+        jobs.append(cmd)
         objs.append(obj)
+    with ThreadPoolExecutor(min(len(jobs), os.cpu_count() or 1, 8)) as pool:
+        list(pool.map(subprocess.check_call, jobs))
     tmp = out + ".tmp"
     cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:

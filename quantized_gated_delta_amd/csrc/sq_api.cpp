@@ -237,6 +237,16 @@ sq_status check_work(const char *name, const void *p, size_t have, size_t need) 
     return SQ_OK;
 }
 
+// beta, GDN's g and their gradients: read and written by the element.
+sq_status check_elems(const sq_seq_desc *d, const char *name, const void *p, bool row_of_channels) {
+    if (d->n_tokens == 0) return SQ_OK;
+    if (row_of_channels) return check_io(name, p, true);
+    if (!p) return fail(SQ_EINVAL, "%s is NULL", name);
+    const int size = d->in_dtype == SQ_F32 ? 4 : 2;
+    if (!aligned(p, size)) return fail(SQ_EINVAL, "%s is not %d-byte aligned", name, size);
+    return SQ_OK;
+}
+
 // Pointers that every sequence call takes.
 sq_status check_seq_io(const sq_seq_desc *d, const int32_t *cu, const void *q, const void *k, const void *v,
                        const void *beta, const void *g, const float *S0) {
@@ -245,7 +255,8 @@ sq_status check_seq_io(const sq_seq_desc *d, const int32_t *cu, const void *q, c
     if (!cu) return fail(SQ_EINVAL, "cu is NULL");
     if (!aligned(cu, 4)) return fail(SQ_EINVAL, "cu is not 4-byte aligned");
     if ((st = check_io("q", q, any)) || (st = check_io("k", k, any)) || (st = check_io("v", v, any)) ||
-        (st = check_io("beta", beta, any)) || (st = check_io("g", g, any)) || (st = check_io("S0", S0, S0 != nullptr)))
+        (st = check_elems(d, "beta", beta, false)) || (st = check_elems(d, "g", g, d->gate == SQ_GATE_KDA)) ||
+        (st = check_io("S0", S0, S0 != nullptr)))
         return st;
     return SQ_OK;
 }
@@ -567,8 +578,8 @@ sq_status sq_chunk_backward(const sq_seq_desc *desc, const int32_t *cu, const vo
     const bool any = desc->n_tokens > 0;
     if ((st = check_seq_io(desc, cu, q, k, v, beta, g, nullptr)) || (st = check_io("dy", dy, any)) ||
         (st = check_io("dS_out", dS_out, dS_out != nullptr)) || (st = check_io("dq", dq, any)) ||
-        (st = check_io("dk", dk, any)) || (st = check_io("dv", dv, any)) || (st = check_io("dbeta", dbeta, any)) ||
-        (st = check_io("dg", dg, any)) || (st = check_io("dS0", dS0, dS0 != nullptr)) ||
+        (st = check_io("dk", dk, any)) || (st = check_io("dv", dv, any)) || (st = check_elems(desc, "dbeta", dbeta, false)) ||
+        (st = check_elems(desc, "dg", dg, desc->gate == SQ_GATE_KDA)) || (st = check_io("dS0", dS0, dS0 != nullptr)) ||
         (st = check_work("save", save, save_bytes, keep)) || (st = check_work("work", work, work_bytes, need)))
         return st;
     if (debug_slots() && (st = check_cu(desc, cu, stream))) return st;

@@ -9,9 +9,11 @@
 //   dk   = row + col,  row_i = -e^{G_i} dV_i S0^T + sum_{j<i} dB_ij k_j e^{G_i - G_j}
 //                      col_j = e^{G_C - G_j} U_j dS_C^T + sum_{i>j} dB_ij k_i e^{G_i - G_j}
 //                                                        + sum_{i>=j} dP_ij q_i e^{G_i - G_j}
-//   dG_i = q_i dq_i + k_i (row_i - col_i)   (GDN: summed over channels)
-//   dG_C += sum_j k_j (e^{G_C - G_j} U_j dS_C^T) + e^{G_C} rowsum(S0 dS_C),   dg_t = sum_{i >= t} dG_i
-// dF needs no division by beta: M has no beta on its left.
+//   dg_t = sum_{i >= t} X_i + sum_{j < t} Z_j + e^{G_C} rowsum(S0 dS_C)   (GDN: summed over channels)
+//     Z_j = k_j (the first term of col_j),  X_i = q_i dq_i + k_i (row_i - the other terms of col_i)
+// dF needs no division by beta: M has no beta on its left.  A pair (i, i) has no decay:
+// it is left out of X, where it would stand with both signs, and what runs to the chunk's
+// end is summed from the front, so that strong gates (small dg) keep their accuracy.
 //
 // Three kernels: the operands (prep, all chunks in parallel), a scan from the last
 // chunk to the first that carries dS and leaves dV and each chunk's dS, shaped like the forward
@@ -330,8 +332,8 @@ template <int D, bool KDA, bool F32> struct GradLds {
     Elem<F32> k[KQ ? kChunk * ROW : 1], q[KQ ? kChunk * ROW : 1];
     float L[KDA ? kChunk * GROW : 1], R[KDA ? kChunk * GROW : 1];
     __attribute__((aligned(16))) float turn[4][320];
+    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], X[kChunk], Z[kChunk], end[D], range[4];
     double G[kChunk];
-    float beta[kChunk], dG[kChunk], end[KDA ? 5 * D : 8], range[4];
 };
 
 template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(256) void grad_kernel(SeqArgs a) {
@@ -434,14 +436,15 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
                 const int row = 16 * w + g4 + i;
                 float e = col <= row ? s.beta[col] : 0.f;
                 if (!KDA && col <= row) e *= exp_of((float)(s.G[row] - s.G[col]));
-                s.dP[row * kBRow + col] = p[i] * e;
+                if (col == row) s.diag[row] = p[i] * e;
+                s.dP[row * kBRow + col] = col < row ? p[i] * e : 0.f;
                 s.dB[row * kBRow + col] = col < row ? -b[i] * e : 0.f;
             }
         }
         __syncthreads();
         const bool fast = !KDA || s.range[w] <= kBlockRange;
-        f4 dg{};      // GDN: sum over channels of dG, this wave's tokens
-        float tail = 0.f;  // GDN: what the chunk's end adds to every dg
+        f4 X{}, Z{};       // GDN: summed over channels, this wave's tokens
+        float tail = 0.f;  // GDN: e^{G_C} S0 . dS
 #pragma unroll 1
         for (int n = 0; n < NT; ++n) {
             const int ch = 16 * n + r;
@@ -483,25 +486,19 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
             f4 kt, qt;
 #pragma unroll
             for (int i = 0; i < 4; ++i) kt[i] = key(16 * w + g4 + i, ch), qt[i] = query(16 * w + g4 + i, ch);
-            float end = kt[0] * col[0] + kt[1] * col[1] + kt[2] * col[2] + kt[3] * col[3];
-            if (n % 4 == w) {  // the channel's lanes r, r + 16, ..: rows of the operand, not columns of the result
+            if (n % 4 == w) {  // lanes l < 16 have the channel's whole row
                 dot += __shfl_xor(dot, 16);
                 dot += __shfl_xor(dot, 32);
                 if constexpr (KDA) {
                     float e = 0.f;
                     for (int b = 0; b < 4; ++b) e += s.L[(16 * b + 15) * GROW + ch];
-                    if (l < 16) s.end[4 * D + ch] = dot * exp_of(e);
+                    if (l < 16) s.end[ch] = dot * exp_of(e);
                 } else if (l < 16) {
                     tail = fmaf(dot, exp_of((float)s.G[kChunk - 1]), tail);
                 }
             }
-            if constexpr (KDA) {
-                end += __shfl_xor(end, 16);
-                end += __shfl_xor(end, 32);
-                if (l < 16) s.end[w * D + ch] = end;
-            } else {
-                tail += end;
-            }
+            const f4 out = col;  // what runs to the chunk's end
+            col = f4{};
             // ---- between the chunk's tokens, 16 by 16
 #pragma unroll
             for (int J = 0; J < 4; ++J) {  // rows of this wave against keys of block J
@@ -582,8 +579,10 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
                     }
                 }
             }
-            const f4 G = qt * dq + kt * (row - col);
-            f4 dk = row + col;
+            const f4 x = qt * dq + kt * (row - col), z = kt * out;
+            const f4 diag = *reinterpret_cast<const f4 *>(s.diag + 16 * w + g4);
+            dq += diag * kt;
+            f4 dk = row + col + out + diag * qt;
             if (share > 1) {
                 if (h > hk * share) dq += sums[512 * n], dk += sums[512 * n + 256];
                 if (h + 1 < (hk + 1) * share) sums[512 * n] = dq, sums[512 * n + 256] = dk;
@@ -597,43 +596,51 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
                 }
             }
             if constexpr (KDA) {
-                // into dG's place once every wave has read L and R of these channels
+                // in the place of L and R, once every wave has read them for these channels
                 __syncthreads();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s.L[(16 * w + g4 + i) * GROW + ch] = G[i];
+                for (int i = 0; i < 4; ++i) s.L[(16 * w + g4 + i) * GROW + ch] = x[i], s.R[(16 * w + g4 + i) * GROW + ch] = z[i];
             } else {
-                dg += G;
+                X += x, Z += z;
             }
         }
         if constexpr (KDA) {
             __syncthreads();
             if (t < D) {
-                float sum = s.end[t] + s.end[D + t] + s.end[2 * D + t] + s.end[3 * D + t] + s.end[4 * D + t];
+                float sum = s.end[t];
+                for (int i = 0; i < kChunk; ++i) {
+                    const float z = s.R[i * GROW + t];
+                    s.R[i * GROW + t] = sum;
+                    sum += z;
+                }
+                sum = 0.f;
                 for (int i = kChunk - 1; i >= 0; --i) {
                     sum += s.L[i * GROW + t];
-                    if (i < rows) st_elem<F32>(a.dg, ((t0 + i) * a.n_heads + h) * D + t, sum);
+                    if (i < rows) st_elem<F32>(a.dg, ((t0 + i) * a.n_heads + h) * D + t, sum + s.R[i * GROW + t]);
                 }
             }
         } else {
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) dg[i] += __shfl_xor(dg[i], off);
+                for (int i = 0; i < 4; ++i) X[i] += __shfl_xor(X[i], off), Z[i] += __shfl_xor(Z[i], off);
 #pragma unroll
-            for (int off = 1; off < 64; off <<= 1) tail += __shfl_xor(tail, off);
-            if (r == 0)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s.dG[16 * w + g4 + i] = dg[i];
+            for (int off = 1; off < 16; off <<= 1) tail += __shfl_xor(tail, off);
+            if (r == 0) {
+                *reinterpret_cast<f4 *>(s.X + 16 * w + g4) = X;
+                *reinterpret_cast<f4 *>(s.Z + 16 * w + g4) = Z;
+            }
             if (l == 0) s.end[w] = tail;
             __syncthreads();
             if (t < kChunk) {
-                float sum = s.dG[t];  // over the tokens from this one on
+                float after = s.X[t], before = t ? s.Z[t - 1] : 0.f;
 #pragma unroll
                 for (int off = 1; off < 64; off <<= 1) {
-                    const float up = __shfl_down(sum, off);
-                    if (t + off < 64) sum += up;
+                    const float x = __shfl_down(after, off), z = __shfl_up(before, off);
+                    if (t + off < 64) after += x;
+                    if (t >= off) before += z;
                 }
-                sum += s.end[0] + s.end[1] + s.end[2] + s.end[3];
+                const float sum = after + before + (s.end[0] + s.end[1] + s.end[2] + s.end[3]);
                 if (t < rows) st_elem<F32>(a.dg, (t0 + t) * a.n_heads + h, sum);
             }
         }

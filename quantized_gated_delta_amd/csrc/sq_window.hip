@@ -322,7 +322,8 @@ __global__ __launch_bounds__(256) void window_kernel(WindowArgs a, HeadTable tab
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = 16 * m + g4 + i;
-                    s[i] = exp_of(sL[(kW - 1) * GROW + row]) * (S[n][m][i] * sr[row] * c);
+                    // the product as sq_dequant_state rounds it
+                    s[i] = exp_of(sL[(kW - 1) * GROW + row]) * (POOL32 ? S[n][m][i] : (float)(((double)S[n][m][i] * sr[row]) * c));
                 }
                 s = mma16(*reinterpret_cast<const f4 *>(sOut + (16 * m + r) * 20 + g4), u, s);
 #pragma unroll
