@@ -165,6 +165,15 @@ template <bool F32> __device__ __forceinline__ float ld_elem(const void *p, int6
     else
         return (float)static_cast<const __bf16 *>(p)[i];
 }
+// The same in two parts, the load and the widening, so that several loads are
+// in flight before the first is waited for.
+template <bool F32> __device__ __forceinline__ uint32_t ld_raw(const void *p, int64_t i) {
+    if constexpr (F32)
+        return static_cast<const uint32_t *>(p)[i];
+    else
+        return static_cast<const uint16_t *>(p)[i];
+}
+template <bool F32> __device__ __forceinline__ float of_raw(uint32_t x) { return __uint_as_float(F32 ? x : x << 16); }
 template <bool F32> __device__ __forceinline__ void st_elem(void *p, int64_t i, float x) {
     if constexpr (F32)
         static_cast<float *>(p)[i] = x;

@@ -66,204 +66,170 @@ template <int D, int BITS> __device__ __forceinline__ void unpack4x16(const uint
     }
 }
 
-template <int D, bool KDA, bool F32, bool YF32, bool POOL32>
-__global__ __launch_bounds__(256) void window_kernel(WindowArgs a, HeadTable tab) {
-    constexpr int MT = D / 16, NT = D / 64, KB = D / 32, GROW = D + 4, KROW = D + 8, CW = D / 4 + 1;
+// Codes of a record, unpacked by 256 threads (D = 64: by the 64 from 128 on).
+template <int D> __device__ __forceinline__ void unpack_record(const uint8_t *rec, uint32_t bits, uint32_t n4, uint32_t n6, uint32_t *sC, int t) {
+    const int u = D == 128 ? t : t - 128;
+    if (u < 0 || u >= D / 4 * (D / 16)) return;
+    const int cg = u % (D / 16), row0 = u / (D / 16) * 4;
+    if (bits == 6) {
+        unpack4x16<D, 6>(rec + row0 * (D * 6 / 8), cg, row0, sC);
+    } else if (bits == 4) {
+        unpack4x16<D, 4>(rec + row0 * (D * 4 / 8), cg, row0, sC);
+    } else if (bits == 8) {
+        unpack4x16<D, 8>(rec + row0 * D, cg, row0, sC);
+    } else if (row0 < (int)n4) {  // per-row widths: four rows share one
+        unpack4x16<D, 4>(rec + row0 * (D / 2), cg, row0, sC);
+    } else if (row0 < (int)(n4 + n6)) {
+        unpack4x16<D, 6>(rec + n4 * (D / 2) + (row0 - n4) * (D * 6 / 8), cg, row0, sC);
+    } else {
+        unpack4x16<D, 8>(rec + n4 * (D / 2) + n6 * (D * 6 / 8) + (row0 - n4 - n6) * D, cg, row0, sC);
+    }
+}
+
+// KEEP: S_out is wanted.  One thread per channel prepares the keys, one the
+// queries, while all unpack; after one barrier each wave works alone: it forms the
+// pairs of tokens for itself (16 x 16, cheaper than waiting for another wave).
+template <int D, bool KDA, bool F32, bool YF32, bool POOL32, bool KEEP>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void window_kernel(WindowArgs a, HeadTable tab) {
+    constexpr int MT = D / 16, NT = D / 64, KB = D / 32, EROW = D + 4, KROW = D + 8, CW = D / 4 + 1;
     constexpr int NQ = YF32 ? 3 : 2;
     __shared__ uint32_t sC[POOL32 ? 1 : D * CW];
-    __shared__ float sL[kW * GROW], sR[kW * GROW];
-    __shared__ uint16_t sK[3 * kW * KROW], sQ[NQ * kW * KROW];
-    __shared__ float sOut[D * 20];  // keys decayed to the window's end, [channel][token]
-    __shared__ float sM[16 * 20], sP[16 * 20], sB[16 * kBRow], sInv[16 * 20], sBeta[kW];
-    __shared__ float sr[D], sc[D], sRange;
+    __shared__ __attribute__((aligned(16))) uint16_t sK[3 * kW * KROW], sQ[NQ * kW * KROW];
+    __shared__ __attribute__((aligned(16))) float sE[KDA ? 3 * kW * EROW : 4];  // keys times e^L, e^-L, queries times e^L
+    __shared__ __attribute__((aligned(16))) float sOut[KEEP ? D * 20 : 4];      // keys decayed to the window's end, [channel][token]
+    __shared__ __attribute__((aligned(16))) float sFade[KEEP ? D : 4], sr[KEEP ? D : 4];
+    __shared__ __attribute__((aligned(16))) float sTurn[4 * 320], sBeta[kW], sL[kW], sR[kW];
+    __shared__ int sSlow[2];
     const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    float *tile = sTurn + w * 320;
     const int b = blockIdx.x / (uint32_t)a.n_heads, h = blockIdx.x % (uint32_t)a.n_heads;
     const int hk = h / (a.n_heads / a.n_key_heads);
     const int L = a.length, len = a.lens ? min(max(a.lens[b], 0), L) : L;
-    const int64_t slot = a.slot[b];
+    const int64_t slot = a.slot[b], tok0 = (int64_t)b * L;
 
-    // ---- the state: codes to LDS, scales
     uint32_t bits = 32, n4 = 0, n6 = 0;
     const uint8_t *rec = nullptr;
+    int64_t codes = 0;
     if constexpr (!POOL32) {
         bits = tab.info[h] & 255, n4 = tab.info[h] >> 8 & 255, n6 = tab.info[h] >> 16 & 255;
         rec = a.base + slot * a.slot_stride + tab.off[h];
-        if (bits != 16) {
-            int64_t codes = (int64_t)D * D * bits / 8;
-            if (bits == 0) codes = (int64_t)D * (4 * n4 + 6 * n6 + 8 * (D - n4 - n6)) / 8;
-            if (t < D / 4 * (D / 16)) {
-                const int cg = t % (D / 16), row0 = t / (D / 16) * 4;
-                if (bits == 6) {
-                    unpack4x16<D, 6>(rec + row0 * (D * 6 / 8), cg, row0, sC);
-                } else if (bits == 4) {
-                    unpack4x16<D, 4>(rec + row0 * (D * 4 / 8), cg, row0, sC);
-                } else if (bits == 8) {
-                    unpack4x16<D, 8>(rec + row0 * D, cg, row0, sC);
-                } else if (row0 < (int)n4) {  // per-row widths: four rows share one
-                    unpack4x16<D, 4>(rec + row0 * (D / 2), cg, row0, sC);
-                } else if (row0 < (int)(n4 + n6)) {
-                    unpack4x16<D, 6>(rec + n4 * (D / 2) + (row0 - n4) * (D * 6 / 8), cg, row0, sC);
-                } else {
-                    unpack4x16<D, 8>(rec + n4 * (D / 2) + n6 * (D * 6 / 8) + (row0 - n4 - n6) * D, cg, row0, sC);
-                }
-            }
-            if (t < D) {
-                sr[t] = reinterpret_cast<const float *>(rec + codes)[t];
-                sc[t] = reinterpret_cast<const float *>(rec + codes)[D + t];
-            }
-        } else if (t < D) {
-            sr[t] = sc[t] = 1.f;
-        }
-    } else if (t < D) {
-        sr[t] = sc[t] = 1.f;
+        codes = bits == 0 ? (int64_t)D * (4 * n4 + 6 * n6 + 8 * (D - n4 - n6)) / 8 : (int64_t)D * D * bits / 8;
     }
+    const bool scaled = !POOL32 && bits != 16;
 
-    // ---- sums of the log-gates up to a token and after it
-    if (t == 0) sRange = 0.f;
-    const int64_t tok0 = (int64_t)b * L;
-    if (t < D) {
-        float g[kW], up = 0.f, down = 0.f;
+    // the raw keys and queries of token r for the pairs (GDN), the columns' scales
+    Frag<F32, 1> rk[KDA ? 1 : KB], rq[KDA ? 1 : KB];
+    if constexpr (!KDA) {
 #pragma unroll
-        for (int i = 0; i < kW; ++i)
-            g[i] = i < len ? fmaxf(ld_elem<F32>(a.g, ((tok0 + i) * a.n_heads + h) * (KDA ? D : 1) + (KDA ? t : 0)), kGateFloor) : 0.f;
-#pragma unroll
-        for (int i = 0; i < kW; ++i) up += g[i], sL[i * GROW + t] = up;
-#pragma unroll
-        for (int i = kW - 1; i >= 0; --i) sR[i * GROW + t] = down, down += g[i];
-    }
-    if (t < kW) sBeta[t] = t < len ? ld_elem<F32>(a.beta, (tok0 + t) * a.n_heads + h) : 0.f;
-    __syncthreads();
-    if (t < D) atomicMax(reinterpret_cast<int *>(&sRange), __float_as_int(fmaxf(-sL[(kW - 1) * GROW + t], 0.f)));
-
-    // ---- the decayed keys and queries
-    for (int u = t; u < kW * D / 8; u += 256) {
-        const int i = u / (D / 8), c = u % (D / 8) * 8;
-        float k[8] = {}, q[8] = {}, x[8];
-        if (i < len) {
-            const int64_t at = ((tok0 + i) * a.n_key_heads + hk) * D + c;
-            widen(load_frag<F32, 1>(static_cast<const Elem<F32> *>(a.k) + at, 0), k);
-            if (a.y) widen(load_frag<F32, 1>(static_cast<const Elem<F32> *>(a.q) + at, 0), q);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float d = exp_of(sL[i * GROW + c + j]) * sr[c + j];
-            sOut[(c + j) * 20 + i] = k[j] * exp_of(sR[i * GROW + c + j]);
-            x[j] = k[j] * d;
-            q[j] *= d;
-        }
-        const Frag<false, 3> fk = make_frag<false, 3>(x);
-        const Frag<false, NQ> fq = make_frag<false, NQ>(q);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf8 *>(sK + p * kW * KROW + i * KROW + c) = fk.t[p];
-#pragma unroll
-        for (int p = 0; p < NQ; ++p) *reinterpret_cast<bf8 *>(sQ + p * kW * KROW + i * KROW + c) = fq.t[p];
-    }
-    __syncthreads();
-
-    // ---- B and M (wave 0), P (wave 1): pairs of tokens
-    if (w < 2) {
-        const void *left = w == 0 ? a.k : a.q;
-        f4 acc{};
-        const bool fast = !KDA || sRange <= kBlockRange;
-        auto row8 = [&](const void *p, int i, int c, float (&x)[8]) {
-            if (i < len && (w == 0 || a.y))
-                widen(load_frag<F32, 1>(static_cast<const Elem<F32> *>(p) + ((tok0 + i) * a.n_key_heads + hk) * D + c, 0), x);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = 0.f;
-        };
-        if (fast) {
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const int c = 32 * kb + g8;
-                float x[8], y[8];
-                row8(left, r, c, x);
-                row8(a.k, r, c, y);
-                if constexpr (KDA) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float e = sL[r * GROW + c + j];
-                        x[j] *= exp_of(e);
-                        y[j] *= exp_of(-e);
-                    }
-                }
-                if constexpr (KDA || F32)
-                    acc = mma<3>(make_frag<false, 3>(x), make_frag<false, 3>(y), acc);
-                else
-                    acc = mma<1>(make_frag<false, 1>(x), make_frag<false, 1>(y), acc);
-            }
-            if constexpr (!KDA) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // the smaller of the two differences that give the sum over (r, row]
-                    const int row = g4 + i;
-                    const float e = row < r ? 0.f : sL[row * GROW] - sL[r * GROW], f = row < r ? 0.f : sR[r * GROW] - sR[row * GROW];
-                    acc[i] *= exp_of(sL[r * GROW] > sR[row * GROW] ? e : f);
-                }
-            }
-        } else {
-            for (int u = 0; u < 136; ++u) {
-                int i = 0, j = u;
-                while (j > i) j -= ++i;
-                float s = 0.f;
-                if (i < len) {
-                    for (int c = l; c < D; c += 64) {
-                        float e = 0.f;
-                        for (int m = j + 1; m <= i; ++m) e += fmaxf(ld_elem<F32>(a.g, ((tok0 + m) * a.n_heads + h) * D + c), kGateFloor);
-                        if (w == 0 || a.y)
-                            s = fmaf(ld_elem<F32>(left, ((tok0 + i) * a.n_key_heads + hk) * D + c) * exp_of(e),
-                                     ld_elem<F32>(a.k, ((tok0 + j) * a.n_key_heads + hk) * D + c), s);
-                    }
-                }
-#pragma unroll
-                for (int off = 32; off; off >>= 1) s += __shfl_xor(s, off);
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    if (g4 + n == i && r == j) acc[n] = s;
+        for (int kb = 0; kb < KB; ++kb) {
+            const int64_t at = ((tok0 + r) * a.n_key_heads + hk) * D + 32 * kb + g8;
+            zero(rk[kb]), zero(rq[kb]);
+            if (r < len) {
+                rk[kb] = load_frag<F32, 1>(static_cast<const Elem<F32> *>(a.k) + at, 0);
+                if (a.y) rq[kb] = load_frag<F32, 1>(static_cast<const Elem<F32> *>(a.q) + at, 0);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = g4 + i;
-            if (w == 0) sB[row * kBRow + r] = r < row ? acc[i] : 0.f;
-            else sP[row * 20 + r] = r <= row ? acc[i] : 0.f;
-        }
     }
-    __syncthreads();
-    if (w == 0) {
-        invert_block(sB, sBeta, sInv, 0, l);
-        __builtin_amdgcn_wave_barrier();
-        f4 nb;  // M = -(I + B diag(beta))^-1 B
+    float cs[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) nb[i] = -sB[(g4 + i) * kBRow + r];
-        const f4 m = mma16(*reinterpret_cast<const f4 *>(sInv + r * 20 + g4), nb, f4{});
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sM[(g4 + i) * 20 + r] = m[i];
-    }
-
-    // ---- the state's columns of this wave, in the result layout
+    for (int n = 0; n < NT; ++n) cs[n] = scaled ? reinterpret_cast<const float *>(rec + codes)[D + (w * NT + n) * 16 + r] : 1.f;
     f4 S[NT][MT];
+    if constexpr (POOL32) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int col = (w * NT + n) * 16 + r;
-        if constexpr (POOL32) {
-            const float *p = reinterpret_cast<const float *>(a.base) + slot * a.slot_stride + (int64_t)h * D * D + col;
+        for (int n = 0; n < NT; ++n) {
+            const float *p = reinterpret_cast<const float *>(a.base) + slot * a.slot_stride + (int64_t)h * D * D + (w * NT + n) * 16 + r;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) S[n][m][i] = p[(16 * m + g4 + i) * D];
-        } else if (bits == 16) {
-            const _Float16 *p = reinterpret_cast<const _Float16 *>(rec) + col;
+        }
+    }
+
+    // ---- a thread per channel: the decayed keys (threads below D), the decayed queries (the next D)
+    const int ch = t % D;
+    const bool keys = t < D;
+    uint32_t rg[kW] = {}, rx[kW] = {}, rv[NT][4];
+    {
+        const void *src = keys || !a.y ? a.k : a.q;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < kW; ++i) {
+            if (i % 4 == 0 && i >= len) break;
+            // past the last token: that one again, its value is not used
+            const int64_t tok = tok0 + min(i, len - 1);
+            rg[i] = ld_raw<F32>(a.g, (tok * a.n_heads + h) * (KDA ? D : 1) + (KDA ? ch : 0));
+            rx[i] = ld_raw<F32>(src, (tok * a.n_key_heads + hk) * D + ch);
+        }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[n][m][i] = (float)p[(16 * m + g4 + i) * D];
-        } else {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const uint32_t x = sC[col * CW + 4 * m + (l >> 4)];
+            for (int i = 0; i < 4; ++i)
+                rv[n][i] = ld_raw<F32>(a.v, ((tok0 + min(g4 + i, L - 1)) * a.n_heads + h) * D + (w * NT + n) * 16 + r);
+    }
+    const uint32_t rbeta = t < kW ? ld_raw<F32>(a.beta, (tok0 + min(t, L - 1)) * a.n_heads + h) : 0;
+    if (t < 2 * D) {
+        float g[kW], x[kW];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[n][m][i] = (float)(int8_t)(x >> (8 * i));
+        for (int i = 0; i < kW; ++i) {
+            g[i] = i < len ? fmaxf(of_raw<F32>(rg[i]), kGateFloor) : 0.f;
+            x[i] = of_raw<F32>(rx[i]);
+        }
+        const float scale = scaled ? reinterpret_cast<const float *>(rec + codes)[ch] : 1.f;
+        float up = 0.f, down = 0.f;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            if (i >= len) break;
+            up += g[i];
+            const float e = x[i] * exp_of(up);
+            __bf16 v[3];
+            split<3>(e * scale, v);
+            uint16_t *at = (keys ? sK : sQ) + i * KROW + ch;
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                if (keys || p < NQ) reinterpret_cast<__bf16 *>(at)[p * kW * KROW] = v[p];
+            if constexpr (KDA) {
+                sE[(keys ? 0 : 2) * kW * EROW + i * EROW + ch] = e;
+                if (keys) sE[kW * EROW + i * EROW + ch] = x[i] * exp_of(-up);
+            } else if (t == 0) {
+                sL[i] = up;
+            }
+        }
+        if (KDA && keys) {
+            const bool slow = __any(up < -kBlockRange);
+            if (l == 0) sSlow[w] = slow;
+        }
+        if (keys && (KEEP || (!KDA && t == 0))) {
+#pragma unroll
+            for (int i = kW - 1; i >= 0; --i) {
+                if constexpr (KEEP) sOut[ch * 20 + i] = i < len ? x[i] * exp_of(down) : 0.f;
+                if (!KDA && t == 0) sR[i] = down;
+                down += g[i];
+            }
+            if constexpr (KEEP) sFade[ch] = exp_of(up), sr[ch] = scale;
+        }
+    }
+    if (t < kW) sBeta[t] = t < len ? of_raw<F32>(rbeta) : 0.f;
+    if constexpr (!POOL32)
+        if (bits != 16) unpack_record<D>(rec, bits, n4, n6, sC, t);
+    __syncthreads();
+
+    // ---- the state's columns of this wave, in the result layout
+    if constexpr (!POOL32) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int col = (w * NT + n) * 16 + r;
+            if (bits == 16) {
+                const _Float16 *p = reinterpret_cast<const _Float16 *>(rec) + col;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[n][m][i] = (float)p[(16 * m + g4 + i) * D];
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint32_t x = sC[col * CW + 4 * m + (l >> 4)];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[n][m][i] = (float)(int8_t)(x >> (8 * i));
+                }
             }
         }
     }
@@ -292,30 +258,102 @@ __global__ __launch_bounds__(256) void window_kernel(WindowArgs a, HeadTable tab
         if (bits == 16) products(std::integral_constant<int, 2>());
         else products(std::integral_constant<int, 1>());
     }
-    __syncthreads();  // M
 
-    const f4 fm = *reinterpret_cast<const f4 *>(sM + r * 20 + g4), fp = *reinterpret_cast<const f4 *>(sP + r * 20 + g4);
+    // ---- pairs of tokens: B and P in the result layout
+    f4 kk{}, qk{};
+    if constexpr (!KDA) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            if constexpr (F32) {
+                float x[8];
+                widen(rk[kb], x);
+                const Frag<false, 3> fk = make_frag<false, 3>(x);
+                widen(rq[kb], x);
+                kk = mma<3>(fk, fk, kk);
+                qk = mma<3>(make_frag<false, 3>(x), fk, qk);
+            } else {
+                kk = mma<1>(rk[kb], rk[kb], kk);
+                qk = mma<1>(rq[kb], rk[kb], qk);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // of the two differences that give the sum over (r, row], the one of smaller sums
+            const int row = g4 + i;
+            const bool in = row < len && r <= row;
+            const float d = !in ? 0.f : sL[r] > sR[row] ? sL[row] - sL[r] : sR[r] - sR[row];
+            kk[i] *= exp_of(d), qk[i] *= exp_of(d);
+        }
+    } else if (!(sSlow[0] | (D == 128 ? sSlow[1] : 0))) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int at = r * EROW + 16 * m + g4;
+            const f4 inv = *reinterpret_cast<const f4 *>(sE + kW * EROW + at);
+            kk = mma16(*reinterpret_cast<const f4 *>(sE + at), inv, kk);
+            qk = mma16(*reinterpret_cast<const f4 *>(sE + 2 * kW * EROW + at), inv, qk);
+        }
+    } else {  // strong gates: each pair by its own sum of log-gates
+        for (int j = 0; j < len; ++j) {
+            float e[D / 64], kj[D / 64];
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                e[c] = 0.f;
+                kj[c] = ld_elem<F32>(a.k, ((tok0 + j) * a.n_key_heads + hk) * D + 64 * c + l);
+            }
+            for (int i = j; i < len; ++i) {
+                float sk = 0.f, sq = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    if (i > j) e[c] += fmaxf(ld_elem<F32>(a.g, ((tok0 + i) * a.n_heads + h) * D + 64 * c + l), kGateFloor);
+                    const int64_t at = ((tok0 + i) * a.n_key_heads + hk) * D + 64 * c + l;
+                    const float x = kj[c] * exp_of(e[c]);
+                    sk = fmaf(x, ld_elem<F32>(a.k, at), sk);
+                    if (a.y) sq = fmaf(x, ld_elem<F32>(a.q, at), sq);
+                }
+#pragma unroll
+                for (int off = 32; off; off >>= 1) sk += __shfl_xor(sk, off), sq += __shfl_xor(sq, off);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    if (g4 + n == i && r == j) kk[n] = sk, qk[n] = sq;
+            }
+        }
+    }
+    // M = (I + N)^-1 (-B) with N = B diag(beta), as (I - N)(I + N^2)(I + N^4)(I + N^8)(-B)
     const f4 beta = *reinterpret_cast<const f4 *>(sBeta + g4);
+    f4 N, m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = g4 + i;
+        const float x = row < len && r < row ? kk[i] : 0.f;
+        m[i] = -x;
+        N[i] = x * sBeta[r];
+        if (!(row < len && r <= row)) qk[i] = 0.f;
+    }
+    f4 fn = turn(tile, N, l);
+    m = mma16(-fn, m, m);
+    for (int reach = 2; reach < len; reach *= 2) {
+        N = mma16(fn, N, f4{});
+        fn = turn(tile, N, l);
+        m = mma16(fn, m, m);
+    }
+    const f4 fm = turn(tile, m, l), fp = turn(tile, qk, l);
+
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int col = (w * NT + n) * 16 + r;
-        const float c = sc[col];
         f4 e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int tok = g4 + i;
-            const float v = tok < len ? ld_elem<F32>(a.v, ((tok0 + tok) * a.n_heads + h) * D + col) : 0.f;
-            e[i] = v - c * ks[n][i];
+            e[i] = tok < len ? of_raw<F32>(rv[n][i]) - cs[n] * ks[n][i] : 0.f;
+            y[n][i] = tok < len ? y[n][i] * cs[n] : 0.f;
         }
         const f4 u = beta * mma16(fm, beta * e, e);
         if (a.y) {
-            const f4 out = mma16(fp, u, y[n] * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (g4 + i < L) st_elem<YF32>(a.y, ((tok0 + g4 + i) * a.n_heads + h) * D + col, g4 + i < len ? out[i] : 0.f);
+            const f4 out = turn(tile, mma16(fp, u, y[n]), l);
+            if (r < L) st_elem4<YF32>(a.y, ((tok0 + r) * a.n_heads + h) * D + (w * NT + n) * 16 + g4, out);
         }
-        if (a.S_out) {
-            float *p = a.S_out + ((int64_t)b * a.n_heads + h) * D * D + col;
+        if constexpr (KEEP) {
+            float *p = a.S_out + ((int64_t)b * a.n_heads + h) * D * D + (w * NT + n) * 16 + g4;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 f4 s;
@@ -323,11 +361,10 @@ __global__ __launch_bounds__(256) void window_kernel(WindowArgs a, HeadTable tab
                 for (int i = 0; i < 4; ++i) {
                     const int row = 16 * m + g4 + i;
                     // the product as sq_dequant_state rounds it
-                    s[i] = exp_of(sL[(kW - 1) * GROW + row]) * (POOL32 ? S[n][m][i] : (float)(((double)S[n][m][i] * sr[row]) * c));
+                    s[i] = sFade[row] * (POOL32 ? S[n][m][i] : (float)(((double)S[n][m][i] * sr[row]) * cs[n]));
                 }
                 s = mma16(*reinterpret_cast<const f4 *>(sOut + (16 * m + r) * 20 + g4), u, s);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p[(int64_t)(16 * m + g4 + i) * D] = s[i];
+                *reinterpret_cast<f4 *>(p + (int64_t)(16 * m + r) * D) = turn(tile, s, l);
             }
         }
     }
@@ -335,7 +372,9 @@ __global__ __launch_bounds__(256) void window_kernel(WindowArgs a, HeadTable tab
 
 template <int D, bool POOL32, bool KDA, bool F32, bool YF32>
 hipError_t launch(const WindowArgs &a, const HeadTable &tab, hipStream_t stream) {
-    hipLaunchKernelGGL((window_kernel<D, KDA, F32, YF32, POOL32>), dim3((uint32_t)a.n * a.n_heads), dim3(256), 0, stream, a, tab);
+    const dim3 grid((uint32_t)a.n * a.n_heads);
+    if (a.S_out) hipLaunchKernelGGL((window_kernel<D, KDA, F32, YF32, POOL32, true>), grid, dim3(256), 0, stream, a, tab);
+    else hipLaunchKernelGGL((window_kernel<D, KDA, F32, YF32, POOL32, false>), grid, dim3(256), 0, stream, a, tab);
     return hipGetLastError();
 }
 
