@@ -41,48 +41,30 @@ template <int N> __device__ __forceinline__ Frag<false, N> tiles_frag(f4 a, f4 b
     return make_frag<false, N>(x);
 }
 
-// 16 codes of BITS bits from consecutive bytes, as sign-extended bytes.
-template <int BITS> struct Row16 { uint32_t w[BITS / 2]; };
-template <int BITS> __device__ __forceinline__ int code_of(const Row16<BITS> &s, int n) {
+// The codes of 4 rows x 16 columns as they lie in a record: 16 codes are
+// bits / 2 words of a row.
+struct Codes { uint32_t w[4][4]; };
+
+template <int BITS> __device__ __forceinline__ int code_of(const uint32_t (&w)[4], int n) {
     const int bit = n * BITS, k = bit >> 5, off = bit & 31;
-    uint32_t x = s.w[k] >> off;
-    if (off + BITS > 32) x |= s.w[k + 1] << (32 - off);
+    uint32_t x = w[k] >> off;
+    if (off + BITS > 32) x |= w[k + 1] << (32 - off);
     return (int)(x << (32 - BITS)) >> (32 - BITS);
 }
-
-// Rows row0 .. + 3, columns 16 cg .. + 15 into LDS as [column][row] bytes.
-template <int D, int BITS> __device__ __forceinline__ void unpack4x16(const uint8_t *p, int cg, int row0, uint32_t *sC) {
-    constexpr int CW = D / 4 + 1, RB = D * BITS / 8;
-    Row16<BITS> s[4];
+template <int D, int BITS> __device__ __forceinline__ void load_codes(const uint8_t *p, int cg, Codes &c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < BITS / 2; ++j) s[i].w[j] = reinterpret_cast<const uint32_t *>(p + i * RB + cg * 2 * BITS)[j];
+        for (int j = 0; j < BITS / 2; ++j) c.w[i][j] = reinterpret_cast<const uint32_t *>(p + i * (D * BITS / 8) + cg * 2 * BITS)[j];
+}
+// ... into LDS as [column][row] bytes, sign-extended: a word holds a column's four rows.
+template <int D, int BITS> __device__ __forceinline__ void spread_codes(const Codes &c, int cg, int row0, uint32_t *sC) {
+    constexpr int CW = D / 4 + 1;
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
-        const uint32_t b = ((uint32_t)code_of<BITS>(s[0], n) & 255) | ((uint32_t)code_of<BITS>(s[1], n) & 255) << 8 |
-                           ((uint32_t)code_of<BITS>(s[2], n) & 255) << 16 | (uint32_t)code_of<BITS>(s[3], n) << 24;
+        const uint32_t b = ((uint32_t)code_of<BITS>(c.w[0], n) & 255) | ((uint32_t)code_of<BITS>(c.w[1], n) & 255) << 8 |
+                           ((uint32_t)code_of<BITS>(c.w[2], n) & 255) << 16 | (uint32_t)code_of<BITS>(c.w[3], n) << 24;
         sC[(16 * cg + n) * CW + row0 / 4] = b;
-    }
-}
-
-// Codes of a record, unpacked by 256 threads (D = 64: by the 64 from 128 on).
-template <int D> __device__ __forceinline__ void unpack_record(const uint8_t *rec, uint32_t bits, uint32_t n4, uint32_t n6, uint32_t *sC, int t) {
-    const int u = D == 128 ? t : t - 128;
-    if (u < 0 || u >= D / 4 * (D / 16)) return;
-    const int cg = u % (D / 16), row0 = u / (D / 16) * 4;
-    if (bits == 6) {
-        unpack4x16<D, 6>(rec + row0 * (D * 6 / 8), cg, row0, sC);
-    } else if (bits == 4) {
-        unpack4x16<D, 4>(rec + row0 * (D * 4 / 8), cg, row0, sC);
-    } else if (bits == 8) {
-        unpack4x16<D, 8>(rec + row0 * D, cg, row0, sC);
-    } else if (row0 < (int)n4) {  // per-row widths: four rows share one
-        unpack4x16<D, 4>(rec + row0 * (D / 2), cg, row0, sC);
-    } else if (row0 < (int)(n4 + n6)) {
-        unpack4x16<D, 6>(rec + n4 * (D / 2) + (row0 - n4) * (D * 6 / 8), cg, row0, sC);
-    } else {
-        unpack4x16<D, 8>(rec + n4 * (D / 2) + n6 * (D * 6 / 8) + (row0 - n4 - n6) * D, cg, row0, sC);
     }
 }
 
@@ -90,15 +72,17 @@ template <int D> __device__ __forceinline__ void unpack_record(const uint8_t *re
 // queries, while all unpack; after one barrier each wave works alone: it forms the
 // pairs of tokens for itself (16 x 16, cheaper than waiting for another wave).
 template <int D, bool KDA, bool F32, bool YF32, bool POOL32, bool KEEP>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void window_kernel(WindowArgs a, HeadTable tab) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void window_kernel(WindowArgs a, HeadTable tab) {
     constexpr int MT = D / 16, NT = D / 64, KB = D / 32, EROW = D + 4, KROW = D + 8, CW = D / 4 + 1;
-    constexpr int NQ = YF32 ? 3 : 2;
+    // terms that y and the differences to v are accurate to; the latter the same whether or
+    // not S_out is wanted, so that y is the same to the bit
+    constexpr int NQ = YF32 ? 3 : 2, NK = 3;
     __shared__ uint32_t sC[POOL32 ? 1 : D * CW];
-    __shared__ __attribute__((aligned(16))) uint16_t sK[3 * kW * KROW], sQ[NQ * kW * KROW];
+    __shared__ __attribute__((aligned(16))) uint16_t sK[NK * kW * KROW], sQ[NQ * kW * KROW];
     __shared__ __attribute__((aligned(16))) float sE[KDA ? 3 * kW * EROW : 4];  // keys times e^L, e^-L, queries times e^L
     __shared__ __attribute__((aligned(16))) float sOut[KEEP ? D * 20 : 4];      // keys decayed to the window's end, [channel][token]
     __shared__ __attribute__((aligned(16))) float sFade[KEEP ? D : 4], sr[KEEP ? D : 4];
-    __shared__ __attribute__((aligned(16))) float sTurn[4 * 320], sBeta[kW], sL[kW], sR[kW];
+    __shared__ __attribute__((aligned(16))) float sTurn[4 * 320], sBeta[kW];
     __shared__ int sSlow[2];
     const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
     float *tile = sTurn + w * 320;
@@ -133,7 +117,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void w
     float cs[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) cs[n] = scaled ? reinterpret_cast<const float *>(rec + codes)[D + (w * NT + n) * 16 + r] : 1.f;
-    f4 S[NT][MT];
+    f4 S[POOL32 ? NT : 1][POOL32 ? MT : 1];
     if constexpr (POOL32) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -145,10 +129,31 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void w
         }
     }
 
+    // this thread's codes (D = 64: threads 128 .. 191); four rows share a width
+    Codes raw;
+    const int unit = D == 128 ? t : t - 128, cg = unit % (D / 16), row0 = unit / (D / 16) * 4;
+    uint32_t width = 0;
+    if constexpr (!POOL32)
+        if (bits != 16 && unit >= 0 && unit < D / 4 * (D / 16)) {
+            width = bits ? bits : row0 < (int)n4 ? 4 : row0 < (int)(n4 + n6) ? 6 : 8;
+            const uint8_t *p = rec;
+            if (bits == 0) {  // rows of 4, then of 6, then of 8 bits
+                if (width == 4) p += row0 * (D / 2);
+                else if (width == 6) p += n4 * (D / 2) + (row0 - n4) * (D * 6 / 8);
+                else p += n4 * (D / 2) + n6 * (D * 6 / 8) + (row0 - n4 - n6) * D;
+            } else {
+                p += row0 * (D / 8) * bits;
+            }
+            if (width == 6) load_codes<D, 6>(p, cg, raw);
+            else if (width == 4) load_codes<D, 4>(p, cg, raw);
+            else load_codes<D, 8>(p, cg, raw);
+        }
+
     // ---- a thread per channel: the decayed keys (threads below D), the decayed queries (the next D)
     const int ch = t % D;
     const bool keys = t < D;
-    uint32_t rg[kW] = {}, rx[kW] = {}, rv[NT][4];
+    uint32_t rg[KDA ? kW : 1] = {}, rx[kW] = {}, rv[NT][4];
+    if constexpr (!KDA) rg[0] = ld_raw<F32>(a.g, (tok0 + min(r, L - 1)) * a.n_heads + h);
     {
         const void *src = keys || !a.y ? a.k : a.q;
 #pragma unroll
@@ -156,7 +161,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void w
             if (i % 4 == 0 && i >= len) break;
             // past the last token: that one again, its value is not used
             const int64_t tok = tok0 + min(i, len - 1);
-            rg[i] = ld_raw<F32>(a.g, (tok * a.n_heads + h) * (KDA ? D : 1) + (KDA ? ch : 0));
+            if constexpr (KDA) rg[i] = ld_raw<F32>(a.g, (tok * a.n_heads + h) * D + ch);
             rx[i] = ld_raw<F32>(src, (tok * a.n_key_heads + hk) * D + ch);
         }
 #pragma unroll
@@ -166,102 +171,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void w
                 rv[n][i] = ld_raw<F32>(a.v, ((tok0 + min(g4 + i, L - 1)) * a.n_heads + h) * D + (w * NT + n) * 16 + r);
     }
     const uint32_t rbeta = t < kW ? ld_raw<F32>(a.beta, (tok0 + min(t, L - 1)) * a.n_heads + h) : 0;
-    if (t < 2 * D) {
-        float g[kW], x[kW];
-#pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            g[i] = i < len ? fmaxf(of_raw<F32>(rg[i]), kGateFloor) : 0.f;
-            x[i] = of_raw<F32>(rx[i]);
-        }
-        const float scale = scaled ? reinterpret_cast<const float *>(rec + codes)[ch] : 1.f;
-        float up = 0.f, down = 0.f;
-#pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            if (i >= len) break;
-            up += g[i];
-            const float e = x[i] * exp_of(up);
-            __bf16 v[3];
-            split<3>(e * scale, v);
-            uint16_t *at = (keys ? sK : sQ) + i * KROW + ch;
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-                if (keys || p < NQ) reinterpret_cast<__bf16 *>(at)[p * kW * KROW] = v[p];
-            if constexpr (KDA) {
-                sE[(keys ? 0 : 2) * kW * EROW + i * EROW + ch] = e;
-                if (keys) sE[kW * EROW + i * EROW + ch] = x[i] * exp_of(-up);
-            } else if (t == 0) {
-                sL[i] = up;
-            }
-        }
-        if (KDA && keys) {
-            const bool slow = __any(up < -kBlockRange);
-            if (l == 0) sSlow[w] = slow;
-        }
-        if (keys && (KEEP || (!KDA && t == 0))) {
-#pragma unroll
-            for (int i = kW - 1; i >= 0; --i) {
-                if constexpr (KEEP) sOut[ch * 20 + i] = i < len ? x[i] * exp_of(down) : 0.f;
-                if (!KDA && t == 0) sR[i] = down;
-                down += g[i];
-            }
-            if constexpr (KEEP) sFade[ch] = exp_of(up), sr[ch] = scale;
-        }
-    }
-    if (t < kW) sBeta[t] = t < len ? of_raw<F32>(rbeta) : 0.f;
-    if constexpr (!POOL32)
-        if (bits != 16) unpack_record<D>(rec, bits, n4, n6, sC, t);
-    __syncthreads();
+    const float scale = scaled ? reinterpret_cast<const float *>(rec + codes)[ch] : 1.f;
 
-    // ---- the state's columns of this wave, in the result layout
-    if constexpr (!POOL32) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int col = (w * NT + n) * 16 + r;
-            if (bits == 16) {
-                const _Float16 *p = reinterpret_cast<const _Float16 *>(rec) + col;
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[n][m][i] = (float)p[(16 * m + g4 + i) * D];
-            } else {
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint32_t x = sC[col * CW + 4 * m + (l >> 4)];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[n][m][i] = (float)(int8_t)(x >> (8 * i));
-                }
-            }
-        }
-    }
-
-    // ---- look-up and read-out of every token
-    f4 ks[NT], y[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) ks[n] = y[n] = f4{};
-    auto products = [&](auto terms) {
-        constexpr int N = decltype(terms)::value;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            const Frag<false, 3> fk = get_tiles<3, KROW>(sK, r, kb, g4);
-            const Frag<false, NQ> fq = get_tiles<NQ, KROW>(sQ, r, kb, g4);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const Frag<false, N> fs = tiles_frag<N>(S[n][2 * kb], S[n][2 * kb + 1]);
-                ks[n] = mma<3>(fk, fs, ks[n]);
-                y[n] = mma<NQ>(fq, fs, y[n]);
-            }
-        }
-    };
-    if constexpr (POOL32) {
-        products(std::integral_constant<int, 3>());
-    } else {
-        if (bits == 16) products(std::integral_constant<int, 2>());
-        else products(std::integral_constant<int, 1>());
-    }
-
-    // ---- pairs of tokens: B and P in the result layout
+    // ---- pairs of tokens (GDN): B and P in the result layout, and the sums of the
+    // log-gates up to token r and after it, in every lane
     f4 kk{}, qk{};
+    float up = 0.f, down = 0.f, eup = 1.f, edown = 1.f;
     if constexpr (!KDA) {
+        const float g = r < len ? fmaxf(of_raw<F32>(rg[0]), kGateFloor) : 0.f;
+        up = down = g;
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) {
+            const float x = __shfl_up(up, off, 16), y = __shfl_down(down, off, 16);
+            if (r >= off) up += x;
+            if (r + off < 16) down += y;
+        }
+        down = __shfl_down(down, 1, 16);
+        if (r == 15) down = 0.f;
+        eup = exp_of(up), edown = exp_of(down);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             if constexpr (F32) {
@@ -280,10 +207,113 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void w
         for (int i = 0; i < 4; ++i) {
             // of the two differences that give the sum over (r, row], the one of smaller sums
             const int row = g4 + i;
+            const float Lr = __shfl(up, row, 16), Rr = __shfl(down, row, 16);
             const bool in = row < len && r <= row;
-            const float d = !in ? 0.f : sL[r] > sR[row] ? sL[row] - sL[r] : sR[r] - sR[row];
-            kk[i] *= exp_of(d), qk[i] *= exp_of(d);
+            const float d = exp_of(!in ? 0.f : up > Rr ? Lr - up : down - Rr);
+            kk[i] *= d, qk[i] *= d;
         }
+    }
+
+    if (t < 2 * D) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            if (i >= len) break;
+            float e, x = of_raw<F32>(rx[i]);
+            if constexpr (KDA) {
+                sum += fmaxf(of_raw<F32>(rg[i]), kGateFloor);
+                e = x * exp_of(sum);
+            } else {
+                e = x * __shfl(eup, i, 16);
+            }
+            __bf16 v[3];
+            split<3>(e * scale, v);
+            __bf16 *at = reinterpret_cast<__bf16 *>(keys ? sK : sQ) + i * KROW + ch;
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                if (p < (keys ? NK : NQ)) at[p * kW * KROW] = v[p];
+            if constexpr (KDA) {
+                sE[(keys ? 0 : 2) * kW * EROW + i * EROW + ch] = e;
+                if (keys) sE[kW * EROW + i * EROW + ch] = x * exp_of(-sum);
+            } else if (KEEP && keys) {
+                sOut[ch * 20 + i] = x * __shfl(edown, i, 16);
+            }
+        }
+        if (KDA && keys) {
+            const bool slow = __any(sum < -kBlockRange);
+            if (l == 0) sSlow[w] = slow;
+        }
+        if constexpr (KEEP) {
+            if (keys) {
+                if constexpr (KDA) {
+                    float after = 0.f;
+#pragma unroll
+                    for (int i = kW - 1; i >= 0; --i) {
+                        if (i >= len) continue;
+                        sOut[ch * 20 + i] = of_raw<F32>(rx[i]) * exp_of(after);
+                        after += fmaxf(of_raw<F32>(rg[i]), kGateFloor);
+                    }
+                }
+                for (int i = len; i < kW; ++i) sOut[ch * 20 + i] = 0.f;
+                sFade[ch] = KDA ? exp_of(sum) : __shfl(eup, 15, 16), sr[ch] = scale;
+            }
+        }
+    }
+    if (t < kW) sBeta[t] = t < len ? of_raw<F32>(rbeta) : 0.f;
+    if constexpr (!POOL32) {
+        if (width == 6) spread_codes<D, 6>(raw, cg, row0, sC);
+        else if (width == 4) spread_codes<D, 4>(raw, cg, row0, sC);
+        else if (width == 8) spread_codes<D, 8>(raw, cg, row0, sC);
+    }
+    __syncthreads();
+
+    // a tile of the state in the result layout: rows 16 m + 4 (l / 16) .. + 3 of this wave's columns
+    auto state = [&](int n, int m) {
+        if constexpr (POOL32) {
+            return S[n][m];
+        } else {
+            const int col = (w * NT + n) * 16 + r;
+            f4 x;
+            if (bits == 16) {
+                const _Float16 *p = reinterpret_cast<const _Float16 *>(rec) + col;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = (float)p[(16 * m + g4 + i) * D];
+            } else {
+                const uint32_t c = sC[col * CW + 4 * m + (l >> 4)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(c >> (8 * i));
+            }
+            return x;
+        }
+    };
+
+    // ---- look-up and read-out of every token
+    f4 ks[NT], y[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) ks[n] = y[n] = f4{};
+    auto products = [&](auto terms) {
+        constexpr int N = decltype(terms)::value;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const Frag<false, NK> fk = get_tiles<NK, KROW>(sK, r, kb, g4);
+            const Frag<false, NQ> fq = get_tiles<NQ, KROW>(sQ, r, kb, g4);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const Frag<false, N> fs = tiles_frag<N>(state(n, 2 * kb), state(n, 2 * kb + 1));
+                ks[n] = mma<NK>(fk, fs, ks[n]);
+                y[n] = mma<NQ>(fq, fs, y[n]);
+            }
+        }
+    };
+    if constexpr (POOL32) {
+        products(std::integral_constant<int, 3>());
+    } else {
+        if (bits == 16) products(std::integral_constant<int, 2>());
+        else products(std::integral_constant<int, 1>());
+    }
+
+    // ---- pairs of tokens (KDA)
+    if constexpr (!KDA) {
     } else if (!(sSlow[0] | (D == 128 ? sSlow[1] : 0))) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -356,12 +386,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void w
             float *p = a.S_out + ((int64_t)b * a.n_heads + h) * D * D + (w * NT + n) * 16 + g4;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
+                const f4 s0 = state(n, m);
                 f4 s;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = 16 * m + g4 + i;
                     // the product as sq_dequant_state rounds it
-                    s[i] = sFade[row] * (POOL32 ? S[n][m][i] : (float)(((double)S[n][m][i] * sr[row]) * cs[n]));
+                    s[i] = sFade[row] * (POOL32 ? s0[i] : (float)(((double)s0[i] * sr[row]) * cs[n]));
                 }
                 s = mma16(*reinterpret_cast<const f4 *>(sOut + (16 * m + r) * 20 + g4), u, s);
                 *reinterpret_cast<f4 *>(p + (int64_t)(16 * m + r) * D) = turn(tile, s, l);
