@@ -27,106 +27,13 @@ namespace sqk {
 namespace {
 
 template <int D, bool F32> __global__ __launch_bounds__(256) void prep_gdn_bwd_kernel(SeqArgs a) {
-    typedef Elem<F32> E;
     constexpr BackwardLayout lay = backward_layout(D, false, F32);
-    constexpr int TROW = D + 16 / (int)sizeof(E);
-    __shared__ union { struct { float B[kChunk * kBRow], P[kChunk * kBRow]; }; E tok[kChunk * TROW]; } s;
-    __shared__ float sInv[4 * 16 * 20], sBeta[kChunk];
-    __shared__ double sG[kChunk];
-    const int t = threadIdx.x, w = t >> 6, l = t & 63;
-    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
-    const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
-    SeqSpan sp;
-    const int32_t c = chunk_at(a, x, sp);
-    if (c < 0) return;
-    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
-    const int rows = min(kChunk, sp.len - c * kChunk);
-    uint8_t *out = a.work + (x * a.n_heads + h) * lay.block;
-
-    gates_gdn<F32>(a, t0, rows, h, sG, sBeta, t);
-    if (h == hk * share) {
-        write_transposed<D, F32>(a.k, a.k_stride, t0, rows, hk, s.tok, reinterpret_cast<E *>(out + lay.KT), t);
-        write_transposed<D, F32>(a.q, a.q_stride, t0, rows, hk, s.tok, reinterpret_cast<E *>(out + lay.QT), t);
-    } else {
-        __syncthreads();
-    }
-    if (t < kChunk) {
-        float *gt = reinterpret_cast<float *>(out + lay.gates);
-        gt[t] = exp_of((float)sG[t]);
-        gt[kChunk + t] = exp_of((float)(sG[kChunk - 1] - sG[t]));
-        gt[2 * kChunk + t] = sBeta[t];
-    }
-    pairs_gdn<D, F32>(a, t0, rows, hk, sG, s.B, s.P, w, l);
-    __syncthreads();
-    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.PT), t);
-    invert_block(s.B, sBeta, sInv + w * 320, w, l);
-    __syncthreads();
-    f4 m[4];
-    solve_column(s.B, sBeta, sInv, w, l, m);
-#pragma unroll
-    for (int I = 0; I < 4; ++I)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s.P[(16 * I + (l >> 4) * 4 + i) * kBRow + 16 * w + (l & 15)] = m[I][i];
-    __syncthreads();
-    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.MT), t);
+    prepare_gdn<D, F32, 3, true>(a, a.work, lay.block, lay.PT, lay.MT, lay.KT, lay.QT, lay.gates);
 }
 
 template <int D, bool F32> __global__ __launch_bounds__(256) void prep_kda_bwd_kernel(SeqArgs a) {
-    typedef Elem<F32> E;
     constexpr BackwardLayout lay = backward_layout(D, true, F32);
-    constexpr int GROW = KdaLds<D, F32>::GROW, ROW = KdaLds<D, F32>::ROW;
-    __shared__ KdaLds<D, F32> s;
-    __shared__ float sInv[4 * 16 * 20];
-    const int t = threadIdx.x, w = t >> 6, l = t & 63;
-    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
-    const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
-    SeqSpan sp;
-    const int32_t c = chunk_at(a, x, sp);
-    if (c < 0) return;
-    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
-    const int rows = min(kChunk, sp.len - c * kChunk);
-    uint8_t *out = a.work + (x * a.n_heads + h) * lay.block;
-
-    load_kda<D, F32>(a, t0, rows, h, hk, s, t);
-    for (int u = t; u < kChunk * D / 8; u += 256) {
-        const int row = u / (2 * D) * 16 + (u & 15), c8 = u % (2 * D) / 16 * 8;
-        float v[8];
-        decayed8<D, F32, 2>(s, s.k, row, c8, 0, v);
-        Operand<F32, 3, D / 32>::put8(reinterpret_cast<E *>(out + lay.K), row, c8, v);
-    }
-    for (int u = t; u < kChunk * D / 8; u += 256) {
-        const int ch = (u >> 7) * 16 + (u & 15), k8 = (u >> 4 & 7) * 8;  // eight tokens of a channel
-        float before = 0.f, vk[8], vq[8];
-        for (int b = 0; b < k8 >> 4; ++b) before += s.L[(16 * b + 15) * GROW + ch];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float e = exp_of(s.L[(k8 + i) * GROW + ch] + before);
-            vk[i] = ld_elem<F32>(s.k, (k8 + i) * ROW + ch) * e;
-            vq[i] = ld_elem<F32>(s.q, (k8 + i) * ROW + ch) * e;
-        }
-        Operand<F32, 3, 2>::put8(reinterpret_cast<E *>(out + lay.KT), ch, k8, vk);
-        Operand<F32, 3, 2>::put8(reinterpret_cast<E *>(out + lay.QT), ch, k8, vq);
-    }
-    float *gt = reinterpret_cast<float *>(out + lay.gates);
-    if (t < kChunk) gt[t] = s.beta[t];
-    if (t < D) {
-        float e = 0.f;
-        for (int b = 0; b < 4; ++b) e += s.L[(16 * b + 15) * GROW + t];
-        gt[kChunk + t] = exp_of(e);
-    }
-    pairs_kda<D, F32, 3>(a, t0, rows, h, s, w, l);
-    __syncthreads();
-    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.PT), t);
-    invert_block(s.B, s.beta, sInv + w * 320, w, l);
-    __syncthreads();
-    f4 m[4];
-    solve_column(s.B, s.beta, sInv, w, l, m);
-#pragma unroll
-    for (int I = 0; I < 4; ++I)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s.P[(16 * I + (l >> 4) * 4 + i) * kBRow + 16 * w + (l & 15)] = m[I][i];
-    __syncthreads();
-    write_square<F32, 3, true>(s.P, reinterpret_cast<E *>(out + lay.MT), t);
+    prepare_kda<D, F32, 3, true>(a, a.work, lay.block, lay.PT, lay.MT, lay.K, 0, lay.KT, lay.QT, lay.gates);
 }
 
 // One (sequence, head), 16 NCT columns of the state's gradient, all chunks backwards.

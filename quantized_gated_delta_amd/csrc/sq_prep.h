@@ -15,8 +15,8 @@
 // layout is the next product's operand layout: no exchange between waves.
 //
 // No exponential of a positive sum is taken where it could overflow: decays
-// between 16-token blocks go through the sum at the later block's start (both
-// factors at most 1).  Inside a block KDA uses the same product with the block's
+// between 16-token blocks go through the ends of the blocks between them (every
+// factor at most 1).  Inside a block KDA uses the same product with the block's
 // start as reference while no channel loses more than e^-kBlockRange over the block, and
 // exponentials of each pair's own sum otherwise.
 #pragma once
@@ -72,17 +72,39 @@ __device__ __forceinline__ void solve_column(const float *sB, const float *sBeta
     }
 }
 
-// A 64 x 64 matrix in LDS as an operand; TRANS: its transpose.
+// Block (I, J) of a 64 x 64 matrix from the result layout into an operand; TRANS:
+// into the operand of its transpose, which is what the layout already holds.
 template <bool F32, int N, bool TRANS>
-__device__ __forceinline__ void write_square(const float *s, Elem<F32> *out, int t) {
+__device__ __forceinline__ void put_block(Elem<F32> *out, int I, int J, f4 x, float *tile, int l) {
+    const int r = l & 15, g4 = (l >> 4) * 4;
+    if (TRANS) put_operand4<F32, N, 2>(out, 16 * J + r, 16 * I + g4, x);
+    else put_operand4<F32, N, 2>(out, 16 * I + r, 16 * J + g4, turn(tile, x, l));
+}
+
+// What a chunk's pairs come to.  Wave w holds blocks (w, j <= w) of B and P in the result
+// layout, zero above the diagonal; writes P and M as operands (TRANS: their transposes).
+// A fragment spans two blocks, so of the zero half the blocks beside the diagonal ones of
+// even rows are written too.
+template <bool F32, int N, bool TRANS>
+__device__ __forceinline__ void solve_pairs(const f4 (&B)[4], const f4 (&P)[4], float *sB, const float *sBeta, float *sInv, float *tile, Elem<F32> *outP,
+                                            Elem<F32> *outM, int w, int l) {
+    const int r = l & 15, g4 = (l >> 4) * 4;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const int u = t + 256 * n, row = (u >> 7) * 16 + (u & 15), k = (u >> 4 & 7) * 8;
-        float x[8];
+    for (int j = 0; j < 4; ++j) {
+        if (j > (w | 1)) continue;
+        put_block<F32, N, TRANS>(outP, w, j, P[j], tile, l);
+        if (j <= w)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = TRANS ? s[(k + i) * kBRow + row] : s[row * kBRow + k + i];
-        Operand<F32, N, 2>::put8(out, row, k, x);
+            for (int i = 0; i < 4; ++i) sB[(16 * w + g4 + i) * kBRow + 16 * j + r] = B[j][i];
     }
+    __builtin_amdgcn_wave_barrier();
+    invert_block(sB, sBeta, sInv + w * 320, w, l);
+    __syncthreads();
+    f4 m[4];
+    solve_column(sB, sBeta, sInv, w, l, m);
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+        if (I >= (w & ~1)) put_block<F32, 3, TRANS>(outM, I, w, m[I], tile, l);
 }
 
 // Row `row` of the tokens t0 .. of a [token][head][d] input as an operand
@@ -97,23 +119,34 @@ __device__ __forceinline__ Frag<F32, 1> token_frag(const void *base, int64_t str
     return f;
 }
 
-// The chunk's keys or queries as [channel][token], through LDS (s: 64 rows of
-// D + 16 bytes).  All threads call it.
-template <int D, bool F32>
-__device__ __forceinline__ void write_transposed(const void *base, int64_t stride, int64_t t0, int rows, int head, Elem<F32> *s,
-                                                 Elem<F32> *out, int t) {
-    constexpr int ROW = D + 16 / (int)sizeof(Elem<F32>), U = D / 8;
-    for (int u = t; u < kChunk * U; u += 256) {
-        const int row = u / U, c = u % U * 8;
-        const Frag<F32, 1> f = token_frag<F32>(base, stride, t0, rows, row, (int64_t)head * D + c);
-        if constexpr (F32) {
-            *reinterpret_cast<f4 *>(s + row * ROW + c) = f.v[0];
-            *reinterpret_cast<f4 *>(s + row * ROW + c + 4) = f.v[1];
-        } else {
-            *reinterpret_cast<bf8 *>(s + row * ROW + c) = f.t[0];
+// The chunk's keys or queries in LDS, [token][D] padded by 16 bytes.
+template <int D, bool F32> struct TokenTile {
+    static constexpr int ROW = D + 16 / (int)sizeof(Elem<F32>), UNITS = kChunk * D / 8 / 256;
+    Frag<F32, 1> f[UNITS];
+    __device__ __forceinline__ void load(const void *base, int64_t stride, int64_t t0, int rows, int head, int t) {
+#pragma unroll
+        for (int n = 0; n < UNITS; ++n) {
+            const int u = t + 256 * n;
+            f[n] = token_frag<F32>(base, stride, t0, rows, u / (D / 8), (int64_t)head * D + u % (D / 8) * 8);
         }
     }
-    __syncthreads();
+    __device__ __forceinline__ void store(Elem<F32> *s, int t) const {
+#pragma unroll
+        for (int n = 0; n < UNITS; ++n) {
+            const int u = t + 256 * n;
+            Elem<F32> *p = s + u / (D / 8) * ROW + u % (D / 8) * 8;
+            if constexpr (F32) {
+                *reinterpret_cast<f4 *>(p) = f[n].v[0];
+                *reinterpret_cast<f4 *>(p + 4) = f[n].v[1];
+            } else {
+                *reinterpret_cast<bf8 *>(p) = f[n].t[0];
+            }
+        }
+    }
+};
+// ... as the operand [channel][token].
+template <int D, bool F32> __device__ __forceinline__ void write_transposed(const Elem<F32> *s, Elem<F32> *out, int t) {
+    constexpr int ROW = TokenTile<D, F32>::ROW;
     for (int u = t; u < D * 8; u += 256) {
         const int ch = (u >> 7) * 16 + (u & 15), k = (u >> 4 & 7) * 8;
         float x[8];
@@ -121,7 +154,6 @@ __device__ __forceinline__ void write_transposed(const void *base, int64_t strid
         for (int i = 0; i < 8; ++i) x[i] = ld_elem<F32>(s, (k + i) * ROW + ch);
         Operand<F32, 1, 2>::put8(out, ch, k, x);
     }
-    __syncthreads();
 }
 
 // GDN: sums of the log-gates (in double: differences of sums lose nothing) and
@@ -145,155 +177,147 @@ __device__ __forceinline__ void gates_gdn(const SeqArgs &a, int64_t t0, int rows
     }
 }
 
-// GDN: B and P of one chunk into LDS (wave w: token rows 16 w .. + 15; blocks
-// above the diagonal are set to zero).
+// GDN: blocks (w, j <= w) of B and P; fq: the wave's queries, s: the chunk's keys.
 template <int D, bool F32>
-__device__ __forceinline__ void pairs_gdn(const SeqArgs &a, int64_t t0, int rows, int hk, const double *sG, float *sB, float *sP, int w, int l) {
-    constexpr int KB = D / 32;
+__device__ __forceinline__ void pairs_gdn(const Elem<F32> *s, const Frag<F32, 1> (&fq)[D / 32], const double *sG, f4 (&B)[4], f4 (&P)[4], int w, int l) {
+    constexpr int KB = D / 32, ROW = TokenTile<D, F32>::ROW;
     const int r = l & 15, g8 = (l >> 4) * 8, g4 = (l >> 4) * 4;
-    Frag<F32, 1> fk[KB], fq[KB];
+    Frag<F32, 1> fk[KB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        const int64_t at = (int64_t)hk * D + kb * 32 + g8;
-        fk[kb] = token_frag<F32>(a.k, a.k_stride, t0, rows, 16 * w + r, at);
-        fq[kb] = token_frag<F32>(a.q, a.q_stride, t0, rows, 16 * w + r, at);
-    }
+    for (int kb = 0; kb < KB; ++kb) fk[kb] = load_frag<F32, 1>(s + (16 * w + r) * ROW + 32 * kb + g8, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        f4 kk{}, qk{};
-        if (j <= w) {
+        B[j] = P[j] = f4{};
+        if (j > w) continue;
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const Frag<F32, 1> b = token_frag<F32>(a.k, a.k_stride, t0, rows, 16 * j + r, (int64_t)hk * D + kb * 32 + g8);
-                kk = mma<1>(fk[kb], b, kk);
-                qk = mma<1>(fq[kb], b, qk);
-            }
+        for (int kb = 0; kb < KB; ++kb) {
+            const Frag<F32, 1> b = load_frag<F32, 1>(s + (16 * j + r) * ROW + 32 * kb + g8, 0);
+            B[j] = mma<1>(fk[kb], b, B[j]);
+            P[j] = mma<1>(fq[kb], b, P[j]);
         }
         const int col = 16 * j + r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 16 * w + g4 + i;
             const float e = col <= row ? exp_of((float)(sG[row] - sG[col])) : 0.f;
-            sB[row * kBRow + col] = col < row ? kk[i] * e : 0.f;
-            sP[row * kBRow + col] = col <= row ? qk[i] * e : 0.f;
+            B[j][i] = col < row ? B[j][i] * e : 0.f;
+            P[j][i] = col <= row ? P[j][i] * e : 0.f;
         }
     }
 }
 
-// KDA: the chunk's keys, queries (as fp32 or bf16) and, per 16-token block and
-// channel, the sums of the log-gates up to a token (L) and after it (R) in LDS.
-template <int D, bool F32> struct KdaLds {
-    static constexpr int ROW = D + 16 / (int)sizeof(Elem<F32>), GROW = D + 4;
-    union {
-        struct { Elem<F32> k[kChunk * ROW], q[kChunk * ROW]; };
-        struct { float B[kChunk * kBRow], P[kChunk * kBRow]; };  // after k and q were read
-    };
-    float L[kChunk * GROW], R[kChunk * GROW];
-    float beta[kChunk];
-    float range[4];  // the largest loss over a block, per block
-};
+// One chunk of GDN, forward (K as [channel][token] once per key head, P, M, gates) or backward
+// (Q as [channel][token] too, the transposes of P and M).
+template <int D, bool F32, int N, bool BWD>
+__device__ __forceinline__ void prepare_gdn(const SeqArgs &a, uint8_t *work, int64_t block, int64_t oP, int64_t oM, int64_t oKT, int64_t oQT, int64_t oGates) {
+    typedef Elem<F32> E;
+    typedef TokenTile<D, F32> Tile;
+    constexpr int KB = D / 32;
+    __shared__ union {
+        __attribute__((aligned(16))) E k[kChunk * Tile::ROW];
+        float B[kChunk * kBRow];  // after k was read
+    } s;
+    __shared__ __attribute__((aligned(16))) E sQ[BWD ? kChunk * Tile::ROW : 8];
+    __shared__ __attribute__((aligned(16))) float sInv[4 * 320], sTurn[4 * 320], sBeta[kChunk];
+    __shared__ double sG[kChunk];
+    const int t = threadIdx.x, w = t >> 6, l = t & 63;
+    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
+    const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+    uint8_t *out = work + (x * a.n_heads + h) * block;
+    const bool first = h == hk * share;  // its block holds what the heads of a key head share
 
-template <int D, bool F32>
-__device__ __forceinline__ void load_kda(const SeqArgs &a, int64_t t0, int rows, int h, int hk, KdaLds<D, F32> &s, int t) {
-    constexpr int ROW = KdaLds<D, F32>::ROW, GROW = KdaLds<D, F32>::GROW, U = D / 8;
-    for (int u = t; u < kChunk * U; u += 256) {
-        const int row = u / U, c = u % U * 8;
-        const Frag<F32, 1> fk = token_frag<F32>(a.k, a.k_stride, t0, rows, row, (int64_t)hk * D + c);
-        const Frag<F32, 1> fq = token_frag<F32>(a.q, a.q_stride, t0, rows, row, (int64_t)hk * D + c);
-        float g[8];
-        if (row < rows)
-            widen(load_frag<F32, 1>(static_cast<const Elem<F32> *>(a.g) + ((t0 + row) * a.n_heads + h) * D + c, 0), g);
-        else
+    Tile tk, tq;
+    Frag<F32, 1> fq[KB];
+    tk.load(a.k, a.k_stride, t0, rows, hk, t);
+    if (BWD && first) tq.load(a.q, a.q_stride, t0, rows, hk, t);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = 0.f;
-        if constexpr (F32) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                *reinterpret_cast<f4 *>(s.k + row * ROW + c + 4 * i) = fk.v[i];
-                *reinterpret_cast<f4 *>(s.q + row * ROW + c + 4 * i) = fq.v[i];
-            }
-        } else {
-            *reinterpret_cast<bf8 *>(s.k + row * ROW + c) = fk.t[0];
-            *reinterpret_cast<bf8 *>(s.q + row * ROW + c) = fq.t[0];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s.L[row * GROW + c + i] = fmaxf(g[i], kGateFloor);
-    }
-    if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
-    if (t < 4) s.range[t] = 0.f;
+    for (int kb = 0; kb < KB; ++kb)
+        fq[kb] = token_frag<F32>(a.q, a.q_stride, t0, rows, 16 * w + (l & 15), (int64_t)hk * D + kb * 32 + (l >> 4) * 8);
+    gates_gdn<F32>(a, t0, rows, h, sG, sBeta, t);
+    tk.store(s.k, t);
+    if (BWD && first) tq.store(sQ, t);
     __syncthreads();
-    for (int u = t; u < 4 * D; u += 256) {
-        const int blk = u / D, c = u % D;
-        float *L = s.L + blk * 16 * GROW + c, *R = s.R + blk * 16 * GROW + c;
-        float g[16], up = 0.f, down = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = L[i * GROW];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) up += g[i], L[i * GROW] = up;
-#pragma unroll
-        for (int i = 15; i >= 0; --i) R[i * GROW] = down, down += g[i];
-        // non-negative floats order as their bits do
-        atomicMax(reinterpret_cast<int *>(&s.range[blk]), __float_as_int(fmaxf(-up, 0.f)));
+    f4 B[4], P[4];
+    pairs_gdn<D, F32>(s.k, fq, sG, B, P, w, l);
+    if (first) {
+        write_transposed<D, F32>(s.k, reinterpret_cast<E *>(out + oKT), t);
+        if (BWD) write_transposed<D, F32>(sQ, reinterpret_cast<E *>(out + oQT), t);
+    }
+    if (t < kChunk) {
+        float *gt = reinterpret_cast<float *>(out + oGates);
+        gt[t] = exp_of((float)sG[t]);
+        gt[kChunk + t] = exp_of((float)(sG[kChunk - 1] - sG[t]));
+        gt[2 * kChunk + t] = sBeta[t];
     }
     __syncthreads();
+    solve_pairs<F32, N, BWD>(B, P, s.B, sBeta, sInv, sTurn + w * 320, reinterpret_cast<E *>(out + oP), reinterpret_cast<E *>(out + oM), w, l);
 }
 
-// Eight channels of a token with a decay each: x_c e^{G}, where the exponent is
-// the sum from the token's block's start (MODE 0), from the chunk's start (1),
-// to the chunk's end (2), or from the token to block I's start (3).
-template <int D, bool F32, int MODE>
-__device__ __forceinline__ void decayed8(const KdaLds<D, F32> &s, const Elem<F32> *x, int tok, int c, int I, float (&out)[8]) {
-    constexpr int ROW = KdaLds<D, F32>::ROW, GROW = KdaLds<D, F32>::GROW;
-    const float *E = (MODE >= 2 ? s.R : s.L) + tok * GROW + c;
-    const int blk = tok >> 4;
-    float e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = E[i];
-    if (MODE == 1)
-        for (int b = 0; b < blk; ++b)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] += s.L[(16 * b + 15) * GROW + c + i];
-    if (MODE >= 2)
-        for (int b = blk + 1; b < (MODE == 2 ? 4 : I); ++b)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] += s.L[(16 * b + 15) * GROW + c + i];
-    widen(load_frag<F32, 1>(x + tok * ROW + c, 0), out);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] *= exp_of(e[i]);
+// ---- KDA.  Lane l of wave w holds token 16 w + l % 16, channels 32 kb + 8 (l / 16) .. + 7:
+// an operand fragment's places, so what it decays is an operand as it stands.  Sums of log-gates
+// over a 16-token block are scans over 16 lanes.
+
+// Sum over the lanes of a group of 16 up to (from) this one.
+template <int CTRL> __device__ __forceinline__ float add_dpp(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float scan_up(float x) {
+    x = add_dpp<0x111>(x);
+    x = add_dpp<0x112>(x);
+    x = add_dpp<0x114>(x);
+    return add_dpp<0x118>(x);
+}
+__device__ __forceinline__ float scan_after(float x) {  // without the lane itself
+    x = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x101, 0xf, 0xf, true));
+    x = add_dpp<0x101>(x);
+    x = add_dpp<0x102>(x);
+    x = add_dpp<0x104>(x);
+    return add_dpp<0x108>(x);
 }
 
-// The diagonal 16 x 16 blocks of B and P by each pair's own sum of log-gates,
-// for gates too strong for a common reference: a lane holds D / 64 channels,
-// sums over channels go across the wave.  Results in the matrix instruction's layout.
+// The diagonal block of B and P of a wave by each pair's own sum of log-gates, for gates too
+// strong for a common reference: a lane holds D / 64 channels, sums over channels
+// go across the wave.
 template <int D, bool F32>
-__device__ __forceinline__ void diagonal_kda(const SeqArgs &a, int64_t t0, int rows, int h, const KdaLds<D, F32> &s, int w, int l, f4 &dk, f4 &dq) {
-    constexpr int ROW = KdaLds<D, F32>::ROW, NC = D / 64;
-    float g[NC][16];
+__device__ __forceinline__ void diagonal_kda(const SeqArgs &a, int64_t t0, int rows, int h, int hk, int w, int l, f4 &dk, f4 &dq) {
+    constexpr int NC = D / 64;
+    uint32_t g[NC][16], k[NC][16], q[NC][16];
+    const int64_t first = t0 + 16 * w;
+    const int n = rows - 16 * w;  // tokens of the block
+    dk = dq = f4{};
+    if (n <= 0) return;
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int row = 16 * w + i;
-            g[n][i] = row < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + row) * a.n_heads + h) * D + 64 * n + l), kGateFloor) : 0.f;
+            const int64_t tok = first + min(i, n - 1);
+            g[c][i] = ld_raw<F32>(a.g, (tok * a.n_heads + h) * D + 64 * c + l);
+            k[c][i] = ld_raw<F32>(a.k, tok * a.k_stride + (int64_t)hk * D + 64 * c + l);
+            q[c][i] = ld_raw<F32>(a.q, tok * a.q_stride + (int64_t)hk * D + 64 * c + l);
         }
 #pragma unroll 1
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < min(n, 16); ++j) {
         float e[NC], kj[NC];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            e[n] = 0.f;
-            kj[n] = ld_elem<F32>(s.k, (16 * w + j) * ROW + 64 * n + l);
+        for (int c = 0; c < NC; ++c) {
+            e[c] = 0.f;
+            kj[c] = ld_elem<F32>(a.k, (first + j) * a.k_stride + (int64_t)hk * D + 64 * c + l);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            if (i < j) continue;
+            if (i < j || i >= n) continue;
             float sk = 0.f, sq = 0.f;
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                if (i > j) e[n] += g[n][i];
-                const float x = kj[n] * exp_of(e[n]);
-                sk = fmaf(x, ld_elem<F32>(s.k, (16 * w + i) * ROW + 64 * n + l), sk);
-                sq = fmaf(x, ld_elem<F32>(s.q, (16 * w + i) * ROW + 64 * n + l), sq);
+            for (int c = 0; c < NC; ++c) {
+                if (i > j) e[c] += fmaxf(of_raw<F32>(g[c][i]), kGateFloor);
+                const float x = kj[c] * exp_of(e[c]);
+                sk = fmaf(x, of_raw<F32>(k[c][i]), sk);
+                sq = fmaf(x, of_raw<F32>(q[c][i]), sq);
             }
 #pragma unroll
             for (int off = 32; off; off >>= 1) {
@@ -305,53 +329,173 @@ __device__ __forceinline__ void diagonal_kda(const SeqArgs &a, int64_t t0, int r
     }
 }
 
-// KDA: B and P of one chunk into LDS, over the keys and queries there (sB, sP
-// share their place; all threads call it).  PQ: terms that P is accurate to.
-template <int D, bool F32, int PQ>
-__device__ __forceinline__ void pairs_kda(const SeqArgs &a, int64_t t0, int rows, int h, KdaLds<D, F32> &s, int w, int l) {
-    constexpr int KB = D / 32, ROW = KdaLds<D, F32>::ROW, GROW = KdaLds<D, F32>::GROW;
-    const int r = l & 15, g8 = (l >> 4) * 8, g4 = (l >> 4) * 4;
-    const bool fast = s.range[w] <= kBlockRange;
-    f4 kk[4], qk[4];
+template <int D, bool F32, int N, bool BWD>
+__device__ __forceinline__ void prepare_kda(const SeqArgs &a, uint8_t *work, int64_t block, int64_t oP, int64_t oM, int64_t oK, int64_t oQ, int64_t oKT, int64_t oQT,
+                                            int64_t oGates) {
+    typedef Elem<F32> E;
+    constexpr int KB = D / 32, ZROW = D + 4;
+    __shared__ union {
+        __attribute__((aligned(16))) float z[kChunk * ZROW];  // [token][channel]
+        float B[kChunk * kBRow];
+    } s;
+    __shared__ __attribute__((aligned(16))) float sInv[4 * 320], sTurn[4 * 320], sBeta[kChunk], sT[4 * D];  // sT: e^(a block's sum)
+    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g8 = (l >> 4) * 8, g4 = (l >> 4) * 4;
+    const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
+    const int h = blockIdx.x % (uint32_t)a.n_heads, hk = h / (a.n_heads / a.n_key_heads);
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+    uint8_t *out = work + (x * a.n_heads + h) * block;
+
+    Frag<F32, 1> rk[KB], rq[KB], rg[KB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f4{};
-#pragma unroll 1
     for (int kb = 0; kb < KB; ++kb) {
-        const int c = kb * 32 + g8;
-        float x[8];
-        decayed8<D, F32, 0>(s, s.k, 16 * w + r, c, 0, x);
-        const Frag<F32, 3> fk = make_frag<F32, 3>(x);
-        decayed8<D, F32, 0>(s, s.q, 16 * w + r, c, 0, x);
-        const Frag<F32, PQ> fq = make_frag<F32, PQ>(x);
+        const int at = kb * 32 + g8;
+        rg[kb] = token_frag<F32>(a.g, (int64_t)a.n_heads * D, t0, rows, 16 * w + r, (int64_t)h * D + at);
+        rk[kb] = token_frag<F32>(a.k, a.k_stride, t0, rows, 16 * w + r, (int64_t)hk * D + at);
+        rq[kb] = token_frag<F32>(a.q, a.q_stride, t0, rows, 16 * w + r, (int64_t)hk * D + at);
+    }
+    if (t < kChunk) sBeta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
+    // e^L (the log-gates of the block up to the token), e^-L, k e^R (R: after the token) to LDS
+    float eL[KB][8], iL[KB][8];
+    bool weak = true;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j > w || (j == w && !fast)) continue;
-            if (j < w) {
-                decayed8<D, F32, 3>(s, s.k, 16 * j + r, c, w, x);
-            } else {  // e^{-L}: the same block's start as reference
-                widen(load_frag<F32, 1>(s.k + (16 * w + r) * ROW + c, 0), x);
+    for (int kb = 0; kb < KB; ++kb) {
+        float g[8], k[8], z[8];
+        widen(rg[kb], g);
+        widen(rk[kb], k);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= exp_of(-s.L[(16 * w + r) * GROW + c + i]);
-            }
-            const Frag<F32, 3> fb = make_frag<F32, 3>(x);
-            kk[j] = mma<3>(fk, fb, kk[j]);
-            qk[j] = mma<PQ>(fq, fb, qk[j]);
+        for (int i = 0; i < 8; ++i) {
+            g[i] = fmaxf(g[i], kGateFloor);
+            const float L = scan_up(g[i]);
+            eL[kb][i] = exp_of(L);
+            iL[kb][i] = exp_of(fminf(-L, kBlockRange));
+            weak &= L >= -kBlockRange;
+            z[i] = k[i] * exp_of(scan_after(g[i]));
+        }
+        float *p = s.z + (16 * w + r) * ZROW + 32 * kb + g8;
+        *reinterpret_cast<f4 *>(p) = f4{z[0], z[1], z[2], z[3]};
+        *reinterpret_cast<f4 *>(p + 4) = f4{z[4], z[5], z[6], z[7]};
+        if (r == 15) {
+            p = sT + w * D + 32 * kb + g8;
+            *reinterpret_cast<f4 *>(p) = f4{eL[kb][0], eL[kb][1], eL[kb][2], eL[kb][3]};
+            *reinterpret_cast<f4 *>(p + 4) = f4{eL[kb][4], eL[kb][5], eL[kb][6], eL[kb][7]};
         }
     }
-    f4 dk{}, dq{};
-    if (!fast) diagonal_kda<D, F32>(a, t0, rows, h, s, w, l, dk, dq);
+    const bool fast = __all(weak);
     __syncthreads();
+
+    // ---- operands by token, and the pairs
+    f4 B[4], P[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int col = 16 * j + r;
-        const bool diag = j == w && !fast;
+    for (int j = 0; j < 4; ++j) B[j] = P[j] = f4{};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+        const int at = 32 * kb + g8;
+        float k[8], q[8], kl[8], ql[8], m[8];
+        widen(rk[kb], k);
+        widen(rq[kb], q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kl[i] = k[i] * eL[kb][i], ql[i] = q[i] * eL[kb][i], m[i] = 1.f;
+        const Frag<F32, 3> fk = make_frag<F32, 3>(kl);
+        const Frag<F32, N> fq = make_frag<F32, N>(ql);
+        if (fast) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = k[i] * iL[kb][i];
+            const Frag<F32, 3> fb = make_frag<F32, 3>(y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j == w) B[j] = mma<3>(fk, fb, B[j]), P[j] = mma<N>(fq, fb, P[j]);
+        }
+        // blocks before this one, the nearest first: m grows into the decay in between
+#pragma unroll
+        for (int j = 2; j >= 0; --j) {
+            if (j >= w) continue;
+            float y[8], f[8];
+            const float *p = s.z + (16 * j + r) * ZROW + at, *pt = sT + j * D + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = p[i] * m[i], f[i] = pt[i];
+            const Frag<F32, 3> fb = make_frag<F32, 3>(y);
+            B[j] = mma<3>(fk, fb, B[j]);
+            P[j] = mma<N>(fq, fb, P[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] *= f[i];
+        }
+        // m is now the decay from the chunk's start to the block's
+        if (BWD) {
+            float y[8];
+            const float *p = s.z + (16 * w + r) * ZROW + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = p[i];
+            for (int b = w + 1; b < 4; ++b)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= sT[b * D + at + i];
+            Operand<F32, 3, KB>::put8(reinterpret_cast<E *>(out + oK), 16 * w + r, at, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) eL[kb][i] *= m[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) kl[i] *= m[i], ql[i] *= m[i];
+            Operand<F32, 3, KB>::put8(reinterpret_cast<E *>(out + oK), 16 * w + r, at, kl);
+            Operand<F32, N, KB>::put8(reinterpret_cast<E *>(out + oQ), 16 * w + r, at, ql);
+        }
+    }
+    if (!fast) {
+        f4 dk, dq;
+        diagonal_kda<D, F32>(a, t0, rows, h, hk, w, l, dk, dq);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j == w) B[j] = dk, P[j] = dq;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = 16 * w + g4 + i;
-            s.B[row * kBRow + col] = col < row ? (diag ? dk[i] : kk[j][i]) : 0.f;
-            s.P[row * kBRow + col] = col <= row ? (diag ? dq[i] : qk[j][i]) : 0.f;
+            const int row = 16 * w + g4 + i, col = 16 * j + r;
+            if (col >= row) B[j][i] = 0.f;
+            if (col > row) P[j][i] = 0.f;
         }
+    float *gt = reinterpret_cast<float *>(out + oGates);
+    if (t < kChunk) gt[t] = sBeta[t];
+    if (t < D) gt[kChunk + t] = sT[t] * sT[D + t] * sT[2 * D + t] * sT[3 * D + t];
+
+    // ---- operands by channel, through LDS
+    auto by_channel = [&](int64_t o, bool to_end) {
+        for (int u = t; u < D * 8; u += 256) {
+            const int ch = (u >> 7) * 16 + (u & 15), k8 = (u >> 4 & 7) * 8;
+            float m = 1.f, v[8];
+            if (to_end)
+                for (int b = (k8 >> 4) + 1; b < 4; ++b) m *= sT[b * D + ch];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = s.z[(k8 + i) * ZROW + ch] * m;
+            Operand<F32, 3, 2>::put8(reinterpret_cast<E *>(out + o), ch, k8, v);
+        }
+    };
+    if (BWD) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                float y[8];
+                widen(which ? rq[kb] : rk[kb], y);
+                float *p = s.z + (16 * w + r) * ZROW + 32 * kb + g8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= eL[kb][i];
+                *reinterpret_cast<f4 *>(p) = f4{y[0], y[1], y[2], y[3]};
+                *reinterpret_cast<f4 *>(p + 4) = f4{y[4], y[5], y[6], y[7]};
+            }
+            __syncthreads();
+            by_channel(which ? oQT : oKT, false);
+        }
+    } else {
+        by_channel(oKT, true);
     }
+    __syncthreads();
+    solve_pairs<F32, N, BWD>(B, P, s.B, sBeta, sInv, sTurn + w * 320, reinterpret_cast<E *>(out + oP), reinterpret_cast<E *>(out + oM), w, l);
 }
 
 } // namespace sqk

@@ -333,15 +333,24 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqArgs &a, int32_t s) {
 }
 
 // The sequence that owns chunk slot x, and the chunk's number in it (negative
-// where x is idle).
+// where x is idle).  The 64 lanes of a wave probe 64 sequences at a time: two dependent
+// loads for up to 64 sequences, where a binary search would wait for six.
 __device__ __forceinline__ int32_t chunk_at(const SeqArgs &a, int64_t x, SeqSpan &r) {
-    int32_t lo = 0, hi = a.n_seq - 1;
-    while (lo < hi) {  // the last s with slot0(s) <= x
-        const int32_t mid = (lo + hi + 1) >> 1;
-        if (seq_span(a, mid).slot0 <= x) lo = mid;
-        else hi = mid - 1;
+    const int l = threadIdx.x & 63;
+    int32_t lo = 0, n = a.n_seq;
+    while (n > 64) {  // the last probed s with slot0(s) <= x
+        const int32_t step = (n + 63) >> 6, s = lo + l * step;
+        const bool before = l * step < n && seq_span(a, min(s, a.n_seq - 1)).slot0 <= x;
+        const int k = max(__popcll(__ballot(before)) - 1, 0);
+        lo += k * step;
+        n = min(step, n - k * step);
     }
-    r = seq_span(a, lo);
+    const SeqSpan mine = seq_span(a, min(lo + l, a.n_seq - 1));
+    const int k = max(__popcll(__ballot(l < n && mine.slot0 <= x)) - 1, 0);
+    r.seq = lo + k;
+    r.t0 = __builtin_amdgcn_readlane((int)mine.t0, k);
+    r.len = __builtin_amdgcn_readlane(mine.len, k);
+    r.slot0 = r.t0 / kChunk + r.seq;
     const int64_t c = x - r.slot0;
     return c >= 0 && c * kChunk < r.len ? (int32_t)c : -1;
 }
