@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
     E *sU = reinterpret_cast<E *>(lds + SMat::BYTES + XMat::BYTES);
     E *sY = KDA ? sU : reinterpret_cast<E *>(lds + SMat::BYTES + 2 * XMat::BYTES);
 
-    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
     // the slices of one (sequence, head) read the same operands: workgroups go
     // to the 8 XCDs in turn, so they are 8 apart to share an L2
     const uint32_t pairs = (uint32_t)a.n_seq * a.n_heads, j = blockIdx.x >> 3;

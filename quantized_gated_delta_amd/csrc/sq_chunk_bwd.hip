@@ -52,7 +52,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
     E *sU = reinterpret_cast<E *>(lds + SMat::BYTES + XMat::BYTES);
     E *sYg = reinterpret_cast<E *>(lds + SMat::BYTES + 2 * XMat::BYTES + 2 * YMat::BYTES);
 
-    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
     float *tile = sTurn + w * 320;
     const uint32_t pairs = (uint32_t)a.n_seq * a.n_heads, j = blockIdx.x >> 3;
     const uint32_t pair = j / SLICES * 8 + (blockIdx.x & 7);
@@ -230,27 +230,35 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
                     a.dS0[state + (int64_t)((w * MT + m) * 16 + g4 + i) * D + c0 + 16 * n + r] = S[m][n][i];
 }
 
-// Gradients of q, k, beta and g of one chunk and key head.  Wave w: tokens 16 w .. + 15.
+// Gradients of q, k, beta and g of one chunk and key head.  Wave w: tokens 16 w .. + 15, whose
+// dY, dV and E stay in registers while the states go by, 16 channels at a time
+// and the next 16 already on their way: one workgroup per CU, all its registers, since with
+// two the loads' latency was waited for at each step.
+// Between tokens, GDN: the decayed dP and dB as bf16 pairs in registers against the keys
+// and queries by channel.  KDA: 16 by 16 in fp32, the decays put on keys and queries.
 // SLICES: the parts of beta's gradient that the scan left.
 template <int D, bool KDA, bool F32> struct GradLds {
     static constexpr bool KQ = !(F32 && KDA && D == 128);  // keys and queries fit beside the rest
-    static constexpr int ROW = D + 16 / (int)sizeof(Elem<F32>), GROW = D + 4;
-    float dP[kChunk * kBRow], dB[kChunk * kBRow];
-    Elem<F32> k[KQ ? kChunk * ROW : 1], q[KQ ? kChunk * ROW : 1];
-    float L[KDA ? kChunk * GROW : 1], R[KDA ? kChunk * GROW : 1];
+    static constexpr int ROW = TokenTile<D, F32>::ROW, GROW = D + 4;
+    __attribute__((aligned(16))) float dP[kChunk * kBRow], dB[kChunk * kBRow];
+    __attribute__((aligned(16))) Elem<F32> k[KQ ? kChunk * ROW : 8], q[KQ ? kChunk * ROW : 8];
+    // KDA: e^L and e^R, L the log-gates of a token's block up to it, R after it
+    float eL[KDA ? kChunk * GROW : 1], eR[KDA ? kChunk * GROW : 1];
     __attribute__((aligned(16))) float turn[4][320];
-    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], X[kChunk], Z[kChunk], end[D], range[4];
+    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], X[kChunk], Z[kChunk], end[D];
     double G[kChunk];
+    int strong[4];
 };
 
-template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(256) void grad_kernel(SeqArgs a) {
+template <int D, bool KDA, bool F32, int SLICES>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void grad_kernel(SeqArgs a) {
     typedef Elem<F32> E;
     constexpr BackwardLayout lay = backward_layout(D, KDA, F32);
     constexpr SaveLayout save = save_layout(D);
     typedef GradLds<D, KDA, F32> Lds;
     constexpr int KB = D / 32, NT = D / 16, ROW = Lds::ROW, GROW = Lds::GROW, N2 = kSaveTerms;
     __shared__ Lds s;
-    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
     const int64_t x = blockIdx.x / (uint32_t)a.n_key_heads;
     const int hk = blockIdx.x % (uint32_t)a.n_key_heads, share = a.n_heads / a.n_key_heads;
     SeqSpan sp;
@@ -260,21 +268,11 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
     const int rows = min(kChunk, sp.len - c * kChunk);
 
     if constexpr (Lds::KQ) {
-        for (int u = t; u < kChunk * D / 8; u += 256) {
-            const int row = u / (D / 8), ch = u % (D / 8) * 8;
-            const Frag<F32, 1> fk = token_frag<F32>(a.k, a.k_stride, t0, rows, row, (int64_t)hk * D + ch);
-            const Frag<F32, 1> fq = token_frag<F32>(a.q, a.q_stride, t0, rows, row, (int64_t)hk * D + ch);
-            if constexpr (F32) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    *reinterpret_cast<f4 *>(s.k + row * ROW + ch + 4 * i) = fk.v[i];
-                    *reinterpret_cast<f4 *>(s.q + row * ROW + ch + 4 * i) = fq.v[i];
-                }
-            } else {
-                *reinterpret_cast<bf8 *>(s.k + row * ROW + ch) = fk.t[0];
-                *reinterpret_cast<bf8 *>(s.q + row * ROW + ch) = fq.t[0];
-            }
-        }
+        TokenTile<D, F32> tk, tq;
+        tk.load(a.k, a.k_stride, t0, rows, hk, t);
+        tq.load(a.q, a.q_stride, t0, rows, hk, t);
+        tk.store(s.k, t);
+        tq.store(s.q, t);
     }
     auto key = [&](int tok, int ch) {
         if constexpr (Lds::KQ) return ld_elem<F32>(s.k, tok * ROW + ch);
@@ -284,55 +282,86 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
         if constexpr (Lds::KQ) return ld_elem<F32>(s.q, tok * ROW + ch);
         else return tok < rows ? ld_elem<F32>(a.q, (t0 + tok) * a.q_stride + (int64_t)hk * D + ch) : 0.f;
     };
-
-    // the sums over the heads that share the key head, in the place of operands that
-    // only the scans read; every lane adds to what it wrote itself
-    f4 *sums = reinterpret_cast<f4 *>(a.work + (x * a.n_heads + hk * share) * lay.block) + t;
+    const uint8_t *shared_blk = a.work + (x * a.n_heads + hk * share) * lay.block;
+    const E *pKT = reinterpret_cast<const E *>(shared_blk + lay.KT), *pQT = reinterpret_cast<const E *>(shared_blk + lay.QT);
+    // the sums over the heads that share the key head; every lane adds to what it wrote itself
+    f4 *sums = reinterpret_cast<f4 *>(a.work + (x * a.n_heads + hk * share) * lay.block + lay.sum) + t;
 
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
         const uint8_t *blk = a.work + (x * a.n_heads + h) * lay.block, *sv = a.save + (x * a.n_heads + h) * save.block;
         const E *pS = reinterpret_cast<const E *>(sv + save.S), *pE = reinterpret_cast<const E *>(sv + save.E);
         const E *pdS = reinterpret_cast<const E *>(blk + lay.dS), *pdV = reinterpret_cast<const E *>(blk + lay.dV);
         __syncthreads();  // the last head's LDS is done with
-        if constexpr (KDA) {
-            for (int u = t; u < kChunk * D; u += 256) {
-                const int row = u / D, ch = u % D;
-                s.L[row * GROW + ch] = row < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + row) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
-            }
-            if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
-            if (t < 4) s.range[t] = 0.f;
-            __syncthreads();
-            for (int u = t; u < 4 * D; u += 256) {
-                const int b = u / D, ch = u % D;
-                float *L = s.L + b * 16 * GROW + ch, *R = s.R + b * 16 * GROW + ch, g[16], up = 0.f, down = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) g[i] = L[i * GROW];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) up += g[i], L[i * GROW] = up;
-#pragma unroll
-                for (int i = 15; i >= 0; --i) R[i * GROW] = down, down += g[i];
-                atomicMax(reinterpret_cast<int *>(&s.range[b]), __float_as_int(fmaxf(-up, 0.f)));
-            }
-        } else {
-            gates_gdn<F32>(a, t0, rows, h, s.G, s.beta, t);
-        }
-        // ---- the pairs' gradients, rows of this wave: dP and dB (GDN: with the decay)
+        // ---- everything that is waited for once per head
         Frag<F32, 1> fy[KB];
-        Frag<F32, N2> fv[KB], fe[KB];
+        Frag<F32, N2> fv[KB], fe[KB], before[3][KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             fy[kb] = token_frag<F32>(a.dy, (int64_t)a.n_heads * D, t0, rows, 16 * w + r, (int64_t)h * D + kb * 32 + g8);
             fv[kb] = Operand<F32, N2, KB>::get(pdV, w, kb, l);
             fe[kb] = Operand<F32, N2, KB>::get(pE, w, kb, l);
         }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (j < w)
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) before[j][kb] = Operand<F32, N2, KB>::get(pE, j, kb, l);
+        // the states of 16 channels, and (GDN) their keys and queries
+        struct Tile { Frag<F32, N2> S[KB], dS[KB]; Frag<F32, 1> k[KDA ? 1 : 2], q[KDA ? 1 : 2]; } next;
+        auto load_tile = [&](int n) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                next.S[kb] = Operand<F32, N2, KB>::get(pS, n, kb, l);
+                next.dS[kb] = Operand<F32, N2, KB>::get(pdS, n, kb, l);
+            }
+            if constexpr (!KDA)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    next.k[kb] = Operand<F32, 1, 2>::get(pKT, n, kb, l);
+                    next.q[kb] = Operand<F32, 1, 2>::get(pQT, n, kb, l);
+                }
+        };
+        load_tile(0);
+        if constexpr (KDA) {
+            uint32_t raw[4 * D / 256][16];
+#pragma unroll
+            for (int u = 0; u < 4 * D / 256; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int tok = (t + 256 * u) / D * 16 + i;
+                    raw[u][i] = tok < rows ? ld_raw<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + (t + 256 * u) % D) : 0;
+                }
+            if (t < 4) s.strong[t] = 0;
+            if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < 4 * D / 256; ++u) {
+                const int b = (t + 256 * u) / D, ch = (t + 256 * u) % D;
+                float up = 0.f, down = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    up += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
+                    s.eL[(16 * b + i) * GROW + ch] = exp_of(up);
+                }
+#pragma unroll
+                for (int i = 15; i >= 0; --i) {
+                    s.eR[(16 * b + i) * GROW + ch] = exp_of(down);
+                    down += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
+                }
+                if (up < -kBlockRange) s.strong[b] = 1;
+            }
+        } else {
+            gates_gdn<F32>(a, t0, rows, h, s.G, s.beta, t);
+        }
         __syncthreads();
+        // ---- the pairs' gradients, rows of this wave: dP and dB (GDN: with the decay)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f4 p{}, b{};
             if (j <= w) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    const Frag<F32, N2> f = j == w ? fe[kb] : Operand<F32, N2, KB>::get(pE, j, kb, l);
+                    const Frag<F32, N2> f = j == w ? fe[kb] : before[j < 3 ? j : 0][kb];
                     p = mma<N2>(fy[kb], f, p);
                     b = mma<N2>(fv[kb], f, b);
                 }
@@ -349,147 +378,168 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
             }
         }
         __syncthreads();
-        const bool fast = !KDA || s.range[w] <= kBlockRange;
+        const bool fast = !KDA || !s.strong[w];
+        // GDN: rows of dP and dB of this wave's tokens, and the columns as rows
+        Frag<F32, N2> rP[2], rB[2], cP[2], cB[2];
+        float in[4], out[4];  // GDN: decay from the chunk's start to a token, and from it to the end times beta
+        if constexpr (!KDA) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                float u[8], v[8];
+                if (kb == 0 || w >= 2) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        u[i] = s.dP[(16 * w + r) * kBRow + 32 * kb + g8 + i];
+                        v[i] = s.dB[(16 * w + r) * kBRow + 32 * kb + g8 + i];
+                    }
+                    rP[kb] = make_frag<F32, N2>(u), rB[kb] = make_frag<F32, N2>(v);
+                }
+                if (kb == 1 || w < 2) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        u[i] = s.dP[(32 * kb + g8 + i) * kBRow + 16 * w + r];
+                        v[i] = s.dB[(32 * kb + g8 + i) * kBRow + 16 * w + r];
+                    }
+                    cP[kb] = make_frag<F32, N2>(u), cB[kb] = make_frag<F32, N2>(v);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = 16 * w + g4 + i;
+                in[i] = exp_of((float)s.G[tok]);
+                out[i] = exp_of((float)(s.G[kChunk - 1] - s.G[tok])) * s.beta[tok];
+            }
+        }
         f4 X{}, Z{};       // GDN: summed over channels, this wave's tokens
         float tail = 0.f;  // GDN: e^{G_C} S0 . dS
 #pragma unroll 1
         for (int n = 0; n < NT; ++n) {
             const int ch = 16 * n + r;
+            const Tile now = next;
+            load_tile(min(n + 1, NT - 1));
             // ---- through the states
             f4 dq{}, row{}, col{};
             float dot = 0.f;  // S0 . dS of one channel, this lane's columns
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const Frag<F32, N2> f0 = Operand<F32, N2, KB>::get(pS, n, kb, l), f1 = Operand<F32, N2, KB>::get(pdS, n, kb, l);
-                dq = mma<N2>(fy[kb], f0, dq);
-                row = mma<N2>(fv[kb], f0, row);
-                col = mma<N2>(fe[kb], f1, col);
-                if (n % 4 == w) {
+                dq = mma<N2>(fy[kb], now.S[kb], dq);
+                row = mma<N2>(fv[kb], now.S[kb], row);
+                col = mma<N2>(fe[kb], now.dS[kb], col);
+            }
+            if (n % 4 == w) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if constexpr (F32) dot = fmaf(f0.v[i / 4][i % 4], f1.v[i / 4][i % 4], dot);
-                        else dot = fmaf((float)f0.t[0][i] + (float)f0.t[1][i], (float)f1.t[0][i] + (float)f1.t[1][i], dot);
+                        if constexpr (F32) dot = fmaf(now.S[kb].v[i / 4][i % 4], now.dS[kb].v[i / 4][i % 4], dot);
+                        else
+                            dot = fmaf((float)now.S[kb].t[0][i] + (float)now.S[kb].t[1][i], (float)now.dS[kb].t[0][i] + (float)now.dS[kb].t[1][i], dot);
                     }
-                }
-            }
-            f4 eL, eR;  // decay to the token from its block's start, and from it to the block's end
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = 16 * w + g4 + i;
-                float in, out;
-                if constexpr (KDA) {
-                    float lo = s.L[tok * GROW + ch], hi = s.R[tok * GROW + ch];
-                    eL[i] = exp_of(lo), eR[i] = exp_of(hi);
-                    for (int b = 0; b < w; ++b) lo += s.L[(16 * b + 15) * GROW + ch];
-                    for (int b = w + 1; b < 4; ++b) hi += s.L[(16 * b + 15) * GROW + ch];
-                    in = exp_of(lo), out = exp_of(hi);
-                } else {
-                    in = exp_of((float)s.G[tok]), out = exp_of((float)(s.G[kChunk - 1] - s.G[tok]));
-                }
-                dq[i] *= in;
-                row[i] *= -in;
-                col[i] *= out * s.beta[tok];
-            }
-            f4 kt, qt;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kt[i] = key(16 * w + g4 + i, ch), qt[i] = query(16 * w + g4 + i, ch);
-            if (n % 4 == w) {  // lanes l < 16 have the channel's whole row
                 dot += __shfl_xor(dot, 16);
                 dot += __shfl_xor(dot, 32);
-                if constexpr (KDA) {
-                    float e = 0.f;
-                    for (int b = 0; b < 4; ++b) e += s.L[(16 * b + 15) * GROW + ch];
-                    if (l < 16) s.end[ch] = dot * exp_of(e);
-                } else if (l < 16) {
-                    tail = fmaf(dot, exp_of((float)s.G[kChunk - 1]), tail);
-                }
             }
-            const f4 out = col;  // what runs to the chunk's end
-            col = f4{};
-            // ---- between the chunk's tokens, 16 by 16
+            f4 eL, eR, kt, qt;
+            float block[4];  // KDA: the decay over each block of 16 tokens
+            if constexpr (KDA) {
 #pragma unroll
-            for (int J = 0; J < 4; ++J) {  // rows of this wave against keys of block J
-                if (J > w || (J == w && !fast)) continue;
-                f4 kj;
+                for (int b = 0; b < 4; ++b) block[b] = s.eL[(16 * b + 15) * GROW + ch];
+                float lo = 1.f, hi = 1.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) lo *= b < w ? block[b] : 1.f, hi *= b > w ? block[b] : 1.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int tok = 16 * J + g4 + i;
-                    kj[i] = key(tok, ch);
-                    if constexpr (KDA) {
-                        float e = J == w ? -s.L[tok * GROW + ch] : s.R[tok * GROW + ch];
-                        for (int b = J + 1; b < w; ++b) e += s.L[(16 * b + 15) * GROW + ch];
-                        kj[i] *= exp_of(e);
+                    const int tok = 16 * w + g4 + i;
+                    eL[i] = s.eL[tok * GROW + ch], eR[i] = s.eR[tok * GROW + ch];
+                    dq[i] *= eL[i] * lo;
+                    row[i] *= -eL[i] * lo;
+                    col[i] *= eR[i] * hi * s.beta[tok];
+                }
+                if (n % 4 == w && l < 16) s.end[ch] = dot * block[0] * block[1] * block[2] * block[3];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dq[i] *= in[i], row[i] *= -in[i], col[i] *= out[i];
+                if (n % 4 == w && l < 16) tail = fmaf(dot, exp_of((float)s.G[kChunk - 1]), tail);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kt[i] = key(16 * w + g4 + i, ch), qt[i] = query(16 * w + g4 + i, ch);
+            const f4 to_end = col;  // what runs to the chunk's end
+            col = f4{};
+            // ---- between the chunk's tokens
+            if constexpr (!KDA) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    if (kb == 0 || w >= 2) {
+                        dq = mma<N2>(rP[kb], now.k[kb], dq);
+                        row = mma<N2>(rB[kb], now.k[kb], row);
+                    }
+                    if (kb == 1 || w < 2) {
+                        col = mma<N2>(cB[kb], now.k[kb], col);
+                        col = mma<N2>(cP[kb], now.q[kb], col);
                     }
                 }
-                const f4 p = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
-                const f4 b = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
-                if constexpr (KDA) {
+            } else {
+                float m = 1.f;  // the decay between the blocks
+#pragma unroll
+                for (int J = 3; J >= 0; --J) {  // rows of this wave against keys of block J
+                    if (J > w || (J == w && !fast)) continue;
+                    f4 kj;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 16 * J + g4 + i;
+                        kj[i] = J == w ? kt[i] * __builtin_amdgcn_rcpf(eL[i]) : key(tok, ch) * (s.eR[tok * GROW + ch] * m);
+                    }
+                    if (J < w) m *= block[J];
+                    const f4 p = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
+                    const f4 b = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
                     dq += eL * mma16(p, kj, f4{});
                     row += eL * mma16(b, kj, f4{});
-                } else {
-                    dq = mma16(p, kj, dq);
-                    row = mma16(b, kj, row);
                 }
-            }
+                m = 1.f;
 #pragma unroll
-            for (int I = 0; I < 4; ++I) {  // keys of this wave against rows of block I
-                if (I < w || (I == w && !fast)) continue;
-                f4 ki, qi, p, b;
+                for (int I = 0; I < 4; ++I) {  // keys of this wave against rows of block I
+                    if (I < w || (I == w && !fast)) continue;
+                    f4 ki, qi, p, b;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 16 * I + g4 + i;
-                    ki[i] = key(tok, ch), qi[i] = query(tok, ch);
-                    if constexpr (KDA) {
-                        const float e = exp_of(s.L[tok * GROW + ch]);
-                        ki[i] *= e, qi[i] *= e;
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 16 * I + g4 + i;
+                        const float e = I == w ? eL[i] : s.eL[tok * GROW + ch];
+                        ki[i] = (I == w ? kt[i] : key(tok, ch)) * e, qi[i] = (I == w ? qt[i] : query(tok, ch)) * e;
+                        p[i] = s.dP[tok * kBRow + 16 * w + r];
+                        b[i] = s.dB[tok * kBRow + 16 * w + r];
                     }
-                    p[i] = s.dP[tok * kBRow + 16 * w + r];
-                    b[i] = s.dB[tok * kBRow + 16 * w + r];
-                }
-                if constexpr (KDA) {
                     f4 o = mma16(b, ki, f4{});
                     o = mma16(p, qi, o);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = 16 * w + g4 + i;
-                        float e = I == w ? -s.L[tok * GROW + ch] : s.R[tok * GROW + ch];
-                        for (int k = w + 1; k < I; ++k) e += s.L[(16 * k + 15) * GROW + ch];
-                        col[i] = fmaf(exp_of(e), o[i], col[i]);
-                    }
-                } else {
-                    col = mma16(b, ki, col);
-                    col = mma16(p, qi, col);
+                    for (int i = 0; i < 4; ++i) col[i] = fmaf(I == w ? __builtin_amdgcn_rcpf(eL[i]) : eR[i] * m, o[i], col[i]);
+                    if (I > w) m *= block[I];
                 }
-            }
-            if (!fast) {  // strong gates: the block's pairs one by one, each by its own sum of log-gates
-                float gs[16];
+                if (!fast) {  // strong gates: the block's pairs one by one, each by its own sum of log-gates
+                    uint32_t gs[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int tok = 16 * w + i;
-                    gs[i] = KDA && tok < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
-                }
+                    for (int i = 0; i < 16; ++i) gs[i] = ld_raw<F32>(a.g, ((t0 + min(16 * w + i, rows - 1)) * a.n_heads + h) * D + ch);
 #pragma unroll 1
-                for (int j = 0; j < 16; ++j) {
-                    float e = 0.f;
-                    const float kj = key(16 * w + j, ch);
+                    for (int j = 0; j < 16; ++j) {
+                        float e = 0.f;
+                        const float kj = key(16 * w + j, ch);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (i < j) continue;
-                        if (i > j) e += gs[i];
-                        const float d = exp_of(e), p = s.dP[(16 * w + i) * kBRow + 16 * w + j], b = s.dB[(16 * w + i) * kBRow + 16 * w + j];
-                        const float k = d * (b * key(16 * w + i, ch) + p * query(16 * w + i, ch));
-                        if (i / 4 == l >> 4) dq[i % 4] = fmaf(p * d, kj, dq[i % 4]), row[i % 4] = fmaf(b * d, kj, row[i % 4]);
-                        if (j >> 2 == l >> 4) {
+                        for (int i = 0; i < 16; ++i) {
+                            if (i <= j) continue;
+                            if (16 * w + i < rows) e += fmaxf(of_raw<F32>(gs[i]), kGateFloor);
+                            const float d = exp_of(e), p = s.dP[(16 * w + i) * kBRow + 16 * w + j], b = s.dB[(16 * w + i) * kBRow + 16 * w + j];
+                            const float k = d * (b * key(16 * w + i, ch) + p * query(16 * w + i, ch));
+                            if (i / 4 == l >> 4) dq[i % 4] = fmaf(p * d, kj, dq[i % 4]), row[i % 4] = fmaf(b * d, kj, row[i % 4]);
+                            if (j >> 2 == l >> 4) {
 #pragma unroll
-                            for (int m = 0; m < 4; ++m) col[m] += (j & 3) == m ? k : 0.f;
+                                for (int y = 0; y < 4; ++y) col[y] += (j & 3) == y ? k : 0.f;
+                            }
                         }
                     }
                 }
             }
-            const f4 x = qt * dq + kt * (row - col), z = kt * out;
+            const f4 gx = qt * dq + kt * (row - col), gz = kt * to_end;
             const f4 diag = *reinterpret_cast<const f4 *>(s.diag + 16 * w + g4);
             dq += diag * kt;
-            f4 dk = row + col + out + diag * qt;
+            f4 dk = row + col + to_end + diag * qt;
             if (share > 1) {
                 if (h > hk * share) dq += sums[512 * n], dk += sums[512 * n + 256];
                 if (h + 1 < (hk + 1) * share) sums[512 * n] = dq, sums[512 * n + 256] = dk;
@@ -503,12 +553,12 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
                 }
             }
             if constexpr (KDA) {
-                // in the place of L and R, once every wave has read them for these channels
+                // in the place of e^L and e^R, once every wave has read them for these channels
                 __syncthreads();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s.L[(16 * w + g4 + i) * GROW + ch] = x[i], s.R[(16 * w + g4 + i) * GROW + ch] = z[i];
+                for (int i = 0; i < 4; ++i) s.eL[(16 * w + g4 + i) * GROW + ch] = gx[i], s.eR[(16 * w + g4 + i) * GROW + ch] = gz[i];
             } else {
-                X += x, Z += z;
+                X += gx, Z += gz;
             }
         }
         if constexpr (KDA) {
@@ -516,14 +566,14 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
             if (t < D) {
                 float sum = s.end[t];
                 for (int i = 0; i < kChunk; ++i) {
-                    const float z = s.R[i * GROW + t];
-                    s.R[i * GROW + t] = sum;
+                    const float z = s.eR[i * GROW + t];
+                    s.eR[i * GROW + t] = sum;
                     sum += z;
                 }
                 sum = 0.f;
                 for (int i = kChunk - 1; i >= 0; --i) {
-                    sum += s.L[i * GROW + t];
-                    if (i < rows) st_elem<F32>(a.dg, ((t0 + i) * a.n_heads + h) * D + t, sum + s.R[i * GROW + t]);
+                    sum += s.eL[i * GROW + t];
+                    if (i < rows) st_elem<F32>(a.dg, ((t0 + i) * a.n_heads + h) * D + t, sum + s.eR[i * GROW + t]);
                 }
             }
         } else {
@@ -540,14 +590,14 @@ template <int D, bool KDA, bool F32, int SLICES> __global__ __launch_bounds__(25
             if (l == 0) s.end[w] = tail;
             __syncthreads();
             if (t < kChunk) {
-                float after = s.X[t], before = t ? s.Z[t - 1] : 0.f;
+                float after = s.X[t], before_t = t ? s.Z[t - 1] : 0.f;
 #pragma unroll
                 for (int off = 1; off < 64; off <<= 1) {
-                    const float x = __shfl_down(after, off), z = __shfl_up(before, off);
-                    if (t + off < 64) after += x;
-                    if (t >= off) before += z;
+                    const float y = __shfl_down(after, off), z = __shfl_up(before_t, off);
+                    if (t + off < 64) after += y;
+                    if (t >= off) before_t += z;
                 }
-                const float sum = after + before + (s.end[0] + s.end[1] + s.end[2] + s.end[3]);
+                const float sum = after + before_t + (s.end[0] + s.end[1] + s.end[2] + s.end[3]);
                 if (t < rows) st_elem<F32>(a.dg, (t0 + t) * a.n_heads + h, sum);
             }
         }

@@ -220,7 +220,7 @@ __device__ __forceinline__ void prepare_gdn(const SeqArgs &a, uint8_t *work, int
     __shared__ __attribute__((aligned(16))) E sQ[BWD ? kChunk * Tile::ROW : 8];
     __shared__ __attribute__((aligned(16))) float sInv[4 * 320], sTurn[4 * 320], sBeta[kChunk];
     __shared__ double sG[kChunk];
-    const int t = threadIdx.x, w = t >> 6, l = t & 63;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63;
     const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
     const int h = blockIdx.x % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
     SeqSpan sp;
@@ -339,7 +339,7 @@ __device__ __forceinline__ void prepare_kda(const SeqArgs &a, uint8_t *work, int
         float B[kChunk * kBRow];
     } s;
     __shared__ __attribute__((aligned(16))) float sInv[4 * 320], sTurn[4 * 320], sBeta[kChunk], sT[4 * D];  // sT: e^(a block's sum)
-    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g8 = (l >> 4) * 8, g4 = (l >> 4) * 4;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g8 = (l >> 4) * 8, g4 = (l >> 4) * 4;
     const int64_t x = blockIdx.x / (uint32_t)a.n_heads;
     const int h = blockIdx.x % (uint32_t)a.n_heads, hk = h / (a.n_heads / a.n_key_heads);
     SeqSpan sp;

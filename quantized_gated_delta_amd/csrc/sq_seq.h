@@ -402,9 +402,10 @@ __host__ __device__ constexpr SaveLayout save_layout(int d) {
 // queries as [channel][token] (KDA: decayed from the chunk's start), KDA's keys
 // decayed to the chunk's end, the gates' factors as forward, and what the
 // backward scan leaves for the gradients: the state's gradient at the chunk's end
-// and v's, two terms each, and the parts of beta's gradient per 16 columns.
+// and v's, two terms each, the parts of beta's gradient per 16 columns, and room to
+// add up q's and k's gradients over heads that share a key head.
 struct BackwardLayout {
-    int64_t MT, PT, KT, QT, K, gates, dS, dV, dbeta, block;
+    int64_t MT, PT, KT, QT, K, gates, dS, dV, dbeta, sum, block;
 };
 __host__ __device__ constexpr BackwardLayout backward_layout(int d, bool kda, bool f32) {
     BackwardLayout l{};
@@ -418,6 +419,7 @@ __host__ __device__ constexpr BackwardLayout backward_layout(int d, bool kda, bo
     l.dV = at, at += plane_bytes(f32, kSaveTerms, kChunk, d);
     l.gates = at, at += 4 * (3 * kChunk + d);
     l.dbeta = at, at += 4 * kChunk * (d / 16);
+    l.sum = at, at += 2 * 4 * kChunk * d;
     l.block = (at + 255) / 256 * 256;
     return l;
 }

@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
     __shared__ __attribute__((aligned(16))) float sFade[KEEP ? D : 4], sr[KEEP ? D : 4];
     __shared__ __attribute__((aligned(16))) float sTurn[4 * 320], sBeta[kW];
     __shared__ int sSlow[2];
-    const int t = threadIdx.x, w = t >> 6, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
     float *tile = sTurn + w * 320;
     const int b = blockIdx.x / (uint32_t)a.n_heads, h = blockIdx.x % (uint32_t)a.n_heads;
     const int hk = h / (a.n_heads / a.n_key_heads);
