@@ -80,23 +80,16 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
 
     auto block_of = [&](int c, int head) { return a.work + ((sp.slot0 + c) * a.n_heads + head) * lay.block; };
     auto rows_of = [&](int c) { return min(kChunk, sp.len - c * kChunk); };
-    auto load_kq = [&](int c) {
+    auto load_kq = [&](int c, int kb) {
         if constexpr (KDA) {
             const uint8_t *b = block_of(c, h);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                fK[kb] = Operand<F32, KN, KB>::get(reinterpret_cast<const E *>(b + lay.K), w, kb, l);
-                fQ[kb] = Operand<F32, QN, KB>::get(reinterpret_cast<const E *>(b + lay.Q), w, kb, l);
-            }
+            fK[kb] = Operand<F32, KN, KB>::get(reinterpret_cast<const E *>(b + lay.K), w, kb, l);
+            fQ[kb] = Operand<F32, QN, KB>::get(reinterpret_cast<const E *>(b + lay.Q), w, kb, l);
         } else {
             // past the end: the last token again; its beta is 0 there and its y is not stored
-            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + r, rows_of(c) - 1);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const int64_t at = (int64_t)hk * D + kb * 32 + g8;
-                fK[kb] = load_frag<F32, KN>(static_cast<const E *>(a.k) + tok * a.k_stride + at, 0);
-                fQ[kb] = load_frag<F32, QN>(static_cast<const E *>(a.q) + tok * a.q_stride + at, 0);
-            }
+            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + r, rows_of(c) - 1), at = (int64_t)hk * D + kb * 32 + g8;
+            fK[kb] = load_frag<F32, KN>(static_cast<const E *>(a.k) + tok * a.k_stride + at, 0);
+            fQ[kb] = load_frag<F32, QN>(static_cast<const E *>(a.q) + tok * a.q_stride + at, 0);
         }
     };
     auto load_v = [&](int c) {
@@ -136,15 +129,19 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         for (int kb = 0; kb < 2; ++kb)
             if (kb == 0 || w >= 2) fP[kb] = Operand<F32, NTY, 2>::get(b, w, kb, l);
     };
-    auto load_kt = [&](int c) {
+    auto load_kt = [&](int c, int m) {
         const E *b = reinterpret_cast<const E *>(block_of(c, KDA ? h : hk * share) + lay.KT);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-                fKT[m][kb] = Operand<F32, KN, 2>::get(b, w * MT + m, kb, l);
+        for (int kb = 0; kb < 2; ++kb) fKT[m][kb] = Operand<F32, KN, 2>::get(b, w * MT + m, kb, l);
     };
-    if (n_chunks > 0) gt = load_gates(0), load_kq(0), load_v(0), load_m(0), load_p(0), load_kt(0);
+    if (n_chunks > 0) {
+        gt = load_gates(0);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) load_kq(0, kb);
+        load_v(0), load_m(0), load_p(0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) load_kt(0, m);
+    }
 
     for (int c = 0; c < n_chunks; ++c) {
         const int next = min(c + 1, n_chunks - 1), rows = rows_of(c);
@@ -167,14 +164,15 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
 #pragma unroll
         for (int n = 0; n < NCT; ++n) ks[n] = y[n] = f4{};
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
             for (int n = 0; n < NCT; ++n) {
                 const Frag<F32, 3> fs = SMat::get(sS, 16 * n + r, kb * 32 + g8);
                 ks[n] = mma<3>(fK[kb], fs, ks[n]);
                 y[n] = mma<NTY>(fs, fQ[kb], y[n]);
             }
-        load_kq(next);
+            load_kq(next, kb);  // between the products: a load that waits for its turn then waits beside them
+        }
         f4 e[NCT];
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
@@ -203,7 +201,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         load_m(next);
         __syncthreads();
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) {
 #pragma unroll
             for (int n = 0; n < NCT; ++n) {
                 S[m][n] = KDA ? S[m][n] * gt.fade[m] : S[m][n] * gt.fade1;
@@ -211,6 +209,8 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
                 for (int kb = 0; kb < 2; ++kb)
                     S[m][n] = mma<3>(fKT[m][kb], XMat::get(sU, 16 * n + r, kb * 32 + g8), S[m][n]);
             }
+            load_kt(next, m);
+        }
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
             if (!KDA) y[n] *= gt.eq;
@@ -225,7 +225,6 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
             if (16 * w + r < rows)
                 st_elem4<YF32>(a.y, ((sp.t0 + (int64_t)c * kChunk + 16 * w + r) * a.n_heads + h) * D + c0 + 16 * n + g4, y[n]);
         }
-        load_kt(next);
         load_p(next);
         gt = gt_next;
     }

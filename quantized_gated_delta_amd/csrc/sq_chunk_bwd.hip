@@ -231,9 +231,8 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
 }
 
 // Gradients of q, k, beta and g of one chunk and key head.  Wave w: tokens 16 w .. + 15, whose
-// dY, dV and E stay in registers while the states go by, 16 channels at a time
-// and the next 16 already on their way: one workgroup per CU, all its registers, since with
-// two the loads' latency was waited for at each step.
+// dY, dV and E stay in registers while the states go by, 16 channels at a time, the next
+// 16 on their way as soon as the last were read.
 // Between tokens, GDN: the decayed dP and dB as bf16 pairs in registers against the keys
 // and queries by channel.  KDA: 16 by 16 in fp32, the decays put on keys and queries.
 // SLICES: the parts of beta's gradient that the scan left.
@@ -307,21 +306,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) before[j][kb] = Operand<F32, N2, KB>::get(pE, j, kb, l);
         // the states of 16 channels, and (GDN) their keys and queries
-        struct Tile { Frag<F32, N2> S[KB], dS[KB]; Frag<F32, 1> k[KDA ? 1 : 2], q[KDA ? 1 : 2]; } next;
-        auto load_tile = [&](int n) {
+        Frag<F32, N2> tS[KB], tdS[KB];
+        Frag<F32, 1> tk[KDA ? 1 : 2], tq[KDA ? 1 : 2];
+        auto load_states = [&](int n) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                next.S[kb] = Operand<F32, N2, KB>::get(pS, n, kb, l);
-                next.dS[kb] = Operand<F32, N2, KB>::get(pdS, n, kb, l);
+                tS[kb] = Operand<F32, N2, KB>::get(pS, n, kb, l);
+                tdS[kb] = Operand<F32, N2, KB>::get(pdS, n, kb, l);
             }
+        };
+        auto load_tokens = [&](int n) {
             if constexpr (!KDA)
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
-                    next.k[kb] = Operand<F32, 1, 2>::get(pKT, n, kb, l);
-                    next.q[kb] = Operand<F32, 1, 2>::get(pQT, n, kb, l);
+                    tk[kb] = Operand<F32, 1, 2>::get(pKT, n, kb, l);
+                    tq[kb] = Operand<F32, 1, 2>::get(pQT, n, kb, l);
                 }
         };
-        load_tile(0);
         if constexpr (KDA) {
             uint32_t raw[4 * D / 256][16];
 #pragma unroll
@@ -329,7 +330,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int tok = (t + 256 * u) / D * 16 + i;
-                    raw[u][i] = tok < rows ? ld_raw<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + (t + 256 * u) % D) : 0;
+                    raw[u][i] = ld_raw<F32>(a.g, ((t0 + min(tok, rows - 1)) * a.n_heads + h) * D + (t + 256 * u) % D);
                 }
             if (t < 4) s.strong[t] = 0;
             if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
@@ -338,6 +339,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
             for (int u = 0; u < 4 * D / 256; ++u) {
                 const int b = (t + 256 * u) / D, ch = (t + 256 * u) % D;
                 float up = 0.f, down = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (16 * b + i >= rows) raw[u][i] = 0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     up += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
@@ -377,6 +381,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                 s.dB[row * kBRow + col] = col < row ? -b[i] * e : 0.f;
             }
         }
+        load_states(0);
+        load_tokens(0);
         __syncthreads();
         const bool fast = !KDA || !s.strong[w];
         // GDN: rows of dP and dB of this wave's tokens, and the columns as rows
@@ -410,34 +416,51 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                 out[i] = exp_of((float)(s.G[kChunk - 1] - s.G[tok])) * s.beta[tok];
             }
         }
+        // KDA: the same in fp32, 16 by 16
+        f4 bP[4], bB[4], dPt[4], dBt[4];
+        if constexpr (KDA) {
+#pragma unroll
+            for (int J = 0; J < 4; ++J) {
+                if (J <= w) {
+                    bP[J] = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
+                    bB[J] = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
+                }
+                if (J >= w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        dPt[J][i] = s.dP[(16 * J + g4 + i) * kBRow + 16 * w + r];
+                        dBt[J][i] = s.dB[(16 * J + g4 + i) * kBRow + 16 * w + r];
+                    }
+            }
+        }
         f4 X{}, Z{};       // GDN: summed over channels, this wave's tokens
         float tail = 0.f;  // GDN: e^{G_C} S0 . dS
 #pragma unroll 1
         for (int n = 0; n < NT; ++n) {
             const int ch = 16 * n + r;
-            const Tile now = next;
-            load_tile(min(n + 1, NT - 1));
+            const int next = min(n + 1, NT - 1);
             // ---- through the states
             f4 dq{}, row{}, col{};
             float dot = 0.f;  // S0 . dS of one channel, this lane's columns
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                dq = mma<N2>(fy[kb], now.S[kb], dq);
-                row = mma<N2>(fv[kb], now.S[kb], row);
-                col = mma<N2>(fe[kb], now.dS[kb], col);
+                dq = mma<N2>(fy[kb], tS[kb], dq);
+                row = mma<N2>(fv[kb], tS[kb], row);
+                col = mma<N2>(fe[kb], tdS[kb], col);
             }
             if (n % 4 == w) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if constexpr (F32) dot = fmaf(now.S[kb].v[i / 4][i % 4], now.dS[kb].v[i / 4][i % 4], dot);
+                        if constexpr (F32) dot = fmaf(tS[kb].v[i / 4][i % 4], tdS[kb].v[i / 4][i % 4], dot);
                         else
-                            dot = fmaf((float)now.S[kb].t[0][i] + (float)now.S[kb].t[1][i], (float)now.dS[kb].t[0][i] + (float)now.dS[kb].t[1][i], dot);
+                            dot = fmaf((float)tS[kb].t[0][i] + (float)tS[kb].t[1][i], (float)tdS[kb].t[0][i] + (float)tdS[kb].t[1][i], dot);
                     }
                 dot += __shfl_xor(dot, 16);
                 dot += __shfl_xor(dot, 32);
             }
+            load_states(next);  // into the registers just read: the rest of this step hides it
             f4 eL, eR, kt, qt;
             float block[4];  // KDA: the decay over each block of 16 tokens
             if constexpr (KDA) {
@@ -469,14 +492,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     if (kb == 0 || w >= 2) {
-                        dq = mma<N2>(rP[kb], now.k[kb], dq);
-                        row = mma<N2>(rB[kb], now.k[kb], row);
+                        dq = mma<N2>(rP[kb], tk[kb], dq);
+                        row = mma<N2>(rB[kb], tk[kb], row);
                     }
                     if (kb == 1 || w < 2) {
-                        col = mma<N2>(cB[kb], now.k[kb], col);
-                        col = mma<N2>(cP[kb], now.q[kb], col);
+                        col = mma<N2>(cB[kb], tk[kb], col);
+                        col = mma<N2>(cP[kb], tq[kb], col);
                     }
                 }
+                load_tokens(next);
             } else {
                 float m = 1.f;  // the decay between the blocks
 #pragma unroll
@@ -489,50 +513,53 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                         kj[i] = J == w ? kt[i] * __builtin_amdgcn_rcpf(eL[i]) : key(tok, ch) * (s.eR[tok * GROW + ch] * m);
                     }
                     if (J < w) m *= block[J];
-                    const f4 p = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
-                    const f4 b = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
-                    dq += eL * mma16(p, kj, f4{});
-                    row += eL * mma16(b, kj, f4{});
+                    dq += eL * mma16(bP[J], kj, f4{});
+                    row += eL * mma16(bB[J], kj, f4{});
                 }
                 m = 1.f;
 #pragma unroll
                 for (int I = 0; I < 4; ++I) {  // keys of this wave against rows of block I
                     if (I < w || (I == w && !fast)) continue;
-                    f4 ki, qi, p, b;
+                    f4 ki, qi;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int tok = 16 * I + g4 + i;
                         const float e = I == w ? eL[i] : s.eL[tok * GROW + ch];
                         ki[i] = (I == w ? kt[i] : key(tok, ch)) * e, qi[i] = (I == w ? qt[i] : query(tok, ch)) * e;
-                        p[i] = s.dP[tok * kBRow + 16 * w + r];
-                        b[i] = s.dB[tok * kBRow + 16 * w + r];
                     }
-                    f4 o = mma16(b, ki, f4{});
-                    o = mma16(p, qi, o);
+                    f4 o = mma16(dBt[I], ki, f4{});
+                    o = mma16(dPt[I], qi, o);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) col[i] = fmaf(I == w ? __builtin_amdgcn_rcpf(eL[i]) : eR[i] * m, o[i], col[i]);
                     if (I > w) m *= block[I];
                 }
                 if (!fast) {  // strong gates: the block's pairs one by one, each by its own sum of log-gates
-                    uint32_t gs[16];
+                    float *gs = s.turn[w];  // [token][channel]
+                    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) gs[i] = ld_raw<F32>(a.g, ((t0 + min(16 * w + i, rows - 1)) * a.n_heads + h) * D + ch);
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 16 * w + g4 + i;
+                        gs[(g4 + i) * 20 + r] = tok < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
+                    }
+                    __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-                    for (int j = 0; j < 16; ++j) {
-                        float e = 0.f;
+                    for (int j = 0; j < 15; ++j) {
+                        float e = 0.f, sum = 0.f;
                         const float kj = key(16 * w + j, ch);
+#pragma unroll 1
+                        for (int i = j + 1; i < 16; ++i) {
+                            e += gs[i * 20 + r];
+                            const float d = exp_of(e), p = d * s.dP[(16 * w + i) * kBRow + 16 * w + j], b = d * s.dB[(16 * w + i) * kBRow + 16 * w + j];
+                            sum = fmaf(b, key(16 * w + i, ch), fmaf(p, query(16 * w + i, ch), sum));
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (i <= j) continue;
-                            if (16 * w + i < rows) e += fmaxf(of_raw<F32>(gs[i]), kGateFloor);
-                            const float d = exp_of(e), p = s.dP[(16 * w + i) * kBRow + 16 * w + j], b = s.dB[(16 * w + i) * kBRow + 16 * w + j];
-                            const float k = d * (b * key(16 * w + i, ch) + p * query(16 * w + i, ch));
-                            if (i / 4 == l >> 4) dq[i % 4] = fmaf(p * d, kj, dq[i % 4]), row[i % 4] = fmaf(b * d, kj, row[i % 4]);
-                            if (j >> 2 == l >> 4) {
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) col[y] += (j & 3) == y ? k : 0.f;
+                            for (int y = 0; y < 4; ++y) {
+                                const bool mine = g4 + y == i;
+                                dq[y] += mine ? p * kj : 0.f;
+                                row[y] += mine ? b * kj : 0.f;
                             }
                         }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) col[y] += g4 + y == j ? sum : 0.f;
                     }
                 }
             }
@@ -565,15 +592,25 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
             __syncthreads();
             if (t < D) {
                 float sum = s.end[t];
-                for (int i = 0; i < kChunk; ++i) {
-                    const float z = s.eR[i * GROW + t];
-                    s.eR[i * GROW + t] = sum;
-                    sum += z;
+#pragma unroll 1
+                for (int b = 0; b < kChunk; b += 16) {
+                    float z[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] = s.eR[(b + i) * GROW + t];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s.eR[(b + i) * GROW + t] = sum, sum += z[i];
                 }
                 sum = 0.f;
-                for (int i = kChunk - 1; i >= 0; --i) {
-                    sum += s.eL[i * GROW + t];
-                    if (i < rows) st_elem<F32>(a.dg, ((t0 + i) * a.n_heads + h) * D + t, sum + s.eR[i * GROW + t]);
+#pragma unroll 1
+                for (int b = kChunk - 16; b >= 0; b -= 16) {
+                    float y[16], z[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = s.eL[(b + i) * GROW + t], z[i] = s.eR[(b + i) * GROW + t];
+#pragma unroll
+                    for (int i = 15; i >= 0; --i) {
+                        sum += y[i];
+                        if (b + i < rows) st_elem<F32>(a.dg, ((t0 + b + i) * a.n_heads + h) * D + t, sum + z[i]);
+                    }
                 }
             }
         } else {
@@ -603,6 +640,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
         }
         if (t < rows) {
             float sum = 0.f;
+#pragma unroll
             for (int i = 0; i < SLICES; ++i) sum += reinterpret_cast<const float *>(blk + lay.dbeta)[i * kChunk + t];
             st_elem<F32>(a.dbeta, (t0 + t) * a.n_heads + h, sum);
         }
