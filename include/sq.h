@@ -321,8 +321,8 @@ sq_status sq_f32_decode_step(float *state_pool, int32_t n_slots, int32_t n_heads
  *   g (log-gate): [n_tokens, n_heads] for GDN, [n_tokens, n_heads, d_k] for KDA
  * Head h reads the key head h / (n_heads / n_key_heads).  q, k and v may be
  * parts of one wider tensor: q_stride, k_stride and v_stride are the elements
- * from one token to the next (0: dense), a multiple of 16 bytes; everything
- * else is dense.  beta, GDN's g and their gradients need only the alignment
+ * from one token to the next (0: dense), a multiple of 16 bytes and at most
+ * 2^24 elements; everything else is dense.  beta, GDN's g and their gradients need only the alignment
  * of their type (a range of tokens may begin anywhere). */
 typedef struct {
     int32_t n_seq;        /* sequences, >= 0 */

@@ -192,9 +192,10 @@ sq_status check_seq(const sq_seq_desc *d) {
     const struct { const char *name; int64_t stride, dense; } st[3] = {
         {"q_stride", d->q_stride, dense_k}, {"k_stride", d->k_stride, dense_k}, {"v_stride", d->v_stride, dense_v}};
     for (const auto &s : st)
-        if (s.stride != 0 && (s.stride < s.dense || s.stride % per16 != 0 || s.stride > INT64_MAX / 16 / (d->n_tokens + 1)))
-            return fail(SQ_EINVAL, "%s = %lld must be 0 or a multiple of %lld, at least %lld", s.name,
+        if (s.stride != 0 && (s.stride < s.dense || s.stride % per16 != 0 || s.stride > 1 << 24))
+            return fail(SQ_EINVAL, "%s = %lld must be 0 or a multiple of %lld, at least %lld and at most 2^24", s.name,
                         (long long)s.stride, (long long)per16, (long long)s.dense);
+    if (dense_v > 1 << 24) return fail(SQ_EUNSUPPORTED, "n_heads * d_v exceeds 2^24");  // 32-bit offsets within a chunk
     return SQ_OK;
 }
 

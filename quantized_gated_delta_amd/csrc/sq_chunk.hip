@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
     if (pair >= pairs) return;
     const int c0 = (int)(j % SLICES) * COLS;
     const int h = pair % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
-    const SeqSpan sp = seq_span(a, pair / (uint32_t)a.n_heads);
+    const SeqSpan sp = wave_span(a, pair / (uint32_t)a.n_heads);
     const int n_chunks = (sp.len + kChunk - 1) / kChunk;
     const int64_t state = (int64_t)pair * D * D;
 
@@ -87,18 +87,21 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
             fQ[kb] = Operand<F32, QN, KB>::get(reinterpret_cast<const E *>(b + lay.Q), w, kb, l);
         } else {
             // past the end: the last token again; its beta is 0 there and its y is not stored
-            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + r, rows_of(c) - 1), at = (int64_t)hk * D + kb * 32 + g8;
-            fK[kb] = load_frag<F32, KN>(static_cast<const E *>(a.k) + tok * a.k_stride + at, 0);
-            fQ[kb] = load_frag<F32, QN>(static_cast<const E *>(a.q) + tok * a.q_stride + at, 0);
+            const int64_t tok = sp.t0 + (int64_t)c * kChunk, at = (int64_t)hk * D + kb * 32;
+            const uint32_t row = min(16 * w + r, rows_of(c) - 1);
+            const void *pk = static_cast<const E *>(a.k) + tok * a.k_stride + at, *pq = static_cast<const E *>(a.q) + tok * a.q_stride + at;
+            fK[kb] = load_frag<F32, KN>(at_bytes<E>(pk, (row * (uint32_t)a.k_stride + g8) * (uint32_t)sizeof(E)), 0);
+            fQ[kb] = load_frag<F32, QN>(at_bytes<E>(pq, (row * (uint32_t)a.q_stride + g8) * (uint32_t)sizeof(E)), 0);
         }
     };
     auto load_v = [&](int c) {
         const int last = rows_of(c) - 1;
+        const void *pv = static_cast<const E *>(a.v) + (sp.t0 + (int64_t)c * kChunk) * a.v_stride + (int64_t)h * D + c0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + g4 + i, last);
+            const uint32_t row = min(16 * w + g4 + i, last);
 #pragma unroll
-            for (int n = 0; n < NCT; ++n) v[n][i] = ld_elem<F32>(a.v, tok * a.v_stride + (int64_t)h * D + c0 + 16 * n + r);
+            for (int n = 0; n < NCT; ++n) v[n][i] = ld_elem<F32>(at_bytes<E>(pv, (row * (uint32_t)a.v_stride + 16 * n + r) * (uint32_t)sizeof(E)), 0);
         }
     };
     auto load_gates = [&](int c) {
@@ -211,6 +214,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
             }
             load_kt(next, m);
         }
+        char *py = static_cast<char *>(a.y) + (((sp.t0 + (int64_t)c * kChunk) * a.n_heads + h) * D + c0) * (YF32 ? 4 : 2);
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
             if (!KDA) y[n] *= gt.eq;
@@ -223,7 +227,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
                         y[n] = mma<NTY>(YMat::get(sY, 16 * n + r, kb * 32 + g8), fP[kb], y[n]);
                 }
             if (16 * w + r < rows)
-                st_elem4<YF32>(a.y, ((sp.t0 + (int64_t)c * kChunk + 16 * w + r) * a.n_heads + h) * D + c0 + 16 * n + g4, y[n]);
+                st_elem4<YF32>(at_bytes<char>(py, ((16 * w + r) * (uint32_t)(a.n_heads * D) + 16 * n + g4) * (YF32 ? 4u : 2u)), 0, y[n]);
         }
         load_p(next);
         gt = gt_next;

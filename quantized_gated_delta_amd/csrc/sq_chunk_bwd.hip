@@ -59,7 +59,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
     if (pair >= pairs) return;
     const int c0 = (int)(j % SLICES) * COLS;
     const int h = pair % (uint32_t)a.n_heads, share = a.n_heads / a.n_key_heads, hk = h / share;
-    const SeqSpan sp = seq_span(a, pair / (uint32_t)a.n_heads);
+    const SeqSpan sp = wave_span(a, pair / (uint32_t)a.n_heads);
     const int n_chunks = (sp.len + kChunk - 1) / kChunk;
     const int64_t state = (int64_t)pair * D * D;
 
@@ -86,23 +86,22 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
             for (int kb = 0; kb < KB; ++kb) fK[kb] = Operand<F32, KN, KB>::get(b, w, kb, l);
         } else {
             // past the end: the last token again; its beta is 0, so its dV is 0 too
-            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(16 * w + r, rows_of(c) - 1);
+            const void *pk = static_cast<const E *>(a.k) + (sp.t0 + (int64_t)c * kChunk) * a.k_stride + (int64_t)hk * D;
+            const uint32_t row = min(16 * w + r, rows_of(c) - 1);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
-                fK[kb] = load_frag<F32, KN>(static_cast<const E *>(a.k) + tok * a.k_stride + (int64_t)hk * D + kb * 32 + g8, 0);
+                fK[kb] = load_frag<F32, KN>(at_bytes<E>(pk, (row * (uint32_t)a.k_stride + kb * 32 + g8) * (uint32_t)sizeof(E)), 0);
         }
     };
     auto load_dy = [&](int c) {
         const int rows = rows_of(c);
+        const void *py = static_cast<const E *>(a.dy) + ((sp.t0 + (int64_t)c * kChunk) * a.n_heads + h) * D + c0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 16 * w + g4 + i;
-            const int64_t tok = sp.t0 + (int64_t)c * kChunk + min(row, rows - 1);
+            const uint32_t at = min(row, rows - 1) * (uint32_t)(a.n_heads * D) + r;
 #pragma unroll
-            for (int n = 0; n < NCT; ++n) {
-                const float x = ld_elem<F32>(a.dy, (tok * a.n_heads + h) * D + c0 + 16 * n + r);
-                dy[n][i] = row < rows ? x : 0.f;
-            }
+            for (int n = 0; n < NCT; ++n) dy[n][i] = of_raw<F32>(ld_raw<F32>(at_bytes<E>(py, (at + 16 * n) * (uint32_t)sizeof(E)), 0));
         }
     };
     auto load_e = [&](int c) {
@@ -164,6 +163,8 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
                 SMat::put4(sS, 16 * n + r, (w * MT + m) * 16 + g4, S[m][n]);
                 put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(blk + lay.dS), (w * MT + m) * 16 + r, c0 + 16 * n + g4, turn(tile, S[m][n], l));
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dy[n][i] = 16 * w + g4 + i < rows ? dy[n][i] : 0.f;
             YMat::put4(sY, 16 * n + r, 16 * w + g4, dy[n]);
         }
         __syncthreads();
@@ -185,6 +186,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
         load_dy(next);
         __syncthreads();
         float db = 0.f;
+        E *pv = static_cast<E *>(a.dv) + ((sp.t0 + (int64_t)c * kChunk) * a.n_heads + h) * D + c0;
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
 #pragma unroll
@@ -197,7 +199,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
             for (int i = 0; i < 4; ++i) db = fmaf(df[i], fe[n][i], db);
             put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(blk + lay.dV), 16 * w + r, c0 + 16 * n + g4, tv);
             if (16 * w + r < rows)
-                st_elem4<F32>(a.dv, ((sp.t0 + (int64_t)c * kChunk + 16 * w + r) * a.n_heads + h) * D + c0 + 16 * n + g4, tv);
+                st_elem4<F32>(at_bytes<char>(pv, ((16 * w + r) * (uint32_t)(a.n_heads * D) + 16 * n + g4) * (uint32_t)sizeof(E)), 0, tv);
         }
         db += __shfl_xor(db, 16);
         db += __shfl_xor(db, 32);

@@ -74,15 +74,31 @@ template <int N> __device__ __forceinline__ void split(float x, __bf16 (&t)[N]) 
     }
 }
 
+// Two at a time: the conversion instruction takes a pair.
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+template <int N> __device__ __forceinline__ void split2(f2 x, bf2 (&t)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        t[i] = __builtin_convertvector(x, bf2);
+        if (i + 1 < N) x -= __builtin_convertvector(t[i], f2);
+    }
+}
+template <int N> __device__ __forceinline__ void split4(f4 x, bf4 (&t)[N]) {
+    bf2 a[N], b[N];
+    split2<N>(f2{x[0], x[1]}, a);
+    split2<N>(f2{x[2], x[3]}, b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = __builtin_shufflevector(a[i], b[i], 0, 1, 2, 3);
+}
+
 template <int N> __device__ __forceinline__ Frag<false, N> frag_of(const float (&x)[8], Frag<false, N> *) {
     Frag<false, N> f;
+    bf4 a[N], b[N];
+    split4<N>(f4{x[0], x[1], x[2], x[3]}, a);
+    split4<N>(f4{x[4], x[5], x[6], x[7]}, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        __bf16 t[N];
-        split<N>(x[i], t);
-#pragma unroll
-        for (int p = 0; p < N; ++p) f.t[p][i] = t[p];
-    }
+    for (int p = 0; p < N; ++p) f.t[p] = __builtin_shufflevector(a[p], b[p], 0, 1, 2, 3, 4, 5, 6, 7);
     return f;
 }
 template <int N> __device__ __forceinline__ Frag<true, N> frag_of(const float (&x)[8], Frag<true, N> *) {
@@ -146,13 +162,7 @@ template <bool F32, int N, int K, int COLS> struct LdsMat {
             *reinterpret_cast<f4 *>(m + col * ROW + k) = x;
         } else {
             bf4 v[N];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                __bf16 t[N];
-                split<N>(x[i], t);
-#pragma unroll
-                for (int p = 0; p < N; ++p) v[p][i] = t[p];
-            }
+            split4<N>(x, v);
 #pragma unroll
             for (int p = 0; p < N; ++p) *reinterpret_cast<bf4 *>(m + p * PLANE + col * ROW + k) = v[p];
         }
@@ -184,11 +194,19 @@ template <bool F32> __device__ __forceinline__ void st_elem4(void *p, int64_t i,
     if constexpr (F32) {
         *reinterpret_cast<f4 *>(static_cast<float *>(p) + i) = x;
     } else {
-        bf4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (__bf16)x[j];
-        *reinterpret_cast<bf4 *>(static_cast<__bf16 *>(p) + i) = v;
+        bf4 v[1];
+        split4<1>(x, v);
+        *reinterpret_cast<bf4 *>(static_cast<__bf16 *>(p) + i) = v[0];
     }
+}
+
+// An address as a wave's base and a lane's 32-bit byte offset: the load takes
+// both as they are, where a 64-bit sum would cost vector instructions.
+template <typename T> __device__ __forceinline__ const T *at_bytes(const void *base, uint32_t bytes) {
+    return reinterpret_cast<const T *>(static_cast<const char *>(base) + bytes);
+}
+template <typename T> __device__ __forceinline__ T *at_bytes(void *base, uint32_t bytes) {
+    return reinterpret_cast<T *>(static_cast<char *>(base) + bytes);
 }
 
 // Operands in the workspace lie as the fragments are read: for every 16 rows
@@ -202,11 +220,11 @@ template <bool F32, int N, int KB> struct Operand {
         Frag<F32, N> f;
         const Elem<F32> *p = m + (tile * KB + kb) * SIZE;
         if constexpr (F32) {
-            f.v[0] = *reinterpret_cast<const f4 *>(p + 4 * lane);
-            f.v[1] = *reinterpret_cast<const f4 *>(p + 256 + 4 * lane);
+            f.v[0] = *at_bytes<f4>(p, 16u * lane);
+            f.v[1] = *at_bytes<f4>(p + 256, 16u * lane);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) f.t[i] = *reinterpret_cast<const bf8 *>(p + 512 * i + 8 * lane);
+            for (int i = 0; i < N; ++i) f.t[i] = *at_bytes<bf8>(p + 512 * i, 16u * lane);
         }
         return f;
     }
@@ -227,38 +245,31 @@ template <bool F32, int N, int KB> struct Operand {
 
 // Four consecutive contracted elements k .. k + 3 of one row, N terms: what a lane
 // of a transposed 16 x 16 result tile holds.
-template <bool F32, int N, int KB>
-__device__ __forceinline__ Elem<F32> *operand4(Elem<F32> *m, int row, int k) {
-    const int lane = (k & 31) / 8 * 16 + (row & 15), half = k >> 2 & 1;
-    Elem<F32> *p = m + ((row >> 4) * KB + (k >> 5)) * Operand<F32, N, KB>::SIZE;
-    return F32 ? p + 256 * half + 4 * lane : p + 8 * lane + 4 * half;
+template <bool F32, int N, int KB> __device__ __forceinline__ uint32_t operand4(int row, int k) {  // bytes
+    const uint32_t lane = (k & 31) / 8 * 16 + (row & 15), half = k >> 2 & 1;
+    const uint32_t frag = ((row >> 4) * KB + (k >> 5)) * (Operand<F32, N, KB>::SIZE * (uint32_t)sizeof(Elem<F32>));
+    return frag + 16 * lane + (F32 ? 1024 : 8) * half;
 }
 template <bool F32, int N, int KB> __device__ __forceinline__ void put_operand4(Elem<F32> *m, int row, int k, f4 x) {
-    Elem<F32> *p = operand4<F32, N, KB>(m, row, k);
+    const uint32_t at = operand4<F32, N, KB>(row, k);
     if constexpr (F32) {
-        *reinterpret_cast<f4 *>(p) = x;
+        *at_bytes<f4>(m, at) = x;
     } else {
         bf4 v[N];
+        split4<N>(x, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __bf16 t[N];
-            split<N>(x[i], t);
-#pragma unroll
-            for (int n = 0; n < N; ++n) v[n][i] = t[n];
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) *reinterpret_cast<bf4 *>(p + 512 * n) = v[n];
+        for (int n = 0; n < N; ++n) *at_bytes<bf4>(m + 512 * n, at) = v[n];
     }
 }
 template <bool F32, int N, int KB> __device__ __forceinline__ f4 get_operand4(const Elem<F32> *m, int row, int k) {
-    const Elem<F32> *p = operand4<F32, N, KB>(const_cast<Elem<F32> *>(m), row, k);
+    const uint32_t at = operand4<F32, N, KB>(row, k);
     if constexpr (F32) {
-        return *reinterpret_cast<const f4 *>(p);
+        return *at_bytes<f4>(m, at);
     } else {
         f4 x{};
 #pragma unroll
         for (int n = N - 1; n >= 0; --n) {
-            const bf4 v = *reinterpret_cast<const bf4 *>(p + 512 * n);
+            const bf4 v = *at_bytes<bf4>(m + 512 * n, at);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] += (float)v[i];
         }
@@ -329,6 +340,16 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqArgs &a, int32_t s) {
     r.t0 = lo;
     r.len = hi - lo;
     r.slot0 = (int64_t)(lo / kChunk) + s;
+    return r;
+}
+// ... of a sequence that the whole wave asks for, in scalar registers: every address
+// that follows from it is then formed by the scalar unit.
+__device__ __forceinline__ SeqSpan wave_span(const SeqArgs &a, int32_t s) {
+    SeqSpan r = seq_span(a, s);
+    r.seq = s;
+    r.t0 = __builtin_amdgcn_readfirstlane((int)r.t0);
+    r.len = __builtin_amdgcn_readfirstlane(r.len);
+    r.slot0 = r.t0 / kChunk + s;
     return r;
 }
 
