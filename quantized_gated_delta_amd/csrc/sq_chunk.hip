@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
     Frag<F32, QN> fQ[KB];
     Frag<F32, 3> fM[2];
     Frag<F32, NTY> fP[2];
-    f4 v[NCT];
+    uint32_t v[NCT][4];  // as loaded: widening them at once would wait for them at once
     // the gates' factors are needed early in a chunk: they are fetched a whole chunk ahead
     struct Gates { f4 eg, ec, beta, fade[MT]; float fade1, eq; } gt{}, gt_next{};
 
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         for (int i = 0; i < 4; ++i) {
             const uint32_t row = min(16 * w + g4 + i, last);
 #pragma unroll
-            for (int n = 0; n < NCT; ++n) v[n][i] = ld_elem<F32>(at_bytes<E>(pv, (row * (uint32_t)a.v_stride + 16 * n + r) * (uint32_t)sizeof(E)), 0);
+            for (int n = 0; n < NCT; ++n) v[n][i] = ld_raw<F32>(at_bytes<E>(pv, (row * (uint32_t)a.v_stride + 16 * n + r) * (uint32_t)sizeof(E)), 0);
         }
     };
     auto load_gates = [&](int c) {
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[n][i] = v[n][i] - (KDA ? ks[n][i] : gt.eg[i] * ks[n][i]);
+            for (int i = 0; i < 4; ++i) e[n][i] = of_raw<F32>(v[n][i]) - (KDA ? ks[n][i] : gt.eg[i] * ks[n][i]);
             XMat::put4(sX, 16 * n + r, 16 * w + g4, e[n] * gt.beta);
         }
         __syncthreads();

@@ -74,7 +74,8 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
 
     Frag<F32, KN> fK[KB], fKT[MT][2], fQT[MT][2];
     Frag<F32, 3> fM[2], fP[2];
-    f4 dy[NCT], fe[NCT];
+    uint32_t rdy[NCT][4];  // as loaded: widening them at once would wait for them at once
+    Raw4<F32, kSaveTerms> fe[NCT];
     struct Gates { f4 eg, ec, beta, fade[MT]; float fade1; } gt{}, gt_next{};
 
     auto block_of = [&](int c, int head) { return a.work + ((sp.slot0 + c) * a.n_heads + head) * lay.block; };
@@ -101,7 +102,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
             const int row = 16 * w + g4 + i;
             const uint32_t at = min(row, rows - 1) * (uint32_t)(a.n_heads * D) + r;
 #pragma unroll
-            for (int n = 0; n < NCT; ++n) dy[n][i] = of_raw<F32>(ld_raw<F32>(at_bytes<E>(py, (at + 16 * n) * (uint32_t)sizeof(E)), 0));
+            for (int n = 0; n < NCT; ++n) rdy[n][i] = ld_raw<F32>(at_bytes<E>(py, (at + 16 * n) * (uint32_t)sizeof(E)), 0);
         }
     };
     auto load_e = [&](int c) {
@@ -156,6 +157,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
         // two places in turn: the last chunk's may still be read
         E *sY = reinterpret_cast<E *>(lds + SMat::BYTES + 2 * XMat::BYTES + (c & 1) * YMat::BYTES);
         gt_next = load_gates(next);
+        f4 dy[NCT];
 #pragma unroll
         for (int n = 0; n < NCT; ++n) {
 #pragma unroll
@@ -164,7 +166,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
                 put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(blk + lay.dS), (w * MT + m) * 16 + r, c0 + 16 * n + g4, turn(tile, S[m][n], l));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dy[n][i] = 16 * w + g4 + i < rows ? dy[n][i] : 0.f;
+            for (int i = 0; i < 4; ++i) dy[n][i] = 16 * w + g4 + i < rows ? of_raw<F32>(rdy[n][i]) : 0.f;
             YMat::put4(sY, 16 * n + r, 16 * w + g4, dy[n]);
         }
         __syncthreads();
@@ -194,9 +196,9 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
                 if (kb == 1 || w < 2) du[n] = mma<3>(fM[kb], XMat::get(sX, 16 * n + r, kb * 32 + g8), du[n]);  // dF
             const f4 dv = du[n] * gt.beta;
             XMat::put4(sU, 16 * n + r, 16 * w + g4, KDA ? -dv : -(dv * gt.eg));
-            const f4 df = turn(tile, du[n], l), tv = turn(tile, dv, l);
+            const f4 df = turn(tile, du[n], l), tv = turn(tile, dv, l), e = sum_of(fe[n]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) db = fmaf(df[i], fe[n][i], db);
+            for (int i = 0; i < 4; ++i) db = fmaf(df[i], e[i], db);
             put_operand4<F32, kSaveTerms, KB>(reinterpret_cast<E *>(blk + lay.dV), 16 * w + r, c0 + 16 * n + g4, tv);
             if (16 * w + r < rows)
                 st_elem4<F32>(at_bytes<char>(pv, ((16 * w + r) * (uint32_t)(a.n_heads * D) + 16 * n + g4) * (uint32_t)sizeof(E)), 0, tv);

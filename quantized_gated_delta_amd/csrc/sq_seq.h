@@ -261,20 +261,26 @@ template <bool F32, int N, int KB> __device__ __forceinline__ void put_operand4(
         for (int n = 0; n < N; ++n) *at_bytes<bf4>(m + 512 * n, at) = v[n];
     }
 }
-template <bool F32, int N, int KB> __device__ __forceinline__ f4 get_operand4(const Elem<F32> *m, int row, int k) {
+// ... read back in two parts, the load and the sum of the terms.
+template <bool F32, int N> struct Raw4 { bf4 t[N]; };
+template <int N> struct Raw4<true, N> { f4 t; };
+template <bool F32, int N, int KB> __device__ __forceinline__ Raw4<F32, N> get_operand4(const Elem<F32> *m, int row, int k) {
     const uint32_t at = operand4<F32, N, KB>(row, k);
+    Raw4<F32, N> x;
     if constexpr (F32) {
-        return *at_bytes<f4>(m, at);
+        x.t = *at_bytes<f4>(m, at);
     } else {
-        f4 x{};
 #pragma unroll
-        for (int n = N - 1; n >= 0; --n) {
-            const bf4 v = *at_bytes<bf4>(m + 512 * n, at);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] += (float)v[i];
-        }
-        return x;
+        for (int n = 0; n < N; ++n) x.t[n] = *at_bytes<bf4>(m + 512 * n, at);
     }
+    return x;
+}
+template <int N> __device__ __forceinline__ f4 sum_of(const Raw4<true, N> &x) { return x.t; }
+template <int N> __device__ __forceinline__ f4 sum_of(const Raw4<false, N> &x) {
+    f4 y{};
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) y += __builtin_convertvector(x.t[n], f4);
+    return y;
 }
 
 // A 16 x 16 result tile turned around through a wave's own LDS (16 x 20
