@@ -146,6 +146,20 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
         for (int m = 0; m < MT; ++m) load_kt(0, m);
     }
 
+    // The slices of a (sequence, head) walk in step, so each operand would be waited for from
+    // HBM by all of them: each touches its share of the lines of the chunk after next, which
+    // brings them to the L2 that the slices share.  KDA alone: 412 -> 370 us for 8192
+    // tokens x 32 heads; GDN's operands are half as many bytes (479 -> 508 us).
+    const uint32_t part = j % SLICES;
+    constexpr uint32_t kLines = (lay.block + 127) / 128, kTouch = KDA ? (kLines + 256 * SLICES - 1) / (256 * SLICES) : 0;
+    uint32_t touched[kTouch + 1] = {};
+    auto touch = [&](int c) {
+#pragma unroll
+        for (uint32_t i = 0; i < kTouch; ++i) {
+            const uint32_t line = (t + 256 * i) * SLICES + part;
+            if (line < kLines) touched[i] = *at_bytes<uint32_t>(block_of(c, h), line * 128);
+        }
+    };
     for (int c = 0; c < n_chunks; ++c) {
         const int next = min(c + 1, n_chunks - 1), rows = rows_of(c);
         gt_next = load_gates(next);
@@ -230,6 +244,9 @@ __global__ __launch_bounds__(256) void scan_kernel(SeqArgs a) {
                 st_elem4<YF32>(at_bytes<char>(py, ((16 * w + r) * (uint32_t)(a.n_heads * D) + 16 * n + g4) * (YF32 ? 4u : 2u)), 0, y[n]);
         }
         load_p(next);
+#pragma unroll
+        for (uint32_t i = 0; i < kTouch; ++i) asm volatile("" ::"v"(touched[i]));  // so that the loads are not dropped
+        touch(min(c + 2, n_chunks - 1));
         gt = gt_next;
     }
     if (a.S_out)

@@ -151,6 +151,17 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
     const int last = n_chunks - 1;
     if (n_chunks > 0) gt = load_gates(last), load_dy(last), load_k(last), load_p(last), load_m(last), load_e(last), load_t(last);
 
+    // KDA's operands of the chunk after next to L2, a share by each slice, as in the forward scan
+    const uint32_t part = j % SLICES;
+    constexpr uint32_t kLines = (lay.dS + 127) / 128, kTouch = KDA ? (kLines + 256 * SLICES - 1) / (256 * SLICES) : 0;
+    uint32_t touched[kTouch + 1] = {};
+    auto touch = [&](int c) {
+#pragma unroll
+        for (uint32_t i = 0; i < kTouch; ++i) {
+            const uint32_t line = (t + 256 * i) * SLICES + part;
+            if (line < kLines) touched[i] = *at_bytes<uint32_t>(block_of(c, h), line * 128);
+        }
+    };
     for (int c = last; c >= 0; --c) {
         const int next = max(c - 1, 0), rows = rows_of(c);
         uint8_t *blk = block_of(c, h);
@@ -222,6 +233,9 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
                 }
             }
         load_t(next);
+#pragma unroll
+        for (uint32_t i = 0; i < kTouch; ++i) asm volatile("" ::"v"(touched[i]));  // so that the loads are not dropped
+        touch(max(c - 2, 0));
         gt = gt_next;
     }
     if (a.dS0)
