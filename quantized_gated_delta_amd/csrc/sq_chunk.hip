@@ -26,7 +26,7 @@ template <int D, bool F32, int N> __global__ __launch_bounds__(256) void prep_gd
     prepare_gdn<D, F32, N, false>(a, a.work, lay.block, lay.P, lay.M, lay.KT, 0, lay.gates);
 }
 
-template <int D, bool F32, int N> __global__ __launch_bounds__(256) void prep_kda_kernel(SeqArgs a) {
+template <int D, bool F32, int N> __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void prep_kda_kernel(SeqArgs a) {
     constexpr ChunkLayout lay = forward_layout(D, true, F32, N);
     prepare_kda<D, F32, N, false>(a, a.work, lay.block, lay.P, lay.M, lay.K, lay.Q, lay.KT, 0, lay.gates);
 }

@@ -31,7 +31,7 @@ template <int D, bool F32> __global__ __launch_bounds__(256) void prep_gdn_bwd_k
     prepare_gdn<D, F32, 3, true>(a, a.work, lay.block, lay.PT, lay.MT, lay.KT, lay.QT, lay.gates);
 }
 
-template <int D, bool F32> __global__ __launch_bounds__(256) void prep_kda_bwd_kernel(SeqArgs a) {
+template <int D, bool F32> __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void prep_kda_bwd_kernel(SeqArgs a) {
     constexpr BackwardLayout lay = backward_layout(D, true, F32);
     prepare_kda<D, F32, 3, true>(a, a.work, lay.block, lay.PT, lay.MT, lay.K, 0, lay.KT, lay.QT, lay.gates);
 }
