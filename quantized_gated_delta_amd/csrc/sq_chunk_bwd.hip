@@ -249,33 +249,249 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
 }
 
 // Gradients of q, k, beta and g of one chunk and key head.  Wave w: tokens 16 w .. + 15, whose
-// dY, dV and E stay in registers while the states go by, 16 channels at a time, the next
-// 16 on their way as soon as the last were read.
-// Between tokens, GDN: the decayed dP and dB as bf16 pairs in registers against the keys
-// and queries by channel.  KDA: 16 by 16 in fp32, the decays put on keys and queries.
+// dY, dV and E stay in registers while the states go by, 16 channels at a time.
 // SLICES: the parts of beta's gradient that the scan left.
-template <int D, bool KDA, bool F32> struct GradLds {
-    static constexpr bool KQ = !(F32 && KDA && D == 128);  // keys and queries fit beside the rest
+//
+// GDN: the decayed dP and dB as bf16 pairs in registers against the keys and
+// queries by channel.  All that the four waves share goes once from memory through the LDS,
+// asked for two steps before it is used, so that two workgroups share a CU (each wave
+// its own loads, one workgroup: 471 us for 8192 tokens x 32 heads, d 128; this 297 us, 4.6 TB/s).
+template <int D, bool F32> struct GradLds {
+    static constexpr int STATE = 64 * D, TOKENS = F32 ? 4096 : 2048;  // bytes of 16 channels
+    static constexpr int SLOT = 2 * STATE + 2 * TOKENS;               // S0, dS, keys, queries
+    static constexpr int TURN = 4 * 320, PAIRS = 2 * kChunk * kBRow;
+    static_assert(PAIRS >= TURN && 2 * SLOT >= 4 * STATE, "");
+    // dP and dB, then each wave's tile to turn; E, then two slots
+    __attribute__((aligned(16))) float pairs[PAIRS];
+    __attribute__((aligned(16))) uint8_t slots[2 * SLOT];
+    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], in[kChunk], to[kChunk], X[kChunk], Z[kChunk], end[4];
+    double G[kChunk];
+};
+
+template <int D, bool F32, int SLICES>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(F32 && D == 128 ? 1 : 2))) void grad_gdn_kernel(SeqArgs a) {
+    typedef Elem<F32> E;
+    constexpr BackwardLayout lay = backward_layout(D, false, F32);
+    constexpr SaveLayout save = save_layout(D);
+    typedef GradLds<D, F32> Lds;
+    constexpr int KB = D / 32, NT = D / 16, N2 = kSaveTerms, PS = D / 64, PT = F32 ? 2 : 1;
+    __shared__ Lds s;
+    float *sP = s.pairs, *sB = s.pairs + kChunk * kBRow;
+    E *sE = reinterpret_cast<E *>(s.slots);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t x = blockIdx.x / (uint32_t)a.n_key_heads;
+    const int hk = blockIdx.x % (uint32_t)a.n_key_heads, share = a.n_heads / a.n_key_heads;
+    SeqSpan sp;
+    const int32_t c = chunk_at(a, x, sp);
+    if (c < 0) return;
+    const int64_t t0 = sp.t0 + (int64_t)c * kChunk;
+    const int rows = min(kChunk, sp.len - c * kChunk);
+    uint8_t *shared_blk = a.work + (x * a.n_heads + hk * share) * lay.block;
+
+    for (int h = hk * share; h < (hk + 1) * share; ++h) {
+        // opaque, or every address made of it would be kept over the loop, in more registers than there are
+        int t = threadIdx.x;
+        asm("" : "+v"(t));
+        const int l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+        // the sums over the heads that share the key head; every lane adds to what it wrote itself
+        f4 *sums = reinterpret_cast<f4 *>(shared_blk + lay.sum) + t;
+        const bool head0 = h == hk * share, headn = h + 1 == (hk + 1) * share;
+        const uint8_t *blk = a.work + (x * a.n_heads + h) * lay.block, *sv = a.save + (x * a.n_heads + h) * save.block;
+        const E *pE = reinterpret_cast<const E *>(sv + save.E), *pdV = reinterpret_cast<const E *>(blk + lay.dV);
+        // this thread's share of 16 channels, from memory and to the LDS
+        f4 part[2 * PS + PT], sum_q{}, sum_k{};
+        auto load_part = [&](int n) {
+#pragma unroll
+            for (int i = 0; i < PS; ++i) {
+                part[i] = *at_bytes<f4>(sv + save.S + n * Lds::STATE, 16u * (t + 256 * i));
+                part[PS + i] = *at_bytes<f4>(blk + lay.dS + n * Lds::STATE, 16u * (t + 256 * i));
+            }
+            if constexpr (F32) {
+                part[2 * PS] = *at_bytes<f4>(shared_blk + lay.KT + n * Lds::TOKENS, 16u * t);
+                part[2 * PS + PT - 1] = *at_bytes<f4>(shared_blk + lay.QT + n * Lds::TOKENS, 16u * t);
+            } else {
+                part[2 * PS] = *at_bytes<f4>(shared_blk + (w < 2 ? lay.KT : lay.QT) + n * Lds::TOKENS, 16u * (t & 127));
+            }
+        };
+        auto load_sums = [&](int n) {
+            if (!head0) sum_q = sums[512 * n], sum_k = sums[512 * n + 256];
+        };
+        auto store_part = [&](int slot) {
+#pragma unroll
+            for (int i = 0; i < 2 * PS + PT; ++i) *reinterpret_cast<f4 *>(s.slots + slot * Lds::SLOT + 16 * (t + 256 * i)) = part[i];
+        };
+
+        const GatesOf gates = load_gates<F32>(a, t0, rows, h, t);
+        Frag<F32, 1> fy[KB];
+        Frag<F32, N2> fv[KB], fe[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            fe[kb] = Operand<F32, N2, KB>::get(pE, w, kb, l);
+            fy[kb] = token_frag<F32>(a.dy, (int64_t)a.n_heads * D, t0, rows, 16 * w + r, (int64_t)h * D + kb * 32 + g8);
+            fv[kb] = Operand<F32, N2, KB>::get(pdV, w, kb, l);
+        }
+        load_part(0);
+        float db[SLICES];
+        if (t < rows)
+#pragma unroll
+            for (int i = 0; i < SLICES; ++i) db[i] = reinterpret_cast<const float *>(blk + lay.dbeta)[i * kChunk + t];
+        __syncthreads();  // the last head's LDS is done with
+        gates_gdn(gates, rows, s.G, s.beta, t);
+        if (w == 0) {  // decay from the chunk's start; to its end, and beta
+            __builtin_amdgcn_wave_barrier();
+            s.in[t] = exp_of((float)s.G[t]);
+            s.to[t] = exp_of((float)(s.G[kChunk - 1] - s.G[t])) * gates.beta;
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) Operand<F32, N2, KB>::put(sE, w, kb, l, fe[kb]);
+        __syncthreads();
+        // ---- the pairs' gradients with their decay, rows of this wave
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f4 p{}, b{};
+            if (j <= w) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const Frag<F32, N2> f = Operand<F32, N2, KB>::get(sE, j, kb, l);
+                    p = mma<N2>(fy[kb], f, p);
+                    b = mma<N2>(fv[kb], f, b);
+                }
+            }
+            const int col = 16 * j + r;
+            const double to_col = s.G[col];
+            const float beta = s.beta[col];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 16 * w + g4 + i;
+                const float e = beta * exp_of((float)(s.G[row] - to_col));
+                if (j == w && col == row) s.diag[row] = p[i] * e;
+                sP[row * kBRow + col] = col < row ? p[i] * e : 0.f;
+                sB[row * kBRow + col] = col < row ? -b[i] * e : 0.f;
+            }
+        }
+        if (t < rows) {
+#pragma unroll
+            for (int i = 1; i < SLICES; ++i) db[0] += db[i];
+            st_elem<F32>(a.dbeta, (t0 + t) * a.n_heads + h, db[0]);
+        }
+        __syncthreads();
+        // Fragments kb of dP's and dB's rows of this wave's tokens, and of their columns.
+        // Below the diagonal, a wave needs both rows or both columns, never all four.
+        auto pairs = [&](const float *m, int kb, bool columns) {
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = columns ? m[(32 * kb + g8 + i) * kBRow + 16 * w + r] : m[(16 * w + r) * kBRow + 32 * kb + g8 + i];
+            return make_frag<F32, N2>(u);
+        };
+        const bool late = w >= 2;  // rows 1, else columns 0
+        const Frag<F32, N2> rP = pairs(sP, 0, false), rB = pairs(sB, 0, false), cP = pairs(sP, 1, true), cB = pairs(sB, 1, true);
+        const Frag<F32, N2> xP = late ? pairs(sP, 1, false) : pairs(sP, 0, true), xB = late ? pairs(sB, 1, false) : pairs(sB, 0, true);
+        f4 X{}, Z{};     // summed over channels, this wave's tokens
+        float tail = 0.f;  // S0 . dS
+        store_part(0);
+        load_part(1);
+        load_sums(0);
+        __syncthreads();
+#pragma unroll 1
+        for (int n = 0; n < NT; ++n) {
+            const uint8_t *slot = s.slots + (n & 1) * Lds::SLOT;
+            const E *tS = reinterpret_cast<const E *>(slot), *tdS = reinterpret_cast<const E *>(slot + Lds::STATE);
+            const E *tK = reinterpret_cast<const E *>(slot + 2 * Lds::STATE), *tQ = reinterpret_cast<const E *>(slot + 2 * Lds::STATE + Lds::TOKENS);
+            f4 dq{}, row{}, end{}, col{};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const Frag<F32, N2> f0 = Operand<F32, N2, KB>::get(tS, 0, kb, l), f1 = Operand<F32, N2, KB>::get(tdS, 0, kb, l);
+                dq = mma<N2>(fy[kb], f0, dq);
+                row = mma<N2>(fv[kb], f0, row);
+                end = mma<N2>(fe[kb], f1, end);
+            }
+            const f4 in = *reinterpret_cast<const f4 *>(s.in + 16 * w + g4);
+            dq *= in, row *= -in, end *= *reinterpret_cast<const f4 *>(s.to + 16 * w + g4);
+            const Frag<F32, 1> k0 = Operand<F32, 1, 2>::get(tK, 0, 0, l), k1 = Operand<F32, 1, 2>::get(tK, 0, 1, l);
+            const Frag<F32, 1> q0 = Operand<F32, 1, 2>::get(tQ, 0, 0, l), q1 = Operand<F32, 1, 2>::get(tQ, 0, 1, l);
+            dq = mma<N2>(rP, k0, dq), row = mma<N2>(rB, k0, row);
+            col = mma<N2>(cB, k1, col), col = mma<N2>(cP, q1, col);
+            if (late) dq = mma<N2>(xP, k1, dq), row = mma<N2>(xB, k1, row);
+            else col = mma<N2>(xB, k0, col), col = mma<N2>(xP, q0, col);
+            const f4 kt = sum_of(get_operand4<F32, 1, 2>(tK, r, 16 * w + g4)), qt = sum_of(get_operand4<F32, 1, 2>(tQ, r, 16 * w + g4));
+            X += qt * dq + kt * (row - col), Z += kt * end;
+            const f4 diag = *reinterpret_cast<const f4 *>(s.diag + 16 * w + g4);
+            dq += diag * kt + sum_q;
+            f4 dk = row + col + end + diag * qt + sum_k;
+            if (headn) {
+                const f4 oq = turn(s.pairs + 320 * w, dq, l), ok = turn(s.pairs + 320 * w, dk, l);
+                if (16 * w + r < rows) {
+                    const int64_t at = ((t0 + 16 * w + r) * a.n_key_heads + hk) * D + 16 * n + g4;
+                    st_elem4<F32>(a.dq, at, oq);
+                    st_elem4<F32>(a.dk, at, ok);
+                }
+            } else {
+                sums[512 * n] = dq, sums[512 * n + 256] = dk;
+            }
+            if (w < KB) {  // 32 columns to each wave
+                const Frag<F32, N2> f0 = Operand<F32, N2, KB>::get(tS, 0, w, l), f1 = Operand<F32, N2, KB>::get(tdS, 0, w, l);
+                float dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (F32) dot = fmaf(f0.v[i / 4][i % 4], f1.v[i / 4][i % 4], dot);
+                    else dot = fmaf((float)f0.t[0][i] + (float)f0.t[1][i], (float)f1.t[0][i] + (float)f1.t[1][i], dot);
+                }
+                tail += dot;
+            }
+            store_part(~n & 1);
+            load_part(min(n + 2, NT - 1));
+            load_sums(min(n + 1, NT - 1));
+            __syncthreads();
+        }
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) X[i] += __shfl_xor(X[i], off), Z[i] += __shfl_xor(Z[i], off);
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) tail += __shfl_xor(tail, off);
+        if (r == 0) {
+            *reinterpret_cast<f4 *>(s.X + 16 * w + g4) = X;
+            *reinterpret_cast<f4 *>(s.Z + 16 * w + g4) = Z;
+        }
+        if (l == 0) s.end[w] = tail;
+        __syncthreads();
+        if (t < kChunk) {
+            float after = s.X[t], before = t ? s.Z[t - 1] : 0.f;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const float y = __shfl_down(after, off), z = __shfl_up(before, off);
+                if (t + off < 64) after += y;
+                if (t >= off) before += z;
+            }
+            const float start = (s.end[0] + s.end[1] + s.end[2] + s.end[3]) * exp_of((float)s.G[kChunk - 1]);
+            if (t < rows) st_elem<F32>(a.dg, (t0 + t) * a.n_heads + h, after + before + start);
+        }
+    }
+}
+
+// KDA: 16 by 16 tokens in fp32, the decays put on keys and queries.  One pass: e^L and e^R of the
+// chunk fill the LDS for one workgroup per CU.
+template <int D, bool F32> struct GradKdaLds {
+    static constexpr bool KQ = !(F32 && D == 128);  // keys and queries fit beside the rest
     static constexpr int ROW = TokenTile<D, F32>::ROW, GROW = D + 4;
     __attribute__((aligned(16))) float dP[kChunk * kBRow], dB[kChunk * kBRow];
     __attribute__((aligned(16))) Elem<F32> k[KQ ? kChunk * ROW : 8], q[KQ ? kChunk * ROW : 8];
-    // KDA: e^L and e^R, L the log-gates of a token's block up to it, R after it
-    float eL[KDA ? kChunk * GROW : 1], eR[KDA ? kChunk * GROW : 1];
+    // L: the log-gates of a token's block up to it, R: after it
+    float eL[kChunk * GROW], eR[kChunk * GROW];
     __attribute__((aligned(16))) float turn[4][320];
-    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], X[kChunk], Z[kChunk], end[D];
-    double G[kChunk];
+    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], end[D];
     int strong[4];
 };
 
-template <int D, bool KDA, bool F32, int SLICES>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void grad_kernel(SeqArgs a) {
+template <int D, bool F32, int SLICES>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void grad_kda_kernel(SeqArgs a) {
     typedef Elem<F32> E;
-    constexpr BackwardLayout lay = backward_layout(D, KDA, F32);
+    constexpr BackwardLayout lay = backward_layout(D, true, F32);
     constexpr SaveLayout save = save_layout(D);
-    typedef GradLds<D, KDA, F32> Lds;
+    typedef GradKdaLds<D, F32> Lds;
     constexpr int KB = D / 32, NT = D / 16, ROW = Lds::ROW, GROW = Lds::GROW, N2 = kSaveTerms;
     __shared__ Lds s;
-    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t x = blockIdx.x / (uint32_t)a.n_key_heads;
     const int hk = blockIdx.x % (uint32_t)a.n_key_heads, share = a.n_heads / a.n_key_heads;
     SeqSpan sp;
@@ -286,6 +502,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
 
     if constexpr (Lds::KQ) {
         TokenTile<D, F32> tk, tq;
+        const int t = threadIdx.x;
         tk.load(a.k, a.k_stride, t0, rows, hk, t);
         tq.load(a.q, a.q_stride, t0, rows, hk, t);
         tk.store(s.k, t);
@@ -299,12 +516,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
         if constexpr (Lds::KQ) return ld_elem<F32>(s.q, tok * ROW + ch);
         else return tok < rows ? ld_elem<F32>(a.q, (t0 + tok) * a.q_stride + (int64_t)hk * D + ch) : 0.f;
     };
-    const uint8_t *shared_blk = a.work + (x * a.n_heads + hk * share) * lay.block;
-    const E *pKT = reinterpret_cast<const E *>(shared_blk + lay.KT), *pQT = reinterpret_cast<const E *>(shared_blk + lay.QT);
-    // the sums over the heads that share the key head; every lane adds to what it wrote itself
-    f4 *sums = reinterpret_cast<f4 *>(a.work + (x * a.n_heads + hk * share) * lay.block + lay.sum) + t;
-
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
+        // opaque, as above
+        int t = threadIdx.x;
+        asm("" : "+v"(t));
+        const int l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+        // the sums over the heads that share the key head; every lane adds to what it wrote itself
+        f4 *sums = reinterpret_cast<f4 *>(a.work + (x * a.n_heads + hk * share) * lay.block + lay.sum) + t;
         const uint8_t *blk = a.work + (x * a.n_heads + h) * lay.block, *sv = a.save + (x * a.n_heads + h) * save.block;
         const E *pS = reinterpret_cast<const E *>(sv + save.S), *pE = reinterpret_cast<const E *>(sv + save.E);
         const E *pdS = reinterpret_cast<const E *>(blk + lay.dS), *pdV = reinterpret_cast<const E *>(blk + lay.dV);
@@ -325,7 +543,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                 for (int kb = 0; kb < KB; ++kb) before[j][kb] = Operand<F32, N2, KB>::get(pE, j, kb, l);
         // the states of 16 channels, and (GDN) their keys and queries
         Frag<F32, N2> tS[KB], tdS[KB];
-        Frag<F32, 1> tk[KDA ? 1 : 2], tq[KDA ? 1 : 2];
         auto load_states = [&](int n) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
@@ -333,50 +550,38 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                 tdS[kb] = Operand<F32, N2, KB>::get(pdS, n, kb, l);
             }
         };
-        auto load_tokens = [&](int n) {
-            if constexpr (!KDA)
+        uint32_t raw[4 * D / 256][16];
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    tk[kb] = Operand<F32, 1, 2>::get(pKT, n, kb, l);
-                    tq[kb] = Operand<F32, 1, 2>::get(pQT, n, kb, l);
-                }
-        };
-        if constexpr (KDA) {
-            uint32_t raw[4 * D / 256][16];
+        for (int u = 0; u < 4 * D / 256; ++u)
 #pragma unroll
-            for (int u = 0; u < 4 * D / 256; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int tok = (t + 256 * u) / D * 16 + i;
-                    raw[u][i] = ld_raw<F32>(a.g, ((t0 + min(tok, rows - 1)) * a.n_heads + h) * D + (t + 256 * u) % D);
-                }
-            if (t < 4) s.strong[t] = 0;
-            if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < 4 * D / 256; ++u) {
-                const int b = (t + 256 * u) / D, ch = (t + 256 * u) % D;
-                float up = 0.f, down = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (16 * b + i >= rows) raw[u][i] = 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    up += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
-                    s.eL[(16 * b + i) * GROW + ch] = exp_of(up);
-                }
-#pragma unroll
-                for (int i = 15; i >= 0; --i) {
-                    s.eR[(16 * b + i) * GROW + ch] = exp_of(down);
-                    down += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
-                }
-                if (up < -kBlockRange) s.strong[b] = 1;
+            for (int i = 0; i < 16; ++i) {
+                const int tok = (t + 256 * u) / D * 16 + i;
+                raw[u][i] = ld_raw<F32>(a.g, ((t0 + min(tok, rows - 1)) * a.n_heads + h) * D + (t + 256 * u) % D);
             }
-        } else {
-            gates_gdn<F32>(a, t0, rows, h, s.G, s.beta, t);
+        if (t < 4) s.strong[t] = 0;
+        if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4 * D / 256; ++u) {
+            const int b = (t + 256 * u) / D, ch = (t + 256 * u) % D;
+            float up = 0.f, down = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (16 * b + i >= rows) raw[u][i] = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                up += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
+                s.eL[(16 * b + i) * GROW + ch] = exp_of(up);
+            }
+#pragma unroll
+            for (int i = 15; i >= 0; --i) {
+                s.eR[(16 * b + i) * GROW + ch] = exp_of(down);
+                down += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
+            }
+            if (up < -kBlockRange) s.strong[b] = 1;
         }
         __syncthreads();
-        // ---- the pairs' gradients, rows of this wave: dP and dB (GDN: with the decay)
+        // ---- the pairs' gradients, rows of this wave
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f4 p{}, b{};
@@ -392,67 +597,30 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = 16 * w + g4 + i;
-                float e = col <= row ? s.beta[col] : 0.f;
-                if (!KDA && col <= row) e *= exp_of((float)(s.G[row] - s.G[col]));
+                const float e = col <= row ? s.beta[col] : 0.f;
                 if (col == row) s.diag[row] = p[i] * e;
                 s.dP[row * kBRow + col] = col < row ? p[i] * e : 0.f;
                 s.dB[row * kBRow + col] = col < row ? -b[i] * e : 0.f;
             }
         }
         load_states(0);
-        load_tokens(0);
         __syncthreads();
-        const bool fast = !KDA || !s.strong[w];
-        // GDN: rows of dP and dB of this wave's tokens, and the columns as rows
-        Frag<F32, N2> rP[2], rB[2], cP[2], cB[2];
-        float in[4], out[4];  // GDN: decay from the chunk's start to a token, and from it to the end times beta
-        if constexpr (!KDA) {
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                float u[8], v[8];
-                if (kb == 0 || w >= 2) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        u[i] = s.dP[(16 * w + r) * kBRow + 32 * kb + g8 + i];
-                        v[i] = s.dB[(16 * w + r) * kBRow + 32 * kb + g8 + i];
-                    }
-                    rP[kb] = make_frag<F32, N2>(u), rB[kb] = make_frag<F32, N2>(v);
-                }
-                if (kb == 1 || w < 2) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        u[i] = s.dP[(32 * kb + g8 + i) * kBRow + 16 * w + r];
-                        v[i] = s.dB[(32 * kb + g8 + i) * kBRow + 16 * w + r];
-                    }
-                    cP[kb] = make_frag<F32, N2>(u), cB[kb] = make_frag<F32, N2>(v);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = 16 * w + g4 + i;
-                in[i] = exp_of((float)s.G[tok]);
-                out[i] = exp_of((float)(s.G[kChunk - 1] - s.G[tok])) * s.beta[tok];
-            }
-        }
-        // KDA: the same in fp32, 16 by 16
+        const bool fast = !s.strong[w];
+        // rows of dP and dB of this wave's tokens, and their columns
         f4 bP[4], bB[4], dPt[4], dBt[4];
-        if constexpr (KDA) {
 #pragma unroll
-            for (int J = 0; J < 4; ++J) {
-                if (J <= w) {
-                    bP[J] = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
-                    bB[J] = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
-                }
-                if (J >= w)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        dPt[J][i] = s.dP[(16 * J + g4 + i) * kBRow + 16 * w + r];
-                        dBt[J][i] = s.dB[(16 * J + g4 + i) * kBRow + 16 * w + r];
-                    }
+        for (int J = 0; J < 4; ++J) {
+            if (J <= w) {
+                bP[J] = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
+                bB[J] = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
             }
+            if (J >= w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dPt[J][i] = s.dP[(16 * J + g4 + i) * kBRow + 16 * w + r];
+                    dBt[J][i] = s.dB[(16 * J + g4 + i) * kBRow + 16 * w + r];
+                }
         }
-        f4 X{}, Z{};       // GDN: summed over channels, this wave's tokens
-        float tail = 0.f;  // GDN: e^{G_C} S0 . dS
 #pragma unroll 1
         for (int n = 0; n < NT; ++n) {
             const int ch = 16 * n + r;
@@ -480,105 +648,84 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
             }
             load_states(next);  // into the registers just read: the rest of this step hides it
             f4 eL, eR, kt, qt;
-            float block[4];  // KDA: the decay over each block of 16 tokens
-            if constexpr (KDA) {
+            float block[4];  // the decay over each block of 16 tokens
 #pragma unroll
-                for (int b = 0; b < 4; ++b) block[b] = s.eL[(16 * b + 15) * GROW + ch];
-                float lo = 1.f, hi = 1.f;
+            for (int b = 0; b < 4; ++b) block[b] = s.eL[(16 * b + 15) * GROW + ch];
+            float lo = 1.f, hi = 1.f;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) lo *= b < w ? block[b] : 1.f, hi *= b > w ? block[b] : 1.f;
+            for (int b = 0; b < 4; ++b) lo *= b < w ? block[b] : 1.f, hi *= b > w ? block[b] : 1.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 16 * w + g4 + i;
-                    eL[i] = s.eL[tok * GROW + ch], eR[i] = s.eR[tok * GROW + ch];
-                    dq[i] *= eL[i] * lo;
-                    row[i] *= -eL[i] * lo;
-                    col[i] *= eR[i] * hi * s.beta[tok];
-                }
-                if (n % 4 == w && l < 16) s.end[ch] = dot * block[0] * block[1] * block[2] * block[3];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dq[i] *= in[i], row[i] *= -in[i], col[i] *= out[i];
-                if (n % 4 == w && l < 16) tail = fmaf(dot, exp_of((float)s.G[kChunk - 1]), tail);
+            for (int i = 0; i < 4; ++i) {
+                const int tok = 16 * w + g4 + i;
+                eL[i] = s.eL[tok * GROW + ch], eR[i] = s.eR[tok * GROW + ch];
+                dq[i] *= eL[i] * lo;
+                row[i] *= -eL[i] * lo;
+                col[i] *= eR[i] * hi * s.beta[tok];
             }
+            if (n % 4 == w && l < 16) s.end[ch] = dot * block[0] * block[1] * block[2] * block[3];
 #pragma unroll
             for (int i = 0; i < 4; ++i) kt[i] = key(16 * w + g4 + i, ch), qt[i] = query(16 * w + g4 + i, ch);
             const f4 to_end = col;  // what runs to the chunk's end
             col = f4{};
             // ---- between the chunk's tokens
-            if constexpr (!KDA) {
+            float m = 1.f;  // the decay between the blocks
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    if (kb == 0 || w >= 2) {
-                        dq = mma<N2>(rP[kb], tk[kb], dq);
-                        row = mma<N2>(rB[kb], tk[kb], row);
-                    }
-                    if (kb == 1 || w < 2) {
-                        col = mma<N2>(cB[kb], tk[kb], col);
-                        col = mma<N2>(cP[kb], tq[kb], col);
-                    }
+            for (int J = 3; J >= 0; --J) {  // rows of this wave against keys of block J
+                if (J > w || (J == w && !fast)) continue;
+                f4 kj;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 16 * J + g4 + i;
+                    kj[i] = J == w ? kt[i] * __builtin_amdgcn_rcpf(eL[i]) : key(tok, ch) * (s.eR[tok * GROW + ch] * m);
                 }
-                load_tokens(next);
-            } else {
-                float m = 1.f;  // the decay between the blocks
+                if (J < w) m *= block[J];
+                dq += eL * mma16(bP[J], kj, f4{});
+                row += eL * mma16(bB[J], kj, f4{});
+            }
+            m = 1.f;
 #pragma unroll
-                for (int J = 3; J >= 0; --J) {  // rows of this wave against keys of block J
-                    if (J > w || (J == w && !fast)) continue;
-                    f4 kj;
+            for (int I = 0; I < 4; ++I) {  // keys of this wave against rows of block I
+                if (I < w || (I == w && !fast)) continue;
+                f4 ki, qi;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = 16 * J + g4 + i;
-                        kj[i] = J == w ? kt[i] * __builtin_amdgcn_rcpf(eL[i]) : key(tok, ch) * (s.eR[tok * GROW + ch] * m);
-                    }
-                    if (J < w) m *= block[J];
-                    dq += eL * mma16(bP[J], kj, f4{});
-                    row += eL * mma16(bB[J], kj, f4{});
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 16 * I + g4 + i;
+                    const float e = I == w ? eL[i] : s.eL[tok * GROW + ch];
+                    ki[i] = (I == w ? kt[i] : key(tok, ch)) * e, qi[i] = (I == w ? qt[i] : query(tok, ch)) * e;
                 }
-                m = 1.f;
+                f4 o = mma16(dBt[I], ki, f4{});
+                o = mma16(dPt[I], qi, o);
 #pragma unroll
-                for (int I = 0; I < 4; ++I) {  // keys of this wave against rows of block I
-                    if (I < w || (I == w && !fast)) continue;
-                    f4 ki, qi;
+                for (int i = 0; i < 4; ++i) col[i] = fmaf(I == w ? __builtin_amdgcn_rcpf(eL[i]) : eR[i] * m, o[i], col[i]);
+                if (I > w) m *= block[I];
+            }
+            if (!fast) {  // strong gates: the block's pairs one by one, each by its own sum of log-gates
+                float *gs = s.turn[w];  // [token][channel]
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = 16 * I + g4 + i;
-                        const float e = I == w ? eL[i] : s.eL[tok * GROW + ch];
-                        ki[i] = (I == w ? kt[i] : key(tok, ch)) * e, qi[i] = (I == w ? qt[i] : query(tok, ch)) * e;
-                    }
-                    f4 o = mma16(dBt[I], ki, f4{});
-                    o = mma16(dPt[I], qi, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) col[i] = fmaf(I == w ? __builtin_amdgcn_rcpf(eL[i]) : eR[i] * m, o[i], col[i]);
-                    if (I > w) m *= block[I];
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 16 * w + g4 + i;
+                    gs[(g4 + i) * 20 + r] = tok < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
                 }
-                if (!fast) {  // strong gates: the block's pairs one by one, each by its own sum of log-gates
-                    float *gs = s.turn[w];  // [token][channel]
-                    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = 16 * w + g4 + i;
-                        gs[(g4 + i) * 20 + r] = tok < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
-                    }
-                    __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-                    for (int j = 0; j < 15; ++j) {
-                        float e = 0.f, sum = 0.f;
-                        const float kj = key(16 * w + j, ch);
+                for (int j = 0; j < 15; ++j) {
+                    float e = 0.f, sum = 0.f;
+                    const float kj = key(16 * w + j, ch);
 #pragma unroll 1
-                        for (int i = j + 1; i < 16; ++i) {
-                            e += gs[i * 20 + r];
-                            const float d = exp_of(e), p = d * s.dP[(16 * w + i) * kBRow + 16 * w + j], b = d * s.dB[(16 * w + i) * kBRow + 16 * w + j];
-                            sum = fmaf(b, key(16 * w + i, ch), fmaf(p, query(16 * w + i, ch), sum));
+                    for (int i = j + 1; i < 16; ++i) {
+                        e += gs[i * 20 + r];
+                        const float d = exp_of(e), p = d * s.dP[(16 * w + i) * kBRow + 16 * w + j], b = d * s.dB[(16 * w + i) * kBRow + 16 * w + j];
+                        sum = fmaf(b, key(16 * w + i, ch), fmaf(p, query(16 * w + i, ch), sum));
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const bool mine = g4 + y == i;
-                                dq[y] += mine ? p * kj : 0.f;
-                                row[y] += mine ? b * kj : 0.f;
-                            }
+                        for (int y = 0; y < 4; ++y) {
+                            const bool mine = g4 + y == i;
+                            dq[y] += mine ? p * kj : 0.f;
+                            row[y] += mine ? b * kj : 0.f;
                         }
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) col[y] += g4 + y == j ? sum : 0.f;
                     }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) col[y] += g4 + y == j ? sum : 0.f;
                 }
             }
             const f4 gx = qt * dq + kt * (row - col), gz = kt * to_end;
@@ -597,63 +744,33 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                     st_elem4<F32>(a.dk, at, ok);
                 }
             }
-            if constexpr (KDA) {
-                // in the place of e^L and e^R, once every wave has read them for these channels
-                __syncthreads();
+            // in the place of e^L and e^R, once every wave has read them for these channels
+            __syncthreads();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s.eL[(16 * w + g4 + i) * GROW + ch] = gx[i], s.eR[(16 * w + g4 + i) * GROW + ch] = gz[i];
-            } else {
-                X += gx, Z += gz;
-            }
+            for (int i = 0; i < 4; ++i) s.eL[(16 * w + g4 + i) * GROW + ch] = gx[i], s.eR[(16 * w + g4 + i) * GROW + ch] = gz[i];
         }
-        if constexpr (KDA) {
-            __syncthreads();
-            if (t < D) {
-                float sum = s.end[t];
+        __syncthreads();
+        if (t < D) {
+            float sum = s.end[t];
 #pragma unroll 1
-                for (int b = 0; b < kChunk; b += 16) {
-                    float z[16];
+            for (int b = 0; b < kChunk; b += 16) {
+                float z[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = s.eR[(b + i) * GROW + t];
+                for (int i = 0; i < 16; ++i) z[i] = s.eR[(b + i) * GROW + t];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s.eR[(b + i) * GROW + t] = sum, sum += z[i];
-                }
-                sum = 0.f;
+                for (int i = 0; i < 16; ++i) s.eR[(b + i) * GROW + t] = sum, sum += z[i];
+            }
+            sum = 0.f;
 #pragma unroll 1
-                for (int b = kChunk - 16; b >= 0; b -= 16) {
-                    float y[16], z[16];
+            for (int b = kChunk - 16; b >= 0; b -= 16) {
+                float y[16], z[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = s.eL[(b + i) * GROW + t], z[i] = s.eR[(b + i) * GROW + t];
+                for (int i = 0; i < 16; ++i) y[i] = s.eL[(b + i) * GROW + t], z[i] = s.eR[(b + i) * GROW + t];
 #pragma unroll
-                    for (int i = 15; i >= 0; --i) {
-                        sum += y[i];
-                        if (b + i < rows) st_elem<F32>(a.dg, ((t0 + b + i) * a.n_heads + h) * D + t, sum + z[i]);
-                    }
+                for (int i = 15; i >= 0; --i) {
+                    sum += y[i];
+                    if (b + i < rows) st_elem<F32>(a.dg, ((t0 + b + i) * a.n_heads + h) * D + t, sum + z[i]);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int off = 1; off < 16; off <<= 1)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) X[i] += __shfl_xor(X[i], off), Z[i] += __shfl_xor(Z[i], off);
-#pragma unroll
-            for (int off = 1; off < 16; off <<= 1) tail += __shfl_xor(tail, off);
-            if (r == 0) {
-                *reinterpret_cast<f4 *>(s.X + 16 * w + g4) = X;
-                *reinterpret_cast<f4 *>(s.Z + 16 * w + g4) = Z;
-            }
-            if (l == 0) s.end[w] = tail;
-            __syncthreads();
-            if (t < kChunk) {
-                float after = s.X[t], before_t = t ? s.Z[t - 1] : 0.f;
-#pragma unroll
-                for (int off = 1; off < 64; off <<= 1) {
-                    const float y = __shfl_down(after, off), z = __shfl_up(before_t, off);
-                    if (t + off < 64) after += y;
-                    if (t >= off) before_t += z;
-                }
-                const float sum = after + before_t + (s.end[0] + s.end[1] + s.end[2] + s.end[3]);
-                if (t < rows) st_elem<F32>(a.dg, (t0 + t) * a.n_heads + h, sum);
             }
         }
         if (t < rows) {
@@ -678,7 +795,9 @@ template <int D, bool KDA, bool F32> hipError_t backward(const SeqArgs &a, hipSt
     const uint32_t pairs = (uint32_t)a.n_seq * a.n_heads;
     hipLaunchKernelGGL((scan_bwd_kernel<D, KDA, F32, NCT>), dim3((pairs + 7) / 8 * 8 * (D / (16 * NCT))), dim3(256), 0, stream, a);
     if ((e = hipGetLastError()) != hipSuccess || a.n_tokens == 0) return e;
-    hipLaunchKernelGGL((grad_kernel<D, KDA, F32, D / (16 * NCT)>), dim3((uint32_t)(slots * a.n_key_heads)), dim3(256), 0, stream, a);
+    const dim3 grid((uint32_t)(slots * a.n_key_heads));
+    if constexpr (KDA) hipLaunchKernelGGL((grad_kda_kernel<D, F32, D / (16 * NCT)>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((grad_gdn_kernel<D, F32, D / (16 * NCT)>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -157,23 +157,23 @@ template <int D, bool F32> __device__ __forceinline__ void write_transposed(cons
 }
 
 // GDN: sums of the log-gates (in double: differences of sums lose nothing) and
-// beta of one chunk, by the first wave.
-template <bool F32>
-__device__ __forceinline__ void gates_gdn(const SeqArgs &a, int64_t t0, int rows, int h, double *sG, float *sBeta, int t) {
+// beta of one chunk, by the first wave: the loads, and what follows them.
+struct GatesOf { float g, beta; };
+template <bool F32> __device__ __forceinline__ GatesOf load_gates(const SeqArgs &a, int64_t t0, int rows, int h, int t) {
+    GatesOf x{};
+    if (t < rows) x = {ld_elem<F32>(a.g, (t0 + t) * a.n_heads + h), ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h)};
+    return x;
+}
+__device__ __forceinline__ void gates_gdn(GatesOf x, int rows, double *sG, float *sBeta, int t) {
     if (t < kChunk) {
-        double g = 0.;
-        float b = 0.f;
-        if (t < rows) {
-            g = (double)fmaxf(ld_elem<F32>(a.g, (t0 + t) * a.n_heads + h), kGateFloor);
-            b = ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h);
-        }
+        double g = t < rows ? (double)fmaxf(x.g, kGateFloor) : 0.;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
             const double up = __shfl_up(g, off);
             if (t >= off) g += up;
         }
         sG[t] = g;
-        sBeta[t] = b;
+        sBeta[t] = x.beta;
     }
 }
 
@@ -238,7 +238,7 @@ __device__ __forceinline__ void prepare_gdn(const SeqArgs &a, uint8_t *work, int
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
         fq[kb] = token_frag<F32>(a.q, a.q_stride, t0, rows, 16 * w + (l & 15), (int64_t)hk * D + kb * 32 + (l >> 4) * 8);
-    gates_gdn<F32>(a, t0, rows, h, sG, sBeta, t);
+    gates_gdn(load_gates<F32>(a, t0, rows, h, t), rows, sG, sBeta, t);
     tk.store(s.k, t);
     if (BWD && first) tq.store(sQ, t);
     __syncthreads();

@@ -228,6 +228,16 @@ template <bool F32, int N, int KB> struct Operand {
         }
         return f;
     }
+    __device__ __forceinline__ static void put(Elem<F32> *m, int tile, int kb, int lane, const Frag<F32, N> &f) {
+        Elem<F32> *p = m + (tile * KB + kb) * SIZE;
+        if constexpr (F32) {
+            *at_bytes<f4>(p, 16u * lane) = f.v[0];
+            *at_bytes<f4>(p + 256, 16u * lane) = f.v[1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) *at_bytes<bf8>(p + 512 * i, 16u * lane) = f.t[i];
+        }
+    }
     // row `row`, contracted elements k .. k + 7 (k a multiple of 8)
     __device__ __forceinline__ static void put8(Elem<F32> *m, int row, int k, const float (&x)[8]) {
         const int lane = (k & 31) / 8 * 16 + (row & 15);
