@@ -469,29 +469,36 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(F32 && D ==
     }
 }
 
-// KDA: 16 by 16 tokens in fp32, the decays put on keys and queries.  One pass: e^L and e^R of the
-// chunk fill the LDS for one workgroup per CU.
+// KDA: 16 by 16 tokens in fp32, the decays put on keys and queries.  e^L and e^R of the
+// chunk fill the LDS for one workgroup per CU: eight waves, the last four with the same tokens
+// as the first and the other half of the channels, so that two share a SIMD (four waves, each
+// with its own loads of the states: 389 us for 4001 tokens x 32 heads, d 128; this 253 us).
 template <int D, bool F32> struct GradKdaLds {
     static constexpr bool KQ = !(F32 && D == 128);  // keys and queries fit beside the rest
     static constexpr int ROW = TokenTile<D, F32>::ROW, GROW = D + 4;
-    __attribute__((aligned(16))) float dP[kChunk * kBRow], dB[kChunk * kBRow];
+    static constexpr int STATE = 64 * D;  // bytes of 16 channels
+    union {
+        struct { __attribute__((aligned(16))) float dP[kChunk * kBRow], dB[kChunk * kBRow]; };
+        __attribute__((aligned(16))) uint8_t states[4 * STATE];  // S0 and dS of 32 channels
+    };
+    float ownP[4][16 * 17], ownB[4][16 * 17];  // the blocks on the diagonal
     __attribute__((aligned(16))) Elem<F32> k[KQ ? kChunk * ROW : 8], q[KQ ? kChunk * ROW : 8];
     // L: the log-gates of a token's block up to it, R: after it
     float eL[kChunk * GROW], eR[kChunk * GROW];
-    __attribute__((aligned(16))) float turn[4][320];
-    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], end[D];
+    __attribute__((aligned(16))) float turn[8][320];
+    __attribute__((aligned(16))) float beta[kChunk], diag[kChunk], end[2][D];
     int strong[4];
 };
 
 template <int D, bool F32, int SLICES>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void grad_kda_kernel(SeqArgs a) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void grad_kda_kernel(SeqArgs a) {
     typedef Elem<F32> E;
     constexpr BackwardLayout lay = backward_layout(D, true, F32);
     constexpr SaveLayout save = save_layout(D);
     typedef GradKdaLds<D, F32> Lds;
     constexpr int KB = D / 32, NT = D / 16, ROW = Lds::ROW, GROW = Lds::GROW, N2 = kSaveTerms;
     __shared__ Lds s;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, half = wave >> 2;
     const int64_t x = blockIdx.x / (uint32_t)a.n_key_heads;
     const int hk = blockIdx.x % (uint32_t)a.n_key_heads, share = a.n_heads / a.n_key_heads;
     SeqSpan sp;
@@ -501,12 +508,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
     const int rows = min(kChunk, sp.len - c * kChunk);
 
     if constexpr (Lds::KQ) {
-        TokenTile<D, F32> tk, tq;
-        const int t = threadIdx.x;
-        tk.load(a.k, a.k_stride, t0, rows, hk, t);
-        tq.load(a.q, a.q_stride, t0, rows, hk, t);
-        tk.store(s.k, t);
-        tq.store(s.q, t);
+        TokenTile<D, F32> tile;
+        tile.load(half ? a.q : a.k, half ? a.q_stride : a.k_stride, t0, rows, hk, threadIdx.x & 255);
+        tile.store(half ? s.q : s.k, threadIdx.x & 255);
     }
     auto key = [&](int tok, int ch) {
         if constexpr (Lds::KQ) return ld_elem<F32>(s.k, tok * ROW + ch);
@@ -522,131 +526,152 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
         asm("" : "+v"(t));
         const int l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
         // the sums over the heads that share the key head; every lane adds to what it wrote itself
-        f4 *sums = reinterpret_cast<f4 *>(a.work + (x * a.n_heads + hk * share) * lay.block + lay.sum) + t;
+        f4 *sums = reinterpret_cast<f4 *>(a.work + (x * a.n_heads + hk * share) * lay.block + lay.sum) + (t & 255);
         const uint8_t *blk = a.work + (x * a.n_heads + h) * lay.block, *sv = a.save + (x * a.n_heads + h) * save.block;
-        const E *pS = reinterpret_cast<const E *>(sv + save.S), *pE = reinterpret_cast<const E *>(sv + save.E);
-        const E *pdS = reinterpret_cast<const E *>(blk + lay.dS), *pdV = reinterpret_cast<const E *>(blk + lay.dV);
-        __syncthreads();  // the last head's LDS is done with
+        const E *pE = reinterpret_cast<const E *>(sv + save.E), *pdV = reinterpret_cast<const E *>(blk + lay.dV);
         // ---- everything that is waited for once per head
+        // a block of tokens and a channel to each thread (d = 64: the last block several times, with the
+        // same values); 32-bit offsets within a chunk
+        int gb = min(t / D, 3), gch = t % D;
+        const uint32_t gate_row = (uint32_t)a.n_heads * D;
+        const void *gates = static_cast<const E *>(a.g) + (t0 * a.n_heads + h) * D;
+        uint32_t raw[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            raw[i] = *at_bytes<RawOf<F32>>(gates, (uint32_t)sizeof(E) * (min(16 * gb + i, rows - 1) * gate_row + gch));
+        const float beta = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
         Frag<F32, 1> fy[KB];
-        Frag<F32, N2> fv[KB], fe[KB], before[3][KB];
+        Frag<F32, N2> fv[KB], fe[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
+            fe[kb] = Operand<F32, N2, KB>::get(pE, w, kb, l);
             fy[kb] = token_frag<F32>(a.dy, (int64_t)a.n_heads * D, t0, rows, 16 * w + r, (int64_t)h * D + kb * 32 + g8);
             fv[kb] = Operand<F32, N2, KB>::get(pdV, w, kb, l);
-            fe[kb] = Operand<F32, N2, KB>::get(pE, w, kb, l);
         }
+        // this thread's share of the states of 32 channels, from memory and to the LDS
+        constexpr int PS = D / 64;
+        f4 part[2 * PS];
+        auto load_part = [&](int step) {
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-            if (j < w)
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) before[j][kb] = Operand<F32, N2, KB>::get(pE, j, kb, l);
-        // the states of 16 channels, and (GDN) their keys and queries
-        Frag<F32, N2> tS[KB], tdS[KB];
-        auto load_states = [&](int n) {
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                tS[kb] = Operand<F32, N2, KB>::get(pS, n, kb, l);
-                tdS[kb] = Operand<F32, N2, KB>::get(pdS, n, kb, l);
+            for (int i = 0; i < PS; ++i) {
+                part[i] = *at_bytes<f4>(sv + save.S + 2 * step * Lds::STATE, 16u * (t + 512 * i));
+                part[PS + i] = *at_bytes<f4>(blk + lay.dS + 2 * step * Lds::STATE, 16u * (t + 512 * i));
             }
         };
-        uint32_t raw[4 * D / 256][16];
+        auto store_part = [&]() {
 #pragma unroll
-        for (int u = 0; u < 4 * D / 256; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int tok = (t + 256 * u) / D * 16 + i;
-                raw[u][i] = ld_raw<F32>(a.g, ((t0 + min(tok, rows - 1)) * a.n_heads + h) * D + (t + 256 * u) % D);
-            }
+            for (int i = 0; i < 2 * PS; ++i) *reinterpret_cast<f4 *>(s.states + 16 * (t + 512 * i)) = part[i];
+        };
+        E *tS = reinterpret_cast<E *>(s.states), *tdS = reinterpret_cast<E *>(s.states + 2 * Lds::STATE);
+        __syncthreads();  // the last head's LDS is done with
         if (t < 4) s.strong[t] = 0;
-        if (t < kChunk) s.beta[t] = t < rows ? ld_elem<F32>(a.beta, (t0 + t) * a.n_heads + h) : 0.f;
-        __syncthreads();
+        if (t < kChunk) s.beta[t] = beta;
+        float up = 0.f, down = 0.f;
 #pragma unroll
-        for (int u = 0; u < 4 * D / 256; ++u) {
-            const int b = (t + 256 * u) / D, ch = (t + 256 * u) % D;
-            float up = 0.f, down = 0.f;
+        for (int i = 0; i < 16; ++i)
+            if (16 * gb + i >= rows) raw[i] = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (16 * b + i >= rows) raw[u][i] = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                up += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
-                s.eL[(16 * b + i) * GROW + ch] = exp_of(up);
-            }
-#pragma unroll
-            for (int i = 15; i >= 0; --i) {
-                s.eR[(16 * b + i) * GROW + ch] = exp_of(down);
-                down += fmaxf(of_raw<F32>(raw[u][i]), kGateFloor);
-            }
-            if (up < -kBlockRange) s.strong[b] = 1;
+        for (int i = 0; i < 16; ++i) {
+            up += fmaxf(of_raw<F32>(raw[i]), kGateFloor);
+            s.eL[(16 * gb + i) * GROW + gch] = exp_of(up);
         }
-        __syncthreads();
-        // ---- the pairs' gradients, rows of this wave
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f4 p{}, b{};
-            if (j <= w) {
+        for (int i = 15; i >= 0; --i) {
+            s.eR[(16 * gb + i) * GROW + gch] = exp_of(down);
+            down += fmaxf(of_raw<F32>(raw[i]), kGateFloor);
+        }
+        if (up < -kBlockRange) s.strong[gb] = 1;
+        float db[SLICES];
+#pragma unroll
+        for (int i = 0; i < SLICES; ++i) db[i] = reinterpret_cast<const float *>(blk + lay.dbeta)[i * kChunk + t % kChunk];
+        if (half == 0)  // E to every wave
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) Operand<F32, N2, KB>::put(tS, w, kb, l, fe[kb]);
+        __syncthreads();
+        // ---- the pairs' gradients, rows of this wave, two blocks of columns
+        f4 p[2]{}, b[2]{};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (2 * half + j <= w)
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    const Frag<F32, N2> f = j == w ? fe[kb] : before[j < 3 ? j : 0][kb];
-                    p = mma<N2>(fy[kb], f, p);
-                    b = mma<N2>(fv[kb], f, b);
+                    const Frag<F32, N2> f = Operand<F32, N2, KB>::get(tS, 2 * half + j, kb, l);
+                    p[j] = mma<N2>(fy[kb], f, p[j]);
+                    b[j] = mma<N2>(fv[kb], f, b[j]);
                 }
-            }
+        load_part(0);
+        if (t < rows) {
+#pragma unroll
+            for (int i = 1; i < SLICES; ++i) db[0] += db[i];
+            st_elem<F32>(a.dbeta, (t0 + t) * a.n_heads + h, db[0]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+            const int j = 2 * half + jj;
             const int col = 16 * j + r;
+            const float beta = s.beta[col];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = 16 * w + g4 + i;
-                const float e = col <= row ? s.beta[col] : 0.f;
-                if (col == row) s.diag[row] = p[i] * e;
-                s.dP[row * kBRow + col] = col < row ? p[i] * e : 0.f;
-                s.dB[row * kBRow + col] = col < row ? -b[i] * e : 0.f;
+                const float e = col <= row ? beta : 0.f;
+                const float dp = col < row ? p[jj][i] * e : 0.f, db = col < row ? -b[jj][i] * e : 0.f;
+                s.dP[row * kBRow + col] = dp;
+                s.dB[row * kBRow + col] = db;
+                if (j == w) {
+                    s.ownP[w][(g4 + i) * 17 + r] = dp, s.ownB[w][(g4 + i) * 17 + r] = db;
+                    if (col == row) s.diag[row] = p[jj][i] * e;
+                }
             }
         }
-        load_states(0);
         __syncthreads();
         const bool fast = !s.strong[w];
-        // rows of dP and dB of this wave's tokens, and their columns
-        f4 bP[4], bB[4], dPt[4], dBt[4];
+        // this wave's rows and columns of its own block; of the other three the rows if before, else the columns
+        auto rows_of = [&](const float *m, int J) { return *reinterpret_cast<const f4 *>(m + (16 * w + r) * kBRow + 16 * J + g4); };
+        auto columns_of = [&](const float *m, int J) {
+            f4 x;
 #pragma unroll
-        for (int J = 0; J < 4; ++J) {
-            if (J <= w) {
-                bP[J] = *reinterpret_cast<const f4 *>(s.dP + (16 * w + r) * kBRow + 16 * J + g4);
-                bB[J] = *reinterpret_cast<const f4 *>(s.dB + (16 * w + r) * kBRow + 16 * J + g4);
-            }
-            if (J >= w)
+            for (int i = 0; i < 4; ++i) x[i] = m[(16 * J + g4 + i) * kBRow + 16 * w + r];
+            return x;
+        };
+        const f4 rowP = rows_of(s.dP, w), rowB = rows_of(s.dB, w), colP = columns_of(s.dP, w), colB = columns_of(s.dB, w);
+        f4 bP[3], bB[3];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    dPt[J][i] = s.dP[(16 * J + g4 + i) * kBRow + 16 * w + r];
-                    dBt[J][i] = s.dB[(16 * J + g4 + i) * kBRow + 16 * w + r];
-                }
+        for (int u = 0; u < 3; ++u) {
+            if (u < w) bP[u] = rows_of(s.dP, u), bB[u] = rows_of(s.dB, u);
+            else bP[u] = columns_of(s.dP, u + 1), bB[u] = columns_of(s.dB, u + 1);
         }
+        __syncthreads();
+        store_part();
+        load_part(1);
+        __syncthreads();
 #pragma unroll 1
-        for (int n = 0; n < NT; ++n) {
+        for (int n = half; n < NT; n += 2) {
             const int ch = 16 * n + r;
-            const int next = min(n + 1, NT - 1);
             // ---- through the states
             f4 dq{}, row{}, col{};
-            float dot = 0.f;  // S0 . dS of one channel, this lane's columns
+            float dot = 0.f;  // S0 . dS of one channel, this lane's columns; by the waves with the fewest pairs
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                dq = mma<N2>(fy[kb], tS[kb], dq);
-                row = mma<N2>(fv[kb], tS[kb], row);
-                col = mma<N2>(fe[kb], tdS[kb], col);
+                const Frag<F32, N2> f0 = Operand<F32, N2, KB>::get(tS, half, kb, l), f1 = Operand<F32, N2, KB>::get(tdS, half, kb, l);
+                dq = mma<N2>(fy[kb], f0, dq);
+                row = mma<N2>(fv[kb], f0, row);
+                col = mma<N2>(fe[kb], f1, col);
             }
-            if (n % 4 == w) {
+            if (w >= 2) {
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
+                for (int u = 0; u < KB / 2; ++u) {
+                    const int kb = (w - 2) * (KB / 2) + u;
+                    const Frag<F32, N2> f0 = Operand<F32, N2, KB>::get(tS, half, kb, l), f1 = Operand<F32, N2, KB>::get(tdS, half, kb, l);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if constexpr (F32) dot = fmaf(tS[kb].v[i / 4][i % 4], tdS[kb].v[i / 4][i % 4], dot);
-                        else
-                            dot = fmaf((float)tS[kb].t[0][i] + (float)tS[kb].t[1][i], (float)tdS[kb].t[0][i] + (float)tdS[kb].t[1][i], dot);
+                        if constexpr (F32) dot = fmaf(f0.v[i / 4][i % 4], f1.v[i / 4][i % 4], dot);
+                        else dot = fmaf((float)f0.t[0][i] + (float)f0.t[1][i], (float)f1.t[0][i] + (float)f1.t[1][i], dot);
                     }
+                }
                 dot += __shfl_xor(dot, 16);
                 dot += __shfl_xor(dot, 32);
             }
-            load_states(next);  // into the registers just read: the rest of this step hides it
             f4 eL, eR, kt, qt;
             float block[4];  // the decay over each block of 16 tokens
 #pragma unroll
@@ -662,45 +687,47 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                 row[i] *= -eL[i] * lo;
                 col[i] *= eR[i] * hi * s.beta[tok];
             }
-            if (n % 4 == w && l < 16) s.end[ch] = dot * block[0] * block[1] * block[2] * block[3];
+            if (w >= 2 && l < 16) s.end[w - 2][ch] = dot * block[0] * block[1] * block[2] * block[3];
 #pragma unroll
             for (int i = 0; i < 4; ++i) kt[i] = key(16 * w + g4 + i, ch), qt[i] = query(16 * w + g4 + i, ch);
             const f4 to_end = col;  // what runs to the chunk's end
             col = f4{};
             // ---- between the chunk's tokens
-            float m = 1.f;  // the decay between the blocks
+            f4 from{}, back{};  // dq and row without e^L
 #pragma unroll
-            for (int J = 3; J >= 0; --J) {  // rows of this wave against keys of block J
-                if (J > w || (J == w && !fast)) continue;
-                f4 kj;
+            for (int u = 0; u < 3; ++u) {
+                const int J = u < w ? u : u + 1;
+                float m = 1.f;  // the decay between the blocks
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 16 * J + g4 + i;
-                    kj[i] = J == w ? kt[i] * __builtin_amdgcn_rcpf(eL[i]) : key(tok, ch) * (s.eR[tok * GROW + ch] * m);
+                for (int b = 1; b < 3; ++b) m *= (J < b && b < w) || (w < b && b < J) ? block[b] : 1.f;
+                f4 kj, e;
+                if (u < w) {  // rows of this wave against keys of block J
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kj[i] = key(16 * J + g4 + i, ch), e[i] = s.eR[(16 * J + g4 + i) * GROW + ch];
+                    kj *= e * m;
+                    from = mma16(bP[u], kj, from);
+                    back = mma16(bB[u], kj, back);
+                } else {  // keys of this wave against rows of block J
+                    f4 qj;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kj[i] = key(16 * J + g4 + i, ch), qj[i] = query(16 * J + g4 + i, ch), e[i] = s.eL[(16 * J + g4 + i) * GROW + ch];
+                    e *= m;
+                    col = mma16(bB[u], kj * e, col);
+                    col = mma16(bP[u], qj * e, col);
                 }
-                if (J < w) m *= block[J];
-                dq += eL * mma16(bP[J], kj, f4{});
-                row += eL * mma16(bB[J], kj, f4{});
             }
-            m = 1.f;
+            col *= eR;
+            if (fast) {
+                f4 inv;
 #pragma unroll
-            for (int I = 0; I < 4; ++I) {  // keys of this wave against rows of block I
-                if (I < w || (I == w && !fast)) continue;
-                f4 ki, qi;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 16 * I + g4 + i;
-                    const float e = I == w ? eL[i] : s.eL[tok * GROW + ch];
-                    ki[i] = (I == w ? kt[i] : key(tok, ch)) * e, qi[i] = (I == w ? qt[i] : query(tok, ch)) * e;
-                }
-                f4 o = mma16(dBt[I], ki, f4{});
-                o = mma16(dPt[I], qi, o);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) col[i] = fmaf(I == w ? __builtin_amdgcn_rcpf(eL[i]) : eR[i] * m, o[i], col[i]);
-                if (I > w) m *= block[I];
+                for (int i = 0; i < 4; ++i) inv[i] = __builtin_amdgcn_rcpf(eL[i]);
+                from = mma16(rowP, kt * inv, from);
+                back = mma16(rowB, kt * inv, back);
+                col += inv * mma16(colP, qt * eL, mma16(colB, kt * eL, f4{}));
             }
+            dq += eL * from, row += eL * back;
             if (!fast) {  // strong gates: the block's pairs one by one, each by its own sum of log-gates
-                float *gs = s.turn[w];  // [token][channel]
+                float *gs = s.turn[wave];  // [token][channel]
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -715,7 +742,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
 #pragma unroll 1
                     for (int i = j + 1; i < 16; ++i) {
                         e += gs[i * 20 + r];
-                        const float d = exp_of(e), p = d * s.dP[(16 * w + i) * kBRow + 16 * w + j], b = d * s.dB[(16 * w + i) * kBRow + 16 * w + j];
+                        const float d = exp_of(e), p = d * s.ownP[w][i * 17 + j], b = d * s.ownB[w][i * 17 + j];
                         sum = fmaf(b, key(16 * w + i, ch), fmaf(p, query(16 * w + i, ch), sum));
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
@@ -737,7 +764,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
                 if (h + 1 < (hk + 1) * share) sums[512 * n] = dq, sums[512 * n + 256] = dk;
             }
             if (h + 1 == (hk + 1) * share) {
-                const f4 oq = turn(s.turn[w], dq, l), ok = turn(s.turn[w], dk, l);
+                const f4 oq = turn(s.turn[wave], dq, l), ok = turn(s.turn[wave], dk, l);
                 if (16 * w + r < rows) {
                     const int64_t at = ((t0 + 16 * w + r) * a.n_key_heads + hk) * D + 16 * n + g4;
                     st_elem4<F32>(a.dq, at, oq);
@@ -748,36 +775,36 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1))) void g
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 4; ++i) s.eL[(16 * w + g4 + i) * GROW + ch] = gx[i], s.eR[(16 * w + g4 + i) * GROW + ch] = gz[i];
+            store_part();
+            load_part(min(n / 2 + 2, NT / 2 - 1));
+            __syncthreads();
         }
+        asm("" : "+v"(gb), "+v"(gch));  // as above
+        // dg: what comes after a token and what came before it, 16 tokens to a thread
+        float y[16], z[16], ys = 0.f, zs = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = s.eL[(16 * gb + i) * GROW + gch], z[i] = s.eR[(16 * gb + i) * GROW + gch];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ys += y[15 - i], zs += z[i];
+        s.dP[gb * D + gch] = ys, s.dB[gb * D + gch] = zs;
         __syncthreads();
-        if (t < D) {
-            float sum = s.end[t];
-#pragma unroll 1
-            for (int b = 0; b < kChunk; b += 16) {
-                float z[16];
+        void *dgates = static_cast<E *>(a.dg) + (t0 * a.n_heads + h) * D;
+        float before = s.end[0][gch] + s.end[1][gch], after = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = s.eR[(b + i) * GROW + t];
+        for (int b = 0; b < 3; ++b)
+            if (b < gb) before += s.dB[b * D + gch];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s.eR[(b + i) * GROW + t] = sum, sum += z[i];
-            }
-            sum = 0.f;
-#pragma unroll 1
-            for (int b = kChunk - 16; b >= 0; b -= 16) {
-                float y[16], z[16];
+        for (int b = 3; b > 0; --b)
+            if (b > gb) after += s.dP[b * D + gch];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = s.eL[(b + i) * GROW + t], z[i] = s.eR[(b + i) * GROW + t];
-#pragma unroll
-                for (int i = 15; i >= 0; --i) {
-                    sum += y[i];
-                    if (b + i < rows) st_elem<F32>(a.dg, ((t0 + b + i) * a.n_heads + h) * D + t, sum + z[i]);
-                }
-            }
+        for (int i = 0; i < 16; ++i) {
+            const float now = z[i];
+            z[i] = before, before += now;
         }
-        if (t < rows) {
-            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < SLICES; ++i) sum += reinterpret_cast<const float *>(blk + lay.dbeta)[i * kChunk + t];
-            st_elem<F32>(a.dbeta, (t0 + t) * a.n_heads + h, sum);
+        for (int i = 15; i >= 0; --i) {
+            after += y[i];
+            if (16 * gb + i < rows) st_elem<F32>(at_bytes<E>(dgates, (uint32_t)sizeof(E) * ((16 * gb + i) * gate_row + gch)), 0, after + z[i]);
         }
     }
 }
@@ -796,7 +823,7 @@ template <int D, bool KDA, bool F32> hipError_t backward(const SeqArgs &a, hipSt
     hipLaunchKernelGGL((scan_bwd_kernel<D, KDA, F32, NCT>), dim3((pairs + 7) / 8 * 8 * (D / (16 * NCT))), dim3(256), 0, stream, a);
     if ((e = hipGetLastError()) != hipSuccess || a.n_tokens == 0) return e;
     const dim3 grid((uint32_t)(slots * a.n_key_heads));
-    if constexpr (KDA) hipLaunchKernelGGL((grad_kda_kernel<D, F32, D / (16 * NCT)>), grid, dim3(256), 0, stream, a);
+    if constexpr (KDA) hipLaunchKernelGGL((grad_kda_kernel<D, F32, D / (16 * NCT)>), grid, dim3(512), 0, stream, a);
     else hipLaunchKernelGGL((grad_gdn_kernel<D, F32, D / (16 * NCT)>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }

@@ -16,6 +16,7 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "sq_internal.h"
 
@@ -177,12 +178,8 @@ template <bool F32> __device__ __forceinline__ float ld_elem(const void *p, int6
 }
 // The same in two parts, the load and the widening, so that several loads are
 // in flight before the first is waited for.
-template <bool F32> __device__ __forceinline__ uint32_t ld_raw(const void *p, int64_t i) {
-    if constexpr (F32)
-        return static_cast<const uint32_t *>(p)[i];
-    else
-        return static_cast<const uint16_t *>(p)[i];
-}
+template <bool F32> using RawOf = std::conditional_t<F32, uint32_t, uint16_t>;
+template <bool F32> __device__ __forceinline__ uint32_t ld_raw(const void *p, int64_t i) { return static_cast<const RawOf<F32> *>(p)[i]; }
 template <bool F32> __device__ __forceinline__ float of_raw(uint32_t x) { return __uint_as_float(F32 ? x : x << 16); }
 template <bool F32> __device__ __forceinline__ void st_elem(void *p, int64_t i, float x) {
     if constexpr (F32)
