@@ -451,7 +451,8 @@ sq_status sq_verify_bytes(int32_t n, int32_t m, size_t *bytes);
  *   tokens: int32 [n, m], the drafts; lens: int32 [n] how many of them count
  *           (held to [0, m]), or NULL for m;
  *   accept_u: fp32 [n, m] uniform in [0, 1); sample_e: fp32 [n, vocab] positive,
- *           exponentially distributed; both may be NULL at temperature 0;
+ *           exponentially distributed (a token with a negative value is not drawn);
+ *           both may be NULL at temperature 0;
  *   accepted, next: int32 [n], outputs.
  * With p, q the softmax of target / temperature and draft / temperature (fp32;
  * q = 1 at the drafted token without draft logits): drafted token x_i stands if all before it

@@ -684,7 +684,6 @@ sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *targe
     a.accepted = accepted; a.next = next;
     a.stats = reinterpret_cast<float2 *>(base + lay.stats);
     a.best = reinterpret_cast<uint64_t *>(base + lay.best);
-    a.done = reinterpret_cast<int32_t *>(base + lay.done);
     const hipError_t err = sqk::launch_verify(a, logits_dtype == SQ_F32, greedy, stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "verify_draft launch");
 }

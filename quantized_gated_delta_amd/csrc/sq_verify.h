@@ -17,23 +17,21 @@ struct VerifyArgs {
     float inv_temperature;
     int32_t *accepted, *next;
     // workspace: per (row, split) a maximum and a sum (greedy: its index); per
-    // request the best score and its token, and a counter
+    // (request, split) the best score and its token
     float2 *stats;
     uint64_t *best;
-    int32_t *done;
     int32_t splits, sample_splits;           // workgroups per row, per request
 };
 
 constexpr int kVerifySplits = 64;    // at most
 constexpr int kVerifySegment = 4096; // at least so many logits per workgroup
 
-struct VerifyLayout { size_t stats, best, done, bytes; };
+struct VerifyLayout { size_t stats, best, bytes; };
 inline VerifyLayout verify_layout(int64_t n, int64_t m) {
     VerifyLayout l;
     l.stats = 0;
     l.best = l.stats + (size_t)(n * (2 * m + 1) * kVerifySplits) * sizeof(float2);
-    l.done = l.best + (size_t)n * sizeof(uint64_t);
-    l.bytes = (l.done + (size_t)n * sizeof(int32_t) + 255) / 256 * 256;
+    l.bytes = (l.best + (size_t)(n * kVerifySplits) * sizeof(uint64_t) + 255) / 256 * 256;
     return l;
 }
 

@@ -13,10 +13,11 @@
 // Bound by reading each logit once: kernel 1 takes every row's maximum and sum in one
 // pass (running maximum, sum rescaled when it grows), a row split over
 // several workgroups where there are few rows.  Kernel 2 joins the parts,
-// decides, and reads the one row that the next token is drawn from; its parts
-// are joined by an atomic maximum over (score, token), whose result no order of
-// the workgroups changes, and written by the last of them (a counter; kernel 1
-// clears both).
+// decides, and reads the one row that the next token is drawn from.  Where
+// several workgroups share it, kernel 3 takes the best of their parts: the end
+// of a kernel orders their writes before its reads on every XCD (instead, an atomic
+// maximum that the last workgroup by a counter read: 24 us for kernel 2 with 64
+// requests of 131072 tokens, where kernels 2 and 3 take 17 + 4).
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -99,7 +100,6 @@ template <bool F32, bool GREEDY> __global__ __launch_bounds__(256) void stats_ke
     const bool is_draft = row >= targets;
     const int b = is_draft ? (int)((row - targets) / a.m) : (int)(row / (a.m + 1));
     const int i = is_draft ? (int)((row - targets) % a.m) : (int)(row % (a.m + 1));
-    if (part == 0 && i == 0 && !is_draft && t == 0) a.done[b] = 0, a.best[b] = 0;
     const int len = length_of(a, b);
     if (is_draft ? i >= len : i > len) return;  // a row that nothing is decided by
     const void *base = is_draft ? a.draft : a.target;
@@ -159,12 +159,14 @@ template <bool F32, bool GREEDY> __global__ __launch_bounds__(256) void stats_ke
     if (t == 0) a.stats[row * a.splits + part] = best;
 }
 
-template <bool F32, bool GREEDY> __global__ __launch_bounds__(256) void decide_kernel(VerifyArgs a) {
-    __shared__ float2 sT[SQ_DRAFT_MAX + 1], sD[SQ_DRAFT_MAX];
-    __shared__ uint64_t sBest[4], sFinal;
-    __shared__ int sOk[SQ_DRAFT_MAX], sLast;
-    const int t = threadIdx.x, w = t >> 6, l = t & 63, part = blockIdx.x, b = blockIdx.y;
-    const int len = length_of(a, b);
+// How many of request b's tokens stand, by the whole workgroup.
+struct DecideLds {
+    float2 target[SQ_DRAFT_MAX + 1], draft[SQ_DRAFT_MAX];  // maximum and sum (greedy: token) of each row
+    uint64_t best[4];
+    int ok[SQ_DRAFT_MAX];
+};
+template <bool F32, bool GREEDY> __device__ __forceinline__ int decide(const VerifyArgs &a, int b, DecideLds &s, int t) {
+    const int w = t >> 6, l = t & 63, len = length_of(a, b);
     const float c = a.inv_temperature * kLog2e;
     const int64_t targets = (int64_t)a.n * (a.m + 1);
     // a row's parts, one wave per row
@@ -175,104 +177,126 @@ template <bool F32, bool GREEDY> __global__ __launch_bounds__(256) void decide_k
         float2 v = l < a.splits ? a.stats[row * a.splits + l] : GREEDY ? no_token() : make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int off = 32; off; off >>= 1) v = merge<GREEDY>(v, shfl_xor2(v, off), c);
-        if (l == 0) (is_draft ? sD[i - len - 1] : sT[i]) = v;
+        if (l == 0) (is_draft ? s.draft[i - len - 1] : s.target[i]) = v;
     }
     __syncthreads();
     if (t < len) {
         const int x = a.tokens[(int64_t)b * a.m + t];
         bool ok = false;
         if (x >= 0 && x < a.vocab) {  // a token outside the vocabulary is rejected
+            const float2 of_t = s.target[t];
             if constexpr (GREEDY) {
-                ok = __float_as_int(sT[t].y) == x;
+                ok = __float_as_int(of_t.y) == x;
             } else {
                 const int64_t row = (int64_t)b * (a.m + 1) + t;
-                const float p = sT[t].y > 0.f ? weight(load1<F32>(a.target, row * a.target_stride + x), sT[t].x, c) / sT[t].y : 0.f;
+                const float p = of_t.y > 0.f ? weight(load1<F32>(a.target, row * a.target_stride + x), of_t.x, c) / of_t.y : 0.f;
                 float q = 1.f;
                 if (a.draft) {
                     const int64_t dr = (int64_t)b * a.m + t;
-                    q = sD[t].y > 0.f ? weight(load1<F32>(a.draft, dr * a.draft_stride + x), sD[t].x, c) / sD[t].y : 0.f;
+                    const float2 of_d = s.draft[t];
+                    q = of_d.y > 0.f ? weight(load1<F32>(a.draft, dr * a.draft_stride + x), of_d.x, c) / of_d.y : 0.f;
                 }
                 ok = a.accept_u[(int64_t)b * a.m + t] * q < p;
             }
         }
-        sOk[t] = ok;
+        s.ok[t] = ok;
     }
     __syncthreads();
     int acc = 0;
-    while (acc < len && sOk[acc]) ++acc;
-    if (part == 0 && t == 0) a.accepted[b] = acc;
-    if constexpr (GREEDY) {
-        if (part == 0 && t == 0) a.next[b] = __float_as_int(sT[acc].y) == kNone ? -1 : __float_as_int(sT[acc].y);
-        return;
-    }
+    while (acc < len && s.ok[acc]) ++acc;
+    return acc;
+}
+
+// The best of r / e (whole: of p / e) over the tokens lo .. hi - 1, by the whole
+// workgroup, as (score, token) ordered as one integer: scores are not negative, the
+// lower token is the larger; 0 where no score is above 0.
+template <bool F32> __device__ __forceinline__ uint64_t draw(const VerifyArgs &a, int b, int acc, DecideLds &s, int lo, int hi, bool whole, int t) {
+    const float c = a.inv_temperature * kLog2e;
     const int64_t trow = ((int64_t)b * (a.m + 1) + acc) * a.target_stride;
     const int64_t drow = ((int64_t)b * a.m + acc) * a.draft_stride;
-    const int bad = acc < len ? a.tokens[(int64_t)b * a.m + acc] : -1;
-    const bool less = acc < len && a.draft;
+    const bool rejected = acc < length_of(a, b), less = rejected && a.draft;
+    const int bad = rejected ? a.tokens[(int64_t)b * a.m + acc] : -1;
     // a row without probabilities: its weights come out as NaN (never above 0) or are held to 0
-    const float tm = sT[acc].x, ti = sT[acc].y > 0.f ? 1.f / sT[acc].y : 0.f;
-    const bool has_q = less && sD[acc].y > 0.f;
-    const float dm = has_q ? sD[acc].x : 0.f, di = has_q ? 1.f / sD[acc].y : 0.f;
+    const float tm = s.target[acc].x, ti = s.target[acc].y > 0.f ? 1.f / s.target[acc].y : 0.f;
+    const bool has_q = less && s.draft[acc].y > 0.f;
+    const float dm = has_q ? s.draft[acc].x : 0.f, di = has_q ? 1.f / s.draft[acc].y : 0.f;
     const float *noise = a.sample_e + (int64_t)b * a.vocab;
-    // the best of r / e (whole: of p / e) over a part of the vocabulary as (score, token),
-    // ordered as one integer: scores are not negative, the lower token is the larger
-    auto scan = [&](int lo, int hi, bool whole) {
-        float score = 0.f;
-        int token = kNone;
-        for (int v = lo + 8 * t; v < hi; v += 2048) {
-            float x[8], q[8], e[8];
-            if (v + 8 <= hi) {
-                load8<F32>(a.target, trow + v, x);
-                if (less) load8<F32>(a.draft, drow + v, q);
-                load8<true>(noise, v, e);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool in = v + j < hi;
-                    x[j] = in ? load1<F32>(a.target, trow + v + j) : -INFINITY;
-                    q[j] = in && less ? load1<F32>(a.draft, drow + v + j) : -INFINITY;
-                    e[j] = in ? noise[v + j] : 1.f;
-                }
-            }
+    float score = 0.f;
+    int token = kNone;
+    for (int v = lo + 8 * t; v < hi; v += 2048) {
+        float x[8], q[8], e[8];
+        if (v + 8 <= hi) {
+            load8<F32>(a.target, trow + v, x);
+            if (less) load8<F32>(a.draft, drow + v, q);
+            load8<true>(noise, v, e);
+        } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float r = __builtin_amdgcn_exp2f((x[j] - tm) * c) * ti;
-                if (!whole) r -= less ? __builtin_amdgcn_exp2f((q[j] - dm) * c) * di : v + j == bad ? 1.f : 0.f;
-                r *= __builtin_amdgcn_rcpf(e[j]);
-                if (r > score) score = r, token = v + j;
+                const bool in = v + j < hi;
+                x[j] = in ? load1<F32>(a.target, trow + v + j) : -INFINITY;
+                q[j] = in && less ? load1<F32>(a.draft, drow + v + j) : -INFINITY;
+                e[j] = in ? noise[v + j] : 1.f;
             }
         }
-        uint64_t best = token == kNone ? 0 : (uint64_t)__float_as_uint(score) << 32 | (uint32_t)(kNone - token);
 #pragma unroll
-        for (int off = 32; off; off >>= 1) {
-            const uint64_t other = __shfl_xor((unsigned long long)best, off);
-            best = other > best ? other : best;
+        for (int j = 0; j < 8; ++j) {
+            float r = __builtin_amdgcn_exp2f((x[j] - tm) * c) * ti;
+            if (!whole) r -= less ? __builtin_amdgcn_exp2f((q[j] - dm) * c) * di : v + j == bad ? 1.f : 0.f;
+            r = fmaxf(r, 0.f) * __builtin_amdgcn_rcpf(e[j]);  // held to 0 first: noise below 0 takes a token out
+            if (r > score) score = r, token = v + j;
         }
-        __syncthreads();
-        if (l == 0) sBest[w] = best;
-        __syncthreads();
-        best = sBest[0];
-        for (int i = 1; i < 4; ++i) best = sBest[i] > best ? sBest[i] : best;
-        return best;
-    };
-    int lo, hi;
-    segment(a.vocab, part, a.sample_splits, lo, hi);
-    uint64_t best = scan(lo, hi, false);
-    if (a.sample_splits > 1) {
-        // the maximum over the request's workgroups does not depend on their order; the last
-        // one to have raised it (the atomic's answer is waited for before the count goes up) reads it
-        if (t == 0) {
-            atomicMax(reinterpret_cast<unsigned long long *>(a.best + b), (unsigned long long)best);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            sLast = atomicAdd(a.done + b, 1) == a.sample_splits - 1;
-            if (sLast) sFinal = __hip_atomic_load(a.best + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        __syncthreads();
-        if (!sLast) return;
-        best = sFinal;
     }
-    if (best == 0) best = scan(0, a.vocab, true);  // nothing left of p after q: draw from p itself
-    if (t == 0) a.next[b] = best == 0 ? -1 : kNone - (int)(uint32_t)best;
+    uint64_t best = token == kNone ? 0 : (uint64_t)__float_as_uint(score) << 32 | (uint32_t)(kNone - token);
+#pragma unroll
+    for (int off = 32; off; off >>= 1) {
+        const uint64_t other = __shfl_xor((unsigned long long)best, off);
+        best = other > best ? other : best;
+    }
+    __syncthreads();
+    if ((t & 63) == 0) s.best[t >> 6] = best;
+    __syncthreads();
+    best = s.best[0];
+    for (int i = 1; i < 4; ++i) best = s.best[i] > best ? s.best[i] : best;
+    return best;
+}
+__device__ __forceinline__ int token_of(uint64_t best) { return best == 0 ? -1 : kNone - (int)(uint32_t)best; }
+
+template <bool F32, bool GREEDY> __global__ __launch_bounds__(256) void decide_kernel(VerifyArgs a) {
+    __shared__ DecideLds s;
+    const int t = threadIdx.x, part = blockIdx.x, b = blockIdx.y;
+    const int acc = decide<F32, GREEDY>(a, b, s, t);
+    if (part == 0 && t == 0) a.accepted[b] = acc;
+    if constexpr (GREEDY) {
+        const int token = __float_as_int(s.target[acc].y);
+        if (t == 0) a.next[b] = token == kNone ? -1 : token;
+    } else {
+        int lo, hi;
+        segment(a.vocab, part, a.sample_splits, lo, hi);
+        uint64_t best = draw<F32>(a, b, acc, s, lo, hi, false, t);
+        if (a.sample_splits > 1) {
+            if (t == 0) a.best[(int64_t)b * a.sample_splits + part] = best;
+            return;
+        }
+        if (best == 0) best = draw<F32>(a, b, acc, s, 0, a.vocab, true, t);  // nothing left of p after q: from p itself
+        if (t == 0) a.next[b] = token_of(best);
+    }
+}
+
+// The best of a request's parts.
+template <bool F32> __global__ __launch_bounds__(256) void pick_kernel(VerifyArgs a) {
+    __shared__ DecideLds s;
+    const int t = threadIdx.x, b = blockIdx.x;
+    uint64_t best = (t & 63) < a.sample_splits ? a.best[(int64_t)b * a.sample_splits + (t & 63)] : 0;
+#pragma unroll
+    for (int off = 32; off; off >>= 1) {
+        const uint64_t other = __shfl_xor((unsigned long long)best, off);
+        best = other > best ? other : best;
+    }
+    if (best == 0) {  // in every wave alike: nothing left of p after q, from p itself
+        const int acc = decide<F32, false>(a, b, s, t);
+        best = draw<F32>(a, b, acc, s, 0, a.vocab, true, t);
+    }
+    if (t == 0) a.next[b] = token_of(best);
 }
 
 template <bool F32, bool GREEDY> hipError_t verify(const VerifyArgs &a, hipStream_t stream) {
@@ -281,6 +305,8 @@ template <bool F32, bool GREEDY> hipError_t verify(const VerifyArgs &a, hipStrea
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((decide_kernel<F32, GREEDY>), dim3(GREEDY ? 1 : a.sample_splits, a.n), dim3(256), 0, stream, a);
+    if constexpr (!GREEDY)
+        if (a.sample_splits > 1) hipLaunchKernelGGL((pick_kernel<F32>), dim3(a.n), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
