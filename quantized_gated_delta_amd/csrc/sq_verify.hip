@@ -18,6 +18,10 @@
 // of a kernel orders their writes before its reads on every XCD (instead, an atomic
 // maximum that the last workgroup by a counter read: 24 us for kernel 2 with 64
 // requests of 131072 tokens, where kernels 2 and 3 take 17 + 4).
+//
+// Measured: 64 requests of 4 drafted tokens, 131072 logits each, bf16, with draft logits
+// 27 + 17 + 4 us (kernel 1 at 5.5 TB/s, 2 at 4.0); 256 requests, 50001 logits, fp32, 28 + 20 + 5 us;
+// one greedy request, 32000 logits, 4 + 3 us, less than the host takes to ask for it.
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -14,6 +14,12 @@
 // layout once the contracted axis is read in that order.  Codes get there
 // through LDS: a lane unpacks 4 rows x 16 columns and writes the four rows'
 // bytes of a column as one word.
+//
+// Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 275 us (453 MB, 1.6 TB/s), 8
+// requests 9.5 us; KDA, 128 requests x 32 heads of up to 4 tokens with S_out, 131 us (2.6 TB/s).
+// Bound by vector issue and latency: unpacking, the keys' terms and the window's small triangular
+// products are 860 vector instructions of each wave at 5 tokens and 6 bits, issued in half of
+// the cycles; the matrix cores are busy in three tenths of them.
 #include "sq_prep.h"
 #include "sq_window.h"
 
