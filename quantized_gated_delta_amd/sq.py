@@ -155,6 +155,8 @@ def _ptr(x) -> Optional[int]:
 
 def _need(t, name, numel, dtypes):
     """Shape / dtype / device check of one tensor argument (marshalling only)."""
+    if getattr(t, "is_cuda", False) and t.dtype in dtypes and t.numel() == numel:
+        return
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
