@@ -15,11 +15,11 @@
 // through LDS: a lane unpacks 4 rows x 16 columns and writes the four rows'
 // bytes of a column as one word.
 //
-// Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 275 us (453 MB, 1.6 TB/s), 8
-// requests 9.5 us; KDA, 128 requests x 32 heads of up to 4 tokens with S_out, 131 us (2.6 TB/s).
+// Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 234 us (453 MB, 1.9 TB/s), 8
+// requests 8.8 us; KDA, 128 requests x 32 heads of up to 4 tokens with S_out, 135 us (2.6 TB/s).
 // Bound by vector issue and latency: unpacking, the keys' terms and the window's small triangular
-// products are 860 vector instructions of each wave at 5 tokens and 6 bits, issued in half of
-// the cycles; the matrix cores are busy in three tenths of them.
+// products are 860 vector instructions of each wave at 5 tokens and 6 bits, issued in six tenths
+// of the cycles; the matrix cores are busy in a third of them.
 #include "sq_prep.h"
 #include "sq_window.h"
 
@@ -88,10 +88,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
     __shared__ __attribute__((aligned(16))) float sE[KDA ? 3 * kW * EROW : 4];  // keys times e^L, e^-L, queries times e^L
     __shared__ __attribute__((aligned(16))) float sOut[KEEP ? D * 20 : 4];      // keys decayed to the window's end, [channel][token]
     __shared__ __attribute__((aligned(16))) float sFade[KEEP ? D : 4], sr[KEEP ? D : 4];
-    __shared__ __attribute__((aligned(16))) float sTurn[4 * 320], sBeta[kW];
+    __shared__ __attribute__((aligned(16))) float sBeta[kW];
     __shared__ int sSlow[2];
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
-    float *tile = sTurn + w * 320;
+    // the waves' tiles to turn, in place of the keys once every wave has read them: GDN then has four workgroups
+    // per CU for three (274 -> 234 us for 512 requests of 5 tokens), with S_out three for two
+    float *tile = reinterpret_cast<float *>(sK) + w * 320;
+    static_assert(sizeof(sK) >= 4 * 320 * sizeof(float), "");
     const int b = blockIdx.x / (uint32_t)a.n_heads, h = blockIdx.x % (uint32_t)a.n_heads;
     const int hk = h / (a.n_heads / a.n_key_heads);
     const int L = a.length, len = a.lens ? min(max(a.lens[b], 0), L) : L;
@@ -354,6 +357,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
             }
         }
     }
+    __syncthreads();
     // M = (I + N)^-1 (-B) with N = B diag(beta), as (I - N)(I + N^2)(I + N^4)(I + N^8)(-B)
     const f4 beta = *reinterpret_cast<const f4 *>(sBeta + g4);
     f4 N, m;
