@@ -222,6 +222,18 @@ def test_nothing_left_of_the_target():
     assert accepted.tolist() == [0] and after.tolist() == [3002]
 
 
+@pytest.mark.parametrize("V", [9, 1000, 70000])
+def test_nothing_left_in_any_number_of_parts(V):
+    """As above, with the vocabulary in one part and in many."""
+    t = torch.full((2, 2, V), -math.inf, device=DEV)
+    t[:, :, V // 2:V // 2 + 3] = 0.0
+    e = torch.ones(2, V, device=DEV)
+    e[0, V // 2 + 1] = e[1, V // 2 + 2] = 0.5
+    tokens = torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    accepted, after = call(t, tokens, draft=t[:, :1].contiguous(), u=torch.full((2, 1), 0.5, device=DEV), e=e)
+    assert accepted.tolist() == [0, 0] and after.tolist() == [V // 2 + 1, V // 2 + 2]
+
+
 def test_padded_rows():
     """Logits as a part of a wider, padded output layer."""
     x = make(4, 3, 1001, seed=5)
