@@ -260,7 +260,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
 // GDN: the decayed dP and dB as bf16 pairs in registers against the keys and
 // queries by channel.  All that the four waves share goes once from memory through the LDS,
 // asked for two steps before it is used, so that two workgroups share a CU (each wave
-// its own loads, one workgroup: 471 us for 8192 tokens x 32 heads, d 128; this 292 us, 4.9 TB/s).
+// its own loads, one workgroup: 451 us for 8192 tokens x 32 heads, d 128; this 292 us, 4.9 TB/s).
 template <int D, bool F32> struct GradLds {
     static constexpr int STATE = 64 * D, TOKENS = F32 ? 4096 : 2048;  // bytes of 16 channels
     static constexpr int SLOT = 2 * STATE + 2 * TOKENS;               // S0, dS, keys, queries
