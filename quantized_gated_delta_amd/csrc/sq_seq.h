@@ -37,8 +37,6 @@ template <bool F32> using Elem = typename ElemOf<F32>::type;
 template <bool F32, int N> struct Frag { bf8 t[N]; };
 template <int N> struct Frag<true, N> { f4 v[2]; };
 
-__device__ __forceinline__ float bf2f(__bf16 x) { return (float)x; }
-
 template <int P, int NA, int NB>
 __device__ __forceinline__ f4 mma(const Frag<false, NA> &a, const Frag<false, NB> &b, f4 c) {
 #pragma unroll
