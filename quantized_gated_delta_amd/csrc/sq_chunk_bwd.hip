@@ -568,8 +568,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             for (int i = 0; i < 2 * PS; ++i) *reinterpret_cast<f4 *>(s.states + 16 * (t + 512 * i)) = part[i];
         };
         E *tS = reinterpret_cast<E *>(s.states), *tdS = reinterpret_cast<E *>(s.states + 2 * Lds::STATE);
-        __syncthreads();  // the last head's LDS is done with
+        // cleared on this side of the barrier, set on the other: the last head's readers are two barriers back
         if (t < 4) s.strong[t] = 0;
+        __syncthreads();  // the last head's LDS is done with
         if (t < kChunk) s.beta[t] = beta;
         float up = 0.f, down = 0.f;
 #pragma unroll
