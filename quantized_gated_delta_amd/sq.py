@@ -483,6 +483,8 @@ class ChunkedDelta:
                 name, self.dtype, (n, heads, self.d), t.dtype, tuple(t.shape)))
         if t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.d):
             raise ValueError("the heads of %s must be dense" % name)
+        if n > 1 and t.stride(0) < heads * self.d:  # an expanded tensor's 0 would mean dense
+            raise ValueError("the tokens of %s must not overlap" % name)
         return t.stride(0) if n > 1 else 0
 
     def _args(self, q, k, v, beta, g, cu, S0):
@@ -570,6 +572,8 @@ class DraftVerifier:
         stride = t.stride(1) if m > 1 else t.stride(0)
         if (self.vocab > 1 and t.stride(2) != 1) or (n > 1 and m > 1 and t.stride(0) != m * stride):
             raise ValueError("the rows of %s must be evenly spaced and dense" % name)
+        if n * m > 1 and stride < self.vocab:  # an expanded tensor's 0 would mean dense
+            raise ValueError("the rows of %s must not overlap" % name)
         return stride if n * m > 1 else 0
 
     def verify(self, target, tokens, accepted, next_token, draft=None, accept_u=None,

@@ -1,0 +1,69 @@
+"""What the Python classes of the sequence and draft-check calls refuse before anything is
+enqueued.  The tensors lie in host memory and say that they are on the device, so no GPU is needed."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_gated_delta_amd as Q
+
+BF = torch.bfloat16
+
+
+class OnDevice(torch.Tensor):
+    is_cuda = property(lambda self: True)
+
+
+def device(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+
+
+def sequence(n=100, heads=4, key_heads=2, d=128):
+    x = dict(q=device(n, key_heads, d), k=device(n, key_heads, d), v=device(n, heads, d), beta=device(n, heads), g=device(n, heads),
+             cu=torch.tensor([0, n], dtype=torch.int32).as_subclass(OnDevice), y=device(n, heads, d))
+    return Q.ChunkedDelta(1, n, heads, d, n_key_heads=key_heads, device="cpu", train=True), x
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_one_token_expanded_to_all(name):
+    """Storage for one token behind a shape of many: the kernels would read past it."""
+    layer, x = sequence()
+    x[name] = x[name][:1].expand(100, -1, -1)
+    assert x[name].stride(0) == 0
+    with pytest.raises(ValueError, match=name):
+        layer.forward(*x.values(), stream=0)
+    y = x.pop("y")
+    grads = [torch.empty(x[n].shape, dtype=BF).as_subclass(OnDevice) for n in ("q", "k", "v", "beta", "g")]
+    with pytest.raises(ValueError, match=name):
+        layer.backward(*x.values(), y, *grads, stream=0)
+
+
+def test_tokens_that_overlap():
+    layer, x = sequence()
+    x["v"] = device(100 * 4 * 128).as_strided((100, 4, 128), (128, 128, 1))
+    with pytest.raises(ValueError, match="v"):
+        layer.forward(*x.values(), stream=0)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1000), (4, 1, 1000), (1, 3, 1000)], ids=str)
+@pytest.mark.parametrize("which", ["target", "draft"])
+def test_one_row_of_logits_expanded(shape, which):
+    checker = Q.DraftVerifier(4, 2, 1000, device="cpu")
+    target, draft = device(4, 3, 1000), device(4, 2, 1000)
+    i32, f32 = dict(dtype=torch.int32), dict(dtype=torch.float32)
+    if which == "target":
+        target = device(*shape).expand(4, 3, 1000)
+    else:
+        draft = device(shape[0], min(shape[1], 2), 1000).expand(4, 2, 1000)
+    with pytest.raises(ValueError, match=which):
+        checker.verify(target, device(4, 2, **i32), device(4, **i32), device(4, **i32), draft=draft, accept_u=device(4, 2, **f32),
+                       sample_e=device(4, 1000, **f32), stream=0)
+
+
+@pytest.mark.parametrize("n,m", [(1, 1), (1, 2), (5, 1)])
+def test_one_row_expanded_over_one_axis(n, m):
+    """Where only one axis has more than one row, its stride is the rows'."""
+    checker = Q.DraftVerifier(n, m, 64, device="cpu")
+    i32, f32 = dict(dtype=torch.int32), dict(dtype=torch.float32)
+    with pytest.raises(ValueError, match="target"):
+        checker.verify(device(1, 1, 64).expand(n, m + 1, 64), device(n, m, **i32), device(n, **i32), device(n, **i32),
+                       accept_u=device(n, m, **f32), sample_e=device(n, 64, **f32), stream=0)
