@@ -15,7 +15,7 @@
 // through LDS: a lane unpacks 4 rows x 16 columns and writes the four rows'
 // bytes of a column as one word.
 //
-// Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 234 us (453 MB, 1.9 TB/s), 8
+// Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 217 us (453 MB, 2.1 TB/s), 8
 // requests 8.8 us; KDA, 128 requests x 32 heads of up to 4 tokens with S_out, 135 us (2.6 TB/s).
 // Bound by vector issue and latency: unpacking, the keys' terms and the window's small triangular
 // products are 860 vector instructions of each wave at 5 tokens and 6 bits, issued in six tenths
@@ -358,24 +358,38 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
         }
     }
     __syncthreads();
-    // M = (I + N)^-1 (-B) with N = B diag(beta), as (I - N)(I + N^2)(I + N^4)(I + N^8)(-B)
+    // M = -B - N M with N = B diag(beta), by forward substitution, four tokens at a time: a lane holds the four rows of
+    // its column, what later rows take of them is one product.  (I - N)(I + N^2)(I + N^4)(I + N^8) for (I + N)^-1 is
+    // not good enough: for keys that resemble each other its partial products grow and cancel, which costs 16 tokens
+    // two digits.
     const f4 beta = *reinterpret_cast<const f4 *>(sBeta + g4);
-    f4 N, m;
+    f4 m;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = g4 + i;
         const float x = row < len && r < row ? kk[i] : 0.f;
         m[i] = -x;
-        N[i] = x * sBeta[r];
+        tile[row * 20 + r] = x * sBeta[r];
         if (!(row < len && r <= row)) qk[i] = 0.f;
     }
-    f4 fn = turn(tile, N, l);
-    m = mma16(-fn, m, m);
-    for (int reach = 2; reach < len; reach *= 2) {
-        N = mma16(fn, N, f4{});
-        fn = turn(tile, N, l);
-        m = mma16(fn, m, m);
+    __builtin_amdgcn_wave_barrier();
+    const f4 later = -*reinterpret_cast<const f4 *>(tile + r * 20 + g4);
+    f4 own[4];  // -N within these four tokens
+#pragma unroll
+    for (int i = 1; i < 4; ++i) own[i] = -*reinterpret_cast<const f4 *>(tile + (g4 + i) * 20 + g4);
+    __builtin_amdgcn_wave_barrier();
+    auto within = [&](f4 x) {
+        x[1] = fmaf(own[1][0], x[0], x[1]);
+        x[2] = fmaf(own[2][1], x[1], fmaf(own[2][0], x[0], x[2]));
+        x[3] = fmaf(own[3][2], x[2], fmaf(own[3][1], x[1], fmaf(own[3][0], x[0], x[3])));
+        return x;
+    };
+#pragma unroll
+    for (int J = 0; J < 3; ++J) {
+        if (4 * J + 4 >= len) break;
+        m = mma16(g4 == 4 * J && r >= 4 * J + 4 ? later : f4{}, within(m), m);
     }
+    m = within(m);
     const f4 fm = turn(tile, m, l), fp = turn(tile, qk, l);
 
 #pragma unroll

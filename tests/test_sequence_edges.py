@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.test_sequence import BF, DEV, F32, batch, check, run
+from tests.test_sequence import BF, DEV, F32, batch, check, check_window, run, window, window_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +30,30 @@ def test_strong_gates_on_shared_key_heads(gate, d, dtype):
         again = run(b, train=True)
         for n in first:
             assert torch.equal(first[n], again[n]), n
+
+
+def alike(shape, cosine, seed):
+    """Unit keys, any two of them at about this cosine (1: one key at every token)."""
+    gen = torch.Generator(DEV).manual_seed(seed)
+    randn = lambda *s: torch.nn.functional.normalize(torch.randn(*s, generator=gen, device=DEV), dim=-1)  # noqa: E731
+    return torch.nn.functional.normalize(cosine ** 0.5 * randn(*shape[:-3], 1, *shape[-2:]) + (1 - cosine) ** 0.5 * randn(*shape), dim=-1)
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("m", [5, 9, 12, 16])
+@pytest.mark.parametrize("cosine,beta", [(0.9, 0.9), (0.99, 0.9), (0.99, 0.99), (1.0, 1.0)])
+def test_window_of_similar_keys(gate, m, cosine, beta):
+    """Drafts that repeat tokens: the pairs' matrix is far from the identity, its powers grow and cancel."""
+    for bits in (32, [4, 6, 8, 16]):
+        b = window_batch(gate, 3, m, 4, 2, 128, F32, bits, gates=(0.0, 0.01), seed=31)
+        b["k"] = alike(b["k"].shape, cosine, 32)
+        b["beta"].fill_(beta)
+        check_window(b, *window(b))
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("cosine,beta", [(0.99, 0.99), (1.0, 1.0)])
+def test_sequence_of_similar_keys(gate, cosine, beta):
+    b = batch(gate, (130, 40), H=2, d=64, dtype=F32, gates=(0.0, 0.01), beta=beta, seed=33)
+    b["k"] = alike(b["k"].shape, cosine, 34)
+    check(b, run(b, train=True), train=True)
