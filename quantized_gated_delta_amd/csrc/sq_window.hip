@@ -15,7 +15,7 @@
 // through LDS: a lane unpacks 4 rows x 16 columns and writes the four rows'
 // bytes of a column as one word.
 //
-// Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 217 us (453 MB, 2.1 TB/s), 8
+// Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 212 us (453 MB, 2.1 TB/s), 8
 // requests 8.8 us; KDA, 128 requests x 32 heads of up to 4 tokens with S_out, 135 us (2.6 TB/s).
 // Bound by vector issue and latency: unpacking, the keys' terms and the window's small triangular
 // products are 860 vector instructions of each wave at 5 tokens and 6 bits, issued in six tenths
@@ -182,22 +182,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
     const uint32_t rbeta = t < kW ? ld_raw<F32>(a.beta, (tok0 + min(t, L - 1)) * a.n_heads + h) : 0;
     const float scale = scaled ? reinterpret_cast<const float *>(rec + codes)[ch] : 1.f;
 
-    // ---- pairs of tokens (GDN): B and P in the result layout, and the sums of the
-    // log-gates up to token r and after it, in every lane
+    // ---- pairs of tokens (GDN): B and P in the result layout, and the sum of the
+    // log-gates up to token r in every lane, in double: differences of sums lose nothing
     f4 kk{}, qk{};
-    float up = 0.f, down = 0.f, eup = 1.f, edown = 1.f;
+    double up = 0.;
+    float eup = 1.f, edown = 1.f;  // the decay up to token r and after it
     if constexpr (!KDA) {
-        const float g = r < len ? fmaxf(of_raw<F32>(rg[0]), kGateFloor) : 0.f;
-        up = down = g;
+        up = r < len ? (double)fmaxf(of_raw<F32>(rg[0]), kGateFloor) : 0.;
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) {
-            const float x = __shfl_up(up, off, 16), y = __shfl_down(down, off, 16);
+            const double x = __shfl_up(up, off, 16);
             if (r >= off) up += x;
-            if (r + off < 16) down += y;
         }
-        down = __shfl_down(down, 1, 16);
-        if (r == 15) down = 0.f;
-        eup = exp_of(up), edown = exp_of(down);
+        eup = exp_of((float)up), edown = exp_of((float)(__shfl(up, 15, 16) - up));
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             if constexpr (F32) {
@@ -214,11 +211,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // of the two differences that give the sum over (r, row], the one of smaller sums
             const int row = g4 + i;
-            const float Lr = __shfl(up, row, 16), Rr = __shfl(down, row, 16);
-            const bool in = row < len && r <= row;
-            const float d = exp_of(!in ? 0.f : up > Rr ? Lr - up : down - Rr);
+            const double to = __shfl(up, row, 16);
+            const float d = exp_of(row < len && r <= row ? (float)(to - up) : 0.f);
             kk[i] *= d, qk[i] *= d;
         }
     }

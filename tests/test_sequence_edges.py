@@ -1,6 +1,8 @@
 """The sequence and window calls where their kernels take another way: gates of unlike strength,
 large batches, keys that resemble each other.  Oracle and tolerances as in test_sequence.py.
 """
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -57,3 +59,14 @@ def test_sequence_of_similar_keys(gate, cosine, beta):
     b = batch(gate, (130, 40), H=2, d=64, dtype=F32, gates=(0.0, 0.01), beta=beta, seed=33)
     b["k"] = alike(b["k"].shape, cosine, 34)
     check(b, run(b, train=True), train=True)
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("reset", [-math.inf, -100.0, -50.0])
+@pytest.mark.parametrize("at", [(0,), (3, 10), (0, 1, 2, 3, 12, 13, 14, 15)], ids=str)
+def test_window_resets_among_weak_gates(gate, reset, at):
+    """Gates that forget everything before and after weak ones: what lies between them keeps its accuracy."""
+    for bits in (32, [6, 4]):
+        b = window_batch(gate, 3, 16, 2, 1, 128, F32, bits, gates=(0.001, 0.1), seed=35)
+        b["g"][:, list(at)] = reset
+        check_window(b, *window(b))
