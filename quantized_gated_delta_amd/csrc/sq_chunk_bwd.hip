@@ -572,13 +572,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         if (t < 4) s.strong[t] = 0;
         __syncthreads();  // the last head's LDS is done with
         if (t < kChunk) s.beta[t] = beta;
-        float up = 0.f, down = 0.f;
+        float up = 0.f, low = 0.f, down = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             if (16 * gb + i >= rows) raw[i] = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             up += fmaxf(of_raw<F32>(raw[i]), kGateFloor);
+            low = fminf(low, up);  // not the last sum alone: a gate above 1 may raise it again
             s.eL[(16 * gb + i) * GROW + gch] = exp_of(up);
         }
 #pragma unroll
@@ -586,7 +587,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             s.eR[(16 * gb + i) * GROW + gch] = exp_of(down);
             down += fmaxf(of_raw<F32>(raw[i]), kGateFloor);
         }
-        if (up < -kBlockRange) s.strong[gb] = 1;
+        if (low < -kBlockRange) s.strong[gb] = 1;
         float db[SLICES];
 #pragma unroll
         for (int i = 0; i < SLICES; ++i) db[i] = reinterpret_cast<const float *>(blk + lay.dbeta)[i * kChunk + t % kChunk];

@@ -219,13 +219,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
     }
 
     if (t < 2 * D) {
-        float sum = 0.f;
+        float sum = 0.f, low = 0.f;
 #pragma unroll
         for (int i = 0; i < kW; ++i) {
             if (i >= len) break;
             float e, x = of_raw<F32>(rx[i]);
             if constexpr (KDA) {
                 sum += fmaxf(of_raw<F32>(rg[i]), kGateFloor);
+                low = fminf(low, sum);  // not the last sum alone: a gate above 1 may raise it again
                 e = x * exp_of(sum);
             } else {
                 e = x * __shfl(eup, i, 16);
@@ -244,7 +245,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
             }
         }
         if (KDA && keys) {
-            const bool slow = __any(sum < -kBlockRange);
+            const bool slow = __any(low < -kBlockRange);
             if (l == 0) sSlow[w] = slow;
         }
         if constexpr (KEEP) {

@@ -70,3 +70,20 @@ def test_window_resets_among_weak_gates(gate, reset, at):
         b = window_batch(gate, 3, 16, 2, 1, 128, F32, bits, gates=(0.001, 0.1), seed=35)
         b["g"][:, list(at)] = reset
         check_window(b, *window(b))
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, F32)])
+def test_gates_above_one_after_a_reset(gate, d, dtype):
+    """The log-gates of a block dip to -95 and come back to -50: the sum at the block's end does not show it."""
+    b = batch(gate, (70,), H=2, Hk=1, d=d, dtype=dtype, gates=(0.0, 0.1), seed=37)
+    b["g"][19], b["g"][20], b["beta"][19] = -95.0, 45.0, 0.0
+    check(b, run(b, train=True), train=True)
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, F32)])
+def test_window_gates_above_one_after_a_reset(gate, d, dtype):
+    b = window_batch(gate, 2, 16, 2, 1, d, dtype, 32, gates=(0.0, 0.1), seed=36)
+    b["g"][:, 3], b["g"][:, 4], b["beta"][:, 3] = -95.0, 45.0, 0.0
+    check_window(b, *window(b))
