@@ -467,7 +467,7 @@ sq_status sq_verify_bytes(int32_t n, int32_t m, size_t *bytes);
  *         overlap need one each.
  * Errors: SQ_EINVAL for NULL or misaligned pointers (4 bytes; logits the size
  * of their type), m, vocab or a stride out of range, a negative or non-finite
- * temperature; SQ_ENOMEM if work_bytes is too small; SQ_EUNSUPPORTED if
+ * temperature or one so small that log2(e) / temperature is not finite; SQ_ENOMEM if work_bytes is too small; SQ_EUNSUPPORTED if
  * n * (2 m + 1) exceeds the grid limit of 65535 rows. */
 sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *target,
                           int64_t target_stride, const void *draft, int64_t draft_stride,

@@ -655,8 +655,9 @@ sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *targe
     if (vocab < 1 || vocab > 0x7FFFFFFF - 65536) return fail(SQ_EINVAL, "vocab = %d is out of range", vocab);
     if (logits_dtype != SQ_F32 && logits_dtype != SQ_BF16)
         return fail(SQ_EINVAL, "logits_dtype must be SQ_F32 or SQ_BF16 (got %d)", (int)logits_dtype);
-    if (!(temperature >= 0.f) || std::isinf(temperature) || (temperature > 0.f && std::isinf(1.f / temperature)))
-        return fail(SQ_EINVAL, "temperature = %g must be 0 or a positive number", (double)temperature);
+    // the kernels scale logits by log2(e) / T
+    if (!(temperature >= 0.f) || std::isinf(temperature) || (temperature > 0.f && std::isinf(1.f / temperature * sqk::kLog2e)))
+        return fail(SQ_EINVAL, "temperature = %g must be 0 or a positive number, and 1 / temperature within fp32", (double)temperature);
     if ((target_stride && target_stride < vocab) || (draft && draft_stride && draft_stride < vocab) ||
         target_stride > INT64_MAX / 16 / 65536 || draft_stride > INT64_MAX / 16 / 65536)
         return fail(SQ_EINVAL, "a row stride must be 0 or at least vocab = %d", vocab);

@@ -8,6 +8,8 @@
 
 namespace sqk {
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
 struct VerifyArgs {
     const void *target, *draft;              // logits; draft or null
     int64_t target_stride, draft_stride;     // elements from row to row

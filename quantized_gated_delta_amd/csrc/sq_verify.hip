@@ -31,8 +31,6 @@
 namespace sqk {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
 // Eight consecutive logits of a row whose start may have any alignment; NaN
 // counts as minus infinity, plus infinity as the largest finite value.
 template <bool F32> __device__ __forceinline__ void load8(const void *base, int64_t at, float (&x)[8]) {

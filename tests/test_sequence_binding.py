@@ -67,3 +67,10 @@ def test_one_row_expanded_over_one_axis(n, m):
     with pytest.raises(ValueError, match="target"):
         checker.verify(device(1, 1, 64).expand(n, m + 1, 64), device(n, m, **i32), device(n, **i32), device(n, **i32),
                        accept_u=device(n, m, **f32), sample_e=device(n, 64, **f32), stream=0)
+
+
+@pytest.mark.parametrize("temperature", [3e-39, 3.5e-39, 4.2e-39])
+def test_temperature_whose_scale_overflows(temperature):
+    """1 / T is still finite, log2(e) / T, which the kernels scale by, is not."""
+    from tests.test_sequence_abi import refused, verify
+    refused(Q.SQ_EINVAL, "temperature", verify, temperature=temperature)
