@@ -411,8 +411,11 @@ sq_status sq_chunk_backward(const sq_seq_desc *desc, const int32_t *cu, const vo
  *   S_out:  fp32 [n, n_heads, d_k, d_v], the state after a request's last
  *           token that counts, or NULL.  sq_quant_state(pool, slot_idx, n, S_out,
  *           ...) stores it: one requantization for the whole window.
- * A speculative step is: one call for y; sq_verify_draft; one call with lens =
- * the accepted tokens, y = NULL and S_out; sq_quant_state.
+ * A speculative step on m drafted tokens is: one call of length m + 1 for y, on
+ * the last sampled token (which no state holds yet) and the drafts after it;
+ * sq_verify_draft on the m + 1 rows of logits that follow from y; the same
+ * window again with lens = accepted + 1, y = NULL and S_out; sq_quant_state.
+ * `next` is then the first token of the following window.
  * Head h reads the key head h / (n_heads / n_key_heads) of q and k.
  * Arithmetic: as sq_chunk_forward; the state is exactly what the record
  * stands for.  Errors: as sq_decode_step, and SQ_EINVAL for a length or key head

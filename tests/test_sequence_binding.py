@@ -74,3 +74,11 @@ def test_temperature_whose_scale_overflows(temperature):
     """1 / T is still finite, log2(e) / T, which the kernels scale by, is not."""
     from tests.test_sequence_abi import refused, verify
     refused(Q.SQ_EINVAL, "temperature", verify, temperature=temperature)
+
+
+def test_header_says_which_tokens_a_speculative_step_keeps():
+    """A window holds the last sampled token and the drafts after it: of those that stand one more is kept than drafts."""
+    from quantized_gated_delta_amd import sq
+    text = " ".join(open(sq.HEADER).read().replace("\n *", " ").split())
+    assert "lens = accepted + 1" in text and "length m + 1" in text
+    assert "lens = the accepted tokens" not in text

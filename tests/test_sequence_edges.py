@@ -7,7 +7,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.test_sequence import BF, DEV, F32, batch, check, check_window, run, window, window_batch
+import quantized_gated_delta_amd as Q
+from tests.test_sequence import BF, DEV, F32, batch, check, check_window, near, recurrence, run, window, window_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,46 @@ def test_window_gates_above_one_after_a_reset(gate, d, dtype):
     b = window_batch(gate, 2, 16, 2, 1, d, dtype, 32, gates=(0.0, 0.1), seed=36)
     b["g"][:, 3], b["g"][:, 4], b["beta"][:, 3] = -95.0, 45.0, 0.0
     check_window(b, *window(b))
+
+
+def test_speculative_step():
+    """The step as the header describes it: a window of the last sampled token and m drafts for y, the draft check, the
+    same window with lens = accepted + 1 into the state.  Against one token at a time in 64 bits."""
+    n, m, H, d, V = 6, 4, 2, 64, 50
+    gen = torch.Generator(DEV).manual_seed(38)
+    table = {x: torch.randn(V, H * d, generator=gen, device=DEV) for x in "qkv"}
+    table.update(beta=torch.rand(V, H, generator=gen, device=DEV), g=-torch.rand(V, H, generator=gen, device=DEV))
+    for x in "qk":
+        table[x] = torch.nn.functional.normalize(table[x].view(V, H, d), dim=-1).view(V, H * d)
+    out = torch.randn(H * d, V, generator=gen, device=DEV)
+    S0 = 0.3 * torch.randn(n, H, d, d, generator=gen, device=DEV)
+    last = torch.randint(0, V, (n,), generator=gen, device=DEV)
+
+    def step(tok, S):  # one token of one request in 64 bits: the best next token and the state
+        row = {x: table[x][tok].to("cpu", torch.float64) for x in table}
+        y, S = recurrence(*(row[x].view(1, H, d) for x in "qkv"), row["beta"].view(1, H), row["g"].view(1, H, 1), S)
+        return int((y.flatten() @ out.to("cpu", torch.float64)).argmax()), S
+
+    # drafts: request i's first i tokens are the best ones, the rest are not
+    drafts, states, best = torch.zeros(n, m, dtype=torch.long, device=DEV), [], []
+    for i in range(n):
+        tok, S, trail = int(last[i]), S0[i].to("cpu", torch.float64), []
+        for j in range(m + 1):
+            tok, S = step(tok, S)
+            trail.append((tok, S))
+            if j < m:
+                drafts[i, j] = tok if j < i else (tok + 1) % V
+                if j >= i:
+                    break
+        states.append(trail[-1][1]), best.append(trail[-1][0])
+    window_tokens = torch.cat([last[:, None], drafts], 1)
+    q, k, v = (table[x][window_tokens].view(n, m + 1, H, d) for x in "qkv")
+    beta, g = (table[x][window_tokens] for x in ("beta", "g"))
+    pool, slot = S0.clone(), torch.arange(n, dtype=torch.int32, device=DEV)
+    y, S = torch.empty_like(v), torch.empty_like(S0)
+    accepted, after = (torch.empty(n, dtype=torch.int32, device=DEV) for _ in range(2))
+    Q.f32_window_update(pool, slot, q, k, v, beta, g, y=y)
+    Q.DraftVerifier(n, m, V).verify((y.flatten(-2) @ out).contiguous(), drafts.to(torch.int32), accepted, after, temperature=0.0)
+    Q.f32_window_update(pool, slot, None, k, v, beta, g, S_out=S, lens=accepted + 1)
+    assert accepted.tolist() == [min(i, m) for i in range(n)] and after.tolist() == best
+    near(S, torch.stack(states), "S")
