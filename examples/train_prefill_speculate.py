@@ -27,13 +27,14 @@ VOCAB, WIDTH, H, HK, D = 64, 128, 4, 2, 64
 
 
 class Delta(torch.autograd.Function):
-    """y of the sequences that cu marks off, with gradients; `layer` is a ChunkedDelta(train=True)."""
+    """y of the sequences that cu marks off, with gradients; `layer` is a ChunkedDelta(train=True), which
+    holds the saved states of one forward call: a second one before the first one's backward needs a layer of its own."""
 
     @staticmethod
     def forward(ctx, layer, cu, q, k, v, beta, g):
         y = torch.empty_like(v)
-        layer.forward(q, k, v, beta, g, cu, y)
-        ctx.layer, ctx.cu = layer, cu
+        call = layer.forward(q, k, v, beta, g, cu, y)
+        ctx.layer, ctx.cu, ctx.call = layer, cu, call
         ctx.save_for_backward(q, k, v, beta, g)
         return y
 
@@ -41,7 +42,7 @@ class Delta(torch.autograd.Function):
     def backward(ctx, dy):
         inputs = ctx.saved_tensors
         grads = [torch.empty_like(x) for x in inputs]
-        ctx.layer.backward(*inputs, ctx.cu, dy.contiguous(), *grads)
+        ctx.layer.backward(*inputs, ctx.cu, dy.contiguous(), *grads, call=ctx.call)
         return (None, None, *grads)
 
 

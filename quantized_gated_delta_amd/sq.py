@@ -447,8 +447,9 @@ class ChunkedDelta:
 
     Holds a workspace for batches of up to n_seq sequences and n_tokens tokens
     in all; a call may bring fewer.  With train=True, also what backward needs
-    of the last forward call, which it belongs to.  Calls that may overlap (on
-    several streams) need an object each.  q, k: [tokens, n_key_heads, d] and
+    of the last forward call, which it belongs to: a second forward takes the
+    first one's place, and backward refuses the number of any call but the last.
+    Calls that may overlap (on several streams) need an object each.  q, k: [tokens, n_key_heads, d] and
     v: [tokens, n_heads, d] may be parts of one wider tensor; every other tensor
     is contiguous."""
 
@@ -468,6 +469,7 @@ class ChunkedDelta:
         work, save = sq_chunk_bytes(self._desc(n_seq, n_tokens), train=True)
         if not train:
             work, save = sq_chunk_bytes(self._desc(n_seq, n_tokens)), None
+        self.calls, self._sizes = 0, None  # forward calls so far, and the last one's batch
         self.work = torch.empty(max(256, work), dtype=torch.uint8, device=device)
         self.save = None if save is None else torch.empty(max(256, save), dtype=torch.uint8,
                                                           device=device)
@@ -503,7 +505,8 @@ class ChunkedDelta:
 
     def forward(self, q, k, v, beta, g, cu, y, S0=None, S_out=None, stream=None):
         """y and, where given, the final states S_out [n_seq, n_heads, d, d]; cu: int32
-        [n_seq + 1] on the device, the tokens at which the sequences begin and end."""
+        [n_seq + 1] on the device, the tokens at which the sequences begin and end.
+        Returns the call's number, for backward."""
         import torch
         desc, n_seq, n = self._args(q, k, v, beta, g, cu, S0)
         _need(y, "y", n * self.n_heads * self.d, (self.y_dtype,))
@@ -511,15 +514,24 @@ class ChunkedDelta:
             _need(S_out, "S_out", n_seq * self.n_heads * self.d * self.d, (torch.float32,))
         sq_chunk_forward(desc, cu, q, k, v, beta, g, S0, y, S_out, self.save, self.work,
                          stream=stream)
+        self.calls, self._sizes = self.calls + 1, (n_seq, n)
+        return self.calls
 
     def backward(self, q, k, v, beta, g, cu, dy, dq, dk, dv, dbeta, dg, S0=None, dS_out=None,
-                 dS0=None, stream=None):
+                 dS0=None, call=None, stream=None):
         """Gradients of the last forward call, which had the same inputs; dy and every gradient in
-        `dtype` and contiguous, dS_out and dS0 [n_seq, n_heads, d, d] fp32 or None."""
+        `dtype` and contiguous, dS_out and dS0 [n_seq, n_heads, d, d] fp32 or None.  call: what
+        that forward returned; raises RuntimeError where another one came after it."""
         import torch
         if self.save is None:
             raise ValueError("backward needs train=True")
         desc, n_seq, n = self._args(q, k, v, beta, g, cu, S0)
+        if self.calls == 0 or (call is not None and call != self.calls):
+            raise RuntimeError("backward of forward call %s, but the saved states are of call %d" % (
+                "?" if call is None else call, self.calls))
+        if self._sizes != (n_seq, n):
+            raise RuntimeError("the last forward call had %d sequences of %d tokens, not %d of %d" % (
+                *self._sizes, n_seq, n))
         H, hk, d, dt = self.n_heads, self.n_key_heads, self.d, (self.dtype,)
         for name, t, numel in (("dy", dy, n * H * d), ("dq", dq, n * hk * d), ("dk", dk, n * hk * d),
                                ("dv", dv, n * H * d), ("dbeta", dbeta, n * H),

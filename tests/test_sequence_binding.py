@@ -82,3 +82,49 @@ def test_header_says_which_tokens_a_speculative_step_keeps():
     text = " ".join(open(sq.HEADER).read().replace("\n *", " ").split())
     assert "lens = accepted + 1" in text and "length m + 1" in text
     assert "lens = the accepted tokens" not in text
+
+
+def gradients(x):
+    return [torch.empty(x[n].shape, dtype=BF).as_subclass(OnDevice) for n in ("q", "k", "v", "beta", "g")]
+
+
+def test_backward_belongs_to_the_last_forward(monkeypatch):
+    """What backward reads is the last forward call's; an earlier one's is refused by its number, a batch of other
+    sizes by those."""
+    from quantized_gated_delta_amd import sq
+    backs = []
+    monkeypatch.setattr(sq, "sq_chunk_forward", lambda *a, **k: None)
+    monkeypatch.setattr(sq, "sq_chunk_backward", lambda *a, **k: backs.append(a))
+    layer, x = sequence()
+    y = x["y"]
+    inputs = [x[n] for n in ("q", "k", "v", "beta", "g", "cu")]
+
+    def back(inputs=inputs, y=y, **kw):
+        layer.backward(*inputs, y, *gradients(x), **kw)
+    with pytest.raises(RuntimeError, match="forward"):
+        back()
+    first = layer.forward(*inputs, y)
+    back(call=first)
+    back()
+    second = layer.forward(*inputs, y)
+    assert second != first
+    with pytest.raises(RuntimeError, match="forward"):
+        back(call=first)
+    back(call=second)
+    back(call=second)   # as often as wanted
+    assert len(backs) == 4
+    layer.forward(*(t[:60] for t in inputs[:5]), inputs[5], y[:60])   # another batch
+    with pytest.raises(RuntimeError, match="forward"):
+        back()
+
+
+def test_a_refused_forward_leaves_what_the_last_one_saved(monkeypatch):
+    from quantized_gated_delta_amd import sq
+    monkeypatch.setattr(sq, "sq_chunk_forward", lambda *a, **k: None)
+    monkeypatch.setattr(sq, "sq_chunk_backward", lambda *a, **k: None)
+    layer, x = sequence()
+    inputs = [x[n] for n in ("q", "k", "v", "beta", "g", "cu")]
+    call = layer.forward(*inputs, x["y"])
+    with pytest.raises(ValueError):
+        layer.forward(*inputs, x["y"][:50])
+    layer.backward(*inputs, x["y"], *gradients(x), call=call)
