@@ -364,7 +364,9 @@ sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work, size_t *save);
  * Arithmetic: states, sums and decays in fp32; matrix products on operands
  * split into bf16 terms so that S_out (and an fp32 y) has fp32 accuracy, a
  * bf16 y 16 bits before its rounding.  Log-gates below -150 act as -150 (their
- * gate is 0 in fp32), so a gate of exactly 0, g = -inf, resets the state.
+ * gate is 0 in fp32), so a gate of exactly 0, g = -inf, resets the state.  A
+ * log-gate of NaN makes its head's results NaN from its token on (and possibly
+ * for earlier tokens of the same chunk of 64).
  * n_seq = 0 is a no-op.  Errors: SQ_EINVAL for a NULL or misaligned pointer, a
  * bad stride or head count, SQ_ENOMEM if a buffer is too small,
  * SQ_EUNSUPPORTED as sq_chunk_bytes. */

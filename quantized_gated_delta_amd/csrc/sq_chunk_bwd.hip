@@ -578,14 +578,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             if (16 * gb + i >= rows) raw[i] = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            up += fmaxf(of_raw<F32>(raw[i]), kGateFloor);
+            up += floor_gate(of_raw<F32>(raw[i]));
             low = fminf(low, up);  // not the last sum alone: a gate above 1 may raise it again
             s.eL[(16 * gb + i) * GROW + gch] = exp_of(up);
         }
 #pragma unroll
         for (int i = 15; i >= 0; --i) {
             s.eR[(16 * gb + i) * GROW + gch] = exp_of(down);
-            down += fmaxf(of_raw<F32>(raw[i]), kGateFloor);
+            down += floor_gate(of_raw<F32>(raw[i]));
         }
         if (low < -kBlockRange) s.strong[gb] = 1;
         float db[SLICES];
@@ -739,7 +739,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = 16 * w + g4 + i;
-                    gs[(g4 + i) * 20 + r] = tok < rows ? fmaxf(ld_elem<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + ch), kGateFloor) : 0.f;
+                    gs[(g4 + i) * 20 + r] = tok < rows ? floor_gate(ld_elem<F32>(a.g, ((t0 + tok) * a.n_heads + h) * D + ch)) : 0.f;
                 }
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll 1

@@ -33,6 +33,8 @@ namespace sqk {
 constexpr float kBlockRange = 60.f;
 // Log-gates below this are as good as minus infinity: e^-150 is 0 in fp32.
 constexpr float kGateFloor = -150.f;
+// Not fmaxf, which would take the floor for a NaN and so forget the state without a word.
+__device__ __forceinline__ float floor_gate(float g) { return __builtin_elementwise_maximum(g, kGateFloor); }
 
 constexpr int kBRow = 68;  // floats in a row of a 64 x 64 matrix in LDS
 
@@ -171,7 +173,7 @@ template <bool F32> __device__ __forceinline__ GatesOf load_gates(const SeqArgs 
 }
 __device__ __forceinline__ void gates_gdn(GatesOf x, int rows, double *sG, float *sBeta, int t) {
     if (t < kChunk) {
-        double g = t < rows ? (double)fmaxf(x.g, kGateFloor) : 0.;
+        double g = t < rows ? (double)floor_gate(x.g) : 0.;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
             const double up = __shfl_up(g, off);
@@ -319,7 +321,7 @@ __device__ __forceinline__ void diagonal_kda(const SeqArgs &a, int64_t t0, int r
             float sk = 0.f, sq = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                if (i > j) e[c] += fmaxf(of_raw<F32>(g[c][i]), kGateFloor);
+                if (i > j) e[c] += floor_gate(of_raw<F32>(g[c][i]));
                 const float x = kj[c] * exp_of(e[c]);
                 sk = fmaf(x, of_raw<F32>(k[c][i]), sk);
                 sq = fmaf(x, of_raw<F32>(q[c][i]), sq);
@@ -373,7 +375,7 @@ __device__ __forceinline__ void prepare_kda(const SeqArgs &a, uint8_t *work, int
         widen(rk[kb], k);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            g[i] = fmaxf(g[i], kGateFloor);
+            g[i] = floor_gate(g[i]);
             const float L = scan_up(g[i]);
             eL[kb][i] = exp_of(L);
             iL[kb][i] = exp_of(fminf(-L, kBlockRange));

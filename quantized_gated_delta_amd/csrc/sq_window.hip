@@ -188,7 +188,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
     double up = 0.;
     float eup = 1.f, edown = 1.f;  // the decay up to token r and after it
     if constexpr (!KDA) {
-        up = r < len ? (double)fmaxf(of_raw<F32>(rg[0]), kGateFloor) : 0.;
+        up = r < len ? (double)floor_gate(of_raw<F32>(rg[0])) : 0.;
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) {
             const double x = __shfl_up(up, off, 16);
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
             if (i >= len) break;
             float e, x = of_raw<F32>(rx[i]);
             if constexpr (KDA) {
-                sum += fmaxf(of_raw<F32>(rg[i]), kGateFloor);
+                sum += floor_gate(of_raw<F32>(rg[i]));
                 low = fminf(low, sum);  // not the last sum alone: a gate above 1 may raise it again
                 e = x * exp_of(sum);
             } else {
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
                     for (int i = kW - 1; i >= 0; --i) {
                         if (i >= len) continue;
                         sOut[ch * 20 + i] = of_raw<F32>(rx[i]) * exp_of(after);
-                        after += fmaxf(of_raw<F32>(rg[i]), kGateFloor);
+                        after += floor_gate(of_raw<F32>(rg[i]));
                     }
                 }
                 for (int i = len; i < kW; ++i) sOut[ch * 20 + i] = 0.f;
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void w
                 float sk = 0.f, sq = 0.f;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    if (i > j) e[c] += fmaxf(ld_elem<F32>(a.g, ((tok0 + i) * a.n_heads + h) * D + 64 * c + l), kGateFloor);
+                    if (i > j) e[c] += floor_gate(ld_elem<F32>(a.g, ((tok0 + i) * a.n_heads + h) * D + 64 * c + l));
                     const int64_t at = ((tok0 + i) * a.n_key_heads + hk) * D + 64 * c + l;
                     const float x = kj[c] * exp_of(e[c]);
                     sk = fmaf(x, ld_elem<F32>(a.k, at), sk);

@@ -131,3 +131,30 @@ def test_speculative_step():
     Q.f32_window_update(pool, slot, None, k, v, beta, g, S_out=S, lens=accepted + 1)
     assert accepted.tolist() == [min(i, m) for i in range(n)] and after.tolist() == best
     near(S, torch.stack(states), "S")
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, F32)])
+def test_a_gate_of_nan_is_seen(gate, d, dtype):
+    """A log-gate that is not a number leaves none in its head's results from its token on, as in the decode step, and
+    none of it in any other head or sequence."""
+    b = batch(gate, (100, 90), H=4, Hk=2, d=d, dtype=dtype, seed=39)
+    clean = run(b, train=True)
+    b["g"][(130, 2) if gate == "gdn" else (130, 2, 7)] = math.nan
+    out = run(b, train=True)
+    assert out["y"][130:, 2].isnan().all() and out["S"][1, 2].isnan().all()
+    for n in ("dv", "dbeta", "dg"):
+        assert out[n][130, 2].isnan().any(), n
+        others = [0, 1, 3]
+        assert torch.equal(out[n][:, others], clean[n][:, others]) and torch.equal(out[n][:100], clean[n][:100]), n
+    for n in ("dq", "dk"):
+        assert out[n][130, 1].isnan().any() and torch.equal(out[n][:, 0], clean[n][:, 0]) and torch.equal(out[n][:100], clean[n][:100]), n
+    assert torch.equal(out["S"][0], clean["S"][0]) and torch.equal(out["y"][:100], clean["y"][:100])
+
+    b = window_batch(gate, 2, 7, 4, 2, d, dtype, [4, 6, 8, 16], seed=40)
+    clean = window(b)
+    b["g"][(1, 3, 2) if gate == "gdn" else (1, 3, 2, 7)] = math.nan
+    y, S = window(b)
+    assert y[1, 3:, 2].isnan().all() and S[1, 2].isnan().all()
+    y[1, :, 2], S[1, 2] = clean[0][1, :, 2], clean[1][1, 2]
+    assert torch.equal(y, clean[0]) and torch.equal(S, clean[1])
