@@ -158,3 +158,66 @@ def test_a_gate_of_nan_is_seen(gate, d, dtype):
     assert y[1, 3:, 2].isnan().all() and S[1, 2].isnan().all()
     y[1, :, 2], S[1, 2] = clean[0][1, :, 2], clean[1][1, 2]
     assert torch.equal(y, clean[0]) and torch.equal(S, clean[1])
+
+
+def ragged(n, seed, longest=40):
+    """Lengths of n sequences: empty ones, short ones, a few of more than one chunk."""
+    gen = torch.Generator().manual_seed(seed)
+    lens = torch.randint(0, longest, (n,), generator=gen).tolist()
+    lens[n // 3], lens[n // 2], lens[-1], lens[0] = 130, 65, 64, 0
+    return tuple(lens)
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (128, F32), (64, BF), (64, F32)])
+def test_batches_of_many_heads_and_sequences(gate, d, dtype):
+    """From 2048 slices of 16 columns on the forward scan takes 32 to a workgroup; an odd number of (sequence, head) pairs."""
+    H, n = 5, (2048 * 16 // d + 4) // 5
+    n += n % 2 == 0
+    assert n * H * d // 16 >= 2048
+    b = batch(gate, ragged(n, 41, 24), H=H, Hk=1, d=d, dtype=dtype, seed=42)
+    check(b, run(b, train=True), train=True)
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_pairs_y_of_the_other_type(gate, dtype):
+    b = batch(gate, ragged(53, 43, 24), H=5, Hk=5, dtype=dtype, start=False, gates=(0.0, 9.0), seed=44)
+    check(b, run(b, y_dtype=F32 if dtype == BF else BF))
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("n", [64, 65, 129])
+def test_many_sequences(gate, n):
+    """The chunks' sequences are found 64 at a time: one round of probes, two."""
+    b = batch(gate, ragged(n, n, 24), H=1, d=64, dtype=F32, skip=3, extra=2, seed=45)
+    check(b, run(b, train=True), train=True)
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+def test_thousands_of_sequences(gate):
+    """Three rounds of probes.  Forward against 64 bits, gradients against those of 60 sequences at a time, which the
+    tests above hold to 64 bits: each within 1e-5 of their norm of them, so 2e-5 of each other."""
+    n = 4200
+    b = batch(gate, ragged(n, n, 2), H=1, d=64, dtype=F32, seed=45)
+    out = run(b, train=True)
+    check(b, out)
+    parts = {x: [] for x in ("dq", "dk", "dv", "dbeta", "dg", "dS0")}
+    for lo in range(0, n, 60):
+        t0, t1 = int(b["cu"][lo]), int(b["cu"][lo + 60])
+        part = {x: b[x][t0:t1].clone() for x in ("q", "k", "v", "beta", "g", "dy")}
+        part.update({x: b[x][lo:lo + 60].clone() for x in ("S0", "dS")}, cu=b["cu"][lo:lo + 61] - t0, case=dict(b["case"], lens=b["case"]["lens"][lo:lo + 60]))
+        got = run(part, train=True)
+        for x in parts:
+            parts[x].append(got[x])
+    for x in parts:
+        want = torch.cat(parts[x])
+        assert (out[x] - want).norm() <= 2e-5 * want.norm(), x
+
+
+@pytest.mark.parametrize("gate", ["gdn", "kda"])
+@pytest.mark.parametrize("low,high", [(3.0, 9.0), (20.0, 60.0), (140.0, 300.0)])
+def test_window_strong_gates_on_a_packed_pool(gate, low, high):
+    for d, dtype in ((128, BF), (64, F32)):
+        b = window_batch(gate, 4, 16, 4, 2, d, dtype, [4, 6, 8, 16], lens=[16, 9, 1, 0], gates=(low, high), seed=46)
+        check_window(b, *window(b))
