@@ -472,8 +472,9 @@ sq_status sq_verify_bytes(int32_t n, int32_t m, size_t *bytes);
  *         overlap need one each.
  * Errors: SQ_EINVAL for NULL or misaligned pointers (4 bytes; logits the size
  * of their type), m, vocab or a stride out of range, a negative or non-finite
- * temperature or one so small that log2(e) / temperature is not finite; SQ_ENOMEM if work_bytes is too small; SQ_EUNSUPPORTED if
- * n * (2 m + 1) exceeds the grid limit of 65535 rows. */
+ * temperature or one so small that log2(e) / temperature is not finite;
+ * SQ_ENOMEM if work_bytes is too small; SQ_EUNSUPPORTED if n * (2 m + 1) exceeds
+ * the grid limit of 65535 rows. */
 sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *target,
                           int64_t target_stride, const void *draft, int64_t draft_stride,
                           sq_dtype logits_dtype, const int32_t *tokens, const int32_t *lens,
@@ -483,7 +484,8 @@ sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *targe
 
 /* Debug check: copy slot_idx[0..n) (device) to the host, synchronising the
  * stream, and verify every entry is in [0, n_slots) and distinct.  Returns
- * SQ_EINVAL with the first offending index in sq_last_error() otherwise. */
+ * SQ_EINVAL with the first offending index in sq_last_error() otherwise, and
+ * SQ_ENOMEM without host memory for the copy. */
 sq_status sq_check_slots(const sq_pool *pool, const int32_t *slot_idx, int32_t n,
                          hipStream_t stream);
 

@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <new>
 #include <vector>
 
@@ -145,6 +146,16 @@ bool debug_slots() {
     return v && v[0] && !(v[0] == '0' && v[1] == 0);
 }
 
+// Host memory for the debug checks' lists: no exception may leave through a C entry point.
+template <typename T> sq_status host_list(std::vector<T> &v, size_t n) {
+    try {
+        v.resize(n);
+    } catch (const std::exception &) {
+        return fail(SQ_ENOMEM, "no host memory for a list of %zu entries", n);
+    }
+    return SQ_OK;
+}
+
 sq_status check_io(const char *name, const void *p, bool need) {
     if (!need) return SQ_OK;
     if (!p) return fail(SQ_EINVAL, "%s is NULL", name);
@@ -201,7 +212,9 @@ sq_status check_seq(const sq_seq_desc *d) {
 
 // With SQ_DEBUG: the sequence list on the host (synchronises the stream).
 sq_status check_cu(const sq_seq_desc *d, const int32_t *cu, hipStream_t stream) {
-    std::vector<int32_t> host((size_t)d->n_seq + 1);
+    std::vector<int32_t> host;
+    sq_status st = host_list(host, (size_t)d->n_seq + 1);
+    if (st) return st;
     hipError_t e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
     e = hipMemcpy(host.data(), cu, sizeof(int32_t) * host.size(), hipMemcpyDeviceToHost);
@@ -515,12 +528,13 @@ sq_status sq_check_slots(const sq_pool *pool, const int32_t *slot_idx, int32_t n
     sq_status st = check_rows(pool, slot_idx, n);
     if (st) return st;
     if (n == 0) return SQ_OK;
-    std::vector<int32_t> host((size_t)n);
+    std::vector<int32_t> host;
+    std::vector<uint8_t> seen;  // zeros
+    if ((st = host_list(host, (size_t)n)) || (st = host_list(seen, (size_t)pool->desc.n_slots))) return st;
     hipError_t e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
     e = hipMemcpy(host.data(), slot_idx, sizeof(int32_t) * (size_t)n, hipMemcpyDeviceToHost);
     if (e != hipSuccess) return hip_fail(e, "hipMemcpy(slot_idx)");
-    std::vector<uint8_t> seen((size_t)pool->desc.n_slots, 0);
     for (int32_t i = 0; i < n; ++i) {
         const int32_t s = host[(size_t)i];
         if (s < 0 || s >= pool->desc.n_slots)

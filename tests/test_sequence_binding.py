@@ -128,3 +128,35 @@ def test_a_refused_forward_leaves_what_the_last_one_saved(monkeypatch):
     with pytest.raises(ValueError):
         layer.forward(*inputs, x["y"][:50])
     layer.backward(*inputs, x["y"], *gradients(x), call=call)
+
+
+OUT_OF_MEMORY = """
+import os, resource, sys
+sys.path.insert(0, %r)
+os.environ["SQ_DEBUG"] = "1"
+import quantized_gated_delta_amd as Q
+from tests.test_sequence_abi import P, BIG
+Q.lib()
+n = 1 << 27   # 512 MB of host memory for the list's copy
+d = Q.seq_desc(n, 0, 1, 64, Q.SQ_GATE_GDN, Q.SQ_BF16, Q.SQ_BF16)
+pool = Q.sq_pool_create(n, 1, 64, 64, [4], Q.SQ_GATE_GDN, P, Q.sq_pool_bytes(n, 1, 64, 64, [4], Q.SQ_GATE_GDN))
+size = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (size + (256 << 20), resource.RLIM_INFINITY))
+for call in (lambda: Q.sq_chunk_forward(d, P, P, P, P, P, P, None, P, P, None, P, save_bytes=0, work_bytes=BIG, stream=0),
+             lambda: Q.sq_check_slots(pool, P, n, 0)):
+    try:
+        call()
+        print("no error")
+    except Q.SQError as e:
+        print("ENOMEM" if e.status == Q.SQ_ENOMEM else e)
+"""
+
+
+def test_debug_checks_without_host_memory():
+    """The copies that the debug checks take of a list may find no memory: an error, not an exception through C."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", OUT_OF_MEMORY % root], capture_output=True, text=True, timeout=100, cwd=root)
+    assert out.returncode == 0 and out.stdout.split() == ["ENOMEM", "ENOMEM"], (out.returncode, out.stdout, out.stderr[-500:])
