@@ -458,16 +458,17 @@ sq_status sq_verify_bytes(int32_t n, int32_t m, size_t *bytes);
  *   accept_u: fp32 [n, m] uniform in [0, 1); sample_e: fp32 [n, vocab] positive,
  *           exponentially distributed (a token with a negative value is not drawn);
  *           both may be NULL at temperature 0;
- *   accepted, next: int32 [n], outputs.
+ *   accepted, next: int32 [n], outputs, apart from tokens, lens and each other.
  * With p, q the softmax of target / temperature and draft / temperature (fp32;
- * q = 1 at the drafted token without draft logits): drafted token x_i stands if all before it
- * do and accept_u_i * q_i(x_i) < p_i(x_i).  next is the argmax of r / sample_e, where
- * r = max(p - q, 0) in the first rejected row and p in the row after the last
- * draft where all stood; r = p if that leaves nothing.  temperature = 0: a token
- * stands if it is the argmax of its target row; next is the argmax.  Ties go
- * to the lower token.  A NaN logit counts as minus infinity; a row without any
- * logit above minus infinity accepts nothing and gives next = -1; drafted tokens
- * outside [0, vocab) are rejected.  n = 0 is a no-op.
+ * q = 1 at the drafted token without draft logits): drafted token x_i stands if
+ * all before it do and accept_u_i * q_i(x_i) < p_i(x_i).  next is the argmax of
+ * r / sample_e, where r = max(p - q, 0) in the first rejected row and p in the
+ * row after the last draft where all stood; r = p if that leaves nothing.
+ * temperature = 0: a token stands if it is the argmax of its target row; next is
+ * the argmax.  Ties go to the lower token.  A NaN logit counts as minus infinity,
+ * plus infinity as the largest finite fp32 value; a row without any logit above
+ * minus infinity accepts nothing and gives next = -1; drafted tokens outside
+ * [0, vocab) are rejected.  n = 0 is a no-op.
  *   work: DEVICE scratch of sq_verify_bytes, 256-byte aligned; calls that may
  *         overlap need one each.
  * Errors: SQ_EINVAL for NULL or misaligned pointers (4 bytes; logits the size

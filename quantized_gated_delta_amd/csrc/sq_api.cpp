@@ -687,6 +687,15 @@ sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *targe
         if (x.p && !aligned(x.p, x.align)) return fail(SQ_EINVAL, "%s is not %d-byte aligned", x.name, (int)x.align);
     }
     if ((st = check_work("work", work, work_bytes, need))) return st;
+    // written by one workgroup of a request while its others read the lists
+    const struct { const char *name; const void *p; size_t count; } list[4] = {
+        {"accepted", accepted, (size_t)n}, {"next", next, (size_t)n}, {"tokens", tokens, (size_t)n * m}, {"lens", lens, lens ? (size_t)n : 0}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = i + 1; j < 4; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(list[i].p), y = reinterpret_cast<uintptr_t>(list[j].p);
+            if (x < y + 4 * list[j].count && y < x + 4 * list[i].count && list[j].count)
+                return fail(SQ_EINVAL, "%s and %s overlap", list[i].name, list[j].name);
+        }
     const sqk::VerifyLayout lay = sqk::verify_layout(n, m);
     uint8_t *base = static_cast<uint8_t *>(work);
     sqk::VerifyArgs a{};

@@ -160,3 +160,12 @@ def test_debug_checks_without_host_memory():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     out = subprocess.run([sys.executable, "-c", OUT_OF_MEMORY % root], capture_output=True, text=True, timeout=100, cwd=root)
     assert out.returncode == 0 and out.stdout.split() == ["ENOMEM", "ENOMEM"], (out.returncode, out.stdout, out.stderr[-500:])
+
+
+def test_outputs_of_the_draft_check_apart_from_its_lists():
+    """accepted is written while other workgroups still read lens and tokens: the same memory is refused."""
+    from tests.test_sequence_abi import P, refused, verify
+    apart = dict(tokens=P, lens=P + 4096, accepted=P + 8192, next_token=P + 12288)
+    for change in (dict(accepted=P + 4096), dict(accepted=P), dict(next_token=P + 4096 + 8), dict(next_token=P + 8192 + 8), dict(accepted=P + 4096 - 4),
+                   dict(next_token=P + 44)):
+        refused(Q.SQ_EINVAL, "overlap", verify, **dict(apart, **change))
