@@ -18,11 +18,12 @@
 // straight into fragments, the next chunk's issued right after their last use.
 //
 // Measured (d 128, bf16): GDN, 12 sequences of 12001 tokens in all, 48 heads, prep
-// 126 us (0.64 GB, 5.1 TB/s: bound by memory) and scan 487 us; KDA, one sequence of 8192
-// tokens, 32 heads, prep 214 and scan 370 us.  The scan is bound by the slices'
-// reading of the same operands from L2 (78 KB per chunk and workgroup for GDN, 168 KB for KDA,
-// 17 to 24 bytes per clock and CU) and, with one workgroup per CU, by the three
-// products' latency: the matrix cores are busy in 12 to 26 % of the cycles, HBM moves 1.2 to 2.4 TB/s.
+// 124 us (0.65 GB, 5.3 TB/s: bound by memory) and scan 479 us; KDA, one sequence of 8192
+// tokens, 32 heads, prep 214 and scan 384 us.  The scan is bound by latency: its waves spend
+// 0.42 to 0.62 of their cycles unable to issue (behind the three products that wait for each
+// other), 0.21 to 0.27 waiting for memory, LDS and barriers.  No unit is near its rate: matrix cores
+// 0.12 to 0.26 busy, vector issue 0.18 to 0.36, HBM 2.2 to 2.9 TB/s, L2 7 TB/s (GDN) to 16 TB/s (KDA,
+// whose slices read 168 KB per chunk and workgroup for GDN's 78).
 // 64 tokens per chunk: the pairs' work grows with the chunk, the number of dependent steps
 // falls with it, and 64 is what four waves of 16 rows hold.
 #include "sq_prep.h"
@@ -289,7 +290,8 @@ template <int D, bool KDA, bool F32, bool YF32> hipError_t forward(const SeqArgs
     // 32 columns read the operands half as often for the same work, but leave half the
     // workgroups: worth it once 16 columns would give 8 workgroups per CU
     // (48 heads x 12 sequences: 487 against 660 us; 32 x 4: 401 against 377 us;
-    // one sequence of 32 heads, KDA: 489 against 374 us)
+    // one sequence of 32 heads, KDA: 489 against 374 us).  The rule does not look at lengths, though
+    // one long sequence among very many short ones has the chain of a single one.
     if (a.n_seq * (int64_t)a.n_heads * (D / 16) >= 2048) launch_scan<D, KDA, F32, NTY, YF32, 2>(a, stream);
     else launch_scan<D, KDA, F32, NTY, YF32, 1>(a, stream);
     return hipGetLastError();

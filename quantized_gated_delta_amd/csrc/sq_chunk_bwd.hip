@@ -22,10 +22,10 @@
 // the forward pass saved.  The heads that share a key head are added up in the
 // registers of one workgroup: in a fixed order, without another pass.
 //
-// Measured (d 128, bf16): GDN, 8192 tokens in 4 sequences, 32 heads on 16 key heads, 69 + 360 + 292 us;
-// KDA, 4001 tokens in 3, 32 heads, 112 + 270 + 225 us.  The scan is bound as the
-// forward one.  The gradients move 1.4 GB (GDN) and 0.63 GB: 4.9 TB/s of the 5.8 that a copy
-// reaches, and 2.8 TB/s, where the latency of the products between tokens is the rest.
+// Measured (d 128, bf16): GDN, 8192 tokens in 4 sequences, 32 heads on 16 key heads, 68 + 384 + 291 us;
+// KDA, 4001 tokens in 3, 32 heads, 111 + 277 + 224 us.  The scan is bound as the
+// forward one.  The gradients move 1.46 GB (GDN) and 0.64 GB: 5.0 TB/s of the 5.8 that a copy
+// reaches, and 2.9 TB/s, where the latency of the products between tokens is the rest.
 #include "sq_prep.h"
 
 namespace sqk {
@@ -260,7 +260,7 @@ template <int D, bool KDA, bool F32, int NCT> __global__ __launch_bounds__(256) 
 // GDN: the decayed dP and dB as bf16 pairs in registers against the keys and
 // queries by channel.  All that the four waves share goes once from memory through the LDS,
 // asked for two steps before it is used, so that two workgroups share a CU (each wave
-// its own loads, one workgroup: 451 us for 8192 tokens x 32 heads, d 128; this 292 us, 4.9 TB/s).
+// its own loads, one workgroup: 451 us for 8192 tokens x 32 heads, d 128; this 291 us, 5.0 TB/s).
 template <int D, bool F32> struct GradLds {
     static constexpr int STATE = 64 * D, TOKENS = F32 ? 4096 : 2048;  // bytes of 16 channels
     static constexpr int SLOT = 2 * STATE + 2 * TOKENS;               // S0, dS, keys, queries
@@ -477,7 +477,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(F32 && D ==
 // KDA: 16 by 16 tokens in fp32, the decays put on keys and queries.  e^L and e^R of the
 // chunk fill the LDS for one workgroup per CU: eight waves, the last four with the same tokens
 // as the first and the other half of the channels, so that two share a SIMD (four waves, each
-// with its own loads of the states: 389 us for 4001 tokens x 32 heads, d 128; this 225 us).
+// with its own loads of the states: 389 us for 4001 tokens x 32 heads, d 128; this 224 us).
 template <int D, bool F32> struct GradKdaLds {
     static constexpr bool KQ = !(F32 && D == 128);  // keys and queries fit beside the rest
     static constexpr int ROW = TokenTile<D, F32>::ROW, GROW = D + 4;

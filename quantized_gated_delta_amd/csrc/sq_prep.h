@@ -20,7 +20,7 @@
 // start as reference while no channel loses more than e^-kBlockRange over the block, and
 // exponentials of each pair's own sum otherwise.
 //
-// Bound by memory for GDN (forward 126 us for 12001 tokens x 48 heads, 5.1 TB/s with what it
+// Bound by memory for GDN (forward 124 us for 12001 tokens x 48 heads, 5.3 TB/s with what it
 // writes), by vector issue and latency for KDA, whose keys and queries are written decayed, in
 // three terms (214 us for 8192 tokens x 32 heads, 4 TB/s).  What a chunk writes is read by
 // the scan's slices, which would otherwise repeat its products eight times.

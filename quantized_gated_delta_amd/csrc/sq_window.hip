@@ -16,10 +16,11 @@
 // bytes of a column as one word.
 //
 // Measured (d 128, bf16, 48 heads, 6 bits): 512 requests of 5 tokens 212 us (453 MB, 2.1 TB/s), 8
-// requests 8.8 us; KDA, 128 requests x 32 heads of up to 4 tokens with S_out, 135 us (2.6 TB/s).
+// requests 8.9 us; KDA, 128 requests x 32 heads of up to 4 tokens with S_out, 133 us (343 MB, 2.6 TB/s).
 // Bound by vector issue and latency: unpacking, the keys' terms and the window's small triangular
-// products are 860 vector instructions of each wave at 5 tokens and 6 bits, issued in six tenths
-// of the cycles; the matrix cores are busy in a third of them.
+// products are 858 vector instructions of each wave at 5 tokens and 6 bits, issued in 0.68
+// of the cycles of busy CUs; the matrix cores are busy in 0.27 of them (KDA with S_out: 0.31 and 0.30, two
+// workgroups per CU).
 #include "sq_prep.h"
 #include "sq_window.h"
 
