@@ -483,6 +483,191 @@ sq_status sq_verify_draft(int32_t n, int32_t m, int32_t vocab, const void *targe
                           int32_t *accepted, int32_t *next, void *work, size_t work_bytes,
                           hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * What stands around a recurrent layer: the short convolution in front of it,
+ * a state-space layer beside the delta rule, and the norms behind and between
+ * blocks.  The pages describe the delta-rule layer alone; these follow the
+ * definitions written here.  Parameters (taps, biases, rates, norm weights, and their
+ * gradients) are fp32, everything that has a token axis is in `dtype` or `in_dtype`.  Every
+ * gradient that is a sum over tokens is added up in a fixed order: equal inputs
+ * give equal bits.  Outputs must not overlap inputs or other outputs unless a call says so;
+ * the calls refuse what they can see of that. */
+
+typedef enum { SQ_ACT_NONE = 0, SQ_ACT_SILU = 1, SQ_ACT_SIGMOID = 2 } sq_act;
+
+/* A causal convolution of every channel with its own taps, over sequences that
+ * lie one after another (what turns a projection's output into q, k and v, or into x, B and C):
+ *   p[t, c] = bias[c] + sum_j weight[c, j] * x[t - width + 1 + j, c],   y = act(p)
+ * where the width - 1 inputs before a sequence are the rows of its S0 (or 0). */
+typedef struct {
+    int32_t n_seq;        /* sequences, >= 0 */
+    int32_t n_channels;   /* >= 1 */
+    int32_t width;        /* taps: 2, 3 or 4 */
+    int64_t n_tokens;     /* tokens of all sequences, < 2^31 - 2^16 */
+    sq_act act;           /* SQ_ACT_NONE or SQ_ACT_SILU */
+    sq_dtype dtype;       /* x, y, states and their gradients */
+    int64_t x_stride;     /* elements from one token of x to the next (0: n_channels), at most 2^24 */
+} sq_conv_desc;
+
+/* Bytes that sq_conv_backward needs as `work`; the largest batch's serve all smaller ones. */
+sq_status sq_conv_bytes(const sq_conv_desc *desc, size_t *work);
+
+/*   cu:     DEVICE int32 [n_seq + 1] as sq_chunk_forward's, with the same rules for a wrong list
+ *           and for tokens that no sequence has;
+ *   x:      [n_tokens, n_channels], may be part of a wider tensor;  y: [n_tokens, n_channels];
+ *   weight: fp32 [n_channels, width];  bias: fp32 [n_channels] or NULL;
+ *   S0:     [n_seq, width - 1, n_channels], the inputs before each sequence, the oldest
+ *           first, or NULL for zeros;
+ *   S_out:  as S0: the last width - 1 inputs of each sequence (of S0 where it is
+ *           shorter), or NULL.  Apart from S0.
+ * Sums in fp32.  n_seq = 0 is a no-op.  Errors: SQ_EINVAL for a NULL or misaligned pointer (the
+ * size of an element), a bad stride or overlapping buffers, SQ_EUNSUPPORTED for another width. */
+sq_status sq_conv_forward(const sq_conv_desc *desc, const int32_t *cu, const void *x,
+                          const float *weight, const float *bias, const void *S0, void *y,
+                          void *S_out, hipStream_t stream);
+
+/* Gradients of sq_conv_forward for the same inputs (nothing is saved: p is formed again).
+ *   dy: [n_tokens, n_channels];  dS_out: gradient of S_out, or NULL for zeros;
+ *   dx: [n_tokens, n_channels];  dweight, dbias: fp32 as weight and bias, written (not
+ *       added to), dbias NULL or not as bias;  dS0: gradient of S0, or NULL;
+ *   work: DEVICE scratch of sq_conv_bytes, 256-byte aligned. */
+sq_status sq_conv_backward(const sq_conv_desc *desc, const int32_t *cu, const void *x,
+                           const float *weight, const float *bias, const void *S0, const void *dy,
+                           const void *dS_out, void *dx, float *dweight, float *dbias, void *dS0,
+                           void *work, size_t work_bytes, hipStream_t stream);
+
+/* One token per request on a pool [n_slots, width - 1, n_channels] of the last
+ * inputs, in place on the listed slots.  x, y: [n, n_channels]; desc's n_seq and n_tokens are not
+ * read.  slot_idx: DEVICE int32 [n], distinct; a request whose slot lies outside
+ * [0, n_slots) is left out: nothing of it is read or written, y included.  With SQ_DEBUG set,
+ * repeated slots are refused (which synchronises the stream). */
+sq_status sq_conv_step(const sq_conv_desc *desc, void *pool, int32_t n_slots,
+                       const int32_t *slot_idx, int32_t n, const void *x, const float *weight,
+                       const float *bias, void *y, hipStream_t stream);
+
+/* The selective state-space recurrence: per (sequence, head) a state S of d_state x d_head,
+ *   S_t = exp(dt_t A) S_{t-1} + dt_t B_t x_t^T,    y_t = S_t^T C_t + D x_t,
+ *   dt_t = softplus(raw_t + dt_bias), or raw_t + dt_bias,
+ * with A, D and dt_bias one number per head, and B, C shared by the n_heads / n_groups heads of a
+ * group:
+ *   x, y: [n_tokens, n_heads, d_head]   raw: [n_tokens, n_heads]
+ *   B, C: [n_tokens, n_groups, d_state]
+ * Strides are elements from one token to the next (0: dense), at most 2^24; those of x, B, C and of
+ * their gradients a multiple of 16 bytes. */
+typedef struct {
+    int32_t n_seq;        /* sequences, >= 0 */
+    int32_t n_heads;      /* 1 .. 16384 */
+    int32_t n_groups;     /* a divisor of n_heads */
+    int32_t d_state;      /* 64 or 128 */
+    int32_t d_head;       /* 64 or 128 */
+    int64_t n_tokens;     /* tokens of all sequences, < 2^31 - 2^16 */
+    int32_t softplus;     /* 0 or 1 */
+    sq_dtype in_dtype;    /* x, raw, B, C and their gradients, and y's gradient */
+    sq_dtype y_dtype;
+    int64_t x_stride, dt_stride, b_stride, c_stride;
+    int64_t dx_stride, ddt_stride, db_stride, dc_stride;  /* of the gradients */
+} sq_scan_desc;
+
+/* Bytes that sq_scan_forward needs as `work`; with save not NULL, *save is what it needs as
+ * `save` for a backward pass, and *work covers sq_scan_backward too.  The largest batch's buffers serve
+ * all smaller ones. */
+sq_status sq_scan_bytes(const sq_scan_desc *desc, size_t *work, size_t *save);
+
+/* Whole sequences, in chunks of 64 tokens.
+ *   cu, S0, S_out, save, work: as sq_chunk_forward's; states fp32 [n_seq, n_heads, d_state, d_head];
+ *           S_out may be S0 itself;
+ *   A: fp32 [n_heads];  D, dt_bias: fp32 [n_heads], or NULL for zeros.
+ * Arithmetic: states, sums and decays in fp32 (running sums of dt A in fp64); matrix products on
+ * operands split into bf16 terms so that S_out (and an fp32 y) has fp32 accuracy, a bf16 y 16 bits
+ * before its rounding.  dt A below -150 acts as -150 (its decay is 0 in fp32).  A NaN of dt makes its
+ * head's results NaN from its token on (and possibly for earlier tokens of the same chunk).
+ * Errors as sq_chunk_forward. */
+sq_status sq_scan_forward(const sq_scan_desc *desc, const int32_t *cu, const void *x,
+                          const void *raw, const float *A, const void *B, const void *C,
+                          const float *D, const float *dt_bias, const float *S0, void *y,
+                          float *S_out, void *save, size_t save_bytes, void *work,
+                          size_t work_bytes, hipStream_t stream);
+
+/* Gradients of sq_scan_forward from the `save` that it filled for the same inputs.
+ *   dy: gradient of y, dense, in in_dtype;  dS_out: fp32, or NULL for zeros;
+ *   dx, draw, dB, dC: in in_dtype, B's and C's summed over the heads of a group, required;
+ *   dA, dD, ddt_bias: fp32 [n_heads], written, the latter two NULL or not as wanted;
+ *   dS0: fp32, or NULL; may be dS_out itself.
+ * Nothing is written for tokens that no sequence has.  fp32 gradients have fp32 accuracy, bf16 ones 16
+ * bits before their rounding.  Overwrites work, leaves save as it is. */
+sq_status sq_scan_backward(const sq_scan_desc *desc, const int32_t *cu, const void *x,
+                           const void *raw, const float *A, const void *B, const void *C,
+                           const float *D, const float *dt_bias, const void *dy,
+                           const float *dS_out, const void *save, size_t save_bytes, void *dx,
+                           void *draw, float *dA, void *dB, void *dC, float *dD, float *ddt_bias,
+                           float *dS0, void *work, size_t work_bytes, hipStream_t stream);
+
+/* One token per request on an fp32 pool [n_slots, n_heads, d_state, d_head], in place on
+ * the listed slots: x, y [n, n_heads, d_head], raw [n, n_heads], B, C [n, n_groups, d_state]; desc's
+ * n_seq and n_tokens are not read.  slot_idx as sq_conv_step's.  fp32 throughout. */
+sq_status sq_scan_step(const sq_scan_desc *desc, float *state_pool, int32_t n_slots,
+                       const int32_t *slot_idx, int32_t n, const void *x, const void *raw,
+                       const float *A, const void *B, const void *C, const float *D,
+                       const float *dt_bias, void *y, hipStream_t stream);
+
+/* The norm behind a layer, with its gate, over rows of d (each group of a token):
+ *   y = rms(x) * weight * act(z),  or, with gate_first, y = rms(x * act(z)) * weight,
+ *   rms(x) = x / sqrt(mean(x^2) + eps).  x, z, y: [n_tokens, n_groups, d]. */
+typedef struct {
+    int64_t n_tokens;     /* >= 0; n_tokens * n_groups < 2^31 */
+    int32_t n_groups;     /* 1 .. 65535 */
+    int32_t d;            /* 1 .. 16384 */
+    int32_t shared_weight; /* weight is [d] for every group; 0: [n_groups, d] */
+    int32_t gate_first;   /* 0 or 1 */
+    sq_act act;           /* SQ_ACT_SILU or SQ_ACT_SIGMOID; SQ_ACT_NONE: no gate, z and dz are NULL */
+    float eps;            /* >= 0 */
+    sq_dtype dtype;
+    int64_t x_stride, z_stride, dx_stride, dz_stride; /* elements from token to token (0: dense) */
+} sq_gated_norm_desc;
+
+/* Bytes that sq_gated_norm_backward needs as `work`. */
+sq_status sq_gated_norm_bytes(const sq_gated_norm_desc *desc, size_t *work);
+/* weight: fp32, or NULL for ones. */
+sq_status sq_gated_norm_forward(const sq_gated_norm_desc *desc, const void *x, const void *z,
+                                const float *weight, void *y, hipStream_t stream);
+/* Gradients for the same inputs.  dweight: fp32, written, or NULL.  dx may be dy itself where both
+ * are dense. */
+sq_status sq_gated_norm_backward(const sq_gated_norm_desc *desc, const void *x, const void *z,
+                                 const float *weight, const void *dy, void *dx, void *dz,
+                                 float *dweight, void *work, size_t work_bytes,
+                                 hipStream_t stream);
+
+/* Between two blocks, over rows of d: the norm behind the first (with post_weight), its scale, the
+ * residual sum, and the norm before the second:
+ *   a = o, or rms(o) * post_weight;   r_out = r + scale * a;   h = rms(r_out) * weight
+ * (h from the r_out before its rounding). */
+typedef struct {
+    int64_t n_rows;       /* >= 0, < 2^31 */
+    int32_t d;            /* 1 .. 16384 */
+    float eps;            /* >= 0 */
+    sq_dtype dtype;       /* o, h and their gradients */
+    sq_dtype res_dtype;   /* r, r_out and their gradients */
+} sq_residual_norm_desc;
+
+/* Bytes that sq_residual_norm_backward needs as `work`. */
+sq_status sq_residual_norm_bytes(const sq_residual_norm_desc *desc, size_t *work);
+/*   r: or NULL for zeros;  post_weight: fp32 [d], or NULL for no norm behind the block;
+ *   scale: fp32 [d], or NULL for 1;  weight: fp32 [d], or NULL for 1;  h: or NULL for the sum alone.
+ * r_out may be r itself. */
+sq_status sq_residual_norm_forward(const sq_residual_norm_desc *desc, const void *o, const void *r,
+                                   const float *post_weight, const float *scale,
+                                   const float *weight, void *r_out, void *h, hipStream_t stream);
+/* Gradients, from o and r as the forward pass had them.
+ *   dh: gradient of h, or NULL where there is none;  dr_out: of r_out, or NULL for zeros;
+ *   d_o: required;  dr: or NULL;  dpost_weight, dscale, dweight: fp32 [d], written, or NULL;
+ *   dr may be dr_out itself, d_o may be dh itself. */
+sq_status sq_residual_norm_backward(const sq_residual_norm_desc *desc, const void *o, const void *r,
+                                    const float *post_weight, const float *scale,
+                                    const float *weight, const void *dh, const void *dr_out,
+                                    void *d_o, void *dr, float *dpost_weight, float *dscale,
+                                    float *dweight, void *work, size_t work_bytes,
+                                    hipStream_t stream);
+
 /* Debug check: copy slot_idx[0..n) (device) to the host, synchronising the
  * stream, and verify every entry is in [0, n_slots) and distinct.  Returns
  * SQ_EINVAL with the first offending index in sq_last_error() otherwise, and

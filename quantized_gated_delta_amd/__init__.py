@@ -15,6 +15,11 @@ from .sq import (SQ_BF16, SQ_EHIP, SQ_EINVAL, SQ_ENOMEM, SQ_EUNSUPPORTED, SQ_F32
                  sq_last_error, sq_pool_bytes, sq_pool_create, sq_pool_destroy, sq_pool_layout,
                  sq_pool_set_row_impact, sq_quant_state, sq_split_step_noalloc,
                  SQ_SPLIT_SCRATCH_BYTES, version)
+from .block import (SQ_ACT_NONE, SQ_ACT_SIGMOID, SQ_ACT_SILU, GatedNorm, ResidualNorm, SelectiveScan, ShortConv, conv_desc, conv_step,
+                    gated_norm_desc, residual_norm_desc, scan_desc, scan_step, sq_conv_backward, sq_conv_bytes, sq_conv_forward,
+                    sq_conv_step, sq_gated_norm_backward, sq_gated_norm_bytes, sq_gated_norm_forward, sq_residual_norm_backward,
+                    sq_residual_norm_bytes, sq_residual_norm_forward, sq_scan_backward, sq_scan_bytes, sq_scan_forward, sq_scan_step)
 
 __all__ = [n for n in dir() if n.startswith(("sq_", "SQ", "StatePool", "ChunkedDelta", "DraftVerifier", "seq_desc", "f32_window",
-                                               "lib", "header", "version"))]
+                                               "lib", "header", "version", "ShortConv", "SelectiveScan", "GatedNorm", "ResidualNorm", "conv_",
+                                               "scan_", "gated_norm", "residual_norm"))]

@@ -23,7 +23,8 @@ LIB_TIMELINE = os.path.join(HERE, "libsq_timeline.so")
 ARCH = "gfx950"
 
 SOURCES = ["sq_kernels.hip", "sq_probe.hip", "sq_chunk.hip", "sq_chunk_bwd.hip",
-           "sq_window.hip", "sq_verify.hip", "sq_api.cpp"]
+           "sq_window.hip", "sq_verify.hip", "sq_conv.hip", "sq_norm.hip", "sq_scan.hip", "sq_scan_bwd.hip",
+           "sq_api.cpp", "sq_block_api.cpp"]
 
 HIP_FLAGS = [
     "--offload-arch=" + ARCH,

@@ -16,6 +16,7 @@
 #include <new>
 #include <vector>
 
+#include "sq_check.h"
 #include "sq_internal.h"
 #include "sq_seq.h"
 #include "sq_verify.h"
@@ -32,8 +33,10 @@ struct sq_pool {
 };
 
 namespace {
-
 thread_local char g_err[512] = "";
+} // namespace
+
+namespace sqk {
 
 sq_status fail(sq_status st, const char *fmt, ...) {
     va_list ap;
@@ -47,7 +50,66 @@ sq_status hip_fail(hipError_t e, const char *what) {
     return fail(SQ_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool debug_slots() {
+    const char *v = std::getenv("SQ_DEBUG");
+    return v && v[0] && !(v[0] == '0' && v[1] == 0);
+}
+
+sq_status check_work(const char *name, const void *p, size_t have, size_t need) {
+    if (need == 0) return SQ_OK;
+    if (!p) return fail(SQ_EINVAL, "%s is NULL", name);
+    if (!aligned(p, 256)) return fail(SQ_EINVAL, "%s is not 256-byte aligned", name);
+    if (have < need) return fail(SQ_ENOMEM, "%s has %zu bytes, %zu are needed", name, have, need);
+    return SQ_OK;
+}
+
+sq_status check_sequences(int32_t n_seq, int64_t n_tokens, const int32_t *cu, hipStream_t stream) {
+    std::vector<int32_t> host;
+    sq_status st = host_list(host, (size_t)n_seq + 1);
+    if (st) return st;
+    hipError_t e = hipStreamSynchronize(stream);
+    if (e != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
+    e = hipMemcpy(host.data(), cu, sizeof(int32_t) * host.size(), hipMemcpyDeviceToHost);
+    if (e != hipSuccess) return hip_fail(e, "hipMemcpy(cu)");
+    for (int32_t i = 0; i <= n_seq; ++i)
+        if (host[(size_t)i] < (i ? host[(size_t)i - 1] : 0) || host[(size_t)i] > n_tokens)
+            return fail(SQ_EINVAL, "cu[%d] = %d must be non-decreasing within [0, %lld]", i, host[(size_t)i],
+                        (long long)n_tokens);
+    return SQ_OK;
+}
+
+sq_status check_slot_list(const int32_t *slot_idx, int32_t n, int32_t n_slots, bool others, hipStream_t stream) {
+    std::vector<int32_t> host;
+    std::vector<uint8_t> seen;  // zeros
+    sq_status st;
+    if ((st = host_list(host, (size_t)n)) || (st = host_list(seen, (size_t)n_slots))) return st;
+    hipError_t e = hipStreamSynchronize(stream);
+    if (e != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
+    e = hipMemcpy(host.data(), slot_idx, sizeof(int32_t) * (size_t)n, hipMemcpyDeviceToHost);
+    if (e != hipSuccess) return hip_fail(e, "hipMemcpy(slot_idx)");
+    for (int32_t i = 0; i < n; ++i) {
+        const int32_t s = host[(size_t)i];
+        if (s < 0 || s >= n_slots) {
+            if (others) continue;
+            return fail(SQ_EINVAL, "slot_idx[%d] = %d is outside [0, %d)", i, s, n_slots);
+        }
+        if (seen[(size_t)s]) return fail(SQ_EINVAL, "slot_idx[%d] = %d is repeated", i, s);
+        seen[(size_t)s] = 1;
+    }
+    return SQ_OK;
+}
+
+} // namespace sqk
+
+using sqk::aligned;
+using sqk::check_sequences;
+using sqk::check_slot_list;
+using sqk::check_work;
+using sqk::debug_slots;
+using sqk::fail;
+using sqk::hip_fail;
+
+namespace {
 
 // Rows of one head with per-key-row widths: non-decreasing widths in
 // {4, 6, 8} that change only at multiples of the rows a wavefront holds per
@@ -136,26 +198,6 @@ sq_status check_rows(const sq_pool *p, const int32_t *slot_idx, int32_t n) {
     return SQ_OK;
 }
 
-// Debug mode: with SQ_DEBUG set to a value other than "0" in the
-// environment (read at each call), every compute entry point on a pool first
-// runs sq_check_slots on its slot indices (which synchronises the stream) and
-// enqueues nothing if one is out of range or repeated: overlapping slots would
-// make the in-place update race.
-bool debug_slots() {
-    const char *v = std::getenv("SQ_DEBUG");
-    return v && v[0] && !(v[0] == '0' && v[1] == 0);
-}
-
-// Host memory for the debug checks' lists: no exception may leave through a C entry point.
-template <typename T> sq_status host_list(std::vector<T> &v, size_t n) {
-    try {
-        v.resize(n);
-    } catch (const std::exception &) {
-        return fail(SQ_ENOMEM, "no host memory for a list of %zu entries", n);
-    }
-    return SQ_OK;
-}
-
 sq_status check_io(const char *name, const void *p, bool need) {
     if (!need) return SQ_OK;
     if (!p) return fail(SQ_EINVAL, "%s is NULL", name);
@@ -210,22 +252,6 @@ sq_status check_seq(const sq_seq_desc *d) {
     return SQ_OK;
 }
 
-// With SQ_DEBUG: the sequence list on the host (synchronises the stream).
-sq_status check_cu(const sq_seq_desc *d, const int32_t *cu, hipStream_t stream) {
-    std::vector<int32_t> host;
-    sq_status st = host_list(host, (size_t)d->n_seq + 1);
-    if (st) return st;
-    hipError_t e = hipStreamSynchronize(stream);
-    if (e != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
-    e = hipMemcpy(host.data(), cu, sizeof(int32_t) * host.size(), hipMemcpyDeviceToHost);
-    if (e != hipSuccess) return hip_fail(e, "hipMemcpy(cu)");
-    for (int32_t i = 0; i <= d->n_seq; ++i)
-        if (host[(size_t)i] < (i ? host[(size_t)i - 1] : 0) || host[(size_t)i] > d->n_tokens)
-            return fail(SQ_EINVAL, "cu[%d] = %d must be non-decreasing within [0, %lld]", i, host[(size_t)i],
-                        (long long)d->n_tokens);
-    return SQ_OK;
-}
-
 sqk::SeqArgs seq_args(const sq_seq_desc *d, const int32_t *cu, const void *q, const void *k, const void *v,
                       const void *beta, const void *g, const float *S0, void *work) {
     sqk::SeqArgs a{};
@@ -241,14 +267,6 @@ sqk::SeqArgs seq_args(const sq_seq_desc *d, const int32_t *cu, const void *q, co
     a.S0 = S0;
     a.work = static_cast<uint8_t *>(work);
     return a;
-}
-
-sq_status check_work(const char *name, const void *p, size_t have, size_t need) {
-    if (need == 0) return SQ_OK;
-    if (!p) return fail(SQ_EINVAL, "%s is NULL", name);
-    if (!aligned(p, 256)) return fail(SQ_EINVAL, "%s is not 256-byte aligned", name);
-    if (have < need) return fail(SQ_ENOMEM, "%s has %zu bytes, %zu are needed", name, have, need);
-    return SQ_OK;
 }
 
 // beta, GDN's g and their gradients: read and written by the element.
@@ -528,21 +546,7 @@ sq_status sq_check_slots(const sq_pool *pool, const int32_t *slot_idx, int32_t n
     sq_status st = check_rows(pool, slot_idx, n);
     if (st) return st;
     if (n == 0) return SQ_OK;
-    std::vector<int32_t> host;
-    std::vector<uint8_t> seen;  // zeros
-    if ((st = host_list(host, (size_t)n)) || (st = host_list(seen, (size_t)pool->desc.n_slots))) return st;
-    hipError_t e = hipStreamSynchronize(stream);
-    if (e != hipSuccess) return hip_fail(e, "hipStreamSynchronize");
-    e = hipMemcpy(host.data(), slot_idx, sizeof(int32_t) * (size_t)n, hipMemcpyDeviceToHost);
-    if (e != hipSuccess) return hip_fail(e, "hipMemcpy(slot_idx)");
-    for (int32_t i = 0; i < n; ++i) {
-        const int32_t s = host[(size_t)i];
-        if (s < 0 || s >= pool->desc.n_slots)
-            return fail(SQ_EINVAL, "slot_idx[%d] = %d is outside [0, %d)", i, s, pool->desc.n_slots);
-        if (seen[(size_t)s]) return fail(SQ_EINVAL, "slot_idx[%d] = %d is repeated", i, s);
-        seen[(size_t)s] = 1;
-    }
-    return SQ_OK;
+    return check_slot_list(slot_idx, n, pool->desc.n_slots, false, stream);
 }
 
 sq_status sq_chunk_bytes(const sq_seq_desc *desc, size_t *work, size_t *save) {
@@ -572,7 +576,7 @@ sq_status sq_chunk_forward(const sq_seq_desc *desc, const int32_t *cu, const voi
         (st = check_io("S_out", S_out, S_out != nullptr)) || (st = check_work("work", work, work_bytes, need)) ||
         (save && (st = check_work("save", save, save_bytes, keep))))
         return st;
-    if (debug_slots() && (st = check_cu(desc, cu, stream))) return st;
+    if (debug_slots() && (st = check_sequences(desc->n_seq, desc->n_tokens, cu, stream))) return st;
     sqk::SeqArgs a = seq_args(desc, cu, q, k, v, beta, g, S0, work);
     a.y = y;
     a.S_out = S_out;
@@ -597,7 +601,7 @@ sq_status sq_chunk_backward(const sq_seq_desc *desc, const int32_t *cu, const vo
         (st = check_elems(desc, "dg", dg, desc->gate == SQ_GATE_KDA)) || (st = check_io("dS0", dS0, dS0 != nullptr)) ||
         (st = check_work("save", save, save_bytes, keep)) || (st = check_work("work", work, work_bytes, need)))
         return st;
-    if (debug_slots() && (st = check_cu(desc, cu, stream))) return st;
+    if (debug_slots() && (st = check_sequences(desc->n_seq, desc->n_tokens, cu, stream))) return st;
     sqk::SeqArgs a = seq_args(desc, cu, q, k, v, beta, g, nullptr, work);
     a.save = static_cast<uint8_t *>(const_cast<void *>(save));
     a.dy = dy; a.dS_out = dS_out;

@@ -1,0 +1,191 @@
+// Shared by the kernels around a recurrent layer (sq_conv.hip, sq_norm.hip, sq_scan.hip):
+// their arguments, ragged batches cut into blocks of tokens, vectors of 8 elements, and the
+// activations.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sq.h"
+#include "sq_seq.h"
+
+namespace sqk {
+
+// ------------------------------------------------------------------ ragged batches
+// Sequence s owns the block slots from cu[s] >> shift + s: one at least, enough for its
+// tokens, and none of another sequence, without a prefix sum over lengths on the host.
+struct Ragged {
+    const int32_t *cu;  // [n_seq + 1]
+    int32_t n_seq, n_tokens;
+};
+struct Block {
+    int32_t seq;   // negative: an idle slot
+    int32_t t0;    // first token of the sequence
+    int32_t len;   // tokens of the sequence
+    int32_t c;     // the block's number in it
+};
+inline int64_t block_slots(int64_t n_tokens, int32_t n_seq, int shift) { return (n_tokens >> shift) + n_seq; }
+
+// Offsets are held inside the tokens, so that a wrong list cannot make a kernel leave its buffers.
+__device__ __forceinline__ void ragged_span(const Ragged &a, int32_t s, int32_t &lo, int32_t &len) {
+    const int32_t n = a.n_tokens;
+    int32_t hi = a.cu[s + 1];
+    lo = a.cu[s];
+    lo = lo < 0 ? 0 : lo > n ? n : lo;
+    hi = hi < lo ? lo : hi > n ? n : hi;
+    len = hi - lo;
+}
+
+// The block on slot x, for a whole wave: its lanes probe 64 sequences at a time.  The first
+// block of a sequence without tokens is no idle slot: its state is still handed on.
+__device__ __forceinline__ Block block_at(const Ragged &a, int64_t x, int shift) {
+    const int l = threadIdx.x & 63;
+    int32_t lo = 0, n = a.n_seq, t0, len;
+    while (n > 64) {  // the last probed s whose first slot is not behind x
+        const int32_t step = (n + 63) >> 6, s = lo + l * step;
+        ragged_span(a, min(s, a.n_seq - 1), t0, len);
+        const bool before = l * step < n && (int64_t)(t0 >> shift) + s <= x;
+        const int k = max(__popcll(__ballot(before)) - 1, 0);
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    ragged_span(a, min(lo + l, a.n_seq - 1), t0, len);
+    const int k = max(__popcll(__ballot(l < n && (int64_t)(t0 >> shift) + lo + l <= x)) - 1, 0);
+    Block b;
+    b.t0 = __builtin_amdgcn_readlane(t0, k);
+    b.len = __builtin_amdgcn_readlane(len, k);
+    const int64_t c = x - ((int64_t)(b.t0 >> shift) + lo + k);
+    const bool live = c == 0 || (c > 0 && (c << shift) < b.len);
+    b.seq = live ? lo + k : -1;
+    b.c = live ? (int32_t)c : 0;
+    return b;
+}
+
+// ------------------------------------------------------------------ vectors of 8 elements
+// What 8 elements are loaded as: one or two vectors of 16 bytes.
+template <bool F32> struct Raw8 { uint4 v[F32 ? 2 : 1]; };
+
+// Elements i .. i + 7 of p.  VEC: 16-byte loads (aligned, all 8 inside); otherwise element by
+// element, those from `left` on as zeros.
+template <bool F32, bool VEC> __device__ __forceinline__ Raw8<F32> load8(const void *p, int64_t i, int left) {
+    Raw8<F32> r;
+    if constexpr (VEC) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const Elem<F32> *>(p) + i);
+        r.v[0] = q[0];
+        if constexpr (F32) r.v[1] = q[1];
+    } else {
+        uint32_t x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = e < left ? ld_raw<F32>(p, i + e) : 0u;
+        if constexpr (F32) {
+            r.v[0] = uint4{x[0], x[1], x[2], x[3]};
+            r.v[1] = uint4{x[4], x[5], x[6], x[7]};
+        } else {
+            r.v[0] = uint4{x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16};
+        }
+    }
+    return r;
+}
+template <bool F32> __device__ __forceinline__ void widen8(const Raw8<F32> &r, float (&x)[8]) {
+    if constexpr (F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            x[4 * h] = __uint_as_float(r.v[h].x), x[4 * h + 1] = __uint_as_float(r.v[h].y);
+            x[4 * h + 2] = __uint_as_float(r.v[h].z), x[4 * h + 3] = __uint_as_float(r.v[h].w);
+        }
+    } else {
+        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+template <bool F32, bool VEC> __device__ __forceinline__ void store8(void *p, int64_t i, const float (&x)[8], int left) {
+    if constexpr (VEC) {
+        if constexpr (F32) {
+            f4 *q = reinterpret_cast<f4 *>(static_cast<float *>(p) + i);
+            q[0] = f4{x[0], x[1], x[2], x[3]};
+            q[1] = f4{x[4], x[5], x[6], x[7]};
+        } else {
+            *reinterpret_cast<bf8 *>(static_cast<__bf16 *>(p) + i) = make_frag<false, 1>(x).t[0];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left) st_elem<F32>(p, i + e, x[e]);
+    }
+}
+
+// ------------------------------------------------------------------ activations
+// 1 / (1 + e^-z): the hardware reciprocal (1 unit) of an exponential of 2^-22.  The exponential's
+// argument is held inside [-150, 88], where it is finite: above, the result is 6e-39.
+__device__ __forceinline__ float sigmoid_of(float z) {
+    const float t = z < -88.f ? 88.f : z > 150.f ? -150.f : -z;  // a NaN stays one
+    return __builtin_amdgcn_rcpf(1.f + exp_of(t));
+}
+// act(z) and its derivative; none: 1 and 0 (no gate).
+__device__ __forceinline__ float gate_of(int act, float z) {
+    const float s = sigmoid_of(z);
+    return act == SQ_ACT_SILU ? z * s : s;
+}
+__device__ __forceinline__ void gate_and_slope(int act, float z, float &value, float &slope) {
+    const float s = sigmoid_of(z);
+    value = act == SQ_ACT_SILU ? z * s : s;
+    slope = act == SQ_ACT_SILU ? s + value * (1.f - s) : s * (1.f - s);
+}
+
+// ------------------------------------------------------------------ arguments
+struct ConvArgs {
+    Ragged seqs;
+    const void *x, *S0, *dy, *dS_out;
+    const float *weight, *bias;
+    void *y, *S_out, *dx, *dS0;
+    float *dweight, *dbias, *partial;
+    int64_t x_stride;
+    int32_t channels, width, silu;
+    // step
+    void *pool;
+    const int32_t *slot;
+    int32_t n, n_slots;
+};
+// Blocks along the tokens of the backward pass: each leaves its sums over tokens in `partial`.
+int conv_blocks(int64_t n_tokens, int32_t n_seq, int32_t channels);
+hipError_t launch_conv_forward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
+hipError_t launch_conv_backward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
+hipError_t launch_conv_step(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
+
+struct GateArgs {
+    const void *x, *z, *dy;
+    const float *weight;
+    void *y, *dx, *dz;
+    float *dweight, *partial;
+    int64_t n_tokens, x_stride, z_stride, dx_stride, dz_stride;
+    int32_t groups, d, act;
+    float eps;
+};
+struct ResidualArgs {
+    const void *o, *r, *dh, *dr_out;
+    const float *post, *scale, *weight;
+    void *r_out, *h, *d_o, *dr;
+    float *dpost, *dscale, *dweight, *partial;
+    int64_t n_rows;
+    int32_t d;
+    float eps;
+};
+constexpr int kNormMax = 16384;  // longest row: 1024 threads of 16 elements
+// Workgroups of a backward pass along the rows: each leaves its sums over rows in `partial`.
+int norm_blocks(int64_t rows, int32_t d);
+hipError_t launch_gate_forward(const GateArgs &a, bool f32, bool vec, bool first, bool shared, hipStream_t stream);
+hipError_t launch_gate_backward(const GateArgs &a, bool f32, bool vec, bool first, bool shared, hipStream_t stream);
+hipError_t launch_residual_forward(const ResidualArgs &a, bool f32, bool res_f32, bool vec, hipStream_t stream);
+hipError_t launch_residual_backward(const ResidualArgs &a, bool f32, bool res_f32, bool vec, hipStream_t stream);
+
+// column[j] = sum over i of part[i][j], i ascending within each of a workgroup's lanes: the
+// second half of every gradient that is a sum over tokens.
+struct SumArgs {
+    const float *part;
+    float *out;
+    int64_t rows, cols, row_stride;
+};
+hipError_t launch_column_sums(const SumArgs *a, int count, hipStream_t stream);
+
+} // namespace sqk

@@ -1,0 +1,180 @@
+// The selective state-space scan's kernels (sq_scan.hip, sq_scan_bwd.hip): arguments, workspaces, a chunk's gates.
+#pragma once
+
+#include "sq_block.h"
+
+namespace sqk {
+
+constexpr int kHeadPart = 64;  // columns of a state that a workgroup has: a head of 128 is two parts, which share its gates
+constexpr int kSegMin = 8;     // shortest segment of a long sequence: 256 tokens
+
+struct ScanArgs {
+    Ragged seqs;
+    const void *x, *raw, *B, *C;
+    const float *A, *D, *bias, *S0;
+    void *y;
+    float *S_out;
+    int64_t x_stride, dt_stride, b_stride, c_stride;
+    int32_t n_heads, n_groups, d_head, softplus;  // d_head: 64 or 128
+    int32_t seg_shift, segments;  // log2 of a segment's tokens; segments: more than one to some sequence
+    float *seg_state, *seg_fade;  // [segment slot][part of a head]: states at the segments' starts, decays over them
+    uint8_t *save, *grad_save;    // [chunk slot][part]: states at the chunks' starts; their gradients at the chunks' ends
+    // backward
+    const void *dy;
+    const float *dS_out;
+    void *dx, *draw, *dB, *dC;
+    float *dA, *dD, *dbias, *dS0;
+    int64_t dx_stride, ddt_stride, db_stride, dc_stride;
+    int32_t subsets;              // of a group's heads, a workgroup each
+    float *group_part;            // [2][subsets][n_tokens][n_groups][d_state]: dB and dC of a subset (subsets > 1)
+    float *head_part;             // [3][chunk slots][n_heads]: sums over a chunk of dA, dbias and dD
+    // step
+    float *pool;
+    const int32_t *slot;
+    int32_t n, n_slots;
+};
+
+// How a call is cut up.  Segments: a workgroup walks the chunks of one, so a long sequence is cut where
+// there would be too few workgroups to fill the card; its states at the segments' starts
+// then come from a pass that forms states alone (about half the work of the whole).
+struct ScanPlan {
+    int seg_shift, subsets;
+    int64_t parts, seg_slots, chunk_slots, state_bytes, fade_bytes, save_bytes, group_bytes, head_bytes;
+};
+ScanPlan scan_plan(const sq_scan_desc &d);
+
+hipError_t launch_scan_forward(const ScanArgs &a, int d_state, bool f32, bool y_f32, hipStream_t stream);
+hipError_t launch_scan_states_back(const ScanArgs &a, int d_state, bool f32, hipStream_t stream);
+hipError_t launch_scan_backward(const ScanArgs &a, int d_state, bool f32, hipStream_t stream);
+hipError_t launch_scan_step(const ScanArgs &a, int d_state, bool f32, bool y_f32, hipStream_t stream);
+
+// ------------------------------------------------------------------ device
+// log(1 + e^v); from 20 on that is v to one part in 10^10.
+__device__ __forceinline__ float softplus_of(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+
+// A chunk's gates in LDS.  G: the running sum of dt A over the chunk, as the sum of two floats, so that
+// a difference of two is exact to fp32 wherever it is small, also behind a strong decay.
+struct Gates {
+    float hi[64], lo[64];  // G
+    float dt[64];
+    float in[64];          // e^G: from the chunk's start to a token
+    float out[64];         // e^{G_end - G}: from a token to the chunk's end
+};
+__device__ __forceinline__ float decay_of(const Gates &g, int i, int j) { return exp_of((g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j])); }
+
+// Inclusive sums over the lanes of a wave.
+__device__ __forceinline__ double wave_scan(double v, int l) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const double u = __shfl_up(v, m, 64);
+        if (l >= m) v += u;
+    }
+    return v;
+}
+
+// One wave forms a chunk's gates, a token to a lane; live: the token is one of the sequence's.
+// Others have no time: they change nothing.
+__device__ __forceinline__ void make_gates(Gates &g, int l, bool live, float raw, float bias, float A, int softplus) {
+    const float v = raw + bias;
+    const float dt = live ? (softplus ? softplus_of(v) : v) : 0.f;
+    double s = (double)dt * (double)A;
+    s = s < -150.0 ? -150.0 : s;  // a NaN stays one
+    if (!live) s = 0.0;
+    const double G = wave_scan(s, l), end = __shfl(G, 63, 64);
+    const float hi = (float)G;
+    g.hi[l] = hi;
+    g.lo[l] = (float)(G - (double)hi);
+    g.dt[l] = dt;
+    g.in[l] = exp_of((float)G);
+    g.out[l] = exp_of((float)(end - G));
+}
+
+// A matrix of 64 rows (tokens) in LDS, rows as they lie in memory and padded by 16 bytes.
+template <bool F32, int COLS> struct TokenMat {
+    typedef Elem<F32> E;
+    static constexpr int ROW = COLS + (F32 ? 4 : 8), SIZE = 64 * ROW;
+    static constexpr int VECS = COLS * (int)sizeof(E) / 16;  // 16-byte vectors of a row
+    // row `row`, elements k .. k + 7 of the contracted axis
+    __device__ __forceinline__ static Frag<F32, 1> get(const E *m, int row, int k) { return load_frag<F32, 1>(m + row * ROW + k, 0); }
+    // ... elements k .. k + 3 and k + 16 .. k + 19: the order in which two result tiles hold 32 rows
+    __device__ __forceinline__ static Frag<F32, 1> get_split(const E *m, int row, int k) {
+        Frag<F32, 1> f;
+        const E *p = m + row * ROW + k;
+        if constexpr (F32) {
+            f.v[0] = *reinterpret_cast<const f4 *>(p);
+            f.v[1] = *reinterpret_cast<const f4 *>(p + 16);
+        } else {
+            f.t[0] = __builtin_shufflevector(*reinterpret_cast<const bf4 *>(p), *reinterpret_cast<const bf4 *>(p + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        return f;
+    }
+};
+
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4v lds_s4v;
+// A fragment of the transposed matrix: row (lane) l % 16 is column col0 + l % 16 of m, contracted elements
+// are its rows row0 + 8 (l / 16) .. + 7.  bf16: the transposing LDS load, where 16 lanes take 4 rows of 16.
+template <bool F32, int N> __device__ __forceinline__ Frag<F32, N> get_t(const Elem<F32> *m, int row_size, int plane, int row0, int col0, int l) {
+    Frag<F32, N> f;
+    const int r = l & 15, g = l >> 4;
+    if constexpr (F32) {
+        const float *p = m + (row0 + 8 * g) * row_size + col0 + r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.v[e / 4][e % 4] = p[e * row_size];
+    } else {
+        const uint16_t *p = m + (row0 + 8 * g + (r >> 2)) * row_size + col0 + (r & 3) * 4;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(p + n * plane));
+            const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(p + n * plane + 4 * row_size));
+            f.t[n] = __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+    return f;
+}
+
+// The 16 x 16 tiles (it, jt), jt <= it, of 64 x 64 pairs of tokens, numbered row by row.
+__device__ __forceinline__ void pair_tile(int n, int &it, int &jt) {
+    it = n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0;
+    jt = n - it * (it + 1) / 2;
+}
+
+// Vectors of a token matrix as a workgroup of T threads loads them: from memory into
+// registers, rows behind the last as zeros, and from there into LDS.
+template <bool F32, int COLS, int T> struct Staged {
+    typedef TokenMat<F32, COLS> M;
+    static constexpr int COUNT = 64 * M::VECS / T;
+    uint4 v[COUNT];
+    __device__ __forceinline__ void load(const void *base, int64_t stride, int rows, int t) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const int row = (i * T + t) / M::VECS, col = (i * T + t) % M::VECS;
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const Elem<F32> *>(base) + row * stride) + col;
+            v[i] = row < rows ? *p : uint4{};
+        }
+    }
+    __device__ __forceinline__ void store(Elem<F32> *m, int t) const {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const int row = (i * T + t) / M::VECS, col = (i * T + t) % M::VECS;
+            *(reinterpret_cast<uint4 *>(m + row * M::ROW) + col) = v[i];
+        }
+    }
+};
+
+// What a part of a head is: its head, group and first column.
+struct Part { int head, group, col; };
+__device__ __forceinline__ Part part_of(const ScanArgs &a, int part) {
+    const int halves = a.d_head / kHeadPart;
+    Part p;
+    p.head = part / halves;
+    p.col = (part - p.head * halves) * kHeadPart;
+    p.group = p.head / (a.n_heads / a.n_groups);
+    return p;
+}
+// Element (0, 0) of a part's state in [sequence][head][d_state][d_head].
+template <int N> __device__ __forceinline__ int64_t state_at(const ScanArgs &a, int seq, const Part &p) {
+    return ((int64_t)seq * a.n_heads + p.head) * N * a.d_head + p.col;
+}
+
+} // namespace sqk
