@@ -158,7 +158,7 @@ sq_status check_scan(const sq_scan_desc *d, bool batch) {
     return SQ_OK;
 }
 size_t scan_work(const sqk::ScanPlan &p, bool train) {
-    return (size_t)(p.state_bytes + p.fade_bytes + (train ? p.save_bytes + p.group_bytes + p.head_bytes : 0));
+    return (size_t)(p.state_bytes + p.fade_bytes + (train ? p.save_bytes + p.group_bytes + p.dots_bytes + p.head_bytes : 0));
 }
 sqk::ScanArgs scan_args(const sq_scan_desc *d, const int32_t *cu, const void *x, const void *raw, const float *A, const void *B, const void *C,
                         const float *D, const float *bias, void *work) {
@@ -180,7 +180,9 @@ sqk::ScanArgs scan_args(const sq_scan_desc *d, const int32_t *cu, const void *x,
         a.seg_fade = reinterpret_cast<float *>(base += p.state_bytes);
         a.grad_save = base += p.fade_bytes;
         a.group_part = reinterpret_cast<float *>(base += p.save_bytes);
-        a.head_part = reinterpret_cast<float *>(base += p.group_bytes);
+        a.dots = reinterpret_cast<float *>(base += p.group_bytes);
+        a.head_part = reinterpret_cast<float *>(base += p.dots_bytes);
+        a.chunk_parts = p.chunk_slots * p.parts;
         a.subsets = p.subsets;
     }
     return a;

@@ -18,7 +18,7 @@ struct ScanArgs {
     int32_t n_heads, n_groups, d_head, softplus;  // d_head: 64 or 128
     int32_t seg_shift, segments;  // log2 of a segment's tokens; segments: more than one to some sequence
     float *seg_state, *seg_fade;  // [segment slot][part of a head]: states at the segments' starts, decays over them
-    uint8_t *save, *grad_save;    // [chunk slot][part]: states at the chunks' starts; their gradients at the chunks' ends
+    uint8_t *save, *grad_save;    // [chunk slot][part][d_state][64] fp32: states at the chunks' starts; their gradients at the chunks' ends
     // backward
     const void *dy;
     const float *dS_out;
@@ -27,6 +27,8 @@ struct ScanArgs {
     int64_t dx_stride, ddt_stride, db_stride, dc_stride;
     int32_t subsets;              // of a group's heads, a workgroup each
     float *group_part;            // [2][subsets][n_tokens][n_groups][d_state]: dB and dC of a subset (subsets > 1)
+    float *dots;                  // [2][chunk slot][part][64]: what the pass back leaves of x's dots with U
+    int64_t chunk_parts;          // chunk slots x parts
     float *head_part;             // [3][chunk slots][n_heads]: sums over a chunk of dA, dbias and dD
     // step
     float *pool;
@@ -39,7 +41,7 @@ struct ScanArgs {
 // then come from a pass that forms states alone (about half the work of the whole).
 struct ScanPlan {
     int seg_shift, subsets;
-    int64_t parts, seg_slots, chunk_slots, state_bytes, fade_bytes, save_bytes, group_bytes, head_bytes;
+    int64_t parts, seg_slots, chunk_slots, state_bytes, fade_bytes, save_bytes, group_bytes, dots_bytes, head_bytes;
 };
 ScanPlan scan_plan(const sq_scan_desc &d);
 
@@ -61,6 +63,22 @@ struct Gates {
     float out[64];         // e^{G_end - G}: from a token to the chunk's end
 };
 __device__ __forceinline__ float decay_of(const Gates &g, int i, int j) { return exp_of((g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j])); }
+
+// Sums over 16 neighbouring lanes, to all of them, by rotations within the row; and over all 64.
+template <int N> __device__ __forceinline__ float rotated(float x) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + N, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_sum(float x) {
+    x += rotated<8>(x);
+    x += rotated<4>(x);
+    x += rotated<2>(x);
+    return x + rotated<1>(x);
+}
+// ... over lanes 16 apart
+__device__ __forceinline__ float rows_sum(float x) {
+    x += __shfl_xor(x, 16, 64);
+    return x + __shfl_xor(x, 32, 64);
+}
 
 // Inclusive sums over the lanes of a wave.
 __device__ __forceinline__ double wave_scan(double v, int l) {
@@ -110,6 +128,11 @@ template <bool F32, int COLS> struct TokenMat {
     }
 };
 
+template <bool F32> __device__ __forceinline__ f4 load4(const Elem<F32> *p) {
+    if constexpr (F32) return *reinterpret_cast<const f4 *>(p);
+    else return __builtin_convertvector(*reinterpret_cast<const bf4 *>(p), f4);
+}
+
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4v lds_s4v;
 // A fragment of the transposed matrix: row (lane) l % 16 is column col0 + l % 16 of m, contracted elements
@@ -139,6 +162,11 @@ __device__ __forceinline__ void pair_tile(int n, int &it, int &jt) {
     jt = n - it * (it + 1) / 2;
 }
 
+// The bf16 matrix instructions round sums downwards, about 2^-25 on average: nothing next to a result, but the
+// same way for all tokens and rows, so that it shows in sums over many (dbias 2e-6 off for 3e-7).  What such sums are
+// formed from is therefore computed with the other sign for every second tile of 16 tokens or rows of the state.
+__device__ __forceinline__ float sign_of(int tile) { return tile & 1 ? -1.f : 1.f; }
+
 // Vectors of a token matrix as a workgroup of T threads loads them: from memory into
 // registers, rows behind the last as zeros, and from there into LDS.
 template <bool F32, int COLS, int T> struct Staged {
@@ -153,11 +181,14 @@ template <bool F32, int COLS, int T> struct Staged {
             v[i] = row < rows ? *p : uint4{};
         }
     }
-    __device__ __forceinline__ void store(Elem<F32> *m, int t) const {
+    // TURN_ROWS, TURN_COLS: rows and columns 16 .. 31, 48 .. 63, ... with their signs turned, see sign_of
+    template <bool TURN_ROWS = false, bool TURN_COLS = false> __device__ __forceinline__ void store(Elem<F32> *m, int t) const {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
             const int row = (i * T + t) / M::VECS, col = (i * T + t) % M::VECS;
-            *(reinterpret_cast<uint4 *>(m + row * M::ROW) + col) = v[i];
+            const int turned = (TURN_ROWS ? row : 0) ^ (TURN_COLS ? col * 16 / (int)sizeof(Elem<F32>) : 0);
+            const uint32_t flip = turned & 16 ? (F32 ? 0x80000000u : 0x80008000u) : 0u;
+            *(reinterpret_cast<uint4 *>(m + row * M::ROW) + col) = uint4{v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip};
         }
     }
 };

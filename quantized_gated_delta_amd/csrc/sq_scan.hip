@@ -11,8 +11,10 @@
 // A workgroup walks one segment of one sequence for 64 columns of one head.  Where sequences are
 // cut (scan_plan), a first pass forms each segment's own state, a second one walks the segments
 // (S = e^{G} S + own), and the main pass starts from those.
-// The gradients' pass back over the chunks is the same recurrence with C, dy and e^G for B, x and
-// e^{G_end - G} dt, from the last chunk to the first.
+// The gradients' pass back over the chunks is the same with C, dy and e^G for B, x and e^{G_end - G} dt, from the
+// last chunk to the first, and what it reads with B is x's gradient: with dS the gradient of the state at a chunk's end,
+//   U_j = sum_{i >= j} (C_i . B_j) L_ij dy_i + e^{G_end - G_j} dS^T B_j,   dx_j = D dy_j + dt_j U_j
+// It leaves dS, and the dots of x_j with U_j and with its second part, for the other gradients (sq_scan_bwd.hip).
 #include "sq_scan.h"
 
 namespace sqk {
@@ -20,19 +22,24 @@ namespace {
 
 // What a pass over the chunks does: form a segment's own state; form y; the same two backwards.
 enum Pass { kOwn, kMain, kOwnBack, kMainBack };
+constexpr int kGates = 4;  // chunks whose gates are formed at once, one by each wave
 
-template <int N, bool F32, int NTY, bool YF32, int PASS> __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a) {
+// The main passes, forwards and (in brackets) backwards.  The state takes up the keys K = B [C] with the
+// columns X = x [dy], and is read by the queries Q = C [B]; a query meets the keys of its own
+// chunk up to [from] its own place in `pairs`.  NT: terms that the results are accurate to.
+template <int N, bool F32, int NT, bool YF32, int PASS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void scan_kernel(ScanArgs a) {
     typedef Elem<F32> E;
-    constexpr bool BACK = PASS >= kOwnBack, Y = PASS == kMain, OWN = PASS == kOwn || PASS == kOwnBack;
+    constexpr bool BACK = PASS >= kOwnBack, READ = PASS == kMain || PASS == kMainBack;
     constexpr int MT = N / 16, KB = N / 32;
     typedef TokenMat<F32, N> KeyMat;
     typedef TokenMat<F32, kHeadPart> XMat;
-    typedef LdsMat<F32, NTY, 64, 64> PairMat;
+    typedef LdsMat<F32, NT, 64, 64> PairMat;
     __shared__ __attribute__((aligned(16))) E sK[KeyMat::SIZE], sX[XMat::SIZE];
-    __shared__ __attribute__((aligned(16))) E sC[Y ? KeyMat::SIZE : 8];
-    __shared__ __attribute__((aligned(16))) uint8_t sP[Y ? PairMat::BYTES : 16];
-    __shared__ Gates gates[2];
-    __shared__ __attribute__((aligned(16))) float sTurn[OWN ? 4 : 4 * 320];
+    __shared__ __attribute__((aligned(16))) E sQ[READ ? KeyMat::SIZE : 8];
+    __shared__ __attribute__((aligned(16))) E pairs[READ ? PairMat::BYTES / sizeof(E) : 8];  // [query][key]
+    __shared__ Gates gates[kGates];
+    __shared__ float dots[2][PASS == kMainBack ? 4 : 1][64];
 
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
     // the heads of a group read the same B and C: workgroups go to the 8 XCDs in turn, and each
@@ -46,114 +53,132 @@ template <int N, bool F32, int NTY, bool YF32, int PASS> __global__ __launch_bou
     if (b.seq < 0) return;
     const Part pt = part_of(a, part);
     const int begin = b.c << a.seg_shift, len = min(b.len - begin, 1 << a.seg_shift), n_chunks = (len + 63) >> 6;
-    const bool last = begin + (1 << a.seg_shift) >= b.len;
     const int64_t t0 = (int64_t)b.t0 + begin, at = state_at<N>(a, b.seq, pt);
     const int64_t chunk0 = ((int64_t)(b.t0 >> 6) + b.seq + (begin >> 6)) * parts + part;  // + c * parts
     float *seg = a.seg_state + (slot * parts + part) * N * kHeadPart;
 
+    // the state: a wave has 16 columns, a lane rows 16 m + 4 (l / 16) .. + 3 of column l % 16, times sign_of(m)
     f4 S[MT];
-    const float *from = OWN ? nullptr : a.segments ? seg : (BACK ? a.dS_out : a.S0);
     {
+        const float *start = BACK ? a.dS_out : a.S0, *p = !READ ? nullptr : a.segments ? seg : start ? start + at : nullptr;
         const int64_t row = a.segments ? kHeadPart : a.d_head;
-        const float *p = from ? (a.segments ? from : from + at) : nullptr;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[m][i] = p ? p[(16 * m + g4 + i) * row + 16 * w + r] : 0.f;
+            for (int i = 0; i < 4; ++i) S[m][i] = p ? sign_of(m) * p[(16 * m + g4 + i) * row + 16 * w + r] : 0.f;
     }
-    const float A = a.A[pt.head], bias = a.bias ? a.bias[pt.head] : 0.f, D = Y && a.D ? a.D[pt.head] : 0.f;
-    const void *keys = BACK ? a.C : a.B, *xs = BACK ? a.dy : a.x;
-    const int64_t key_stride = BACK ? a.c_stride : a.b_stride, x_stride = BACK ? (int64_t)a.n_heads * a.d_head : a.x_stride;
+    const float A = a.A[pt.head], bias = a.bias ? a.bias[pt.head] : 0.f, D = READ && a.D ? a.D[pt.head] : 0.f;
+    const int64_t y_stride = (int64_t)a.n_heads * a.d_head, column = (int64_t)pt.head * a.d_head + pt.col;
+    const int64_t k_stride = BACK ? a.c_stride : a.b_stride, q_stride = BACK ? a.b_stride : a.c_stride, x_stride = BACK ? y_stride : a.x_stride;
+    const E *pk = static_cast<const E *>(BACK ? a.C : a.B) + t0 * k_stride + (int64_t)pt.group * N;
+    const E *pq = static_cast<const E *>(BACK ? a.B : a.C) + t0 * q_stride + (int64_t)pt.group * N;
+    const E *px = static_cast<const E *>(BACK ? a.dy : a.x) + t0 * x_stride + column;
 
-    Staged<F32, N, 256> rK, rC;
-    Staged<F32, kHeadPart, 256> rX;
-    auto rows_of = [&](int c) { return min(64, len - c * 64); };
-    auto load = [&](int c) {
-        const int64_t tok = t0 + (int64_t)c * 64;
-        const int rows = rows_of(c);
-        rK.load(static_cast<const E *>(keys) + tok * key_stride + (int64_t)pt.group * N, key_stride, rows, t);
-        rX.load(static_cast<const E *>(xs) + tok * x_stride + (int64_t)pt.head * a.d_head + pt.col, x_stride, rows, t);
-        if (Y) rC.load(static_cast<const E *>(a.C) + tok * a.c_stride + (int64_t)pt.group * N, a.c_stride, rows, t);
-    };
-    auto load_raw = [&](int c) {
-        const int rows = rows_of(c);
-        return ld_elem<F32>(a.raw, (t0 + (int64_t)c * 64 + min(l, rows - 1)) * a.dt_stride + pt.head);
-    };
     const int first = BACK ? n_chunks - 1 : 0, step = BACK ? -1 : 1;
-    if (n_chunks > 0) {
-        load(first);
-        if (w == 0) make_gates(gates[0], l, l < rows_of(first), load_raw(first), bias, A, a.softplus);
-    }
-    if (Y) {  // the tiles beside the diagonal that a contraction over 32 tokens meets and no pair fills
-        if (w < 2) PairMat::put4(reinterpret_cast<E *>(sP), 32 * w + r, 32 * w + 16 + g4, f4{});
-    }
+    auto rows_of = [&](int c) { return min(64, len - c * 64); };
+    Staged<F32, N, 256> rK, rQ;
+    Staged<F32, kHeadPart, 256> rX;
+    auto load = [&](int c) {
+        const int rows = rows_of(c);
+        rK.load(pk + (int64_t)c * 64 * k_stride, k_stride, rows, t);
+        rX.load(px + (int64_t)c * 64 * x_stride, x_stride, rows, t);
+        if (READ) rQ.load(pq + (int64_t)c * 64 * q_stride, q_stride, rows, t);
+    };
+    // what wave w forms gates from: its chunk of the kGates from the k-th on
+    float raw = 0.f;
+    auto load_raw = [&](int k) {
+        if (k + w < n_chunks) {
+            const int c = first + (k + w) * step;
+            raw = ld_elem<F32>(a.raw, (t0 + (int64_t)c * 64 + min(l, rows_of(c) - 1)) * a.dt_stride + pt.head);
+        }
+    };
+    load_raw(0);
+    if (n_chunks > 0) load(first);
+    // tiles beside the diagonal that a contraction over 32 keys meets and no pair fills
+    if (READ && w < 2) PairMat::put4(pairs, 32 * w + (BACK ? 16 : 0) + r, 32 * w + (BACK ? 0 : 16) + g4, f4{});
     float fade = 1.f;
     for (int k = 0; k < n_chunks; ++k) {
         const int c = first + k * step, rows = rows_of(c);
-        const Gates &g = gates[k & 1];
-        rK.store(sK, t);
+        const Gates &g = gates[k % kGates];
+        // signs: the state's odd tiles of rows are turned, and so is what every second tile of queries reads
+        rK.template store<false, true>(sK, t);
         rX.store(sX, t);
-        if (Y) rC.store(sC, t);
+        if (READ) rQ.template store<true, true>(sQ, t);
+        if (k % kGates == 0 && k + w < n_chunks) make_gates(gates[w], l, l < rows_of(first + (k + w) * step), raw, bias, A, a.softplus);
         __syncthreads();
-        if (k + 1 < n_chunks) {
-            load(c + step);
-            if (w == (k & 3)) make_gates(gates[~k & 1], l, l < rows_of(c + step), load_raw(c + step), bias, A, a.softplus);
-        }
-        uint8_t *keep = BACK ? a.grad_save : a.save;
-        if (!OWN && keep) {
-            E *p = reinterpret_cast<E *>(keep + (chunk0 + (int64_t)c * parts) * N * kHeadPart * 4);
+        if (k % kGates == 0) load_raw(k + kGates);
+        if (k + 1 < n_chunks) load(c + step);
+        float *keep = reinterpret_cast<float *>(BACK ? a.grad_save : a.save);
+        if (READ && keep) {  // [row][column], fp32
+            keep += (chunk0 + (int64_t)c * parts) * N * kHeadPart;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                put_operand4<F32, kSaveTerms, 2>(p, 16 * m + r, 16 * w + g4, turn(sTurn + w * 320, S[m], l));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) keep[(16 * m + g4 + i) * kHeadPart + 16 * w + r] = sign_of(m) * S[m][i];
         }
-        if (Y) {
-            // pairs, as the operand of x: token i's row holds (C_i . B_j) L_ij dt_j
+        if (READ) {
             for (int n = w; n < 10; n += 4) {
-                int it, jt;
-                pair_tile(n, it, jt);
+                int hi, lo;
+                pair_tile(n, hi, lo);
+                const int kt = BACK ? hi : lo, qt = BACK ? lo : hi, q = 16 * qt + r;
                 f4 p{};
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-                    p = mma<1>(KeyMat::get(sK, 16 * jt + r, 32 * kb + g8), KeyMat::get(sC, 16 * it + r, 32 * kb + g8), p);
-                const int i = 16 * it + r;
+                for (int kb = 0; kb < KB; ++kb) p = mma<1>(KeyMat::get(sK, 16 * kt + r, 32 * kb + g8), KeyMat::get(sQ, q, 32 * kb + g8), p);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * jt + g4 + e;
-                    p[e] = j <= i ? p[e] * decay_of(g, i, j) * g.dt[j] : 0.f;
+                    const int key = 16 * kt + g4 + e;
+                    if (BACK) p[e] = key >= q ? p[e] * decay_of(g, key, q) : 0.f;
+                    else p[e] = key <= q ? p[e] * decay_of(g, q, key) * g.dt[key] : 0.f;
                 }
-                PairMat::put4(reinterpret_cast<E *>(sP), i, 16 * jt + g4, p);
+                PairMat::put4(pairs, q, 16 * kt + g4, p);
             }
             __syncthreads();
         }
         Frag<F32, 1> fx[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) fx[kb] = get_t<F32, 1>(sX, XMat::ROW, 0, 32 * kb, 16 * w, l);
-        if (Y) {
-            // transposed, y's columns as the result's rows: a lane then holds four neighbours of one token
+        if (READ) {
+            // transposed, the result's columns as its rows: a lane then holds four neighbours of one token
             f4 y[4] = {};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 float s[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[e] = S[2 * kb + e / 4][e % 4];
-                const Frag<F32, NTY> fs = make_frag<F32, NTY>(s);
+                const Frag<F32, NT> fs = make_frag<F32, NT>(s);
 #pragma unroll
-                for (int it = 0; it < 4; ++it) y[it] = mma<NTY>(fs, KeyMat::get_split(sC, 16 * it + r, 32 * kb + g4), y[it]);
+                for (int qt = 0; qt < 4; ++qt) y[qt] = mma<NT>(fs, KeyMat::get_split(sQ, 16 * qt + r, 32 * kb + g4), y[qt]);
             }
-            char *py = static_cast<char *>(a.y) + ((t0 + (int64_t)c * 64) * a.n_heads + pt.head) * a.d_head * (YF32 ? 4 : 2);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const int i = 16 * it + r;
-                y[it] *= g.in[i];
+            for (int qt = 0; qt < 4; ++qt) {
+                const int q = 16 * qt + r;
+                const int64_t tok = t0 + (int64_t)c * 64 + q;
+                y[qt] *= BACK ? g.out[q] : g.in[q];
+                const f4 own = load4<F32>(sX + q * XMat::ROW + 16 * w + g4);
+                f4 x{};
+                float z = 0.f, u = 0.f;
+                if (BACK) {
+                    if (q < rows) x = load4<F32>(static_cast<const E *>(a.x) + tok * a.x_stride + column + 16 * w + g4);
+                    z = sign_of(qt) * ((x[0] * y[qt][0] + x[1] * y[qt][1]) + (x[2] * y[qt][2] + x[3] * y[qt][3]));
+                }
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
-                    if (kb == 0 || it >= 2) y[it] = mma<NTY>(fx[kb], PairMat::get(reinterpret_cast<E *>(sP), i, 32 * kb + g8), y[it]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[it][e] = fmaf(D, ld_elem<F32>(sX, i * XMat::ROW + 16 * w + g4 + e), y[it][e]);
-                if (i < rows) st_elem4<YF32>(py, (int64_t)i * a.n_heads * a.d_head + pt.col + 16 * w + g4, y[it]);
+                    if (BACK ? kb == 1 || qt < 2 : kb == 0 || qt >= 2) y[qt] = mma<NT>(fx[kb], PairMat::get(pairs, q, 32 * kb + g8), y[qt]);
+                y[qt] *= sign_of(qt);
+                if (BACK) {
+                    u = (x[0] * y[qt][0] + x[1] * y[qt][1]) + (x[2] * y[qt][2] + x[3] * y[qt][3]);
+                    z = rows_sum(z), u = rows_sum(u);
+                    if (l < 16) dots[0][w][q] = z * g.dt[q], dots[1][w][q] = u;
+                    y[qt] *= g.dt[q];
+                }
+                y[qt] += own * D;
+                if (q < rows) {
+                    if (BACK) st_elem4<F32>(a.dx, tok * a.dx_stride + column + 16 * w + g4, y[qt]);
+                    else st_elem4<YF32>(a.y, tok * y_stride + column + 16 * w + g4, y[qt]);
+                }
             }
         }
-        // the state: the scaled x as the right operand, three terms, so that the state has fp32 accuracy
+        // the state: the scaled X as the right operand, three terms, so that the state has fp32 accuracy
         Frag<F32, 3> fs[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -175,17 +200,20 @@ template <int N, bool F32, int NTY, bool YF32, int PASS> __global__ __launch_bou
             for (int kb = 0; kb < 2; ++kb) S[m] = mma<3>(get_t<F32, 1>(sK, KeyMat::ROW, 0, 32 * kb, 16 * m, l), fs[kb], S[m]);
         }
         __syncthreads();
+        if (PASS == kMainBack && w < 2)  // 0: z, 1: u
+            a.dots[(w * a.chunk_parts + chunk0 + (int64_t)c * parts) * 64 + l] = (dots[w][0][l] + dots[w][1][l]) + (dots[w][2][l] + dots[w][3][l]);
     }
-    float *to = OWN ? seg : BACK ? (b.c == 0 ? a.dS0 : nullptr) : (last ? a.S_out : nullptr);
+    const bool end = BACK ? b.c == 0 : begin + (1 << a.seg_shift) >= b.len;
+    float *to = !READ ? seg : !end ? nullptr : BACK ? a.dS0 : a.S_out;
     if (to) {
-        const int64_t row = OWN ? kHeadPart : a.d_head;
-        if (!OWN) to += at;
+        const int64_t row = READ ? a.d_head : kHeadPart;
+        if (READ) to += at;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) to[(16 * m + g4 + i) * row + 16 * w + r] = S[m][i];
+            for (int i = 0; i < 4; ++i) to[(16 * m + g4 + i) * row + 16 * w + r] = sign_of(m) * S[m][i];
     }
-    if (OWN && t == 0) a.seg_fade[slot * parts + part] = fade;
+    if (!READ && t == 0) a.seg_fade[slot * parts + part] = fade;
 }
 
 // States at the segments' starts (BACK: their gradients at the segments' ends) in the place of the segments' own.
@@ -210,9 +238,9 @@ template <int N, bool BACK> __global__ __launch_bounds__(256) void join_kernel(S
     }
 }
 
-template <int N, bool F32, int NTY, bool YF32, int PASS> hipError_t launch_pass(const ScanArgs &a, hipStream_t stream) {
+template <int N, bool F32, int NT, bool YF32, int PASS> hipError_t launch_pass(const ScanArgs &a, hipStream_t stream) {
     const int64_t parts = (int64_t)a.n_heads * (a.d_head / kHeadPart), slots = block_slots(a.seqs.n_tokens, a.seqs.n_seq, a.seg_shift);
-    hipLaunchKernelGGL((scan_kernel<N, F32, NTY, YF32, PASS>), dim3((uint32_t)((parts + 7) / 8 * 8 * slots)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((scan_kernel<N, F32, NT, YF32, PASS>), dim3((uint32_t)((parts + 7) / 8 * 8 * slots)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 template <int N, bool BACK> hipError_t launch_join(const ScanArgs &a, hipStream_t stream) {
@@ -228,7 +256,7 @@ template <int N, bool F32, bool YF32> hipError_t forward(const ScanArgs &a, hipS
 template <int N, bool F32> hipError_t back(const ScanArgs &a, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (a.segments && ((e = launch_pass<N, F32, 2, false, kOwnBack>(a, stream)) != hipSuccess || (e = launch_join<N, true>(a, stream)) != hipSuccess)) return e;
-    return launch_pass<N, F32, 2, false, kMainBack>(a, stream);
+    return launch_pass<N, F32, 3, false, kMainBack>(a, stream);
 }
 
 // One token of one head a workgroup; a thread has 4 columns of every 16th (d_head 128: 8th) row.  Bound by memory: the
@@ -308,6 +336,7 @@ ScanPlan scan_plan(const sq_scan_desc &d) {
     p.subsets = 1;
     while (p.subsets * 2 <= share && units * p.subsets < 512) p.subsets *= 2;
     p.group_bytes = (rows < 1024 * 64 ? rows : 1024 * 64) * d.d_state * 2 * 4;
+    p.dots_bytes = 2 * 4 * 64 * p.chunk_slots * p.parts;
     p.head_bytes = (3 * 4 * p.chunk_slots * d.n_heads + 255) / 256 * 256;
     return p;
 }
