@@ -61,66 +61,77 @@ __device__ __forceinline__ Block block_at(const Ragged &a, int64_t x, int shift)
     return b;
 }
 
-// ------------------------------------------------------------------ vectors of 8 elements
-// What 8 elements are loaded as: one or two vectors of 16 bytes.
-template <bool F32> struct Raw8 { uint4 v[F32 ? 2 : 1]; };
+// ------------------------------------------------------------------ vectors of elements
+// What N elements (4 or 8) are loaded as.
+template <bool F32, int N> struct Raw { uint32_t v[N * (F32 ? 4 : 2) / 4]; };
+template <bool F32> using Raw8 = Raw<F32, 8>;
 
-// Elements i .. i + 7 of p.  VEC: 16-byte loads (aligned, all 8 inside); otherwise element by
+// Elements i .. i + N - 1 of p.  VEC: 16-byte loads (8 bytes for 4 of bf16; aligned, all inside); otherwise element by
 // element, those from `left` on as zeros.
-template <bool F32, bool VEC> __device__ __forceinline__ Raw8<F32> load8(const void *p, int64_t i, int left) {
-    Raw8<F32> r;
+template <bool F32, bool VEC, int N> __device__ __forceinline__ Raw<F32, N> load_n(const void *p, int64_t i, int left) {
+    Raw<F32, N> r;
+    constexpr int WORDS = sizeof(r.v) / 4;
     if constexpr (VEC) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const Elem<F32> *>(p) + i);
-        r.v[0] = q[0];
-        if constexpr (F32) r.v[1] = q[1];
-    } else {
-        uint32_t x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = e < left ? ld_raw<F32>(p, i + e) : 0u;
-        if constexpr (F32) {
-            r.v[0] = uint4{x[0], x[1], x[2], x[3]};
-            r.v[1] = uint4{x[4], x[5], x[6], x[7]};
+        const Elem<F32> *q = static_cast<const Elem<F32> *>(p) + i;
+        if constexpr (WORDS == 2) {
+            *reinterpret_cast<uint2 *>(r.v) = *reinterpret_cast<const uint2 *>(q);
         } else {
-            r.v[0] = uint4{x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16};
+#pragma unroll
+            for (int k = 0; k < WORDS; k += 4) *reinterpret_cast<uint4 *>(r.v + k) = reinterpret_cast<const uint4 *>(q)[k / 4];
         }
+    } else {
+        uint32_t x[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = e < left ? ld_raw<F32>(p, i + e) : 0u;
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) r.v[k] = F32 ? x[k] : x[2 * k] | x[2 * k + 1] << 16;
     }
     return r;
 }
-template <bool F32> __device__ __forceinline__ void widen8(const Raw8<F32> &r, float (&x)[8]) {
-    if constexpr (F32) {
+template <bool F32, int N> __device__ __forceinline__ void widen_n(const Raw<F32, N> &r, float (&x)[N]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            x[4 * h] = __uint_as_float(r.v[h].x), x[4 * h + 1] = __uint_as_float(r.v[h].y);
-            x[4 * h + 2] = __uint_as_float(r.v[h].z), x[4 * h + 3] = __uint_as_float(r.v[h].w);
-        }
-    } else {
-        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int e = 0; e < N; ++e) x[e] = __uint_as_float(F32 ? r.v[e] : e & 1 ? r.v[e / 2] & 0xffff0000u : r.v[e / 2] << 16);
 }
-template <bool F32, bool VEC> __device__ __forceinline__ void store8(void *p, int64_t i, const float (&x)[8], int left) {
+template <bool F32, bool VEC, int N> __device__ __forceinline__ void store_n(void *p, int64_t i, const float (&x)[N], int left) {
     if constexpr (VEC) {
-        if constexpr (F32) {
-            f4 *q = reinterpret_cast<f4 *>(static_cast<float *>(p) + i);
-            q[0] = f4{x[0], x[1], x[2], x[3]};
-            q[1] = f4{x[4], x[5], x[6], x[7]};
-        } else {
-            *reinterpret_cast<bf8 *>(static_cast<__bf16 *>(p) + i) = make_frag<false, 1>(x).t[0];
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            const f4 v{x[k], x[k + 1], x[k + 2], x[k + 3]};
+            if constexpr (F32 || N == 4) st_elem4<F32>(p, i + k, v);
         }
+        if constexpr (!F32 && N == 8) *reinterpret_cast<bf8 *>(static_cast<__bf16 *>(p) + i) = make_frag<false, 1>(x).t[0];
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < N; ++e)
             if (e < left) st_elem<F32>(p, i + e, x[e]);
     }
 }
+template <bool F32, bool VEC> __device__ __forceinline__ Raw8<F32> load8(const void *p, int64_t i, int left) { return load_n<F32, VEC, 8>(p, i, left); }
+template <bool F32> __device__ __forceinline__ void widen8(const Raw8<F32> &r, float (&x)[8]) { widen_n<F32, 8>(r, x); }
+template <bool F32, bool VEC> __device__ __forceinline__ void store8(void *p, int64_t i, const float (&x)[8], int left) { store_n<F32, VEC, 8>(p, i, x, left); }
+
+// ------------------------------------------------------------------ sums over lanes
+// Sums over 16 neighbouring lanes, to all of them, by rotations within the row; and over all 64.
+template <int N> __device__ __forceinline__ float rotated(float x) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + N, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_sum(float x) {
+    x += rotated<8>(x);
+    x += rotated<4>(x);
+    x += rotated<2>(x);
+    return x + rotated<1>(x);
+}
+// ... over lanes 16 apart
+__device__ __forceinline__ float rows_sum(float x) {
+    x += __shfl_xor(x, 16, 64);
+    return x + __shfl_xor(x, 32, 64);
+}
 
 // ------------------------------------------------------------------ activations
-// 1 / (1 + e^-z): the hardware reciprocal (1 unit) of an exponential of 2^-22.  The exponential's
-// argument is held inside [-150, 88], where it is finite: above, the result is 6e-39.
+// 1 / (1 + e^-z), by the hardware's exponential and reciprocal.  The exponential's argument is rounded, which
+// is |z| 2^-24 of e^-z, and so less than 2^-26 of the result for any z; infinities give 0 and 1, a NaN stays one.
 __device__ __forceinline__ float sigmoid_of(float z) {
-    const float t = z < -88.f ? 88.f : z > 150.f ? -150.f : -z;  // a NaN stays one
-    return __builtin_amdgcn_rcpf(1.f + exp_of(t));
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z));
 }
 // act(z) and its derivative; none: 1 and 0 (no gate).
 __device__ __forceinline__ float gate_of(int act, float z) {
@@ -179,8 +190,8 @@ hipError_t launch_gate_backward(const GateArgs &a, bool f32, bool vec, bool firs
 hipError_t launch_residual_forward(const ResidualArgs &a, bool f32, bool res_f32, bool vec, hipStream_t stream);
 hipError_t launch_residual_backward(const ResidualArgs &a, bool f32, bool res_f32, bool vec, hipStream_t stream);
 
-// column[j] = sum over i of part[i][j], i ascending within each of a workgroup's lanes: the
-// second half of every gradient that is a sum over tokens.
+// out[j] = sum over i of part[i][j], in a fixed order: the second half of every gradient that is a sum
+// over tokens.
 struct SumArgs {
     const float *part;
     float *out;

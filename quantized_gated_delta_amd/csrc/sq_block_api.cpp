@@ -255,7 +255,7 @@ sq_status sq_conv_forward(const sq_conv_desc *desc, const int32_t *cu, const voi
     if (debug_slots() && (st = check_sequences(desc->n_seq, desc->n_tokens, cu, stream))) return st;
     sqk::ConvArgs a = conv_args(desc, cu, x, weight, bias);
     a.S0 = S0; a.y = y; a.S_out = S_out;
-    const void *const p[] = {x, S0, y, S_out};
+    const void *const p[] = {x, S0, y, S_out, weight};
     const hipError_t err = sqk::launch_conv_forward(a, desc->dtype == SQ_F32, vectors(desc->dtype, c, xs, p), stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "conv_forward launch");
 }
@@ -280,7 +280,7 @@ sq_status sq_conv_backward(const sq_conv_desc *desc, const int32_t *cu, const vo
     sqk::ConvArgs a = conv_args(desc, cu, x, weight, bias);
     a.S0 = S0; a.dy = dy; a.dS_out = dS_out; a.dx = dx; a.dweight = dweight; a.dbias = dbias; a.dS0 = dS0;
     a.partial = static_cast<float *>(work);
-    const void *const p[] = {x, S0, dy, dS_out, dx, dS0};
+    const void *const p[] = {x, S0, dy, dS_out, dx, dS0, weight};
     const hipError_t err = sqk::launch_conv_backward(a, desc->dtype == SQ_F32, vectors(desc->dtype, c, xs, p), stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "conv_backward launch");
 }
@@ -292,7 +292,6 @@ sq_status sq_conv_step(const sq_conv_desc *desc, void *pool, int32_t n_slots, co
     if (n == 0) return SQ_OK;
     const int e = size_of(desc->dtype);
     const int64_t c = desc->n_channels, xs = stride_or(desc->x_stride, c);
-    if ((int64_t)n * ((c + 7) / 8) > 0x7FFFFFFFll) return fail(SQ_EUNSUPPORTED, "n * n_channels exceeds the grid limit");
     const Arg args[] = {{kx, x, true, false, n, c * e, xs * e, (uintptr_t)e}, dense("weight", weight, true, false, c * desc->width * 4, 4),
                         dense("bias", bias, false, false, c * 4, 4), dense("pool", pool, true, true, (int64_t)n_slots * (desc->width - 1) * c * e, e),
                         dense(ky, y, true, true, n * c * e, e), dense("slot_idx", slot_idx, true, false, 4ll * n, 4)};
@@ -300,7 +299,7 @@ sq_status sq_conv_step(const sq_conv_desc *desc, void *pool, int32_t n_slots, co
     if (debug_slots() && (st = check_slot_list(slot_idx, n, n_slots, true, stream))) return st;
     sqk::ConvArgs a = conv_args(desc, nullptr, x, weight, bias);
     a.pool = pool; a.slot = slot_idx; a.n = n; a.n_slots = n_slots; a.y = y;
-    const void *const p[] = {x, pool, y};
+    const void *const p[] = {x, pool, y, weight};
     const hipError_t err = sqk::launch_conv_step(a, desc->dtype == SQ_F32, vectors(desc->dtype, c, xs, p), stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "conv_step launch");
 }
@@ -419,7 +418,7 @@ sq_status sq_gated_norm_forward(const sq_gated_norm_desc *desc, const void *x, c
     if ((st = check_args(args, same))) return st;
     sqk::GateArgs a = gate_args(desc, x, z, weight);
     a.y = y;
-    const void *const p[] = {x, z, y};
+    const void *const p[] = {x, z, y, weight};
     const bool vec = vectors(desc->dtype, desc->d, xs, p) && (zs * e) % 16 == 0;
     const hipError_t err = sqk::launch_gate_forward(a, desc->dtype == SQ_F32, vec, desc->gate_first && gate, desc->shared_weight, stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "gated_norm_forward launch");
@@ -443,7 +442,7 @@ sq_status sq_gated_norm_backward(const sq_gated_norm_desc *desc, const void *x, 
     if ((st = check_args(args, same)) || (dweight && (st = check_work("work", work, work_bytes, need)))) return st;
     sqk::GateArgs a = gate_args(desc, x, z, weight);
     a.dy = dy; a.dx = dx; a.dz = dz; a.dweight = dweight; a.partial = static_cast<float *>(work);
-    const void *const p[] = {x, z, dy, dx, dz};
+    const void *const p[] = {x, z, dy, dx, dz, weight};
     const bool vec = vectors(desc->dtype, desc->d, xs, p) && (zs * e) % 16 == 0 && (dxs * e) % 16 == 0 && (dzs * e) % 16 == 0;
     const hipError_t err = sqk::launch_gate_backward(a, desc->dtype == SQ_F32, vec, desc->gate_first && gate, desc->shared_weight, stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "gated_norm_backward launch");
@@ -473,7 +472,7 @@ sq_status sq_residual_norm_forward(const sq_residual_norm_desc *desc, const void
     sqk::ResidualArgs a{};
     a.o = o; a.r = r; a.post = post_weight; a.scale = scale; a.weight = weight; a.r_out = r_out; a.h = h;
     a.n_rows = n; a.d = desc->d; a.eps = desc->eps;
-    const void *const p[] = {o, r, r_out, h};
+    const void *const p[] = {o, r, r_out, h, post_weight, scale, weight};
     const hipError_t err = sqk::launch_residual_forward(a, desc->dtype == SQ_F32, desc->res_dtype == SQ_F32, vectors(desc->dtype, d, 0, p), stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "residual_norm_forward launch");
 }
@@ -500,7 +499,7 @@ sq_status sq_residual_norm_backward(const sq_residual_norm_desc *desc, const voi
     a.o = o; a.r = r; a.post = post_weight; a.scale = scale; a.weight = weight; a.dh = dh; a.dr_out = dr_out;
     a.d_o = d_o; a.dr = dr; a.dpost = dpost_weight; a.dscale = dscale; a.dweight = dweight; a.partial = static_cast<float *>(work);
     a.n_rows = n; a.d = desc->d; a.eps = desc->eps;
-    const void *const p[] = {o, r, dh, dr_out, d_o, dr};
+    const void *const p[] = {o, r, dh, dr_out, d_o, dr, post_weight, scale, weight};
     const hipError_t err = sqk::launch_residual_backward(a, desc->dtype == SQ_F32, desc->res_dtype == SQ_F32, vectors(desc->dtype, d, 0, p), stream);
     return err == hipSuccess ? SQ_OK : hip_fail(err, "residual_norm_backward launch");
 }

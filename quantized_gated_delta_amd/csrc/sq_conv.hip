@@ -6,8 +6,9 @@
 //   db = sum_t dp[t];  dS0 is dx at the W - 1 places before the sequence.
 //
 // Bound by memory: one input and one output per element and a handful of operations.  A lane has 8
-// neighbouring channels (16 bytes of bf16) and walks a run of tokens with the last W - 1 inputs in
-// registers, so an input is read (W - 1 + run) / run times, and that by a lane of the same L2.
+// neighbouring channels (16 bytes of bf16; backwards 4, whose sums and windows leave room for four waves per SIMD) and walks a
+// run of tokens with the last W - 1 inputs in registers, so an input is read (W - 1 + run) / run times, and
+// that by a lane of the same L2.
 #include "sq_block.h"
 
 namespace sqk {
@@ -17,74 +18,92 @@ constexpr int kRunShift = 4, kRun = 1 << kRunShift;          // tokens of a lane
 constexpr int kBlockShift = kRunShift + 2;                   // ... of a workgroup's four waves
 constexpr int kBackShift = 5, kBackRun = 1 << kBackShift;    // backward
 constexpr int kBackBlockShift = kBackShift + 2;
+constexpr int kWide = 8, kNarrow = 4;                        // channels of a lane, forward and backward
+constexpr int kStepRows = 8;                                 // most requests of a lane in a step
 
 // Row `at` of sequence b as the convolution sees it: a token, a row of S0 before them, or zeros.
-template <bool F32, bool VEC, int W>
-__device__ __forceinline__ Raw8<F32> input_row(const ConvArgs &a, const Block &b, int at, int c0, int left) {
-    if (at >= 0) return load8<F32, VEC>(a.x, (int64_t)(b.t0 + at) * a.x_stride + c0, left);
-    if (a.S0) return load8<F32, VEC>(a.S0, ((int64_t)b.seq * (W - 1) + W - 1 + at) * a.channels + c0, left);
-    return Raw8<F32>{};
+template <bool F32, bool VEC, int W, int N>
+__device__ __forceinline__ Raw<F32, N> input_row(const ConvArgs &a, const Block &b, int at, int c0, int left) {
+    if (at >= 0) return load_n<F32, VEC, N>(a.x, (int64_t)(b.t0 + at) * a.x_stride + c0, left);
+    if (a.S0) return load_n<F32, VEC, N>(a.S0, ((int64_t)b.seq * (W - 1) + W - 1 + at) * a.channels + c0, left);
+    return Raw<F32, N>{};
 }
 
-template <int W> __device__ __forceinline__ void load_taps(const ConvArgs &a, int c0, int left, float (&w)[W][8], float (&bias)[8]) {
+// The taps and biases of a lane's channels.  Taps of neighbouring channels lie one after another: 16 bytes at a time.
+template <bool VEC, int W, int N> __device__ __forceinline__ void load_taps(const ConvArgs &a, int c0, int left, float (&w)[W][N], float (&bias)[N]) {
+    float flat[W * N];
+    const float *p = a.weight + (int64_t)c0 * W;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int i = 0; i < W * N; i += 4) {
+        if constexpr (VEC) {
+            *reinterpret_cast<f4 *>(flat + i) = *reinterpret_cast<const f4 *>(p + i);
+        } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = e < left ? a.weight[(int64_t)(c0 + e) * W + j] : 0.f;
+            for (int k = i; k < i + 4; ++k) flat[k] = k < left * W ? p[k] : 0.f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][e] = flat[e * W + j];
         bias[e] = a.bias && e < left ? a.bias[c0 + e] : 0.f;
     }
 }
 
 template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv_forward_kernel(ConvArgs a) {
+    constexpr int N = kWide;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
     const Block b = block_at(a.seqs, blockIdx.x, kBlockShift);
-    const int c0 = (blockIdx.y * 64 + l) * 8, left = a.channels - c0;
+    const int c0 = (blockIdx.y * 64 + l) * N, left = a.channels - c0;
     if (b.seq < 0 || left <= 0) return;
     const int first = (b.c << kBlockShift) + wave * kRun, last = min(first + kRun, b.len);
     const bool ends = wave == 0 && ((b.c + 1) << kBlockShift) >= b.len;  // the sequence's last block
     if (a.S_out && ends)
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
-            float v[8];
-            widen8<F32>(input_row<F32, VEC, W>(a, b, b.len - (W - 1) + i, c0, left), v);
-            store8<F32, VEC>(a.S_out, ((int64_t)b.seq * (W - 1) + i) * a.channels + c0, v, left);
+            float v[N];
+            widen_n<F32, N>(input_row<F32, VEC, W, N>(a, b, b.len - (W - 1) + i, c0, left), v);
+            store_n<F32, VEC, N>(a.S_out, ((int64_t)b.seq * (W - 1) + i) * a.channels + c0, v, left);
         }
     if (first >= last) return;
-    float w[W][8], bias[8], x[W][8];  // x: the input and those before it, the oldest first
-    load_taps<W>(a, c0, left, w, bias);
+    float w[W][N], bias[N], x[4][N];  // x: input t of a run lies in x[(t - first) % 4], so that no window moves
+    Raw<F32, N> before[W - 1];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) widen8<F32>(input_row<F32, VEC, W>(a, b, first - (W - 1) + j, c0, left), x[j]);
+    for (int k = 1; k < W; ++k) before[k - 1] = input_row<F32, VEC, W, N>(a, b, first - k, c0, left);
+    load_taps<VEC, W, N>(a, c0, left, w, bias);
+#pragma unroll
+    for (int k = 1; k < W; ++k) widen_n<F32, N>(before[k - 1], x[4 - k]);
     constexpr int kAhead = 8;  // loads in flight
     for (int t0 = first; t0 < last; t0 += kAhead) {
-        Raw8<F32> raw[kAhead];
+        Raw<F32, N> raw[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) raw[i] = load8<F32, VEC>(a.x, (int64_t)(b.t0 + min(t0 + i, last - 1)) * a.x_stride + c0, left);
+        for (int i = 0; i < kAhead; ++i) raw[i] = load_n<F32, VEC, N>(a.x, (int64_t)(b.t0 + min(t0 + i, last - 1)) * a.x_stride + c0, left);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            widen8<F32>(raw[i], x[W - 1]);
-            float y[8];
+            widen_n<F32, N>(raw[i], x[i & 3]);
+            float y[N];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < N; ++e) {
                 float p = bias[e];
 #pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(w[j][e], x[j][e], p);
+                for (int k = 0; k < W; ++k) p = fmaf(w[W - 1 - k][e], x[(i - k) & 3][e], p);
                 y[e] = a.silu ? gate_of(SQ_ACT_SILU, p) : p;
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) x[j][e] = x[j + 1][e];
             }
-            if (t0 + i < last) store8<F32, VEC>(a.y, (int64_t)(b.t0 + t0 + i) * a.channels + c0, y, left);
+            if (t0 + i < last) store_n<F32, VEC, N>(a.y, (int64_t)(b.t0 + t0 + i) * a.channels + c0, y, left);
         }
     }
 }
 
 // Every workgroup walks the blocks blockIdx.x, + gridDim.x, ... and leaves its sums of dw and db in
-// partial[blockIdx.x][channels][W + 1].
-template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a, int64_t slots) {
-    __shared__ float lds[64 * 8 * (W + 1)];
+// partial[blockIdx.x][W + 1][channels].
+template <bool F32, bool VEC, int W>
+__global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a, int64_t slots) {
+    constexpr int N = kNarrow;
+    __shared__ float lds[64 * N * (W + 1)];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
-    const int c0 = (blockIdx.y * 64 + l) * 8, left = a.channels - c0;
-    float w[W][8], bias[8], dw[W + 1][8] = {};
-    load_taps<W>(a, c0, left, w, bias);
+    const int c0 = (blockIdx.y * 64 + l) * N, left = a.channels - c0;
+    float w[W][N] = {}, bias[N] = {}, dw[W + 1][N] = {};
+    if (left > 0) load_taps<VEC, W, N>(a, c0, left, w, bias);
     for (int64_t slot = blockIdx.x; slot < slots; slot += gridDim.x) {
         const Block b = block_at(a.seqs, slot, kBackBlockShift);
         if (b.seq < 0) continue;
@@ -93,67 +112,76 @@ template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv
         if (first >= last && !begins) continue;
         if (left <= 0) continue;
         // gradient of input `at` (a token, or before them a row of S0), sum: what came through the taps
-        auto store = [&](int at, float (&sum)[8]) {
+        auto store = [&](int at, float (&sum)[N]) {
             const int row = at - (b.len - (W - 1));  // its row of S_out
             if (a.dS_out && row >= 0) {
-                float v[8];
-                widen8<F32>(load8<F32, VEC>(a.dS_out, ((int64_t)b.seq * (W - 1) + row) * a.channels + c0, left), v);
+                float v[N];
+                widen_n<F32, N>(load_n<F32, VEC, N>(a.dS_out, ((int64_t)b.seq * (W - 1) + row) * a.channels + c0, left), v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] += v[e];
+                for (int e = 0; e < N; ++e) sum[e] += v[e];
             }
-            if (at >= 0) store8<F32, VEC>(a.dx, (int64_t)(b.t0 + at) * a.channels + c0, sum, left);
-            else if (a.dS0) store8<F32, VEC>(a.dS0, ((int64_t)b.seq * (W - 1) + W - 1 + at) * a.channels + c0, sum, left);
+            if (at >= 0) store_n<F32, VEC, N>(a.dx, (int64_t)(b.t0 + at) * a.channels + c0, sum, left);
+            else if (a.dS0) store_n<F32, VEC, N>(a.dS0, ((int64_t)b.seq * (W - 1) + W - 1 + at) * a.channels + c0, sum, left);
         };
-        // x: inputs t - W + 1 .. t; d: dp of t - W + 1 .. t, as far as they are known
-        float x[W][8], d[W][8] = {};
+        // x, d: input and dp of token t of the run in [(t - first) % 4], so that no window moves
+        float x[4][N], d[4][N] = {};
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) widen8<F32>(input_row<F32, VEC, W>(a, b, first - (W - 1) + j, c0, left), x[j]);
+        for (int k = 1; k < W; ++k) widen_n<F32, N>(input_row<F32, VEC, W, N>(a, b, first - k, c0, left), x[4 - k]);
+        Raw<F32, N> rx[4] = {}, ry[4] = {};
+        auto load = [&](int t0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = min(t0 + i, b.len - 1);  // past the end: not used
+                if (b.len > 0) {
+                    rx[i] = load_n<F32, VEC, N>(a.x, (int64_t)(b.t0 + t) * a.x_stride + c0, left);
+                    ry[i] = load_n<F32, VEC, N>(a.dy, (int64_t)(b.t0 + t) * a.channels + c0, left);
+                }
+            }
+        };
+        // four tokens from t0 on.  WHOLE: all of the run, none among its first W - 1, so that what they reach is the run's too
+        auto four = [&](int t0, int stop, auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            Raw<F32, N> cx[4], cy[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cx[i] = rx[i], cy[i] = ry[i];
+            if (t0 + 4 < stop) load(t0 + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = t0 + i;
+                if (!WHOLE && t >= stop) break;
+                float dy[N], sum[N];
+                widen_n<F32, N>(cx[i], x[i]);
+                widen_n<F32, N>(cy[i], dy);
+                const bool inside = WHOLE || t < b.len, mine = WHOLE || t < last;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    float p = bias[e], value, slope = 1.f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) p = fmaf(w[W - 1 - k][e], x[(i - k) & 3][e], p);
+                    if (a.silu) gate_and_slope(SQ_ACT_SILU, p, value, slope);
+                    d[i][e] = inside ? dy[e] * slope : 0.f;
+                    if (mine) {
+#pragma unroll
+                        for (int k = 0; k < W; ++k) dw[W - 1 - k][e] = fmaf(d[i][e], x[(i - k) & 3][e], dw[W - 1 - k][e]);
+                        dw[W][e] += d[i][e];
+                    }
+                    // input t - W + 1 has all its dp now: that of k tokens before t meets tap k
+                    sum[e] = 0.f;
+#pragma unroll
+                    for (int k = W - 1; k >= 0; --k) sum[e] = fmaf(w[k][e], d[(i - k) & 3][e], sum[e]);
+                }
+                const int at = t - (W - 1);
+                if (WHOLE || at >= first || begins) store(at, sum);
+            }
+        };
         // dp of the W - 1 tokens behind the run reaches its last inputs; the first run also has the
         // inputs before the sequence
-        constexpr int kAhead = 4;
         const int stop = last + W - 1;
-        for (int t0 = first; t0 < stop; t0 += kAhead) {
-            Raw8<F32> rx[kAhead] = {}, ry[kAhead] = {};
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int t = t0 + i;
-                if (t < b.len && t < stop) {
-                    rx[i] = load8<F32, VEC>(a.x, (int64_t)(b.t0 + t) * a.x_stride + c0, left);
-                    ry[i] = load8<F32, VEC>(a.dy, (int64_t)(b.t0 + t) * a.channels + c0, left);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int t = t0 + i;
-                if (t < stop) {
-                    float dy[8], sum[8];
-                    widen8<F32>(rx[i], x[W - 1]);
-                    widen8<F32>(ry[i], dy);
-                    const bool inside = t < b.len, mine = t < last;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float p = bias[e], value, slope = 1.f;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) p = fmaf(w[j][e], x[j][e], p);
-                        if (a.silu) gate_and_slope(SQ_ACT_SILU, p, value, slope);
-                        d[W - 1][e] = inside ? dy[e] * slope : 0.f;
-                        if (mine) {
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dw[j][e] = fmaf(d[W - 1][e], x[j][e], dw[j][e]);
-                            dw[W][e] += d[W - 1][e];
-                        }
-                        // input t - W + 1 has all its dp now: d[j] meets tap W - 1 - j
-                        sum[e] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) sum[e] = fmaf(w[W - 1 - j][e], d[j][e], sum[e]);
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) x[j][e] = x[j + 1][e], d[j][e] = d[j + 1][e];
-                    }
-                    const int at = t - (W - 1);
-                    if (at >= first || begins) store(at, sum);
-                }
-            }
-        }
+        load(first);
+        four(first, stop, std::false_type{});
+        int t0 = first + 4;
+        for (; t0 + 4 <= last; t0 += 4) four(t0, stop, std::true_type{});
+        for (; t0 < stop; t0 += 4) four(t0, stop, std::false_type{});
     }
     // the four waves' sums, in their order
     const int64_t row = (int64_t)a.channels * (W + 1);
@@ -163,15 +191,15 @@ template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv
 #pragma unroll
             for (int j = 0; j <= W; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float &s = lds[(j * 8 + e) * 64 + l];
+                for (int e = 0; e < N; ++e) {
+                    float &s = lds[(j * N + e) * 64 + l];
                     s = (other ? s : 0.f) + dw[j][e];
                 }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < 64 * 8 * (W + 1); i += 256) {
-        const int lane = i & 63, e = i >> 6 & 7, j = i >> 9, c = (blockIdx.y * 64 + lane) * 8 + e;
-        if (c < a.channels) a.partial[blockIdx.x * row + (int64_t)j * a.channels + c] = lds[i];
+    for (int i = threadIdx.x; i < 64 * N * (W + 1); i += 256) {
+        const int lane = i / N % 64, e = i % N, j = i / (64 * N), c = (blockIdx.y * 64 + lane) * N + e;
+        if (c < a.channels) a.partial[blockIdx.x * row + (int64_t)j * a.channels + c] = lds[(j * N + e) * 64 + lane];
     }
 }
 
@@ -198,33 +226,38 @@ template <int W> __global__ __launch_bounds__(256) void conv_sums_kernel(ConvArg
     }
 }
 
-// One token a request on a pool of the last inputs [n_slots, W - 1, channels], in place.
-template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a) {
-    const int per_row = (a.channels + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.n * per_row) return;
-    const int r = (int)(i / per_row), c0 = (int)(i - (int64_t)r * per_row) * 8, left = a.channels - c0;
-    const int32_t slot = a.slot[r];
-    if (slot < 0 || slot >= a.n_slots) return;
-    const int64_t at = (int64_t)slot * (W - 1) * a.channels + c0;
-    Raw8<F32> raw[W];
+// One token a request on a pool of the last inputs [n_slots, W - 1, channels], in place.  A lane has the
+// same 8 channels of `rows` requests, whose taps it loads once.
+template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int rows) {
+    constexpr int N = kWide;
+    const int c0 = (blockIdx.y * 256 + threadIdx.x) * N, left = a.channels - c0, r0 = blockIdx.x * rows;
+    if (left <= 0) return;
+    float w[W][N], bias[N];
+    load_taps<VEC, W, N>(a, c0, left, w, bias);
+    for (int r = r0; r < min(r0 + rows, a.n); ++r) {
+        const int32_t slot = a.slot[r];
+        if (slot < 0 || slot >= a.n_slots) continue;
+        const int64_t at = (int64_t)slot * (W - 1) * a.channels + c0;
+        Raw<F32, N> raw[W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) raw[j] = load8<F32, VEC>(a.pool, at + (int64_t)j * a.channels, left);
-    raw[W - 1] = load8<F32, VEC>(a.x, r * a.x_stride + c0, left);
-    float w[W][8], p[8];
-    load_taps<W>(a, c0, left, w, p);
+        for (int j = 0; j < W - 1; ++j) raw[j] = load_n<F32, VEC, N>(a.pool, at + (int64_t)j * a.channels, left);
+        raw[W - 1] = load_n<F32, VEC, N>(a.x, r * a.x_stride + c0, left);
+        float p[N];
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        float x[8];
-        widen8<F32>(raw[j], x);
+        for (int e = 0; e < N; ++e) p[e] = bias[e];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = fmaf(w[j][e], x[e], p[e]);
-        if (j > 0) store8<F32, VEC>(a.pool, at + (int64_t)(j - 1) * a.channels, x, left);
+        for (int j = 0; j < W; ++j) {
+            float x[N];
+            widen_n<F32, N>(raw[j], x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) p[e] = fmaf(w[j][e], x[e], p[e]);
+            if (j > 0) store_n<F32, VEC, N>(a.pool, at + (int64_t)(j - 1) * a.channels, x, left);
+        }
+        if (a.silu)
+#pragma unroll
+            for (int e = 0; e < N; ++e) p[e] = gate_of(SQ_ACT_SILU, p[e]);
+        store_n<F32, VEC, N>(a.y, (int64_t)r * a.channels + c0, p, left);
     }
-    if (a.silu)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = gate_of(SQ_ACT_SILU, p[e]);
-    store8<F32, VEC>(a.y, (int64_t)r * a.channels + c0, p, left);
 }
 
 template <typename F> void pick(bool b, F f) {
@@ -236,19 +269,19 @@ template <typename F> void pick_width(int w, F f) {
     else if (w == 3) f(std::integral_constant<int, 3>{});
     else f(std::integral_constant<int, 4>{});
 }
-uint32_t tiles_of(int channels) { return (channels + 511) / 512; }
+uint32_t tiles_of(int channels, int per_lane) { return (channels + 64 * per_lane - 1) / (64 * per_lane); }
 
 } // namespace
 
-// About 2048 workgroups in all: two rounds of four per CU.
+// Up to 4096 workgroups in all, each with as many blocks of tokens as the others.
 int conv_blocks(int64_t n_tokens, int32_t n_seq, int32_t channels) {
-    const int64_t slots = block_slots(n_tokens, n_seq, kBackBlockShift), most = 2048 / tiles_of(channels);
-    const int64_t blocks = slots < most ? slots : most;
-    return (int)(blocks < 1 ? 1 : blocks);
+    const int64_t slots = block_slots(n_tokens, n_seq, kBackBlockShift), most = 4096 / tiles_of(channels, kNarrow);
+    const int64_t turns = most > 0 ? (slots + most - 1) / most : slots;
+    return (int)(turns > 0 ? (slots + turns - 1) / turns : 1);
 }
 
 hipError_t launch_conv_forward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream) {
-    const dim3 grid((uint32_t)block_slots(a.seqs.n_tokens, a.seqs.n_seq, kBlockShift), tiles_of(a.channels));
+    const dim3 grid((uint32_t)block_slots(a.seqs.n_tokens, a.seqs.n_seq, kBlockShift), tiles_of(a.channels, kWide));
     pick(f32, [&](auto F) { pick(vec, [&](auto V) { pick_width(a.width, [&](auto W) {
         hipLaunchKernelGGL((conv_forward_kernel<F.value, V.value, W.value>), grid, dim3(256), 0, stream, a);
     }); }); });
@@ -258,7 +291,7 @@ hipError_t launch_conv_forward(const ConvArgs &a, bool f32, bool vec, hipStream_
 hipError_t launch_conv_backward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream) {
     const int64_t slots = block_slots(a.seqs.n_tokens, a.seqs.n_seq, kBackBlockShift);
     const int blocks = conv_blocks(a.seqs.n_tokens, a.seqs.n_seq, a.channels);
-    const dim3 grid(blocks, tiles_of(a.channels));
+    const dim3 grid(blocks, tiles_of(a.channels, kNarrow));
     pick(f32, [&](auto F) { pick(vec, [&](auto V) { pick_width(a.width, [&](auto W) {
         hipLaunchKernelGGL((conv_backward_kernel<F.value, V.value, W.value>), grid, dim3(256), 0, stream, a, slots);
     }); }); });
@@ -271,9 +304,13 @@ hipError_t launch_conv_backward(const ConvArgs &a, bool f32, bool vec, hipStream
 }
 
 hipError_t launch_conv_step(const ConvArgs &a, bool f32, bool vec, hipStream_t stream) {
-    const int64_t lanes = (int64_t)a.n * ((a.channels + 7) / 8);
+    // as many requests to a lane as leave 512 lanes to a CU
+    const int tiles = (a.channels + 256 * kWide - 1) / (256 * kWide);
+    const int64_t most = (int64_t)a.n * tiles / 512;
+    const int rows = most < 1 ? 1 : most < kStepRows ? (int)most : kStepRows;
+    const dim3 grid((a.n + rows - 1) / rows, tiles);
     pick(f32, [&](auto F) { pick(vec, [&](auto V) { pick_width(a.width, [&](auto W) {
-        hipLaunchKernelGGL((conv_step_kernel<F.value, V.value, W.value>), dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((conv_step_kernel<F.value, V.value, W.value>), grid, dim3(256), 0, stream, a, rows);
     }); }); });
     return hipGetLastError();
 }

@@ -64,22 +64,6 @@ struct Gates {
 };
 __device__ __forceinline__ float decay_of(const Gates &g, int i, int j) { return exp_of((g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j])); }
 
-// Sums over 16 neighbouring lanes, to all of them, by rotations within the row; and over all 64.
-template <int N> __device__ __forceinline__ float rotated(float x) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + N, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float row_sum(float x) {
-    x += rotated<8>(x);
-    x += rotated<4>(x);
-    x += rotated<2>(x);
-    return x + rotated<1>(x);
-}
-// ... over lanes 16 apart
-__device__ __forceinline__ float rows_sum(float x) {
-    x += __shfl_xor(x, 16, 64);
-    return x + __shfl_xor(x, 32, 64);
-}
-
 // Inclusive sums over the lanes of a wave.
 __device__ __forceinline__ double wave_scan(double v, int l) {
 #pragma unroll
