@@ -149,6 +149,7 @@ sq_status check_scan(const sq_scan_desc *d, bool batch) {
         (st = check_stride("dx_stride", d->dx_stride, wide, per)) || (st = check_stride("ddt_stride", d->ddt_stride, d->n_heads, 1)) ||
         (st = check_stride("db_stride", d->db_stride, keys, per)) || (st = check_stride("dc_stride", d->dc_stride, keys, per)))
         return st;
+    if (wide > kMaxStride || keys > kMaxStride) return fail(SQ_EUNSUPPORTED, "n_heads * d_head or n_groups * d_state exceeds 2^24");  // 32-bit offsets within a chunk
     if (batch) {
         const sqk::ScanPlan p = sqk::scan_plan(*d);
         const int64_t grid = 0x7FFFFFFFll;

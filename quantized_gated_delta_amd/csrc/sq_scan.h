@@ -54,7 +54,7 @@ hipError_t launch_scan_step(const ScanArgs &a, int d_state, bool f32, bool y_f32
 // log(1 + e^v); from 20 on that is v to one part in 10^10.
 __device__ __forceinline__ float softplus_of(float v) { return v > 20.f ? v : log1pf(expf(v)); }
 
-// A chunk's gates in LDS.  G: the running sum of dt A over the chunk, as the sum of two floats, so that
+// A chunk's gates in LDS.  G: the running sum of dt A over the chunk, times log2(e), as the sum of two floats, so that
 // a difference of two is exact to fp32 wherever it is small, also behind a strong decay.
 struct Gates {
     float hi[64], lo[64];  // G
@@ -62,7 +62,11 @@ struct Gates {
     float in[64];          // e^G: from the chunk's start to a token
     float out[64];         // e^{G_end - G}: from a token to the chunk's end
 };
-__device__ __forceinline__ float decay_of(const Gates &g, int i, int j) { return exp_of((g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j])); }
+// From token j to a token i behind it; 0 where `live` is false.
+__device__ __forceinline__ float decay_of(const Gates &g, int i, int j, bool live) {
+    const float d = (g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j]);
+    return __builtin_amdgcn_exp2f(live ? d : -__builtin_inff());
+}
 
 // Inclusive sums over the lanes of a wave.
 __device__ __forceinline__ double wave_scan(double v, int l) {
@@ -74,6 +78,12 @@ __device__ __forceinline__ double wave_scan(double v, int l) {
     return v;
 }
 
+// 2^x of an fp64 x: its leading float goes through the hardware's exponential, the rest is first order.
+__device__ __forceinline__ float exp2_of(double x) {
+    const float hi = (float)x, r = __builtin_amdgcn_exp2f(hi);
+    return fmaf(r, (float)(x - (double)hi) * 0.69314718055994530942f, r);
+}
+
 // One wave forms a chunk's gates, a token to a lane; live: the token is one of the sequence's.
 // Others have no time: they change nothing.
 __device__ __forceinline__ void make_gates(Gates &g, int l, bool live, float raw, float bias, float A, int softplus) {
@@ -82,13 +92,13 @@ __device__ __forceinline__ void make_gates(Gates &g, int l, bool live, float raw
     double s = (double)dt * (double)A;
     s = s < -150.0 ? -150.0 : s;  // a NaN stays one
     if (!live) s = 0.0;
-    const double G = wave_scan(s, l), end = __shfl(G, 63, 64);
+    const double G = wave_scan(s * 1.4426950408889634074, l), end = __shfl(G, 63, 64);
     const float hi = (float)G;
     g.hi[l] = hi;
     g.lo[l] = (float)(G - (double)hi);
     g.dt[l] = dt;
-    g.in[l] = exp_of((float)G);
-    g.out[l] = exp_of((float)(end - G));
+    g.in[l] = exp2_of(G);
+    g.out[l] = exp2_of(end - G);
 }
 
 // A matrix of 64 rows (tokens) in LDS, rows as they lie in memory and padded by 16 bytes.
@@ -152,17 +162,24 @@ __device__ __forceinline__ void pair_tile(int n, int &it, int &jt) {
 __device__ __forceinline__ float sign_of(int tile) { return tile & 1 ? -1.f : 1.f; }
 
 // Vectors of a token matrix as a workgroup of T threads loads them: from memory into
-// registers, rows behind the last as zeros, and from there into LDS.
+// registers (behind the last row: it again), and from there into LDS.
 template <bool F32, int COLS, int T> struct Staged {
     typedef TokenMat<F32, COLS> M;
     static constexpr int COUNT = 64 * M::VECS / T;
     uint4 v[COUNT];
-    __device__ __forceinline__ void load(const void *base, int64_t stride, int rows, int t) {
+    __device__ __forceinline__ void load(const void *base, uint32_t stride, int rows, int t) {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
-            const int row = (i * T + t) / M::VECS, col = (i * T + t) % M::VECS;
-            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const Elem<F32> *>(base) + row * stride) + col;
-            v[i] = row < rows ? *p : uint4{};
+            const uint32_t row = min((i * T + t) / M::VECS, rows - 1), col = (i * T + t) % M::VECS;
+            v[i] = *at_bytes<uint4>(base, row * (stride * (uint32_t)sizeof(Elem<F32>)) + col * 16);
+        }
+    }
+    // rows from `rows` on as zeros
+    __device__ __forceinline__ void clear(int rows, int t) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const bool live = (i * T + t) / M::VECS < rows;
+            v[i] = uint4{live ? v[i].x : 0u, live ? v[i].y : 0u, live ? v[i].z : 0u, live ? v[i].w : 0u};
         }
     }
     // TURN_ROWS, TURN_COLS: rows and columns 16 .. 31, 48 .. 63, ... with their signs turned, see sign_of

@@ -27,7 +27,7 @@ constexpr int kGates = 4;  // chunks whose gates are formed at once, one by each
 // The main passes, forwards and (in brackets) backwards.  The state takes up the keys K = B [C] with the
 // columns X = x [dy], and is read by the queries Q = C [B]; a query meets the keys of its own
 // chunk up to [from] its own place in `pairs`.  NT: terms that the results are accurate to.
-template <int N, bool F32, int NT, bool YF32, int PASS>
+template <int N, bool F32, int NT, bool YF32, int PASS, bool SAVE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void scan_kernel(ScanArgs a) {
     typedef Elem<F32> E;
     constexpr bool BACK = PASS >= kOwnBack, READ = PASS == kMain || PASS == kMainBack;
@@ -63,13 +63,22 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         const float *start = BACK ? a.dS_out : a.S0, *p = !READ ? nullptr : a.segments ? seg : start ? start + at : nullptr;
         const int64_t row = a.segments ? kHeadPart : a.d_head;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) S[m] = f4{};
+        if (p) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[m][i] = p ? sign_of(m) * p[(16 * m + g4 + i) * row + 16 * w + r] : 0.f;
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[m][i] = p[(16 * m + g4 + i) * row + 16 * w + r];
+#pragma unroll
+            for (int m = 1; m < MT; m += 2) S[m] = -S[m];
+        }
     }
     const float A = a.A[pt.head], bias = a.bias ? a.bias[pt.head] : 0.f, D = READ && a.D ? a.D[pt.head] : 0.f;
     const int64_t y_stride = (int64_t)a.n_heads * a.d_head, column = (int64_t)pt.head * a.d_head + pt.col;
     const int64_t k_stride = BACK ? a.c_stride : a.b_stride, q_stride = BACK ? a.b_stride : a.c_stride, x_stride = BACK ? y_stride : a.x_stride;
+    constexpr int OUT = BACK ? sizeof(E) : YF32 ? 4 : 2;  // bytes of an element of y [of x's gradient]
+    const int64_t out_stride = BACK ? a.dx_stride : y_stride;
+    const uint32_t out_bytes = (uint32_t)out_stride * OUT;
     const E *pk = static_cast<const E *>(BACK ? a.C : a.B) + t0 * k_stride + (int64_t)pt.group * N;
     const E *pq = static_cast<const E *>(BACK ? a.B : a.C) + t0 * q_stride + (int64_t)pt.group * N;
     const E *px = static_cast<const E *>(BACK ? a.dy : a.x) + t0 * x_stride + column;
@@ -78,11 +87,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
     auto rows_of = [&](int c) { return min(64, len - c * 64); };
     Staged<F32, N, 256> rK, rQ;
     Staged<F32, kHeadPart, 256> rX;
+    Raw<F32, 4> next_x[PASS == kMainBack ? 4 : 1];  // what U's dots are with: a lane's four columns of a token of each tile
     auto load = [&](int c) {
         const int rows = rows_of(c);
-        rK.load(pk + (int64_t)c * 64 * k_stride, k_stride, rows, t);
-        rX.load(px + (int64_t)c * 64 * x_stride, x_stride, rows, t);
-        if (READ) rQ.load(pq + (int64_t)c * 64 * q_stride, q_stride, rows, t);
+        if (PASS == kMainBack)
+#pragma unroll
+            for (int qt = 0; qt < 4; ++qt)
+                next_x[qt] = load_n<F32, true, 4>(at_bytes<E>(static_cast<const E *>(a.x) + (t0 + (int64_t)c * 64) * a.x_stride + column,
+                                                             (min(16 * qt + r, rows - 1) * (uint32_t)a.x_stride + 16 * w + g4) * (uint32_t)sizeof(E)), 0, 4);
+        rK.load(pk + (int64_t)c * 64 * k_stride, (uint32_t)k_stride, rows, t);
+        rX.load(px + (int64_t)c * 64 * x_stride, (uint32_t)x_stride, rows, t);
+        if (READ) rQ.load(pq + (int64_t)c * 64 * q_stride, (uint32_t)q_stride, rows, t);
     };
     // what wave w forms gates from: its chunk of the kGates from the k-th on
     float raw = 0.f;
@@ -102,24 +117,29 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         const Gates &g = gates[k % kGates];
         // signs: the state's odd tiles of rows are turned, and so is what every second tile of queries reads
         rK.template store<false, true>(sK, t);
+        rX.clear(rows, t);  // behind the end: what nothing is taken up of
         rX.store(sX, t);
         if (READ) rQ.template store<true, true>(sQ, t);
         if (k % kGates == 0 && k + w < n_chunks) make_gates(gates[w], l, l < rows_of(first + (k + w) * step), raw, bias, A, a.softplus);
+        Raw<F32, 4> this_x[PASS == kMainBack ? 4 : 1];
+#pragma unroll
+        for (int qt = 0; qt < (PASS == kMainBack ? 4 : 1); ++qt) this_x[qt] = next_x[qt];
         __syncthreads();
         if (k % kGates == 0) load_raw(k + kGates);
         if (k + 1 < n_chunks) load(c + step);
-        float *keep = reinterpret_cast<float *>(BACK ? a.grad_save : a.save);
-        if (READ && keep) {  // [row][column], fp32
-            keep += (chunk0 + (int64_t)c * parts) * N * kHeadPart;
+        if (SAVE) {  // [row][column], fp32
+            float *keep = reinterpret_cast<float *>(BACK ? a.grad_save : a.save) + (chunk0 + (int64_t)c * parts) * N * kHeadPart;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) keep[(16 * m + g4 + i) * kHeadPart + 16 * w + r] = sign_of(m) * S[m][i];
+                for (int i = 0; i < 4; ++i) *at_bytes<float>(keep + (16 * m + i) * kHeadPart, (g4 * kHeadPart + 16 * w + r) * 4) = sign_of(m) * S[m][i];
         }
         if (READ) {
-            for (int n = w; n < 10; n += 4) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {  // ten tiles: w, w + 4 and, for two waves, w + 8
+                if (j == 2 && w >= 2) break;
                 int hi, lo;
-                pair_tile(n, hi, lo);
+                pair_tile(w + 4 * j, hi, lo);
                 const int kt = BACK ? hi : lo, qt = BACK ? lo : hi, q = 16 * qt + r;
                 f4 p{};
 #pragma unroll
@@ -127,8 +147,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = 16 * kt + g4 + e;
-                    if (BACK) p[e] = key >= q ? p[e] * decay_of(g, key, q) : 0.f;
-                    else p[e] = key <= q ? p[e] * decay_of(g, q, key) * g.dt[key] : 0.f;
+                    const bool live = BACK ? key >= q : key <= q;
+                    const float L = BACK ? decay_of(g, key, q, live) : decay_of(g, q, key, live) * g.dt[key];
+                    p[e] = live ? p[e] * L : 0.f;
                 }
                 PairMat::put4(pairs, q, 16 * kt + g4, p);
             }
@@ -139,7 +160,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         for (int kb = 0; kb < 2; ++kb) fx[kb] = get_t<F32, 1>(sX, XMat::ROW, 0, 32 * kb, 16 * w, l);
         if (READ) {
             // transposed, the result's columns as its rows: a lane then holds four neighbours of one token
-            f4 y[4] = {};
+            f4 y[4] = {}, y_out[4];
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 float s[8];
@@ -148,17 +169,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
                 const Frag<F32, NT> fs = make_frag<F32, NT>(s);
 #pragma unroll
                 for (int qt = 0; qt < 4; ++qt) y[qt] = mma<NT>(fs, KeyMat::get_split(sQ, 16 * qt + r, 32 * kb + g4), y[qt]);
+                __builtin_amdgcn_sched_barrier(0);  // four blocks' operands at once would not fit the registers
             }
 #pragma unroll
             for (int qt = 0; qt < 4; ++qt) {
                 const int q = 16 * qt + r;
-                const int64_t tok = t0 + (int64_t)c * 64 + q;
                 y[qt] *= BACK ? g.out[q] : g.in[q];
                 const f4 own = load4<F32>(sX + q * XMat::ROW + 16 * w + g4);
-                f4 x{};
-                float z = 0.f, u = 0.f;
+                float x[4], z = 0.f, u = 0.f;
                 if (BACK) {
-                    if (q < rows) x = load4<F32>(static_cast<const E *>(a.x) + tok * a.x_stride + column + 16 * w + g4);
+                    widen_n<F32, 4>(this_x[PASS == kMainBack ? qt : 0], x);
                     z = sign_of(qt) * ((x[0] * y[qt][0] + x[1] * y[qt][1]) + (x[2] * y[qt][2] + x[3] * y[qt][3]));
                 }
 #pragma unroll
@@ -172,10 +192,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
                     y[qt] *= g.dt[q];
                 }
                 y[qt] += own * D;
-                if (q < rows) {
-                    if (BACK) st_elem4<F32>(a.dx, tok * a.dx_stride + column + 16 * w + g4, y[qt]);
-                    else st_elem4<YF32>(a.y, tok * y_stride + column + 16 * w + g4, y[qt]);
-                }
+                y_out[qt] = y[qt];
+            }
+            // whole chunks store without branches, so that the next one's loads are waited for by count and
+            // not for the stores behind them
+            char *py = static_cast<char *>(BACK ? a.dx : a.y) + ((t0 + (int64_t)c * 64) * out_stride + column) * OUT;
+            if (rows == 64) {
+#pragma unroll
+                for (int qt = 0; qt < 4; ++qt) st_elem4<OUT == 4>(at_bytes<char>(py, (16 * qt + r) * out_bytes + (16 * w + g4) * OUT), 0, y_out[qt]);
+            } else {
+#pragma unroll
+                for (int qt = 0; qt < 4; ++qt)
+                    if (16 * qt + r < rows) st_elem4<OUT == 4>(at_bytes<char>(py, (16 * qt + r) * out_bytes + (16 * w + g4) * OUT), 0, y_out[qt]);
+                __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
             }
         }
         // the state: the scaled X as the right operand, three terms, so that the state has fp32 accuracy
@@ -198,10 +227,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
             S[m] *= whole;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) S[m] = mma<3>(get_t<F32, 1>(sK, KeyMat::ROW, 0, 32 * kb, 16 * m, l), fs[kb], S[m]);
+            if (m % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();
-        if (PASS == kMainBack && w < 2)  // 0: z, 1: u
-            a.dots[(w * a.chunk_parts + chunk0 + (int64_t)c * parts) * 64 + l] = (dots[w][0][l] + dots[w][1][l]) + (dots[w][2][l] + dots[w][3][l]);
+        if (PASS == kMainBack) {  // 0: z, 1: u; waves 2 and 3 store the same again
+            const int n = w & 1;
+            a.dots[(n * a.chunk_parts + chunk0 + (int64_t)c * parts) * 64 + l] = (dots[n][0][l] + dots[n][1][l]) + (dots[n][2][l] + dots[n][3][l]);
+        }
     }
     const bool end = BACK ? b.c == 0 : begin + (1 << a.seg_shift) >= b.len;
     float *to = !READ ? seg : !end ? nullptr : BACK ? a.dS0 : a.S_out;
@@ -238,9 +270,9 @@ template <int N, bool BACK> __global__ __launch_bounds__(256) void join_kernel(S
     }
 }
 
-template <int N, bool F32, int NT, bool YF32, int PASS> hipError_t launch_pass(const ScanArgs &a, hipStream_t stream) {
+template <int N, bool F32, int NT, bool YF32, int PASS, bool SAVE = false> hipError_t launch_pass(const ScanArgs &a, hipStream_t stream) {
     const int64_t parts = (int64_t)a.n_heads * (a.d_head / kHeadPart), slots = block_slots(a.seqs.n_tokens, a.seqs.n_seq, a.seg_shift);
-    hipLaunchKernelGGL((scan_kernel<N, F32, NT, YF32, PASS>), dim3((uint32_t)((parts + 7) / 8 * 8 * slots)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((scan_kernel<N, F32, NT, YF32, PASS, SAVE>), dim3((uint32_t)((parts + 7) / 8 * 8 * slots)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 template <int N, bool BACK> hipError_t launch_join(const ScanArgs &a, hipStream_t stream) {
@@ -251,12 +283,13 @@ template <int N, bool BACK> hipError_t launch_join(const ScanArgs &a, hipStream_
 template <int N, bool F32, bool YF32> hipError_t forward(const ScanArgs &a, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (a.segments && ((e = launch_pass<N, F32, 2, false, kOwn>(a, stream)) != hipSuccess || (e = launch_join<N, false>(a, stream)) != hipSuccess)) return e;
-    return launch_pass<N, F32, YF32 ? 3 : 2, YF32, kMain>(a, stream);
+    constexpr int NT = YF32 ? 3 : 2;
+    return a.save ? launch_pass<N, F32, NT, YF32, kMain, true>(a, stream) : launch_pass<N, F32, NT, YF32, kMain>(a, stream);
 }
 template <int N, bool F32> hipError_t back(const ScanArgs &a, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (a.segments && ((e = launch_pass<N, F32, 2, false, kOwnBack>(a, stream)) != hipSuccess || (e = launch_join<N, true>(a, stream)) != hipSuccess)) return e;
-    return launch_pass<N, F32, 3, false, kMainBack>(a, stream);
+    return launch_pass<N, F32, 3, false, kMainBack, true>(a, stream);
 }
 
 // One token of one head a workgroup; a thread has 4 columns of every 16th (d_head 128: 8th) row.  Bound by memory: the

@@ -74,8 +74,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
     auto load = [&](int v) {
         const Part pt = part_of(a, v);
         const int64_t col = (int64_t)pt.head * a.d_head + pt.col;
-        rX.load(static_cast<const E *>(a.x) + t0 * a.x_stride + col, a.x_stride, rows, t);
-        rY.load(static_cast<const E *>(a.dy) + t0 * y_stride + col, y_stride, rows, t);
+        rX.load(static_cast<const E *>(a.x) + t0 * a.x_stride + col, (uint32_t)a.x_stride, rows, t);
+        rY.load(static_cast<const E *>(a.dy) + t0 * y_stride + col, (uint32_t)y_stride, rows, t);
         const int64_t at = ((slot * parts + v) * N + 16 * nt + r) * kHeadPart + g8;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -85,8 +85,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
     };
     {
         Staged<F32, N, kThreads> rB, rC;
-        rB.load(static_cast<const E *>(a.B) + t0 * a.b_stride + (int64_t)group * N, a.b_stride, rows, t);
-        rC.load(static_cast<const E *>(a.C) + t0 * a.c_stride + (int64_t)group * N, a.c_stride, rows, t);
+        rB.load(static_cast<const E *>(a.B) + t0 * a.b_stride + (int64_t)group * N, (uint32_t)a.b_stride, rows, t);
+        rC.load(static_cast<const E *>(a.C) + t0 * a.c_stride + (int64_t)group * N, (uint32_t)a.c_stride, rows, t);
         load(v0);
         rB.store(s.B, t);
         rC.store(s.C, t);
@@ -125,6 +125,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
         for (int q = 0; q < count; ++q) {
             const Gates &g = s.g[q];
             auto &sum = s.sums[q & 1];
+            rX.clear(rows, t);
+            rY.clear(rows, t);
             rX.store(s.x, t);
             rY.template store<true>(s.dy, t);
             const Frag<F32, 3> fS[2] = {operand_of<F32, 3>(rS[0]), operand_of<F32, 3>(rS[1])};
@@ -151,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = 16 * it[k] + g4 + e;
-                        const float vv = i >= j ? decay_of(g, i, j) * dt * xy[e] : 0.f;
+                        const float vv = i >= j ? decay_of(g, i, j, i >= j) * dt * xy[e] : 0.f;
                         V[k][e] += vv;
                         W[e] = i > j ? vv * cb[k][e] : 0.f;
                         if (i == j) sum.diag[i] = xy[e];
