@@ -17,6 +17,8 @@
 // It leaves dS, and the dots of x_j with U_j and with its second part, for the other gradients (sq_scan_bwd.hip).
 #include "sq_scan.h"
 
+#include <cstdint>
+
 namespace sqk {
 namespace {
 
@@ -88,8 +90,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
     Staged<F32, N, 256> rK, rQ;
     Staged<F32, kHeadPart, 256> rX;
     Raw<F32, 4> next_x[PASS == kMainBack ? 4 : 1];  // what U's dots are with: a lane's four columns of a token of each tile
-    auto load = [&](int c) {
-        const int rows = rows_of(c);
+    auto load = [&](int c, int t) {
+        const int rows = rows_of(c), r = t & 15, g4 = (t & 63) / 16 * 4;
         if (PASS == kMainBack)
 #pragma unroll
             for (int qt = 0; qt < 4; ++qt)
@@ -108,13 +110,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         }
     };
     load_raw(0);
-    if (n_chunks > 0) load(first);
+    if (n_chunks > 0) load(first, t);
     // tiles beside the diagonal that a contraction over 32 keys meets and no pair fills
     if (READ && w < 2) PairMat::put4(pairs, 32 * w + (BACK ? 16 : 0) + r, 32 * w + (BACK ? 0 : 16) + g4, f4{});
     float fade = 1.f;
     for (int k = 0; k < n_chunks; ++k) {
         const int c = first + k * step, rows = rows_of(c);
         const Gates &g = gates[k % kGates];
+        // addresses in LDS are formed again for each chunk, not kept in registers
+        int lane = threadIdx.x;
+        asm volatile("" : "+v"(lane));
+        const int t = lane, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
         // signs: the state's odd tiles of rows are turned, and so is what every second tile of queries reads
         rK.template store<false, true>(sK, t);
         rX.clear(rows, t);  // behind the end: what nothing is taken up of
@@ -126,7 +132,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         for (int qt = 0; qt < (PASS == kMainBack ? 4 : 1); ++qt) this_x[qt] = next_x[qt];
         __syncthreads();
         if (k % kGates == 0) load_raw(k + kGates);
-        if (k + 1 < n_chunks) load(c + step);
+        if (k + 1 < n_chunks) load(c + step, t);
         if (SAVE) {  // [row][column], fp32
             float *keep = reinterpret_cast<float *>(BACK ? a.grad_save : a.save) + (chunk0 + (int64_t)c * parts) * N * kHeadPart;
 #pragma unroll
@@ -363,11 +369,17 @@ ScanPlan scan_plan(const sq_scan_desc &d) {
     p.state_bytes = most * p.parts * state;
     p.fade_bytes = (most * p.parts * 4 + 255) / 256 * 256;
     p.save_bytes = p.chunk_slots * p.parts * state;
-    // the gradients' workgroups: a chunk and a subset of a group's heads, 512 to 1023 of them where there are so
-    // many heads; the sums over a subset then take less than 1024 x 64 rows of d_state, in smaller batches too
+    // the gradients' workgroups, one to a CU: a chunk and a subset of a group's heads.  Of up to 1023 workgroups (the sums over
+    // a subset then take less than 1024 x 64 rows of d_state, in smaller batches too), as many subsets as
+    // take the fewest rounds of 256 times heads, with two heads' time to begin and end (132 chunks x 32 heads: 3 subsets
+    // 170 us, 4 subsets, which need a third round, 203 us)
     const int64_t share = d.n_heads / d.n_groups, units = p.chunk_slots * d.n_groups, rows = d.n_tokens * d.n_heads;
     p.subsets = 1;
-    while (p.subsets * 2 <= share && units * p.subsets < 512) p.subsets *= 2;
+    int64_t least = INT64_MAX;
+    for (int64_t n = 1; n <= share && (n == 1 || units * n < 1024); ++n) {
+        const int64_t cost = (units * n + 255) / 256 * ((share + n - 1) / n + 2);
+        if (cost < least) least = cost, p.subsets = (int)n;
+    }
     p.group_bytes = (rows < 1024 * 64 ? rows : 1024 * 64) * d.d_state * 2 * 4;
     p.dots_bytes = 2 * 4 * 64 * p.chunk_slots * p.parts;
     p.head_bytes = (3 * 4 * p.chunk_slots * d.n_heads + 255) / 256 * 256;

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
 
     Staged<F32, kHeadPart, kThreads> rX, rY;
     Row8 rS[2], rD[2];
-    auto load = [&](int v) {
+    auto load = [&](int v, int t, int r, int g8) {
         const Part pt = part_of(a, v);
         const int64_t col = (int64_t)pt.head * a.d_head + pt.col;
         rX.load(static_cast<const E *>(a.x) + t0 * a.x_stride + col, (uint32_t)a.x_stride, rows, t);
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
         Staged<F32, N, kThreads> rB, rC;
         rB.load(static_cast<const E *>(a.B) + t0 * a.b_stride + (int64_t)group * N, (uint32_t)a.b_stride, rows, t);
         rC.load(static_cast<const E *>(a.C) + t0 * a.c_stride + (int64_t)group * N, (uint32_t)a.c_stride, rows, t);
-        load(v0);
+        load(v0, t, r, g8);
         rB.store(s.B, t);
         rC.store(s.C, t);
     }
@@ -123,6 +123,11 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
             make_gates(s.g[w], l, l < rows, raw, bias, A, a.softplus);
         }
         for (int q = 0; q < count; ++q) {
+            // addresses in LDS are formed again for each part: kept from part to part, they would be spilled, and reading
+            // them back would wait for the next part's loads
+            int lane = threadIdx.x;
+            asm volatile("" : "+v"(lane));
+            const int t = lane, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
             const Gates &g = s.g[q];
             auto &sum = s.sums[q & 1];
             rX.clear(rows, t);
@@ -137,9 +142,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
 #pragma unroll
                 for (int k = 0; k < 8; ++k) e0 = fmaf(rS[kb].v[k / 4][k % 4], rD[kb].v[k / 4][k % 4], e0);
             __syncthreads();
-            if (first + q + 1 < v1) load(first + q + 1);
-            e0 = rows_sum(row_sum(e0));
-            if (tt0 == 0 && l == 0) sum.e[nt] = e0;
+            if (first + q + 1 < v1) load(first + q + 1, t, r, g8);
+            sum.e[nt] = rows_sum(row_sum(e0));  // waves with the same rows of the state: the same
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (k < tiles) {
@@ -153,10 +157,14 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = 16 * it[k] + g4 + e;
-                        const float vv = i >= j ? decay_of(g, i, j, i >= j) * dt * xy[e] : 0.f;
+                        const float L = decay_of(g, i, j, i >= j) * dt, vv = i >= j ? L * xy[e] : 0.f;
                         V[k][e] += vv;
                         W[e] = i > j ? vv * cb[k][e] : 0.f;
-                        if (i == j) sum.diag[i] = xy[e];
+                    }
+                    if (it[k] == jt[k]) {  // dy . x: the diagonal, a lane of each row of 16
+                        const int e = r - g4;
+                        const float d = e == 0 ? xy[0] : e == 1 ? xy[1] : e == 2 ? xy[2] : xy[3];
+                        if (e >= 0 && e < 4) sum.diag[j] = d;
                     }
                     float down = (W[0] + W[1]) + (W[2] + W[3]);
                     if (it[k] == jt[k]) {  // the sums of column j over rows i, i + 1, ..., where j < i
@@ -172,10 +180,10 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
                     const float all = row_sum(down);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) W[e] = row_sum(W[e]);
-                    const int n = w + 8 * k;
-                    if (l < 16) sum.col[n][l] = down;
-                    if (l == 0) sum.all[n] = all;
-                    if (r == 0) *reinterpret_cast<f4 *>(&sum.row[n][g4]) = W;
+                    const int n = w + 8 * k;  // lanes that have the same sum store it all
+                    sum.col[n][r] = down;
+                    sum.all[n] = all;
+                    *reinterpret_cast<f4 *>(&sum.row[n][g4]) = W;
                 }
             }
 #pragma unroll
@@ -192,8 +200,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
                 dB[k] += d * (g.out[i] * g.dt[i]);
                 const f4 key = load4<F32>(s.C + i * KeyMat::ROW + 16 * nt + g4);
                 float dot = (c[0] * key[0] + c[1] * key[1]) + (c[2] * key[2] + c[3] * key[3]);
-                dot = rows_sum(dot);
-                if (l < 16) sum.r[nt][i] = dot;
+                sum.r[nt][i] = rows_sum(dot);
             }
             __syncthreads();
             if (w == q) {  // a token to a lane
