@@ -7,6 +7,7 @@ namespace sqk {
 
 constexpr int kHeadPart = 64;  // columns of a state that a workgroup has: a head of 128 is two parts, which share its gates
 constexpr int kSegMin = 8;     // shortest segment of a long sequence: 256 tokens
+constexpr int kSegGroups = 512;  // workgroups that sequences are cut into segments for
 
 struct ScanArgs {
     Ragged seqs;
@@ -194,14 +195,15 @@ template <bool F32, int COLS, int T> struct Staged {
     }
 };
 
-// What a part of a head is: its head, group and first column.
+// What a part of a head is: its head, group and first column.  The same for a whole wave, so in scalar registers, where
+// a division alone would not leave them: every address that follows is then formed by the scalar unit.
 struct Part { int head, group, col; };
 __device__ __forceinline__ Part part_of(const ScanArgs &a, int part) {
-    const int halves = a.d_head / kHeadPart;
+    const bool whole = a.d_head == kHeadPart;
     Part p;
-    p.head = part / halves;
-    p.col = (part - p.head * halves) * kHeadPart;
-    p.group = p.head / (a.n_heads / a.n_groups);
+    p.head = whole ? part : part >> 1;
+    p.col = whole ? 0 : (part & 1) * kHeadPart;
+    p.group = __builtin_amdgcn_readfirstlane(p.head / (a.n_heads / a.n_groups));
     return p;
 }
 // Element (0, 0) of a part's state in [sequence][head][d_state][d_head].

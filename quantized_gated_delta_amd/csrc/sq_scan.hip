@@ -48,16 +48,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
     // XCD gets neighbouring heads
     const int parts = a.n_heads * (a.d_head / kHeadPart), each = (parts + 7) / 8;
     const uint32_t turn_of = blockIdx.x >> 3;
-    const int part = (blockIdx.x & 7) * each + turn_of % each;
+    const uint32_t slot = __builtin_amdgcn_readfirstlane(turn_of / each);
+    const int part = (blockIdx.x & 7) * each + (turn_of - slot * each);
     if (part >= parts) return;
-    const int64_t slot = turn_of / each;
     const Block b = block_at(a.seqs, slot, a.seg_shift);
     if (b.seq < 0) return;
     const Part pt = part_of(a, part);
     const int begin = b.c << a.seg_shift, len = min(b.len - begin, 1 << a.seg_shift), n_chunks = (len + 63) >> 6;
     const int64_t t0 = (int64_t)b.t0 + begin, at = state_at<N>(a, b.seq, pt);
     const int64_t chunk0 = ((int64_t)(b.t0 >> 6) + b.seq + (begin >> 6)) * parts + part;  // + c * parts
-    float *seg = a.seg_state + (slot * parts + part) * N * kHeadPart;
+    float *seg = a.seg_state + ((int64_t)slot * parts + part) * N * kHeadPart;
 
     // the state: a wave has 16 columns, a lane rows 16 m + 4 (l / 16) .. + 3 of column l % 16, times sign_of(m)
     f4 S[MT];
@@ -90,8 +90,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
     Staged<F32, N, 256> rK, rQ;
     Staged<F32, kHeadPart, 256> rX;
     Raw<F32, 4> next_x[PASS == kMainBack ? 4 : 1];  // what U's dots are with: a lane's four columns of a token of each tile
-    auto load = [&](int c, int t) {
-        const int rows = rows_of(c), r = t & 15, g4 = (t & 63) / 16 * 4;
+    auto load = [&](int c) {
+        const int rows = rows_of(c);
         if (PASS == kMainBack)
 #pragma unroll
             for (int qt = 0; qt < 4; ++qt)
@@ -110,17 +110,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         }
     };
     load_raw(0);
-    if (n_chunks > 0) load(first, t);
+    if (n_chunks > 0) load(first);
     // tiles beside the diagonal that a contraction over 32 keys meets and no pair fills
     if (READ && w < 2) PairMat::put4(pairs, 32 * w + (BACK ? 16 : 0) + r, 32 * w + (BACK ? 0 : 16) + g4, f4{});
     float fade = 1.f;
     for (int k = 0; k < n_chunks; ++k) {
         const int c = first + k * step, rows = rows_of(c);
         const Gates &g = gates[k % kGates];
-        // addresses in LDS are formed again for each chunk, not kept in registers
-        int lane = threadIdx.x;
-        asm volatile("" : "+v"(lane));
-        const int t = lane, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
         // signs: the state's odd tiles of rows are turned, and so is what every second tile of queries reads
         rK.template store<false, true>(sK, t);
         rX.clear(rows, t);  // behind the end: what nothing is taken up of
@@ -132,7 +128,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         for (int qt = 0; qt < (PASS == kMainBack ? 4 : 1); ++qt) this_x[qt] = next_x[qt];
         __syncthreads();
         if (k % kGates == 0) load_raw(k + kGates);
-        if (k + 1 < n_chunks) load(c + step, t);
+        if (k + 1 < n_chunks) load(c + step);
         if (SAVE) {  // [row][column], fp32
             float *keep = reinterpret_cast<float *>(BACK ? a.grad_save : a.save) + (chunk0 + (int64_t)c * parts) * N * kHeadPart;
 #pragma unroll
@@ -251,7 +247,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
 #pragma unroll
             for (int i = 0; i < 4; ++i) to[(16 * m + g4 + i) * row + 16 * w + r] = sign_of(m) * S[m][i];
     }
-    if (!READ && t == 0) a.seg_fade[slot * parts + part] = fade;
+    if (!READ && t == 0) a.seg_fade[(int64_t)slot * parts + part] = fade;
 }
 
 // States at the segments' starts (BACK: their gradients at the segments' ends) in the place of the segments' own.
@@ -359,13 +355,14 @@ ScanPlan scan_plan(const sq_scan_desc &d) {
     ScanPlan p{};
     p.parts = (int64_t)d.n_heads * (d.d_head / kHeadPart);
     const int64_t state = (int64_t)d.d_state * kHeadPart * 4;
-    // segments of at least 256 tokens, as many as make about 1024 workgroups
+    // segments of at least 256 tokens, as many as make 512 workgroups, two to a CU (1024: as long in the passes over the
+    // chunks, and twice as many states to join, 15 us for 8 at 8192 tokens x 32 heads)
     p.seg_shift = kSegMin;
-    while (p.seg_shift < 30 && (d.n_tokens >> p.seg_shift) * p.parts > 1024) ++p.seg_shift;
+    while (p.seg_shift < 30 && (d.n_tokens >> p.seg_shift) * p.parts > kSegGroups) ++p.seg_shift;
     p.seg_slots = block_slots(d.n_tokens, d.n_seq, p.seg_shift);
     p.chunk_slots = block_slots(d.n_tokens, d.n_seq, 6);
-    // the slots of any smaller batch too: at most 1024 workgroups' or one to 256 tokens
-    const int64_t by_tokens = d.n_tokens >> kSegMin, by_parts = 1024 / p.parts + 1, most = (by_tokens < by_parts ? by_tokens : by_parts) + d.n_seq;
+    // the slots of any smaller batch too: at most those workgroups' or one to 256 tokens
+    const int64_t by_tokens = d.n_tokens >> kSegMin, by_parts = kSegGroups / p.parts + 1, most = (by_tokens < by_parts ? by_tokens : by_parts) + d.n_seq;
     p.state_bytes = most * p.parts * state;
     p.fade_bytes = (most * p.parts * 4 + 255) / 256 * 256;
     p.save_bytes = p.chunk_slots * p.parts * state;

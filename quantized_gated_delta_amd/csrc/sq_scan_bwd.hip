@@ -55,10 +55,11 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
 
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
     const uint32_t sets = (uint32_t)a.n_groups * a.subsets;
-    const int64_t slot = blockIdx.x / sets;
-    const int set = (int)(blockIdx.x % sets), subset = set % a.subsets, group = set / a.subsets;
+    const int64_t slot = __builtin_amdgcn_readfirstlane(blockIdx.x / sets);
+    const int set = (int)(blockIdx.x - (uint32_t)slot * sets), group = __builtin_amdgcn_readfirstlane(set / a.subsets), subset = set - group * a.subsets;
     const int halves = a.d_head / kHeadPart, share = a.n_heads / a.n_groups, parts = a.n_heads * halves;
-    const int h0 = group * share + share * subset / a.subsets, h1 = group * share + share * (subset + 1) / a.subsets;
+    const int h0 = group * share + __builtin_amdgcn_readfirstlane(share * subset / a.subsets),
+              h1 = group * share + __builtin_amdgcn_readfirstlane(share * (subset + 1) / a.subsets);
     const Block b = block_at(a.seqs, slot, 6);
     const int rows = b.seq < 0 ? 0 : min(64, b.len - b.c * 64);
     if (rows <= 0) {  // its sums are read all the same
