@@ -177,65 +177,90 @@ def sq_residual_norm_backward(desc, o, r, post_weight, scale, weight, dh, dr_out
 
 
 # ------------------------------------------------------------------ checks of tensors
-def _codes():
-    import torch
-    return {torch.float32: SQ_F32, torch.bfloat16: SQ_BF16}
+_torch = None
+
+
+def _load():
+    """torch, once an object or a call needs it (the binding itself imports without)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def _type(t, what):
-    codes = _codes()
-    if t not in codes:
+    code = {_torch.float32: SQ_F32, _torch.bfloat16: SQ_BF16}.get(t)
+    if code is None:
         raise TypeError("%s must be float32 or bfloat16, got %s" % (what, t))
-    return codes[t]
+    return code
 
 
 def _home(t):
-    """The device of a call's tensors, which has to be the current one."""
-    import torch
-    dev = t.device
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError("the tensors are on %s, but the current device is cuda:%d" % (dev, torch.cuda.current_device()))
+    """The number of the device of a call's tensors, which has to be the current one."""
+    dev = t.get_device()
+    if dev >= 0 and dev != _torch.cuda.current_device():
+        raise ValueError("the tensors are on cuda:%d, but the current device is cuda:%d" % (dev, _torch.cuda.current_device()))
     return dev
 
 
-def _tensor(name, t, shape, dtype, dev):
-    """A dense tensor of this shape and type on the call's device."""
-    if t.is_cuda and t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return
-    if not t.is_cuda or t.device != dev:
-        raise ValueError("%s must be a device tensor on %s" % (name, dev))
+def _fits(name, t, shape, dtype, dev):
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("%s must be a device tensor, on the device of the others" % name)
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _tensor(name, t, shape, dtype, dev):
+    """The address of a dense tensor of this shape and type on the call's device."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fits(name, t, shape, dtype, dev)
     raise ValueError("%s must be contiguous" % name)
 
 
+def _maybe(name, t, shape, dtype, dev):
+    return None if t is None else _tensor(name, t, shape, dtype, dev)
+
+
 def _tokens(name, t, shape, dtype, dev):
-    """A tensor whose rows [1:] are dense, a part of a wider one at most; returns its token stride (0: dense)."""
-    if not t.is_cuda or t.device != dev:
-        raise ValueError("%s must be a device tensor on %s" % (name, dev))
-    if t.dtype != dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.is_contiguous():
-        return 0
-    row = 1
+    """The address and the token stride (0: dense) of a tensor whose rows [1:] are dense, a part of a wider one at most."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), 0
+    except AttributeError:
+        pass
+    _fits(name, t, shape, dtype, dev)
+    row, strides = 1, t.stride()
     for i in range(len(shape) - 1, 0, -1):
-        if shape[i] > 1 and t.stride(i) != row:
+        if shape[i] > 1 and strides[i] != row:
             raise ValueError("the rows of %s must be dense" % name)
         row *= shape[i]
     if shape[0] < 2:
-        return 0
-    if t.stride(0) < row:  # an expanded tensor's 0 would mean dense
+        return t.data_ptr(), 0
+    if strides[0] < row:  # an expanded tensor's 0 would mean dense
         raise ValueError("the tokens of %s must not overlap" % name)
-    return t.stride(0)
+    return t.data_ptr(), strides[0]
 
 
 def _room(nbytes, device):
-    import torch
-    return torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
+    return _torch.empty(max(256, nbytes), dtype=_torch.uint8, device=device)
+
+
+def _span(buf):
+    return (None, 0) if buf is None else (buf.data_ptr(), buf.numel())
+
+
+def _copy(desc):
+    """A call's own descriptor: the object's may be in use by another thread."""
+    return type(desc).from_buffer_copy(desc)
 
 
 # ------------------------------------------------------------------ short convolution
@@ -247,74 +272,52 @@ class ShortConv:
     dense; weight [n_channels, width], bias [n_channels] and their gradients are fp32."""
 
     def __init__(self, n_seq: int, n_tokens: int, n_channels: int, width: int, act="silu", dtype=None, device="cuda", train=False):
-        import torch
+        torch = _load()
         self.dtype = torch.bfloat16 if dtype is None else dtype
-        self._code = _type(self.dtype, "dtype")
         self.n_seq, self.n_tokens, self.n_channels, self.width = int(n_seq), int(n_tokens), int(n_channels), int(width)
         self.act = ACTS[act]
-        nbytes = sq_conv_bytes(self._desc(n_seq, n_tokens))
+        self._desc = conv_desc(n_seq, n_tokens, n_channels, width, self.act, _type(self.dtype, "dtype"))
+        nbytes = sq_conv_bytes(self._desc)
         self.work = _room(nbytes, device) if train else None
 
-    def _desc(self, n_seq, n_tokens, x_stride=0):
-        return conv_desc(n_seq, n_tokens, self.n_channels, self.width, self.act, self._code, x_stride)
-
     def _args(self, x, weight, cu, bias, S0):
-        import torch
-        f32, n, n_seq, c = torch.float32, x.shape[0], cu.numel() - 1, self.n_channels
-        dev = _home(x)
+        f32, n, n_seq, c = _torch.float32, x.shape[0], cu.numel() - 1, self.n_channels
+        dev, desc = _home(x), _copy(self._desc)
         if n_seq < 0:
             raise ValueError("cu needs one entry more than there are sequences")
-        _tensor("cu", cu, (n_seq + 1,), torch.int32, dev)
-        stride = _tokens("x", x, (n, c), self.dtype, dev)
-        _tensor("weight", weight, (c, self.width), f32, dev)
-        if bias is not None:
-            _tensor("bias", bias, (c,), f32, dev)
-        if S0 is not None:
-            _tensor("S0", S0, (n_seq, self.width - 1, c), self.dtype, dev)
-        return self._desc(n_seq, n, stride), dev, n, n_seq
+        desc.n_seq, desc.n_tokens = n_seq, n
+        at = _tensor("cu", cu, (n_seq + 1,), _torch.int32, dev)
+        px, desc.x_stride = _tokens("x", x, (n, c), self.dtype, dev)
+        return (desc, at, px, _tensor("weight", weight, (c, self.width), f32, dev), _maybe("bias", bias, (c,), f32, dev),
+                _maybe("S0", S0, (n_seq, self.width - 1, c), self.dtype, dev)), dev, (n, c), (n_seq, self.width - 1, c)
 
     def forward(self, x, weight, cu, y, bias=None, S0=None, S_out=None, stream=None):
         """y [tokens, n_channels]; S0, S_out [n_seq, width - 1, n_channels]: the inputs before each sequence, and its
         last ones; cu: int32 [n_seq + 1], the tokens at which the sequences begin and end."""
-        desc, dev, n, n_seq = self._args(x, weight, cu, bias, S0)
-        _tensor("y", y, (n, self.n_channels), self.dtype, dev)
-        if S_out is not None:
-            _tensor("S_out", S_out, (n_seq, self.width - 1, self.n_channels), self.dtype, dev)
-        sq_conv_forward(desc, cu, x, weight, bias, S0, y, S_out, stream)
+        args, dev, tokens, state = self._args(x, weight, cu, bias, S0)
+        sq_conv_forward(*args, _tensor("y", y, tokens, self.dtype, dev), _maybe("S_out", S_out, state, self.dtype, dev), stream)
 
     def backward(self, x, weight, cu, dy, dx, dweight, bias=None, dbias=None, S0=None, dS_out=None, dS0=None, stream=None):
         """Gradients for the inputs of a forward call; dweight and dbias are written, not added to."""
-        import torch
         if self.work is None:
             raise ValueError("backward needs train=True")
-        desc, dev, n, n_seq = self._args(x, weight, cu, bias, S0)
-        c, f32, state = self.n_channels, torch.float32, (n_seq, self.width - 1, self.n_channels)
-        _tensor("dy", dy, (n, c), self.dtype, dev)
-        _tensor("dx", dx, (n, c), self.dtype, dev)
-        _tensor("dweight", dweight, (c, self.width), f32, dev)
-        if dbias is not None:
-            _tensor("dbias", dbias, (c,), f32, dev)
-        for name, t in (("dS_out", dS_out), ("dS0", dS0)):
-            if t is not None:
-                _tensor(name, t, state, self.dtype, dev)
-        sq_conv_backward(desc, cu, x, weight, bias, S0, dy, dS_out, dx, dweight, dbias, dS0, self.work, stream=stream)
+        args, dev, tokens, state = self._args(x, weight, cu, bias, S0)
+        c, f32, dt = self.n_channels, _torch.float32, self.dtype
+        sq_conv_backward(*args, _tensor("dy", dy, tokens, dt, dev), _maybe("dS_out", dS_out, state, dt, dev), _tensor("dx", dx, tokens, dt, dev),
+                         _tensor("dweight", dweight, (c, self.width), f32, dev), _maybe("dbias", dbias, (c,), f32, dev),
+                         _maybe("dS0", dS0, state, dt, dev), *_span(self.work), stream)
 
 
 def conv_step(pool, slot_idx, x, weight, y, bias=None, act="silu", stream=None) -> None:
     """One token per request on a pool [n_slots, width - 1, n_channels] of the last inputs, in place on the
     listed slots, which are distinct; x, y [n, n_channels].  Requests whose slot is outside the pool are left out."""
-    import torch
+    torch = _load()
     n_slots, before, c = pool.shape
-    n, dev = slot_idx.numel(), _home(pool)
-    code = _type(pool.dtype, "pool")
-    _tensor("pool", pool, (n_slots, before, c), pool.dtype, dev)
-    _tensor("slot_idx", slot_idx, (n,), torch.int32, dev)
-    stride = _tokens("x", x, (n, c), pool.dtype, dev)
-    _tensor("weight", weight, (c, before + 1), torch.float32, dev)
-    _tensor("y", y, (n, c), pool.dtype, dev)
-    if bias is not None:
-        _tensor("bias", bias, (c,), torch.float32, dev)
-    sq_conv_step(conv_desc(0, 0, c, before + 1, ACTS[act], code, stride), pool, n_slots, slot_idx, n, x, weight, bias, y, stream)
+    n, dt, f32, dev = slot_idx.numel(), pool.dtype, torch.float32, _home(pool)
+    px, stride = _tokens("x", x, (n, c), dt, dev)
+    sq_conv_step(conv_desc(0, 0, c, before + 1, ACTS[act], _type(dt, "pool"), stride), _tensor("pool", pool, (n_slots, before, c), dt, dev), n_slots,
+                 _tensor("slot_idx", slot_idx, (n,), torch.int32, dev), n, px, _tensor("weight", weight, (c, before + 1), f32, dev),
+                 _maybe("bias", bias, (c,), f32, dev), _tensor("y", y, (n, c), dt, dev), stream)
 
 
 # ------------------------------------------------------------------ selective scan
@@ -330,49 +333,44 @@ class SelectiveScan:
 
     def __init__(self, n_seq: int, n_tokens: int, n_heads: int, d_head: int, d_state: int, n_groups: int = 1, softplus=True, dtype=None,
                  y_dtype=None, device="cuda", train=False):
-        import torch
+        torch = _load()
         self.dtype = torch.bfloat16 if dtype is None else dtype
         self.y_dtype = self.dtype if y_dtype is None else y_dtype
-        self._types = (_type(self.dtype, "dtype"), _type(self.y_dtype, "y_dtype"))
         self.n_seq, self.n_tokens = int(n_seq), int(n_tokens)
         self.n_heads, self.n_groups, self.d_head, self.d_state = int(n_heads), int(n_groups), int(d_head), int(d_state)
         self.softplus = bool(softplus)
-        sizes = sq_scan_bytes(self._desc(n_seq, n_tokens), train=bool(train))
+        self._desc = scan_desc(n_seq, n_tokens, n_heads, d_head, d_state, n_groups, self.softplus, _type(self.dtype, "dtype"),
+                               _type(self.y_dtype, "y_dtype"))
+        sizes = sq_scan_bytes(self._desc, train=bool(train))
         work, save = sizes if train else (sizes, None)
         self.calls, self._sizes = 0, None  # forward calls so far, and the last one's batch
         self.work = _room(work, device)
         self.save = None if save is None else _room(save, device)
 
-    def _desc(self, n_seq, n_tokens, *strides):
-        return scan_desc(n_seq, n_tokens, self.n_heads, self.d_head, self.d_state, self.n_groups, self.softplus, *self._types, *strides)
-
     def _inputs(self, x, dt, A, B, C, cu, D, dt_bias, S0):
-        import torch
-        f32, n, n_seq, h = torch.float32, x.shape[0], cu.numel() - 1, self.n_heads
-        dev, keys = _home(x), (n, self.n_groups, self.d_state)
+        f32, n, n_seq, h, to = _torch.float32, x.shape[0], cu.numel() - 1, self.n_heads, self.dtype
+        dev, keys, desc = _home(x), (n, self.n_groups, self.d_state), _copy(self._desc)
         if n_seq < 0:
             raise ValueError("cu needs one entry more than there are sequences")
-        _tensor("cu", cu, (n_seq + 1,), torch.int32, dev)
-        strides = (_tokens("x", x, (n, h, self.d_head), self.dtype, dev), _tokens("dt", dt, (n, h), self.dtype, dev),
-                   _tokens("B", B, keys, self.dtype, dev), _tokens("C", C, keys, self.dtype, dev))
-        _tensor("A", A, (h,), f32, dev)
-        for name, t in (("D", D), ("dt_bias", dt_bias)):
-            if t is not None:
-                _tensor(name, t, (h,), f32, dev)
-        if S0 is not None:
-            _tensor("S0", S0, (n_seq, h, self.d_state, self.d_head), f32, dev)
-        return dev, n, n_seq, strides
+        desc.n_seq, desc.n_tokens = n_seq, n
+        at = _tensor("cu", cu, (n_seq + 1,), _torch.int32, dev)
+        px, desc.x_stride = _tokens("x", x, (n, h, self.d_head), to, dev)
+        pt, desc.dt_stride = _tokens("dt", dt, (n, h), to, dev)
+        pb, desc.b_stride = _tokens("B", B, keys, to, dev)
+        pc, desc.c_stride = _tokens("C", C, keys, to, dev)
+        state = (n_seq, h, self.d_state, self.d_head)
+        return (desc, at, px, pt, _tensor("A", A, (h,), f32, dev), pb, pc, _maybe("D", D, (h,), f32, dev),
+                _maybe("dt_bias", dt_bias, (h,), f32, dev)), _maybe("S0", S0, state, f32, dev), dev, n, state
 
     def forward(self, x, dt, A, B, C, cu, y, D=None, dt_bias=None, S0=None, S_out=None, stream=None):
         """y [tokens, n_heads, d_head] and, where given, the final states S_out; cu: int32 [n_seq + 1] on the device, the
         tokens at which the sequences begin and end.  Returns the call's number, for backward."""
-        import torch
-        dev, n, n_seq, strides = self._inputs(x, dt, A, B, C, cu, D, dt_bias, S0)
-        _tensor("y", y, (n, self.n_heads, self.d_head), self.y_dtype, dev)
-        if S_out is not None:
-            _tensor("S_out", S_out, (n_seq, self.n_heads, self.d_state, self.d_head), torch.float32, dev)
-        sq_scan_forward(self._desc(n_seq, n, *strides), cu, x, dt, A, B, C, D, dt_bias, S0, y, S_out, self.save, self.work, stream=stream)
-        self.calls, self._sizes = self.calls + 1, (n_seq, n)
+        args, start, dev, n, state = self._inputs(x, dt, A, B, C, cu, D, dt_bias, S0)
+        py = _tensor("y", y, (n, self.n_heads, self.d_head), self.y_dtype, dev)
+        save, save_bytes = _span(self.save)
+        work, work_bytes = _span(self.work)
+        sq_scan_forward(*args, start, py, _maybe("S_out", S_out, state, _torch.float32, dev), save, work, save_bytes, work_bytes, stream)
+        self.calls, self._sizes = self.calls + 1, (state[0], n)
         return self.calls
 
     def backward(self, x, dt, A, B, C, cu, dy, dx, ddt, dA, dB, dC, D=None, dt_bias=None, dD=None, ddt_bias=None, S0=None, dS_out=None,
@@ -380,51 +378,45 @@ class SelectiveScan:
         """Gradients of the last forward call, which had the same inputs; dy dense and in `dtype`; dA, dD and ddt_bias
         are written, not added to.  call: what that forward returned; raises RuntimeError where another one came
         after it."""
-        import torch
         if self.save is None:
             raise ValueError("backward needs train=True")
-        dev, n, n_seq, strides = self._inputs(x, dt, A, B, C, cu, D, dt_bias, S0)
+        args, _, dev, n, state = self._inputs(x, dt, A, B, C, cu, D, dt_bias, S0)
         if self.calls == 0 or (call is not None and call != self.calls):
             raise RuntimeError("backward of forward call %s, but the saved states are of call %d" % (
                 "?" if call is None else call, self.calls))
-        if self._sizes != (n_seq, n):
-            raise RuntimeError("the last forward call had %d sequences of %d tokens, not %d of %d" % (*self._sizes, n_seq, n))
-        f32, h, keys = torch.float32, self.n_heads, (n, self.n_groups, self.d_state)
-        _tensor("dy", dy, (n, h, self.d_head), self.dtype, dev)
-        strides += (_tokens("dx", dx, (n, h, self.d_head), self.dtype, dev), _tokens("ddt", ddt, (n, h), self.dtype, dev),
-                    _tokens("dB", dB, keys, self.dtype, dev), _tokens("dC", dC, keys, self.dtype, dev))
-        _tensor("dA", dA, (h,), f32, dev)
-        for name, t in (("dD", dD), ("ddt_bias", ddt_bias)):
-            if t is not None:
-                _tensor(name, t, (h,), f32, dev)
-        for name, t in (("dS_out", dS_out), ("dS0", dS0)):
-            if t is not None:
-                _tensor(name, t, (n_seq, h, self.d_state, self.d_head), f32, dev)
-        sq_scan_backward(self._desc(n_seq, n, *strides), cu, x, dt, A, B, C, D, dt_bias, dy, dS_out, self.save, dx, ddt, dA, dB, dC, dD,
-                         ddt_bias, dS0, self.work, stream=stream)
+        if self._sizes != (state[0], n):
+            raise RuntimeError("the last forward call had %d sequences of %d tokens, not %d of %d" % (*self._sizes, state[0], n))
+        f32, to, h, desc = _torch.float32, self.dtype, self.n_heads, args[0]
+        wide, keys = (n, h, self.d_head), (n, self.n_groups, self.d_state)
+        pdx, desc.dx_stride = _tokens("dx", dx, wide, to, dev)
+        pdt, desc.ddt_stride = _tokens("ddt", ddt, (n, h), to, dev)
+        pdb, desc.db_stride = _tokens("dB", dB, keys, to, dev)
+        pdc, desc.dc_stride = _tokens("dC", dC, keys, to, dev)
+        save, save_bytes = _span(self.save)
+        work, work_bytes = _span(self.work)
+        sq_scan_backward(*args, _tensor("dy", dy, wide, to, dev), _maybe("dS_out", dS_out, state, f32, dev), save, pdx, pdt,
+                         _tensor("dA", dA, (h,), f32, dev), pdb, pdc, _maybe("dD", dD, (h,), f32, dev), _maybe("ddt_bias", ddt_bias, (h,), f32, dev),
+                         _maybe("dS0", dS0, state, f32, dev), work, save_bytes, work_bytes, stream)
 
 
 def scan_step(pool, slot_idx, x, dt, A, B, C, y, D=None, dt_bias=None, softplus=True, stream=None) -> None:
     """One token per request on an fp32 pool [n_slots, n_heads, d_state, d_head], in place on the listed slots, which
     are distinct: x, y [n, n_heads, d_head], dt [n, n_heads], B, C [n, n_groups, d_state].  Requests whose slot is outside the
     pool are left out."""
-    import torch
+    torch = _load()
     n_slots, h, ns, p = pool.shape
-    n, dev, f32 = slot_idx.numel(), _home(pool), torch.float32
-    _tensor("pool", pool, (n_slots, h, ns, p), f32, dev)
-    _tensor("slot_idx", slot_idx, (n,), torch.int32, dev)
+    n, dev, f32, to = slot_idx.numel(), _home(pool), torch.float32, x.dtype
     if B.dim() != 3:
         raise ValueError("B must be [n, n_groups, d_state]")
-    types, keys = (_type(x.dtype, "x"), _type(y.dtype, "y")), (n, B.shape[1], ns)
-    strides = (_tokens("x", x, (n, h, p), x.dtype, dev), _tokens("dt", dt, (n, h), x.dtype, dev), _tokens("B", B, keys, x.dtype, dev),
-               _tokens("C", C, keys, x.dtype, dev))
-    _tensor("A", A, (h,), f32, dev)
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            _tensor(name, t, (h,), f32, dev)
-    _tensor("y", y, (n, h, p), y.dtype, dev)
-    sq_scan_step(scan_desc(0, 0, h, p, ns, keys[1], softplus, *types, *strides), pool, n_slots, slot_idx, n, x, dt, A, B, C, D, dt_bias, y,
-                 stream)
+    keys = (n, B.shape[1], ns)
+    px, xs = _tokens("x", x, (n, h, p), to, dev)
+    pt, ts = _tokens("dt", dt, (n, h), to, dev)
+    pb, bs = _tokens("B", B, keys, to, dev)
+    pc, cs = _tokens("C", C, keys, to, dev)
+    sq_scan_step(scan_desc(0, 0, h, p, ns, keys[1], softplus, _type(to, "x"), _type(y.dtype, "y"), xs, ts, bs, cs),
+                 _tensor("pool", pool, (n_slots, h, ns, p), f32, dev), n_slots, _tensor("slot_idx", slot_idx, (n,), torch.int32, dev), n, px, pt,
+                 _tensor("A", A, (h,), f32, dev), pb, pc, _maybe("D", D, (h,), f32, dev), _maybe("dt_bias", dt_bias, (h,), f32, dev),
+                 _tensor("y", y, (n, h, p), y.dtype, dev), stream)
 
 
 # ------------------------------------------------------------------ norms
@@ -438,49 +430,42 @@ class GatedNorm:
 
     def __init__(self, n_groups: int, d: int, act="silu", gate_first=False, shared_weight=True, eps=1e-6, dtype=None, device="cuda",
                  train=False, n_tokens=None):
-        import torch
+        torch = _load()
         self.dtype = torch.bfloat16 if dtype is None else dtype
-        self._code = _type(self.dtype, "dtype")
         self.n_groups, self.d, self.act, self.eps = int(n_groups), int(d), ACTS[act], float(eps)
         self.gate_first, self.shared_weight = bool(gate_first), bool(shared_weight)
         most = (1 << 31) // max(1, self.n_groups) - 1
-        nbytes = sq_gated_norm_bytes(self._desc(most if n_tokens is None else n_tokens))
+        self._desc = gated_norm_desc(most if n_tokens is None else n_tokens, n_groups, d, self.shared_weight, self.gate_first, self.act,
+                                     self.eps, _type(self.dtype, "dtype"))
+        nbytes = sq_gated_norm_bytes(self._desc)
         self.work = _room(nbytes, device) if train else None
-
-    def _desc(self, n_tokens, *strides):
-        return gated_norm_desc(n_tokens, self.n_groups, self.d, self.shared_weight, self.gate_first, self.act, self.eps, self._code, *strides)
+        self._wide = (self.d,) if self.shared_weight else (self.n_groups, self.d)
 
     def _args(self, x, z, weight):
-        import torch
-        dev, shape = _home(x), (x.shape[0], self.n_groups, self.d)
-        xs = _tokens("x", x, shape, self.dtype, dev)
+        dev, shape, desc = _home(x), (x.shape[0], self.n_groups, self.d), _copy(self._desc)
+        desc.n_tokens = shape[0]
+        px, desc.x_stride = _tokens("x", x, shape, self.dtype, dev)
         if (z is None) != (self.act == SQ_ACT_NONE):
             raise ValueError("z is needed with a gate, and only then")
-        zs = 0 if z is None else _tokens("z", z, shape, self.dtype, dev)
-        wide = (self.d,) if self.shared_weight else (self.n_groups, self.d)
-        if weight is not None:
-            _tensor("weight", weight, wide, torch.float32, dev)
-        return dev, shape, wide, xs, zs
+        pz, desc.z_stride = (None, 0) if z is None else _tokens("z", z, shape, self.dtype, dev)
+        return desc, px, pz, _maybe("weight", weight, self._wide, _torch.float32, dev), dev, shape
 
     def forward(self, x, z, weight, y, stream=None):
-        dev, shape, _, xs, zs = self._args(x, z, weight)
-        _tensor("y", y, shape, self.dtype, dev)
-        sq_gated_norm_forward(self._desc(shape[0], xs, zs), x, z, weight, y, stream)
+        desc, px, pz, pw, dev, shape = self._args(x, z, weight)
+        sq_gated_norm_forward(desc, px, pz, pw, _tensor("y", y, shape, self.dtype, dev), stream)
 
     def backward(self, x, z, weight, dy, dx, dz, dweight=None, stream=None):
         """Gradients for the inputs of a forward call; dweight is written, not added to."""
-        import torch
-        dev, shape, wide, xs, zs = self._args(x, z, weight)
-        _tensor("dy", dy, shape, self.dtype, dev)
-        dxs = _tokens("dx", dx, shape, self.dtype, dev)
+        desc, px, pz, pw, dev, shape = self._args(x, z, weight)
+        pdy = _tensor("dy", dy, shape, self.dtype, dev)
+        pdx, desc.dx_stride = _tokens("dx", dx, shape, self.dtype, dev)
         if (dz is None) != (z is None):
             raise ValueError("dz is needed with a gate, and only then")
-        dzs = 0 if dz is None else _tokens("dz", dz, shape, self.dtype, dev)
-        if dweight is not None:
-            _tensor("dweight", dweight, wide, torch.float32, dev)
-            if self.work is None:
-                raise ValueError("dweight needs train=True")
-        sq_gated_norm_backward(self._desc(shape[0], xs, zs, dxs, dzs), x, z, weight, dy, dx, dz, dweight, self.work, stream=stream)
+        pdz, desc.dz_stride = (None, 0) if dz is None else _tokens("dz", dz, shape, self.dtype, dev)
+        pdw = _maybe("dweight", dweight, self._wide, _torch.float32, dev)
+        if pdw is not None and self.work is None:
+            raise ValueError("dweight needs train=True")
+        sq_gated_norm_backward(desc, px, pz, pw, pdy, pdx, pdz, pdw, *_span(self.work), stream)
 
 
 class ResidualNorm:
@@ -490,50 +475,36 @@ class ResidualNorm:
     gradients fp32 [d].  train=True holds backward's workspace."""
 
     def __init__(self, d: int, eps=1e-6, dtype=None, res_dtype=None, device="cuda", train=False):
-        import torch
+        torch = _load()
         self.dtype = torch.bfloat16 if dtype is None else dtype
         self.res_dtype = self.dtype if res_dtype is None else res_dtype
-        self._types = (_type(self.dtype, "dtype"), _type(self.res_dtype, "res_dtype"))
         self.d, self.eps = int(d), float(eps)
-        nbytes = sq_residual_norm_bytes(self._desc((1 << 31) - 1))
+        self._desc = residual_norm_desc((1 << 31) - 1, d, eps, _type(self.dtype, "dtype"), _type(self.res_dtype, "res_dtype"))
+        nbytes = sq_residual_norm_bytes(self._desc)
         self.work = _room(nbytes, device) if train else None
 
-    def _desc(self, n_rows):
-        return residual_norm_desc(n_rows, self.d, self.eps, *self._types)
-
-    def _args(self, o, r, params):
-        import torch
-        dev, shape = _home(o), o.shape
+    def _args(self, o, r, post_weight, scale, weight):
+        dev, shape, desc, row, f32 = _home(o), o.shape, _copy(self._desc), (self.d,), _torch.float32
         if o.dim() < 1 or shape[-1] != self.d:
             raise ValueError("o has shape %s, expected [..., %d]" % (tuple(shape), self.d))
-        _tensor("o", o, shape, self.dtype, dev)
-        if r is not None:
-            _tensor("r", r, shape, self.res_dtype, dev)
-        for name, t in params:
-            if t is not None:
-                _tensor(name, t, (self.d,), torch.float32, dev)
-        return dev, shape, o.numel() // self.d
+        desc.n_rows = o.numel() // self.d
+        return (desc, _tensor("o", o, shape, self.dtype, dev), _maybe("r", r, shape, self.res_dtype, dev), _maybe("post_weight", post_weight, row, f32, dev),
+                _maybe("scale", scale, row, f32, dev), _maybe("weight", weight, row, f32, dev)), dev, shape
 
     def forward(self, o, r, r_out, weight=None, h=None, post_weight=None, scale=None, stream=None):
         """r None: zeros; h None: the sum alone; r_out may be r."""
-        dev, shape, n = self._args(o, r, (("weight", weight), ("post_weight", post_weight), ("scale", scale)))
-        _tensor("r_out", r_out, shape, self.res_dtype, dev)
-        if h is not None:
-            _tensor("h", h, shape, self.dtype, dev)
-        sq_residual_norm_forward(self._desc(n), o, r, post_weight, scale, weight, r_out, h, stream)
+        args, dev, shape = self._args(o, r, post_weight, scale, weight)
+        sq_residual_norm_forward(*args, _tensor("r_out", r_out, shape, self.res_dtype, dev), _maybe("h", h, shape, self.dtype, dev), stream)
 
     def backward(self, o, r, dh, dr_out, do, dr, weight=None, dweight=None, post_weight=None, dpost_weight=None, scale=None, dscale=None,
                  stream=None):
         """Gradients from o and r as the forward call had them (so not from an r that r_out took the place of); dh, dr_out, dr
         and the parameters' gradients may be None; the latter are written, not added to."""
-        params = (("weight", weight), ("dweight", dweight), ("post_weight", post_weight), ("dpost_weight", dpost_weight), ("scale", scale),
-                  ("dscale", dscale))
-        dev, shape, n = self._args(o, r, params)
-        _tensor("do", do, shape, self.dtype, dev)
-        for name, t, dtype in (("dh", dh, self.dtype), ("dr_out", dr_out, self.res_dtype), ("dr", dr, self.res_dtype)):
-            if t is not None:
-                _tensor(name, t, shape, dtype, dev)
-        if self.work is None and (dweight is not None or dpost_weight is not None or dscale is not None):
+        args, dev, shape = self._args(o, r, post_weight, scale, weight)
+        row, f32 = (self.d,), _torch.float32
+        pdo = _tensor("do", do, shape, self.dtype, dev)
+        grads = [_maybe(name, t, row, f32, dev) for name, t in (("dpost_weight", dpost_weight), ("dscale", dscale), ("dweight", dweight))]
+        if self.work is None and any(g is not None for g in grads):
             raise ValueError("gradients of parameters need train=True")
-        sq_residual_norm_backward(self._desc(n), o, r, post_weight, scale, weight, dh, dr_out, do, dr, dpost_weight, dscale, dweight, self.work,
-                                  stream=stream)
+        sq_residual_norm_backward(*args, _maybe("dh", dh, shape, self.dtype, dev), _maybe("dr_out", dr_out, shape, self.res_dtype, dev), pdo,
+                                  _maybe("dr", dr, shape, self.res_dtype, dev), *grads, *_span(self.work), stream)
