@@ -295,7 +295,8 @@ template <int N, bool F32> hipError_t back(const ScanArgs &a, hipStream_t stream
 }
 
 // One token of one head a workgroup; a thread has 4 columns of every 16th (d_head 128: 8th) row.  Bound by memory: the
-// state goes through registers once.
+// state goes through registers once, past the caches, which no other reader would find it in (512 requests x 64 heads, 2.1 GB:
+// 385 us, 5.6 TB/s; through the caches 417).
 template <int N, int P, bool F32, bool YF32> __global__ __launch_bounds__(256) void step_kernel(ScanArgs a) {
     constexpr int LANES = P / 4, ROWS = 256 / LANES, COUNT = N / ROWS;
     __shared__ float sB[N], sC[N], sum[4][P];
@@ -307,7 +308,7 @@ template <int N, int P, bool F32, bool YF32> __global__ __launch_bounds__(256) v
     float *p = a.pool + ((int64_t)slot * a.n_heads + h) * N * P + row * P + col;
     f4 S[COUNT];
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) S[i] = *reinterpret_cast<const f4 *>(p + i * ROWS * P);
+    for (int i = 0; i < COUNT; ++i) S[i] = __builtin_nontemporal_load(reinterpret_cast<const f4 *>(p + i * ROWS * P));
     for (int i = t; i < N; i += 256) {
         sB[i] = ld_elem<F32>(a.B, req * a.b_stride + (int64_t)group * N + i);
         sC[i] = ld_elem<F32>(a.C, req * a.c_stride + (int64_t)group * N + i);
@@ -328,7 +329,7 @@ template <int N, int P, bool F32, bool YF32> __global__ __launch_bounds__(256) v
             S[i][e] = fmaf(S[i][e], fade, k * x[e]);
             y[e] = fmaf(S[i][e], c, y[e]);
         }
-        *reinterpret_cast<f4 *>(p + i * ROWS * P) = S[i];
+        __builtin_nontemporal_store(S[i], reinterpret_cast<f4 *>(p + i * ROWS * P));
     }
 #pragma unroll
     for (int m = LANES; m < 64; m <<= 1)
