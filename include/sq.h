@@ -579,8 +579,10 @@ sq_status sq_scan_bytes(const sq_scan_desc *desc, size_t *work, size_t *save);
  *   A: fp32 [n_heads];  D, dt_bias: fp32 [n_heads], or NULL for zeros.
  * Arithmetic: states, sums and decays in fp32 (running sums of dt A in fp64); matrix products on
  * operands split into bf16 terms so that S_out (and an fp32 y) has fp32 accuracy, a bf16 y 16 bits
- * before its rounding.  dt A below -150 acts as -150 (its decay is 0 in fp32).  A NaN of dt makes its
- * head's results NaN from its token on (and possibly for earlier tokens of the same chunk).
+ * before its rounding.  dt A below -150 acts as -150 (its decay is 0 in fp32); a positive one makes the state
+ * grow, and beyond fp32's range over a chunk its results are infinite or NaN.  A NaN or an infinity among a token's
+ * inputs makes its head's results NaN (B, C: its group's) from its token on, and possibly for earlier tokens of the
+ * same chunk; other heads, groups and sequences are not touched by it.
  * Errors as sq_chunk_forward. */
 sq_status sq_scan_forward(const sq_scan_desc *desc, const int32_t *cu, const void *x,
                           const void *raw, const float *A, const void *B, const void *C,
@@ -612,7 +614,8 @@ sq_status sq_scan_step(const sq_scan_desc *desc, float *state_pool, int32_t n_sl
 
 /* The norm behind a layer, with its gate, over rows of d (each group of a token):
  *   y = rms(x) * weight * act(z),  or, with gate_first, y = rms(x * act(z)) * weight,
- *   rms(x) = x / sqrt(mean(x^2) + eps).  x, z, y: [n_tokens, n_groups, d]. */
+ *   rms(x) = x / sqrt(mean(x^2) + eps), the squares summed in fp32 (so |x| under 1e19 / sqrt(d)).
+ * x, z, y: [n_tokens, n_groups, d]; y may be x itself where x is dense. */
 typedef struct {
     int64_t n_tokens;     /* >= 0; n_tokens * n_groups < 2^31 */
     int32_t n_groups;     /* 1 .. 65535 */

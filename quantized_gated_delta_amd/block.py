@@ -327,7 +327,8 @@ class SelectiveScan:
 
     For batches of up to n_seq sequences and n_tokens tokens in all.  With train=True, also what backward needs
     of the last forward call, which it belongs to: a second forward takes the first one's place, and
-    backward refuses the number of any call but the last.  x [tokens, n_heads, d_head], dt [tokens, n_heads], B and C
+    backward refuses the number of any call but the last (a replayed graph's calls have no number: give a graph an object
+    of its own).  x [tokens, n_heads, d_head], dt [tokens, n_heads], B and C
     [tokens, n_groups, d_state] and their gradients may be parts of wider tensors; A, D, dt_bias and their gradients
     are fp32 [n_heads], states fp32 [n_seq, n_heads, d_state, d_head]."""
 

@@ -183,8 +183,9 @@ struct ResidualArgs {
     float eps;
 };
 constexpr int kNormMax = 16384;  // longest row: 1024 threads of 16 elements
-// Workgroups of a backward pass along the rows: each leaves its sums over rows in `partial`.
-int norm_blocks(int64_t rows, int32_t d);
+// Workgroups of a backward pass along the rows (512 in all groups that have weights of their own): each leaves its sums
+// over rows in `partial`.
+int norm_blocks(int64_t rows, int32_t d, int32_t groups);
 hipError_t launch_gate_forward(const GateArgs &a, bool f32, bool vec, bool first, bool shared, hipStream_t stream);
 hipError_t launch_gate_backward(const GateArgs &a, bool f32, bool vec, bool first, bool shared, hipStream_t stream);
 hipError_t launch_residual_forward(const ResidualArgs &a, bool f32, bool res_f32, bool vec, hipStream_t stream);

@@ -401,7 +401,7 @@ sq_status sq_gated_norm_bytes(const sq_gated_norm_desc *desc, size_t *work) {
     sq_status st = check_gate(desc);
     if (st) return st;
     if (!work) return fail(SQ_EINVAL, "work is NULL");
-    *work = (size_t)sqk::norm_blocks(gate_rows(desc), desc->d) * (desc->shared_weight ? 1 : desc->n_groups) * desc->d * sizeof(float);
+    *work = (size_t)sqk::norm_blocks(gate_rows(desc), desc->d, desc->shared_weight ? 1 : desc->n_groups) * (desc->shared_weight ? 1 : desc->n_groups) * desc->d * sizeof(float);
     return SQ_OK;
 }
 
@@ -453,7 +453,7 @@ sq_status sq_residual_norm_bytes(const sq_residual_norm_desc *desc, size_t *work
     sq_status st = check_residual(desc);
     if (st) return st;
     if (!work) return fail(SQ_EINVAL, "work is NULL");
-    *work = (size_t)sqk::norm_blocks(desc->n_rows, desc->d) * 3 * desc->d * sizeof(float);
+    *work = (size_t)sqk::norm_blocks(desc->n_rows, desc->d, 1) * 3 * desc->d * sizeof(float);
     return SQ_OK;
 }
 

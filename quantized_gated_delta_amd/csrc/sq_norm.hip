@@ -459,9 +459,9 @@ static uint32_t forward_blocks(int64_t rows, int32_t d, int64_t at_most) {
     return (uint32_t)(turns < fit ? turns : fit > 1 ? fit : 1);
 }
 
-int norm_blocks(int64_t rows, int32_t d) {
-    const int64_t turns = (rows + rows_at_once(d, vectors_of(d)) - 1) / rows_at_once(d, vectors_of(d));
-    return (int)(turns < 512 ? (turns > 0 ? turns : 1) : 512);
+int norm_blocks(int64_t rows, int32_t d, int32_t groups) {
+    const int64_t turns = (rows + rows_at_once(d, vectors_of(d)) - 1) / rows_at_once(d, vectors_of(d)), most = groups < 512 ? 512 / groups : 1;
+    return (int)(turns < 1 ? 1 : turns < most ? turns : most);
 }
 
 hipError_t launch_column_sums(const SumArgs *a, int count, hipStream_t stream) {
@@ -491,7 +491,7 @@ hipError_t launch_gate_forward(const GateArgs &a, bool f32, bool vec, bool first
 hipError_t launch_gate_backward(const GateArgs &a, bool f32, bool vec, bool first, bool shared, hipStream_t stream) {
     const int k = vectors_of(a.d);
     const int64_t rows = shared ? a.n_tokens * a.groups : a.n_tokens;
-    const int blocks = norm_blocks(rows, a.d);
+    const int blocks = norm_blocks(rows, a.d, shared ? 1 : a.groups);
     const dim3 grid(blocks, shared ? 1 : a.groups), block(threads_of(a.d, k));
     pick(f32, [&](auto F) { pick(vec, [&](auto V) { pick(first, [&](auto G) { pick(shared, [&](auto S) { pick_row(a.d, [&](auto R) {
         hipLaunchKernelGGL((gate_backward_kernel<F.value, V.value, G.value, S.value, R.K, R.T>), grid, block, 0, stream, a, (uint32_t)rows);
@@ -513,7 +513,7 @@ hipError_t launch_residual_forward(const ResidualArgs &a, bool f32, bool res_f32
 }
 
 hipError_t launch_residual_backward(const ResidualArgs &a, bool f32, bool res_f32, bool vec, hipStream_t stream) {
-    const int k = vectors_of(a.d), blocks = norm_blocks(a.n_rows, a.d);
+    const int k = vectors_of(a.d), blocks = norm_blocks(a.n_rows, a.d, 1);
     const dim3 grid(blocks), block(threads_of(a.d, k));
     pick(f32, [&](auto F) { pick(res_f32, [&](auto R) { pick(vec, [&](auto V) { pick_row(a.d, [&](auto W) {
         hipLaunchKernelGGL((residual_backward_kernel<F.value, R.value, V.value, W.K, W.T>), grid, block, 0, stream, a);

@@ -222,6 +222,57 @@ def test_many_short_sequences_and_many_heads():
     check(b, run(b))
 
 
+def test_long_sequences_in_long_segments():
+    """Many chunks on many heads: segments of 512 tokens, sequences that end inside one."""
+    for lens in ((9000,), (513, 4100, 1, 511)):
+        b = batch(lens=lens, H=16, N=64, dtype=F32)
+        check(b, run(b, train=False))
+
+
+def test_steps_of_time_as_a_part_of_a_projection():
+    b = batch(lens=(70, 30), H=3)
+    want = run(b)
+    wide = torch.full((100, 11), float("nan"), dtype=BF, device=DEV)
+    wide[:, 4:7] = b["dt"]
+    grad = torch.full((100, 9), 7.0, dtype=BF, device=DEV)
+    out = dict(y=torch.empty_like(want["y"]), S=torch.empty_like(want["S"]), **gradients(b))
+    out["ddt"] = grad[:, 1:4]
+    run(dict(b, dt=wide[:, 4:7]), out=out)
+    for k in want:
+        assert torch.equal(out[k], want[k]), k
+    assert (grad[:, 0] == 7).all() and (grad[:, 4:] == 7).all()
+
+
+def test_infinite_inputs_stay_in_their_group_and_sequence():
+    b = batch(lens=(150, 80), H=4, G=2)
+    clean = run(b, train=False)
+    b["B"][100, 1, 5] = float("inf")
+    out = run(b, train=False)
+    assert not torch.isfinite(out["y"][100:150, 2:]).all()
+    assert torch.equal(out["y"][:150, :2], clean["y"][:150, :2]) and torch.equal(out["y"][:64], clean["y"][:64])
+    assert torch.equal(out["y"][150:], clean["y"][150:]) and torch.equal(out["S"][1], clean["S"][1])
+
+
+def test_debug_mode_refuses_lists(monkeypatch):
+    b = batch(lens=(20, 30), H=2, N=64)
+    monkeypatch.setenv("SQ_DEBUG", "1")
+    run(b)
+    b["cu"][1] = 60
+    with pytest.raises(Q.SQError, match="cu"):
+        run(b, train=False)
+    pool, y = torch.zeros(4, 2, 64, 64, device=DEV), torch.empty(3, 2, 64, dtype=BF, device=DEV)
+    args = [b[k][:3] for k in ("x", "dt")] + [b["A"]] + [b[k][:3] for k in ("B", "C")] + [y]
+    slots = lambda *s: torch.tensor(s, dtype=torch.int32, device=DEV)  # noqa: E731
+    Q.scan_step(pool, slots(-1, 2, -1), *args)
+    with pytest.raises(Q.SQError, match="repeated"):
+        Q.scan_step(pool, slots(1, 2, 1), *args)
+    x = torch.zeros(3, 16, dtype=BF, device=DEV)
+    conv = [torch.zeros(4, 3, 16, dtype=BF, device=DEV), x, torch.zeros(16, 4, device=DEV), torch.empty_like(x)]
+    Q.conv_step(conv[0], slots(9, 2, -1), *conv[1:])
+    with pytest.raises(Q.SQError, match="repeated"):
+        Q.conv_step(conv[0], slots(2, 0, 2), *conv[1:])
+
+
 def test_gradients_against_differences():
     """The gradient of a weighted sum of y and S along a random direction, by central differences in 64 bits."""
     b = batch(lens=(37, 5), H=2, dtype=F32)
