@@ -501,7 +501,7 @@ typedef enum { SQ_ACT_NONE = 0, SQ_ACT_SILU = 1, SQ_ACT_SIGMOID = 2 } sq_act;
  * where the width - 1 inputs before a sequence are the rows of its S0 (or 0). */
 typedef struct {
     int32_t n_seq;        /* sequences, >= 0 */
-    int32_t n_channels;   /* >= 1 */
+    int32_t n_channels;   /* 1 .. 2^23 */
     int32_t width;        /* taps: 2, 3 or 4 */
     int64_t n_tokens;     /* tokens of all sequences, < 2^31 - 2^16 */
     sq_act act;           /* SQ_ACT_NONE or SQ_ACT_SILU */
@@ -521,7 +521,8 @@ sq_status sq_conv_bytes(const sq_conv_desc *desc, size_t *work);
  *   S_out:  as S0: the last width - 1 inputs of each sequence (of S0 where it is
  *           shorter), or NULL.  Apart from S0.
  * Sums in fp32.  n_seq = 0 is a no-op.  Errors: SQ_EINVAL for a NULL or misaligned pointer (the
- * size of an element), a bad stride or overlapping buffers, SQ_EUNSUPPORTED for another width. */
+ * size of an element), a bad stride or overlapping buffers, SQ_EUNSUPPORTED for another width, or for
+ * n_tokens / 64 + n_seq from 2^24 on. */
 sq_status sq_conv_forward(const sq_conv_desc *desc, const int32_t *cu, const void *x,
                           const float *weight, const float *bias, const void *S0, void *y,
                           void *S_out, hipStream_t stream);
@@ -529,7 +530,7 @@ sq_status sq_conv_forward(const sq_conv_desc *desc, const int32_t *cu, const voi
 /* Gradients of sq_conv_forward for the same inputs (nothing is saved: p is formed again).
  *   dy: [n_tokens, n_channels];  dS_out: gradient of S_out, or NULL for zeros;
  *   dx: [n_tokens, n_channels];  dweight, dbias: fp32 as weight and bias, written (not
- *       added to), dbias NULL or not as bias;  dS0: gradient of S0, or NULL;
+ *       added to; zeros where n_seq = 0), dbias NULL or not as bias;  dS0: gradient of S0, or NULL;
  *   work: DEVICE scratch of sq_conv_bytes, 256-byte aligned. */
 sq_status sq_conv_backward(const sq_conv_desc *desc, const int32_t *cu, const void *x,
                            const float *weight, const float *bias, const void *S0, const void *dy,
@@ -593,7 +594,7 @@ sq_status sq_scan_forward(const sq_scan_desc *desc, const int32_t *cu, const voi
 /* Gradients of sq_scan_forward from the `save` that it filled for the same inputs.
  *   dy: gradient of y, dense, in in_dtype;  dS_out: fp32, or NULL for zeros;
  *   dx, draw, dB, dC: in in_dtype, B's and C's summed over the heads of a group, required;
- *   dA, dD, ddt_bias: fp32 [n_heads], written, the latter two NULL or not as wanted;
+ *   dA, dD, ddt_bias: fp32 [n_heads], written (zeros where n_seq = 0), the latter two NULL or not as wanted;
  *   dS0: fp32, or NULL; may be dS_out itself.
  * Nothing is written for tokens that no sequence has.  fp32 gradients have fp32 accuracy, bf16 ones 16
  * bits before their rounding.  Overwrites work, leaves save as it is. */

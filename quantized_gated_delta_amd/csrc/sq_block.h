@@ -162,6 +162,7 @@ struct ConvArgs {
 int conv_blocks(int64_t n_tokens, int32_t n_seq, int32_t channels);
 hipError_t launch_conv_forward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
 hipError_t launch_conv_backward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
+hipError_t launch_conv_sums(const ConvArgs &a, int blocks, hipStream_t stream);  // blocks 0: zeros
 hipError_t launch_conv_step(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
 
 struct GateArgs {

@@ -22,6 +22,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = 0x7FFFFFFFll - 65536;  // block numbers and ends of blocks stay in 32 bits
 constexpr int64_t kMaxStride = 1 << 24;
+constexpr int64_t kMaxThreads = 0xFFFFFFFFll;  // of a grid's axis
 
 int size_of(sq_dtype t) { return t == SQ_F32 ? 4 : 2; }
 bool is_type(sq_dtype t) { return t == SQ_F32 || t == SQ_BF16; }
@@ -108,10 +109,11 @@ sq_status check_conv(const sq_conv_desc *d, bool batch) {
     if (!d) return fail(SQ_EINVAL, "desc is NULL");
     sq_status st;
     if (batch && (st = check_batch(d->n_seq, d->n_tokens))) return st;
-    if (d->n_channels < 1 || d->n_channels > kMaxStride) return fail(SQ_EINVAL, "n_channels = %d must be in [1, 2^24]", d->n_channels);
+    if (d->n_channels < 1 || d->n_channels > (1 << 23)) return fail(SQ_EINVAL, "n_channels = %d must be in [1, 2^23]", d->n_channels);
     if (d->width < 2 || d->width > 4) return fail(SQ_EUNSUPPORTED, "width must be 2, 3 or 4 (got %d)", d->width);
     if (d->act != SQ_ACT_NONE && d->act != SQ_ACT_SILU) return fail(SQ_EUNSUPPORTED, "act must be SQ_ACT_NONE or SQ_ACT_SILU (got %d)", (int)d->act);
     if (!is_type(d->dtype)) return fail(SQ_EINVAL, "dtype must be SQ_F32 or SQ_BF16 (got %d)", (int)d->dtype);
+    if (batch && sqk::block_slots(d->n_tokens, d->n_seq, 6) > kMaxThreads / 256) return fail(SQ_EUNSUPPORTED, "n_tokens / 64 + n_seq exceeds the grid limit");
     return check_stride("x_stride", d->x_stride, d->n_channels, 1);
 }
 sqk::ConvArgs conv_args(const sq_conv_desc *d, const int32_t *cu, const void *x, const float *weight, const float *bias) {
@@ -152,8 +154,7 @@ sq_status check_scan(const sq_scan_desc *d, bool batch) {
     if (wide > kMaxStride || keys > kMaxStride) return fail(SQ_EUNSUPPORTED, "n_heads * d_head or n_groups * d_state exceeds 2^24");  // 32-bit offsets within a chunk
     if (batch) {
         const sqk::ScanPlan p = sqk::scan_plan(*d);
-        const int64_t grid = 0x7FFFFFFFll;
-        if (p.seg_slots > grid / ((p.parts + 7) / 8 * 8) || p.chunk_slots > grid / p.parts || p.chunk_slots > grid / ((int64_t)d->n_groups * p.subsets))
+        if (p.seg_slots > kMaxThreads / 256 / ((p.parts + 7) / 8 * 8) || p.chunk_slots > kMaxThreads / 512 / ((int64_t)d->n_groups * p.subsets))
             return fail(SQ_EUNSUPPORTED, "n_tokens or n_seq times n_heads exceeds the grid limit");
     }
     return SQ_OK;
@@ -267,7 +268,13 @@ sq_status sq_conv_backward(const sq_conv_desc *desc, const int32_t *cu, const vo
     size_t need = 0;
     sq_status st = sq_conv_bytes(desc, &need);
     if (st) return st;
-    if (desc->n_seq == 0) return SQ_OK;
+    if (desc->n_seq == 0) {
+        if (!aligned(dweight, 4) || !aligned(dbias, 4)) return fail(SQ_EINVAL, "dweight or dbias is not 4-byte aligned");
+        sqk::ConvArgs a = conv_args(desc, nullptr, nullptr, nullptr, nullptr);
+        a.dweight = dweight; a.dbias = dbias;
+        const hipError_t err = sqk::launch_conv_sums(a, 0, stream);
+        return err == hipSuccess ? SQ_OK : hip_fail(err, "conv_backward launch");
+    }
     const int e = size_of(desc->dtype);
     const int64_t c = desc->n_channels, n = desc->n_tokens, xs = stride_or(desc->x_stride, c), state = desc->n_seq * (int64_t)(desc->width - 1) * c * e;
     const Arg args[] = {{kx, x, true, false, n, c * e, xs * e, (uintptr_t)e}, dense("weight", weight, true, false, c * desc->width * 4, 4),
@@ -291,6 +298,7 @@ sq_status sq_conv_step(const sq_conv_desc *desc, void *pool, int32_t n_slots, co
     sq_status st = check_conv(desc, false);
     if (st || (st = check_step(pool, n_slots, slot_idx, n))) return st;
     if (n == 0) return SQ_OK;
+    if (n > (1 << 27) - 8) return fail(SQ_EUNSUPPORTED, "n exceeds the grid limit");  // 8 requests to a workgroup where there are many
     const int e = size_of(desc->dtype);
     const int64_t c = desc->n_channels, xs = stride_or(desc->x_stride, c);
     const Arg args[] = {{kx, x, true, false, n, c * e, xs * e, (uintptr_t)e}, dense("weight", weight, true, false, c * desc->width * 4, 4),
@@ -348,7 +356,13 @@ sq_status sq_scan_backward(const sq_scan_desc *desc, const int32_t *cu, const vo
     size_t need = 0, keep = 0;
     sq_status st = sq_scan_bytes(desc, &need, &keep);
     if (st) return st;
-    if (desc->n_seq == 0) return SQ_OK;
+    if (desc->n_seq == 0) {
+        if (!aligned(dA, 4) || !aligned(dD, 4) || !aligned(ddt_bias, 4)) return fail(SQ_EINVAL, "dA, dD or ddt_bias is not 4-byte aligned");
+        const int64_t h = desc->n_heads;
+        const sqk::SumArgs s[3] = {{nullptr, dA, 0, h, h}, {nullptr, dD, 0, h, h}, {nullptr, ddt_bias, 0, h, h}};
+        const hipError_t err = sqk::launch_column_sums(s, 3, stream);
+        return err == hipSuccess ? SQ_OK : hip_fail(err, "scan_backward launch");
+    }
     const int e = size_of(desc->in_dtype);
     const int64_t n = desc->n_tokens, h = desc->n_heads, wide = h * desc->d_head, keys = (int64_t)desc->n_groups * desc->d_state;
     const int64_t state = desc->n_seq * h * desc->d_state * desc->d_head * 4;
@@ -382,7 +396,7 @@ sq_status sq_scan_step(const sq_scan_desc *desc, float *state_pool, int32_t n_sl
     if (n == 0) return SQ_OK;
     const int e = size_of(desc->in_dtype), ey = size_of(desc->y_dtype);
     const int64_t h = desc->n_heads, wide = h * desc->d_head, keys = (int64_t)desc->n_groups * desc->d_state;
-    if (n * h > 0x7FFFFFFFll) return fail(SQ_EUNSUPPORTED, "n * n_heads exceeds the grid limit");
+    if (n * h > kMaxThreads / 256) return fail(SQ_EUNSUPPORTED, "n * n_heads exceeds the grid limit");
     const Arg args[] = {{kx, x, true, false, n, wide * e, stride_or(desc->x_stride, wide) * e, 16}, {"raw", raw, true, false, n, h * e, stride_or(desc->dt_stride, h) * e, (uintptr_t)e},
                         dense("A", A, true, false, h * 4, 4), {"B", B, true, false, n, keys * e, stride_or(desc->b_stride, keys) * e, 16},
                         {"C", C, true, false, n, keys * e, stride_or(desc->c_stride, keys) * e, 16}, dense("D", D, false, false, h * 4, 4),

@@ -221,8 +221,11 @@ template <int W> __global__ __launch_bounds__(256) void conv_sums_kernel(ConvArg
     __syncthreads();
     if (w == 0 && c < a.channels) {
         const float sum = (lds[0][l] + lds[1][l]) + (lds[2][l] + lds[3][l]);
-        if (j < W) a.dweight[(int64_t)c * W + j] = sum;
-        else if (a.dbias) a.dbias[c] = sum;
+        if (j == W) {
+            if (a.dbias) a.dbias[c] = sum;
+        } else if (a.dweight) {
+            a.dweight[(int64_t)c * W + j] = sum;
+        }
     }
 }
 
@@ -296,7 +299,11 @@ hipError_t launch_conv_backward(const ConvArgs &a, bool f32, bool vec, hipStream
         hipLaunchKernelGGL((conv_backward_kernel<F.value, V.value, W.value>), grid, dim3(256), 0, stream, a, slots);
     }); }); });
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    return e == hipSuccess ? launch_conv_sums(a, blocks, stream) : e;
+}
+
+hipError_t launch_conv_sums(const ConvArgs &a, int blocks, hipStream_t stream) {
+    if (!a.dweight && !a.dbias) return hipSuccess;
     pick_width(a.width, [&](auto W) {
         hipLaunchKernelGGL(conv_sums_kernel<W.value>, dim3((a.channels + 63) / 64, W.value + 1), dim3(256), 0, stream, a, blocks);
     });

@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
             a.dots[(n * a.chunk_parts + chunk0 + (int64_t)c * parts) * 64 + l] = (dots[n][0][l] + dots[n][1][l]) + (dots[n][2][l] + dots[n][3][l]);
         }
     }
-    const bool end = BACK ? b.c == 0 : begin + (1 << a.seg_shift) >= b.len;
+    const bool end = BACK ? b.c == 0 : b.len - begin <= 1 << a.seg_shift;
     float *to = !READ ? seg : !end ? nullptr : BACK ? a.dS0 : a.S_out;
     if (to) {
         const int64_t row = READ ? a.d_head : kHeadPart;
@@ -258,7 +258,7 @@ template <int N, bool BACK> __global__ __launch_bounds__(256) void join_kernel(S
     int32_t lo, len;
     ragged_span(a.seqs, s, lo, len);
     const Part pt = part_of(a, part);
-    const int count = max(1, (len + (1 << a.seg_shift) - 1) >> a.seg_shift);
+    const int count = max(1, ((len - 1) >> a.seg_shift) + 1);
     const int64_t slot0 = (int64_t)(lo >> a.seg_shift) + s;
     const float *start = BACK ? a.dS_out : a.S0;
     f4 S{};

@@ -47,7 +47,9 @@ def conv_step(dsc=None, **kw):
     (dict(n_seq=-1), Q.SQ_EINVAL, "n_seq"), (dict(n_tokens=-1), Q.SQ_EINVAL, "n_tokens"), (dict(n_tokens=(1 << 31) - 1), Q.SQ_EUNSUPPORTED, "n_tokens"),
     (dict(n_channels=0), Q.SQ_EINVAL, "n_channels"), (dict(width=1), Q.SQ_EUNSUPPORTED, "width"), (dict(width=5), Q.SQ_EUNSUPPORTED, "width"),
     (dict(act=Q.SQ_ACT_SIGMOID), Q.SQ_EUNSUPPORTED, "act"), (dict(dtype=7), Q.SQ_EINVAL, "dtype"), (dict(x_stride=63), Q.SQ_EINVAL, "x_stride"),
-    (dict(x_stride=-64), Q.SQ_EINVAL, "x_stride"), (dict(x_stride=(1 << 24) + 1), Q.SQ_EINVAL, "x_stride")], ids=str)
+    (dict(x_stride=-64), Q.SQ_EINVAL, "x_stride"), (dict(x_stride=(1 << 24) + 1), Q.SQ_EINVAL, "x_stride"),
+    (dict(n_channels=(1 << 23) + 1), Q.SQ_EINVAL, "n_channels"), (dict(n_tokens=1 << 30), Q.SQ_EUNSUPPORTED, "grid"),
+    (dict(n_seq=1 << 24), Q.SQ_EUNSUPPORTED, "grid")], ids=str)
 def test_conv_descriptor(kw, status, text):
     refused(status, text, Q.sq_conv_bytes, conv_desc(**kw))
     refused(status, text, conv_forward, conv_desc(**kw))
@@ -82,12 +84,13 @@ def test_conv_sizes():
     assert all(Q.sq_conv_bytes(conv_desc(n_tokens=t, n_seq=s)) <= most for t in (0, 1, 63, 100, 5000, 99999) for s in (0, 1, 49))
     for kw, text in ((dict(n_slots=0), "n_slots"), (dict(n=-1), "n must")):
         refused(Q.SQ_EINVAL, text, conv_step, **kw)
+    refused(Q.SQ_EUNSUPPORTED, "grid", conv_step, n=1 << 27)
 
 
 def test_conv_no_ops():
     none = conv_desc(n_seq=0, n_tokens=0)
     conv_forward(none, cu=None, x=None, y=None)
-    conv_backward(none, cu=None, x=None, dy=None, dx=None, dweight=None, work=None)
+    conv_backward(none, cu=None, x=None, dy=None, dx=None, dweight=None, dbias=None, work=None)
     conv_step(n=0, pool=None, slot_idx=None, x=None, y=None)
 
 
@@ -121,7 +124,7 @@ def scan_step(dsc=None, **kw):
     (dict(x_stride=255), Q.SQ_EINVAL, "x_stride"), (dict(x_stride=260), Q.SQ_EINVAL, "x_stride"), (dict(b_stride=252), Q.SQ_EINVAL, "b_stride"),
     (dict(c_stride=1 << 25), Q.SQ_EINVAL, "c_stride"), (dict(dt_stride=3), Q.SQ_EINVAL, "dt_stride"), (dict(dx_stride=257), Q.SQ_EINVAL, "dx_stride"),
     (dict(ddt_stride=-1), Q.SQ_EINVAL, "ddt_stride"), (dict(db_stride=257), Q.SQ_EINVAL, "db_stride"), (dict(dc_stride=257), Q.SQ_EINVAL, "dc_stride"),
-    (dict(n_tokens=1 << 30, n_heads=16384), Q.SQ_EUNSUPPORTED, "grid")], ids=str)
+    (dict(n_tokens=1 << 30, n_heads=16384), Q.SQ_EUNSUPPORTED, "grid"), (dict(n_seq=1 << 22), Q.SQ_EUNSUPPORTED, "grid")], ids=str)
 def test_scan_descriptor(kw, status, text):
     refused(status, text, Q.sq_scan_bytes, scan_desc(**kw))
     refused(status, text, scan_forward, scan_desc(**kw))
@@ -180,7 +183,7 @@ def test_the_largest_batchs_buffers_serve_smaller_ones(heads, groups):
 def test_scan_no_ops():
     none = scan_desc(n_seq=0, n_tokens=0)
     scan_forward(none, cu=None, x=None, y=None, work=None)
-    scan_backward(none, cu=None, x=None, dy=None, dx=None, work=None)
+    scan_backward(none, cu=None, x=None, dy=None, dx=None, work=None, dA=None, dD=None, ddt_bias=None)
     scan_step(n=0, state_pool=None, slot_idx=None, x=None, y=None)
 
 

@@ -253,6 +253,15 @@ def test_infinite_inputs_stay_in_their_group_and_sequence():
     assert torch.equal(out["y"][150:], clean["y"][150:]) and torch.equal(out["S"][1], clean["S"][1])
 
 
+def test_empty_batches_leave_zeros_for_the_parameters():
+    for lens in ((), (0, 0)):
+        b = batch(lens=lens, H=3, N=64)
+        out = run(b)
+        assert all((out[k] == 0).all() for k in ("dA", "dD", "dbias")), lens
+        if lens:
+            assert torch.equal(out["S"], b["S0"]) and torch.equal(out["dS0"], b["dS"])
+
+
 def test_debug_mode_refuses_lists(monkeypatch):
     b = batch(lens=(20, 30), H=2, N=64)
     monkeypatch.setenv("SQ_DEBUG", "1")

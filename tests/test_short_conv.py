@@ -202,3 +202,12 @@ def test_steps_follow_the_convolution():
         Q.conv_step(S, slot, b["x"][t:t + 1], b["weight"], out, bias=b["bias"])
         assert torch.equal(out[0], whole["y"][t])
     assert torch.equal(S, whole["S"])
+
+
+def test_empty_batches_leave_zeros_for_the_parameters():
+    for lens in ((), (0, 0)):
+        b = batch(lens=lens, C=72, dtype=F32)
+        out = run(b)
+        assert (out["dweight"] == 0).all() and (out["dbias"] == 0).all(), lens
+        if lens:
+            assert torch.equal(out["S"], b["S0"]) and torch.equal(out["dS0"], b["dS"])
