@@ -63,10 +63,19 @@ struct Gates {
     float in[64];          // e^G: from the chunk's start to a token
     float out[64];         // e^{G_end - G}: from a token to the chunk's end
 };
-// From token j to a token i behind it; 0 where `live` is false.
-__device__ __forceinline__ float decay_of(const Gates &g, int i, int j, bool live) {
-    const float d = (g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j]);
-    return __builtin_amdgcn_exp2f(live ? d : -__builtin_inff());
+// x times the decays between four neighbouring tokens from `four` on and token `one`; LATER: the four are the later ones.
+// Pairs that do not meet get 0 by a choice between two values: as `live ? x * decay : 0`, each of the four, its loads
+// with it, goes behind a branch of its own (64 x 64 pairs of a chunk: 3000 cycles for 1750).
+template <bool LATER> __device__ __forceinline__ f4 decayed(const Gates &g, f4 x, int four, int one) {
+    const f4 hi = *reinterpret_cast<const f4 *>(&g.hi[four]), lo = *reinterpret_cast<const f4 *>(&g.lo[four]);
+    const float one_hi = g.hi[one], one_lo = g.lo[one];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float d = LATER ? (hi[e] - one_hi) + (lo[e] - one_lo) : (one_hi - hi[e]) + (one_lo - lo[e]);
+        const float v = x[e] * __builtin_amdgcn_exp2f(d);
+        x[e] = (LATER ? four + e >= one : four + e <= one) ? v : 0.f;
+    }
+    return x;
 }
 
 // Inclusive sums over the lanes of a wave.
@@ -102,17 +111,23 @@ __device__ __forceinline__ void make_gates(Gates &g, int l, bool live, float raw
     g.out[l] = exp2_of(end - G);
 }
 
+// Where row `row` of a PLACED token matrix lies in LDS: of each eight, the first four on the even places, so that the transposing
+// loads, which take four rows at once, two of those fours for 32 lanes, meet every bank once (passes over the chunks: 2 %
+// less; not where such loads are few, as addresses then cost more).
+__device__ __forceinline__ int place_of(int row) { return (row & ~7) | (row & 3) << 1 | (row >> 2 & 1); }
+
 // A matrix of 64 rows (tokens) in LDS, rows as they lie in memory and padded by 16 bytes.
-template <bool F32, int COLS> struct TokenMat {
+template <bool F32, int COLS, bool PLACED = true> struct TokenMat {
     typedef Elem<F32> E;
     static constexpr int ROW = COLS + (F32 ? 4 : 8), SIZE = 64 * ROW;
     static constexpr int VECS = COLS * (int)sizeof(E) / 16;  // 16-byte vectors of a row
+    __device__ __forceinline__ static int at(int row) { return PLACED ? place_of(row) : row; }
     // row `row`, elements k .. k + 7 of the contracted axis
-    __device__ __forceinline__ static Frag<F32, 1> get(const E *m, int row, int k) { return load_frag<F32, 1>(m + row * ROW + k, 0); }
+    __device__ __forceinline__ static Frag<F32, 1> get(const E *m, int row, int k) { return load_frag<F32, 1>(m + at(row) * ROW + k, 0); }
     // ... elements k .. k + 3 and k + 16 .. k + 19: the order in which two result tiles hold 32 rows
     __device__ __forceinline__ static Frag<F32, 1> get_split(const E *m, int row, int k) {
         Frag<F32, 1> f;
-        const E *p = m + row * ROW + k;
+        const E *p = m + at(row) * ROW + k;
         if constexpr (F32) {
             f.v[0] = *reinterpret_cast<const f4 *>(p);
             f.v[1] = *reinterpret_cast<const f4 *>(p + 16);
@@ -128,23 +143,46 @@ template <bool F32> __device__ __forceinline__ f4 load4(const Elem<F32> *p) {
     else return __builtin_convertvector(*reinterpret_cast<const bf4 *>(p), f4);
 }
 
+// c[n] += a[n] b[n], or with one a or b for all: products of the same terms one after another, so that each
+// accumulates while the others are issued (with their operands loaded ahead: the state's reading 2000 cycles for 1420 of a
+// chunk, its update 1450 for 1120).
+template <int P, int COUNT, bool ONE_A, bool ONE_B, int NA, int NB>
+__device__ __forceinline__ void mma_all(const Frag<false, NA> *a, const Frag<false, NB> *b, f4 *c) {
+#pragma unroll
+    for (int s = P - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int n = 0; n < COUNT; ++n)
+                    c[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[ONE_A ? 0 : n].t[i], b[ONE_B ? 0 : n].t[s - i], c[n], 0, 0, 0);
+}
+template <int P, int COUNT, bool ONE_A, bool ONE_B, int NA, int NB>
+__device__ __forceinline__ void mma_all(const Frag<true, NA> *a, const Frag<true, NB> *b, f4 *c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int n = 0; n < COUNT; ++n)
+            c[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[ONE_A ? 0 : n].v[i / 4][i % 4], b[ONE_B ? 0 : n].v[i / 4][i % 4], c[n], 0, 0, 0);
+}
+
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4v lds_s4v;
 // A fragment of the transposed matrix: row (lane) l % 16 is column col0 + l % 16 of m, contracted elements
 // are its rows row0 + 8 (l / 16) .. + 7.  bf16: the transposing LDS load, where 16 lanes take 4 rows of 16.
-template <bool F32, int N> __device__ __forceinline__ Frag<F32, N> get_t(const Elem<F32> *m, int row_size, int plane, int row0, int col0, int l) {
+template <bool F32, int N, bool PLACED = true> __device__ __forceinline__ Frag<F32, N> get_t(const Elem<F32> *m, int row_size, int plane, int row0, int col0, int l) {
     Frag<F32, N> f;
     const int r = l & 15, g = l >> 4;
     if constexpr (F32) {
         const float *p = m + (row0 + 8 * g) * row_size + col0 + r;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f.v[e / 4][e % 4] = p[e * row_size];
+        for (int e = 0; e < 8; ++e) f.v[e / 4][e % 4] = p[(PLACED ? place_of(e) : e) * row_size];
     } else {
-        const uint16_t *p = m + (row0 + 8 * g + (r >> 2)) * row_size + col0 + (r & 3) * 4;
+        const uint16_t *p = m + (row0 + 8 * g + (r >> 2) * (PLACED ? 2 : 1)) * row_size + col0 + (r & 3) * 4;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(p + n * plane));
-            const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(p + n * plane + 4 * row_size));
+            const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(p + n * plane + (PLACED ? 1 : 4) * row_size));
             f.t[n] = __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
         }
     }
@@ -164,8 +202,8 @@ __device__ __forceinline__ float sign_of(int tile) { return tile & 1 ? -1.f : 1.
 
 // Vectors of a token matrix as a workgroup of T threads loads them: from memory into
 // registers (behind the last row: it again), and from there into LDS.
-template <bool F32, int COLS, int T> struct Staged {
-    typedef TokenMat<F32, COLS> M;
+template <bool F32, int COLS, int T, bool PLACED = true> struct Staged {
+    typedef TokenMat<F32, COLS, PLACED> M;
     static constexpr int COUNT = 64 * M::VECS / T;
     uint4 v[COUNT];
     __device__ __forceinline__ void load(const void *base, uint32_t stride, int rows, int t) {
@@ -190,7 +228,7 @@ template <bool F32, int COLS, int T> struct Staged {
             const int row = (i * T + t) / M::VECS, col = (i * T + t) % M::VECS;
             const int turned = (TURN_ROWS ? row : 0) ^ (TURN_COLS ? col * 16 / (int)sizeof(Elem<F32>) : 0);
             const uint32_t flip = turned & 16 ? (F32 ? 0x80000000u : 0x80008000u) : 0u;
-            *(reinterpret_cast<uint4 *>(m + row * M::ROW) + col) = uint4{v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip};
+            *(reinterpret_cast<uint4 *>(m + M::at(row) * M::ROW) + col) = uint4{v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip};
         }
     }
 };

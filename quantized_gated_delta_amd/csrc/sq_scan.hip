@@ -117,6 +117,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
     for (int k = 0; k < n_chunks; ++k) {
         const int c = first + k * step, rows = rows_of(c);
         const Gates &g = gates[k % kGates];
+        // addresses in LDS are formed again for each chunk where there is no room to keep them
+        int lane = threadIdx.x;
+        if (PASS == kMainBack) asm volatile("" : "+v"(lane));
+        const int t = lane, l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
         // signs: the state's odd tiles of rows are turned, and so is what every second tile of queries reads
         rK.template store<false, true>(sK, t);
         rX.clear(rows, t);  // behind the end: what nothing is taken up of
@@ -137,24 +141,30 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
                 for (int i = 0; i < 4; ++i) *at_bytes<float>(keep + (16 * m + i) * kHeadPart, (g4 * kHeadPart + 16 * w + r) * 4) = sign_of(m) * S[m][i];
         }
         if (READ) {
+            // ten tiles: w, w + 4, w + 8; the last one three times rather than behind a branch, so that each step is
+            // taken for a wave's three together
+            int kt[3], qt[3];
+            f4 p[3] = {};
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {  // ten tiles: w, w + 4 and, for two waves, w + 8
-                if (j == 2 && w >= 2) break;
+            for (int j = 0; j < 3; ++j) {
                 int hi, lo;
-                pair_tile(w + 4 * j, hi, lo);
-                const int kt = BACK ? hi : lo, qt = BACK ? lo : hi, q = 16 * qt + r;
-                f4 p{};
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) p = mma<1>(KeyMat::get(sK, 16 * kt + r, 32 * kb + g8), KeyMat::get(sQ, q, 32 * kb + g8), p);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = 16 * kt + g4 + e;
-                    const bool live = BACK ? key >= q : key <= q;
-                    const float L = BACK ? decay_of(g, key, q, live) : decay_of(g, q, key, live) * g.dt[key];
-                    p[e] = live ? p[e] * L : 0.f;
-                }
-                PairMat::put4(pairs, q, 16 * kt + g4, p);
+                pair_tile(min(w + 4 * j, 9), hi, lo);
+                kt[j] = BACK ? hi : lo, qt[j] = BACK ? lo : hi;
             }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                Frag<F32, 1> fk[3], fq[3];
+#pragma unroll
+                for (int j = 0; j < 3; ++j) fk[j] = KeyMat::get(sK, 16 * kt[j] + r, 32 * kb + g8), fq[j] = KeyMat::get(sQ, 16 * qt[j] + r, 32 * kb + g8);
+                mma_all<1, 3, false, false>(fk, fq, p);
+            }
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                p[j] = decayed<BACK>(g, p[j], 16 * kt[j] + g4, 16 * qt[j] + r);
+                if (!BACK) p[j] *= *reinterpret_cast<const f4 *>(&g.dt[16 * kt[j] + g4]);
+            }
+#pragma unroll
+            for (int j = 0; j < 3; ++j) PairMat::put4(pairs, 16 * qt[j] + r, 16 * kt[j] + g4, p[j]);
             __syncthreads();
         }
         Frag<F32, 1> fx[2];
@@ -163,21 +173,32 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         if (READ) {
             // transposed, the result's columns as its rows: a lane then holds four neighbours of one token
             f4 y[4] = {}, y_out[4];
+            // a block's operands, the next one's on their way (main pass 87 -> 81 us, pass back, which has fewer registers
+            // left, 100 without and 102 with; 8192 tokens x 32 heads)
+            constexpr bool AHEAD = PASS == kMain;
+            Frag<F32, 1> fq[AHEAD ? 2 : 1][4];
+            auto queries = [&](int kb) {
+#pragma unroll
+                for (int qt = 0; qt < 4; ++qt) fq[AHEAD ? kb & 1 : 0][qt] = KeyMat::get_split(sQ, 16 * qt + r, 32 * kb + g4);
+            };
+            if (AHEAD) queries(0);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
+                if (!AHEAD) queries(kb);
+                else if (kb + 1 < KB) queries(kb + 1);
+                __builtin_amdgcn_sched_barrier(0);  // all blocks' operands at once would not fit the registers
                 float s[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[e] = S[2 * kb + e / 4][e % 4];
                 const Frag<F32, NT> fs = make_frag<F32, NT>(s);
-#pragma unroll
-                for (int qt = 0; qt < 4; ++qt) y[qt] = mma<NT>(fs, KeyMat::get_split(sQ, 16 * qt + r, 32 * kb + g4), y[qt]);
-                __builtin_amdgcn_sched_barrier(0);  // four blocks' operands at once would not fit the registers
+                mma_all<NT, 4, true, false>(&fs, fq[AHEAD ? kb & 1 : 0], y);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int qt = 0; qt < 4; ++qt) {
                 const int q = 16 * qt + r;
                 y[qt] *= BACK ? g.out[q] : g.in[q];
-                const f4 own = load4<F32>(sX + q * XMat::ROW + 16 * w + g4);
+                const f4 own = load4<F32>(sX + XMat::at(q) * XMat::ROW + 16 * w + g4);
                 float x[4], z = 0.f, u = 0.f;
                 if (BACK) {
                     widen_n<F32, 4>(this_x[PASS == kMainBack ? qt : 0], x);
@@ -225,11 +246,30 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
         const float whole = g.in[63];
         fade *= whole;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            S[m] *= whole;
+        for (int m = 0; m < MT; ++m) S[m] *= whole;
+        if (READ) {
+            constexpr bool AHEAD = PASS == kMain;
+            Frag<F32, 1> fk[AHEAD ? 2 : 1][4];  // of four tiles of rows
+            auto keys = [&](int n) {
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) S[m] = mma<3>(get_t<F32, 1>(sK, KeyMat::ROW, 0, 32 * kb, 16 * m, l), fs[kb], S[m]);
-            if (m % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                for (int m = 0; m < 4; ++m) fk[AHEAD ? n & 1 : 0][m] = get_t<F32, 1>(sK, KeyMat::ROW, 0, 32 * (n & 1), 16 * (n / 2 * 4 + m), l);
+            };
+            if (AHEAD) keys(0);
+#pragma unroll
+            for (int n = 0; n < MT / 2; ++n) {
+                if (!AHEAD) keys(n);
+                else if (n + 1 < MT / 2) keys(n + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                mma_all<3, 4, false, true>(fk[AHEAD ? n & 1 : 0], &fs[n & 1], S + n / 2 * 4);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {  // as the compiler orders it: 28 us, in the order above 29 (8192 tokens x 32 heads)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) S[m] = mma<3>(get_t<F32, 1>(sK, KeyMat::ROW, 0, 32 * kb, 16 * m, l), fs[kb], S[m]);
+                if (m % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
         }
         __syncthreads();
         if (PASS == kMainBack) {  // 0: z, 1: u; waves 2 and 3 store the same again

@@ -22,10 +22,17 @@ namespace {
 
 constexpr int kThreads = 512, kBatch = 8;
 
+// The decay from token j to a token i behind it; 0 where `live` is false.  (sq_scan.h's `decayed` is no faster here, with a wave's
+// one or two tiles beside its products over the state, and takes registers that are short: 170 us for 166.)
+__device__ __forceinline__ float decay_of(const Gates &g, int i, int j, bool live) {
+    const float d = (g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j]);
+    return __builtin_amdgcn_exp2f(live ? d : -__builtin_inff());
+}
+
 template <int N, bool F32> struct GradLds {
     typedef Elem<F32> E;
-    E B[TokenMat<F32, N>::SIZE], C[TokenMat<F32, N>::SIZE];
-    E x[TokenMat<F32, kHeadPart>::SIZE], dy[TokenMat<F32, kHeadPart>::SIZE];  // at the end V, [j][i]
+    E B[TokenMat<F32, N, false>::SIZE], C[TokenMat<F32, N, false>::SIZE];
+    E x[TokenMat<F32, kHeadPart, false>::SIZE], dy[TokenMat<F32, kHeadPart, false>::SIZE];  // at the end V, [j][i]
     Gates g[kBatch];
     // of two parts in turn: sums of W over a tile's rows (on the diagonal: what dg has of it), its columns and all of it;
     // dy . x; r and <S0, dS> by rows of the state
@@ -47,8 +54,8 @@ template <int N, bool F32>
 __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slots) {
     typedef Elem<F32> E;
     constexpr int NT = N / 16, KB = N / 32, TT = NT / 2;  // TT: token tiles of a wave in the products over the state
-    typedef TokenMat<F32, N> KeyMat;
-    typedef TokenMat<F32, kHeadPart> XMat;
+    typedef TokenMat<F32, N, false> KeyMat;
+    typedef TokenMat<F32, kHeadPart, false> XMat;
     typedef LdsMat<F32, 2, 64, 64> PairMat;
     __shared__ __attribute__((aligned(16))) GradLds<N, F32> s;
     static_assert(sizeof(s.x) + sizeof(s.dy) >= PairMat::BYTES, "V takes the place of x and dy");
@@ -70,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
     // the products over the state: rows 16 nt .., token tiles tt0 ..
     const int nt = w % NT, tt0 = w / NT * TT, v0 = h0 * halves, v1 = h1 * halves;
 
-    Staged<F32, kHeadPart, kThreads> rX, rY;
+    Staged<F32, kHeadPart, kThreads, false> rX, rY;
     Row8 rS[2], rD[2];
     auto load = [&](int v, int t, int r, int g8) {
         const Part pt = part_of(a, v);
@@ -85,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
         }
     };
     {
-        Staged<F32, N, kThreads> rB, rC;
+        Staged<F32, N, kThreads, false> rB, rC;
         rB.load(static_cast<const E *>(a.B) + t0 * a.b_stride + (int64_t)group * N, (uint32_t)a.b_stride, rows, t);
         rC.load(static_cast<const E *>(a.C) + t0 * a.c_stride + (int64_t)group * N, (uint32_t)a.c_stride, rows, t);
         load(v0, t, r, g8);
@@ -261,11 +268,11 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
     __syncthreads();
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-        const Frag<F32, 1> fB = get_t<F32, 1>(s.B, KeyMat::ROW, 0, 32 * kb, 16 * nt, l), fC = get_t<F32, 1>(s.C, KeyMat::ROW, 0, 32 * kb, 16 * nt, l);
+        const Frag<F32, 1> fB = get_t<F32, 1, false>(s.B, KeyMat::ROW, 0, 32 * kb, 16 * nt, l), fC = get_t<F32, 1, false>(s.C, KeyMat::ROW, 0, 32 * kb, 16 * nt, l);
 #pragma unroll
         for (int k = 0; k < TT; ++k) {
             const int tile = tt0 + k;
-            if (kb == 0 || tile >= 2) dC[k] = mma<2>(fB, get_t<F32, 2>(pair, PairMat::ROW, PairMat::PLANE, 32 * kb, 16 * tile, l), dC[k]);
+            if (kb == 0 || tile >= 2) dC[k] = mma<2>(fB, get_t<F32, 2, false>(pair, PairMat::ROW, PairMat::PLANE, 32 * kb, 16 * tile, l), dC[k]);
             if (kb == 1 || tile < 2) dB[k] = mma<2>(fC, PairMat::get(pair, 16 * tile + r, 32 * kb + g8), dB[k]);
         }
     }
