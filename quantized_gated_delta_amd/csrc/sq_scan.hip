@@ -29,6 +29,10 @@ constexpr int kGates = 4;  // chunks whose gates are formed at once, one by each
 // The main passes, forwards and (in brackets) backwards.  The state takes up the keys K = B [C] with the
 // columns X = x [dy], and is read by the queries Q = C [B]; a query meets the keys of its own
 // chunk up to [from] its own place in `pairs`.  NT: terms that the results are accurate to.
+// What bounds it: two workgroups to a CU by registers and LDS, which hold LDS (0.44 of the cycles) and vector instructions
+// (0.39) busy with the matrix units at 0.21; a chunk takes 8000 cycles alone.  8192 tokens x 64 heads, d_state 128, d_head
+// 64, bf16: own pass 44 us, main pass 100 to 105; x 32 heads in training, with the states saved: 28, 74 to 81, back 27 and 91
+// to 100.
 template <int N, bool F32, int NT, bool YF32, int PASS, bool SAVE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void scan_kernel(ScanArgs a) {
     typedef Elem<F32> E;
@@ -290,7 +294,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
     if (!READ && t == 0) a.seg_fade[(int64_t)slot * parts + part] = fade;
 }
 
-// States at the segments' starts (BACK: their gradients at the segments' ends) in the place of the segments' own.
+// States at the segments' starts (BACK: their gradients at the segments' ends) in the place of the segments' own: bound by
+// memory and its latency (8 segments of 64 heads, 34 MB: 7 us).
 template <int N, bool BACK> __global__ __launch_bounds__(256) void join_kernel(ScanArgs a) {
     const int parts = a.n_heads * (a.d_head / kHeadPart), part = blockIdx.y;
     const int e = (blockIdx.z * 256 + threadIdx.x) * 4, n = e / kHeadPart, p = e % kHeadPart;
@@ -409,8 +414,8 @@ ScanPlan scan_plan(const sq_scan_desc &d) {
     p.save_bytes = p.chunk_slots * p.parts * state;
     // the gradients' workgroups, one to a CU: a chunk and a subset of a group's heads.  Of up to 1023 workgroups (the sums over
     // a subset then take less than 1024 x 64 rows of d_state, in smaller batches too), as many subsets as
-    // take the fewest rounds of 256 times heads, with two heads' time to begin and end (132 chunks x 32 heads: 3 subsets
-    // 170 us, 4 subsets, which need a third round, 203 us)
+    // take the fewest rounds of 256 times heads, with two heads' time to begin and end (132 chunks x 32 heads, when the kernel
+    // took 183 us with 3 subsets: 4, which need a third round, 195; now 166 with 3)
     const int64_t share = d.n_heads / d.n_groups, units = p.chunk_slots * d.n_groups, rows = d.n_tokens * d.n_heads;
     p.subsets = 1;
     int64_t least = INT64_MAX;

@@ -15,6 +15,8 @@
 // A workgroup has a chunk and some heads of a group, one part after another; dB and dC stay in registers.
 // Eight waves: in the products over the state, wave w has 16 of its rows; the next part's states and tokens
 // are in flight meanwhile.  Of kBatch parts at once, each wave forms the gates of one before, and its dg after.
+// One workgroup to a CU, whose waves wait 0.59 of their cycles: for the states' 64 KB a head (8192 tokens x 32 heads, d_state
+// 128, d_head 64, bf16, 330 MB: 166 us, 2.0 TB/s; 153 with them in L2), at the barriers, and in 396 workgroups on 256 CUs.
 #include "sq_scan.h"
 
 namespace sqk {
