@@ -164,8 +164,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
             }
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
-                p[j] = decayed<BACK>(g, p[j], 16 * kt[j] + g4, 16 * qt[j] + r);
                 if (!BACK) p[j] *= *reinterpret_cast<const f4 *>(&g.dt[16 * kt[j] + g4]);
+                p[j] = decayed<BACK>(g, p[j], 16 * kt[j] + g4, 16 * qt[j] + r);  // behind dt, whose NaN stays with the pairs that meet
             }
 #pragma unroll
             for (int j = 0; j < 3; ++j) PairMat::put4(pairs, 16 * qt[j] + r, 16 * kt[j] + g4, p[j]);

@@ -253,6 +253,17 @@ def test_infinite_inputs_stay_in_their_group_and_sequence():
     assert torch.equal(out["y"][150:], clean["y"][150:]) and torch.equal(out["S"][1], clean["S"][1])
 
 
+def test_nan_of_a_time_step_reaches_later_tokens_alone():
+    for dtype in (BF, F32):
+        b = batch(lens=(150, 80), H=4, G=2, dtype=dtype)
+        clean = run(b, train=False)
+        b["dt"][100, 1] = float("nan")
+        out = run(b, train=False)
+        assert torch.isnan(out["y"][100:150, 1]).all() and torch.isnan(out["S"][0, 1]).all()
+        out["y"][100:150, 1], out["S"][0, 1] = clean["y"][100:150, 1], clean["S"][0, 1]
+        assert torch.equal(out["y"], clean["y"]) and torch.equal(out["S"], clean["S"])
+
+
 def test_empty_batches_leave_zeros_for_the_parameters():
     for lens in ((), (0, 0)):
         b = batch(lens=lens, H=3, N=64)
