@@ -79,7 +79,8 @@ def gate_run(b, layer=None, out=None, backward=True):
 
 
 GATES = [dict(T=1, G=1, d=1), dict(T=3, G=2, d=7), dict(T=70, G=3, d=64), dict(T=600, G=4, d=128), dict(T=9, G=1, d=520), dict(T=5, G=2, d=1024), dict(T=4, G=1, d=4096),
-         dict(T=3, G=1, d=5000), dict(T=700, G=1, d=2048), dict(T=2, G=1, d=9001), dict(T=2, G=1, d=16384), dict(T=33, G=2, d=96, wide=24), dict(T=33, G=2, d=96, wide=3)]
+         dict(T=3, G=1, d=5000), dict(T=700, G=1, d=2048), dict(T=2, G=1, d=9001), dict(T=2, G=1, d=16384), dict(T=33, G=2, d=96, wide=24), dict(T=33, G=2, d=96, wide=3),
+         dict(T=40, G=600, d=16)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])

@@ -264,6 +264,17 @@ def test_nan_of_a_time_step_reaches_later_tokens_alone():
         assert torch.equal(out["y"], clean["y"]) and torch.equal(out["S"], clean["S"])
 
 
+def test_gradients_of_states_in_place():
+    for lens in ((70, 3), (900, 300)):
+        b = batch(lens=lens, H=2, N=64)
+        want = run(b)
+        out = dict(y=torch.empty_like(want["y"]), S=torch.empty_like(want["S"]), **gradients(b))
+        b["dS"] = out["dS0"] = b["dS"].clone()
+        run(b, out=out)
+        for k in want:
+            assert torch.equal(out[k], want[k]), (lens, k)
+
+
 def test_empty_batches_leave_zeros_for_the_parameters():
     for lens in ((), (0, 0)):
         b = batch(lens=lens, H=3, N=64)
