@@ -158,8 +158,9 @@ struct ConvArgs {
     const int32_t *slot;
     int32_t n, n_slots;
 };
-// Blocks along the tokens of the backward pass: each leaves its sums over tokens in `partial`.
-int conv_blocks(int64_t n_tokens, int32_t n_seq, int32_t channels);
+// Most workgroups along the tokens of the backward pass of a batch of up to these sizes: each leaves its sums over tokens in
+// `partial`.
+int64_t conv_partials(int64_t n_tokens, int32_t n_seq, int32_t channels);
 hipError_t launch_conv_forward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
 hipError_t launch_conv_backward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream);
 hipError_t launch_conv_sums(const ConvArgs &a, int blocks, hipStream_t stream);  // blocks 0: zeros

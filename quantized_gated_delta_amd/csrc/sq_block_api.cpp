@@ -239,7 +239,7 @@ sq_status sq_conv_bytes(const sq_conv_desc *desc, size_t *work) {
     sq_status st = check_conv(desc, true);
     if (st) return st;
     if (!work) return fail(SQ_EINVAL, "work is NULL");
-    *work = (size_t)sqk::conv_blocks(desc->n_tokens, desc->n_seq, desc->n_channels) * desc->n_channels * (desc->width + 1) * sizeof(float);
+    *work = (size_t)sqk::conv_partials(desc->n_tokens, desc->n_seq, desc->n_channels) * desc->n_channels * (desc->width + 1) * sizeof(float);
     return SQ_OK;
 }
 

@@ -11,6 +11,8 @@
 // that by a lane of the same L2.
 #include "sq_block.h"
 
+#include <algorithm>
+
 namespace sqk {
 namespace {
 
@@ -280,10 +282,14 @@ uint32_t tiles_of(int channels, int per_lane) { return (channels + 64 * per_lane
 
 } // namespace
 
-// Up to 4096 workgroups in all, each with as many blocks of tokens as the others.
-int conv_blocks(int64_t n_tokens, int32_t n_seq, int32_t channels) {
-    const int64_t slots = block_slots(n_tokens, n_seq, kBackBlockShift), most = 4096 / tiles_of(channels, kNarrow);
-    const int64_t turns = most > 0 ? (slots + most - 1) / most : slots;
+// Up to 4096 workgroups in all ...
+static int64_t most_blocks(int32_t channels) { return std::max<int64_t>(4096 / tiles_of(channels, kNarrow), 1); }
+int64_t conv_partials(int64_t n_tokens, int32_t n_seq, int32_t channels) {
+    return std::max<int64_t>(std::min(block_slots(n_tokens, n_seq, kBackBlockShift), most_blocks(channels)), 1);
+}
+// ... each with as many blocks of tokens as the others: just behind a full turn of them, fewer than a smaller batch has.
+static int conv_blocks(int64_t slots, int32_t channels) {
+    const int64_t turns = (slots + most_blocks(channels) - 1) / most_blocks(channels);
     return (int)(turns > 0 ? (slots + turns - 1) / turns : 1);
 }
 
@@ -297,7 +303,7 @@ hipError_t launch_conv_forward(const ConvArgs &a, bool f32, bool vec, hipStream_
 
 hipError_t launch_conv_backward(const ConvArgs &a, bool f32, bool vec, hipStream_t stream) {
     const int64_t slots = block_slots(a.seqs.n_tokens, a.seqs.n_seq, kBackBlockShift);
-    const int blocks = conv_blocks(a.seqs.n_tokens, a.seqs.n_seq, a.channels);
+    const int blocks = conv_blocks(slots, a.channels);
     const dim3 grid(blocks, tiles_of(a.channels, kNarrow));
     pick(f32, [&](auto F) { pick(vec, [&](auto V) { pick_width(a.width, [&](auto W) {
         hipLaunchKernelGGL((conv_backward_kernel<F.value, V.value, W.value>), grid, dim3(256), 0, stream, a, slots);

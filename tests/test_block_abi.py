@@ -87,6 +87,22 @@ def test_conv_sizes():
     refused(Q.SQ_EUNSUPPORTED, "grid", conv_step, n=1 << 27)
 
 
+@pytest.mark.parametrize("width", [2, 4])
+@pytest.mark.parametrize("channels", [64, 2048, 8192, 10240, 65536, 1 << 21], ids=str)
+def test_the_largest_batchs_convolution_workspace_serves_smaller_ones(channels, width):
+    """Also where a batch's blocks of 128 tokens are just more than one, two or three turns of the workgroups."""
+    size = lambda t, s: Q.sq_conv_bytes(conv_desc(n_tokens=t, n_seq=s, n_channels=channels, width=width))  # noqa: E731
+    turn = max(1, 4096 // (-(-channels // 256)))
+    for slots in (turn - 1, turn, turn + 1, 2 * turn, 2 * turn + 1, 3 * turn + 2):
+        most = size(slots * 128, 4)
+        for t in {0, 1, 5000} | {(k * turn + j) * 128 for k in (1, 2, 3) for j in (-5, -4, -1, 0, 1)}:
+            for s in (0, 1, 3, 4):
+                if 0 <= t <= slots * 128:
+                    assert size(t, s) <= most, (slots, t, s)
+        for s in (1, turn // 2, turn, turn + 1, slots):  # as many short sequences
+            assert size(0, min(s, slots)) <= size(0, slots), (slots, s)
+
+
 def test_conv_no_ops():
     none = conv_desc(n_seq=0, n_tokens=0)
     conv_forward(none, cu=None, x=None, y=None)

@@ -211,3 +211,14 @@ def test_empty_batches_leave_zeros_for_the_parameters():
         assert (out["dweight"] == 0).all() and (out["dbias"] == 0).all(), lens
         if lens:
             assert torch.equal(out["S"], b["S0"]) and torch.equal(out["dS0"], b["dS"])
+
+
+# ------------------------------------------------------------------ many blocks
+# 8192 channels are 32 tiles, of which the gradients have 128 workgroups each, 16384 channels 64 tiles of 64: more blocks
+# of 128 tokens than that, and a workgroup walks over several.
+def test_one_object_for_its_largest_batch_and_for_smaller_ones():
+    """Batches of 131 slots in two turns, and smaller ones of up to 128 in one: more blocks, in the same workspace."""
+    layer = Q.ShortConv(129, 400, 8192, 4, train=True)
+    for n in (129, 125, 60, 1):
+        b = batch(lens=[1 + i % 5 for i in range(n)], C=8192, seed=n)
+        check(b, run(b, layer=layer))
