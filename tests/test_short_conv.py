@@ -216,9 +216,44 @@ def test_empty_batches_leave_zeros_for_the_parameters():
 # ------------------------------------------------------------------ many blocks
 # 8192 channels are 32 tiles, of which the gradients have 128 workgroups each, 16384 channels 64 tiles of 64: more blocks
 # of 128 tokens than that, and a workgroup walks over several.
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", [dict(lens=[i % 6 for i in range(300)], C=8192, W=2), dict(lens=[1 + i % 5 for i in range(300)], C=8190, W=3),
+                                  dict(lens=[i % 6 for i in range(200)], C=8192), dict(lens=[130, 3, 257, 40] * 9, C=16384)],
+                         ids=["three-w2", "three-odd", "two", "long"])
+def test_a_workgroup_takes_several_blocks(case, dtype):
+    b = batch(dtype=dtype, **case)
+    check(b, run(b))
+
+
 def test_one_object_for_its_largest_batch_and_for_smaller_ones():
     """Batches of 131 slots in two turns, and smaller ones of up to 128 in one: more blocks, in the same workspace."""
     layer = Q.ShortConv(129, 400, 8192, 4, train=True)
     for n in (129, 125, 60, 1):
         b = batch(lens=[1 + i % 5 for i in range(n)], C=8192, seed=n)
         check(b, run(b, layer=layer))
+
+
+def test_more_sequences_than_one_search_tells_apart():
+    """4200 sequences: the search for a block's sequence goes through two steps of 64 lanes."""
+    b = batch(lens=[i % 3 for i in range(4200)], C=24)
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n,C,W", [(1100, 41, 4), (2100, 2056, 3), (2103, 2056, 2)], ids=str)
+def test_step_with_several_requests_to_a_lane(n, C, W, dtype):
+    """Two requests to a lane, and eight, the last lanes' fewer; some without a slot."""
+    b = batch(lens=(1,) * n, C=C, W=W, dtype=dtype, wide=7)
+    pool = torch.randn(n + 3, W - 1, C, device=DEV).to(dtype)
+    before = pool.clone()
+    slot = torch.randperm(n + 3, device=DEV)[:n].to(torch.int32)
+    b["S0"] = pool[slot.long()].clone()
+    out = slot.clone()
+    out[::97] = -1
+    y = torch.full((n, C), 7.0, dtype=dtype, device=DEV)
+    Q.conv_step(pool, out, b["x"], b["weight"], y, bias=b["bias"])
+    left = out < 0
+    assert (y[left] == 7).all() and torch.equal(pool[slot[left].long()], before[slot[left].long()])
+    keep = ~left
+    c = dict(b, case=dict(b["case"], lens=[1] * int(keep.sum())), x=b["x"][keep], dy=b["dy"][keep], S0=b["S0"][keep], dS=b["dS"][keep])
+    check(c, dict(y=y[keep], S=pool[slot[keep].long()]))
