@@ -139,9 +139,12 @@ __device__ __forceinline__ float gate_of(int act, float z) {
     return act == SQ_ACT_SILU ? z * s : s;
 }
 __device__ __forceinline__ void gate_and_slope(int act, float z, float &value, float &slope) {
-    const float s = sigmoid_of(z);
+    const float e = __builtin_amdgcn_exp2f(-1.44269504088896340736f * z), s = __builtin_amdgcn_rcpf(1.f + e);
+    // 1 - sigma = e^-z sigma: as a difference it would have few bits where sigma is near 1.  Where e^-z is infinite sigma is 0,
+    // and so is the slope
+    const float rest = fminf(e, 3e38f) * s;
     value = act == SQ_ACT_SILU ? z * s : s;
-    slope = act == SQ_ACT_SILU ? s + value * (1.f - s) : s * (1.f - s);
+    slope = act == SQ_ACT_SILU ? fmaf(value, rest, s) : s * rest;
 }
 
 // ------------------------------------------------------------------ arguments

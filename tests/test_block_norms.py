@@ -246,3 +246,46 @@ def test_gradients_against_differences():
             return (got["h"] * b["dh"].to(F64)).sum() + (got["r_out"] * b["dr_out"].to(F64)).sum()
         diff = (loss(1e-6) - loss(-1e-6)) / 2e-6
         assert abs((out[g].to(F64) * d).sum() - diff) <= 1e-4 * (out[g].to(F64) * d).abs().sum(), k
+
+
+# ------------------------------------------------------------------ gates far from 0
+@pytest.mark.parametrize("dtype", [BF], ids=["bf16"])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_gates_are_accurate_relative_to_themselves(act, dtype):
+    """Gates and slopes of any size, not against the largest.  Rows of +1 and -1 and no eps, so that y and dz are the gate and its
+    slope with x's sign.  Tolerances, in 2^-24: the exponential 2 and its argument's rounding, which is put back to |z| / 22 (ln 2 as a
+    float) with 1 for the step, so under 7; 1 + e^-z and its reciprocal 1 and 2 more; the product with z 1: under 11, so 2^-20 for the
+    gate.  What is left to 1, e^-z times the gate's 10, has under 18; a slope is a product of the two or their sum: under 30, 2^-19 of
+    its terms' absolute values.  bf16: the argument's rounding stays, 80 in the gate and 160 in what is left: 2^-17 and 2^-16, and 2^-8
+    of the value at the end."""
+    z = torch.linspace(-80, 80, 8 * 4001, device=DEV).view(-1, 1, 8).to(dtype)
+    x = torch.ones_like(z)
+    x[..., ::2] = -1
+    y, dx, dz = (torch.empty_like(z) for _ in range(3))
+    layer = Q.GatedNorm(1, 8, act=act, eps=0.0, dtype=dtype)
+    layer.forward(x, z, None, y)
+    layer.backward(x, z, None, torch.ones_like(z), dx, dz)
+    v, x = z.to(F64), x.to(F64)
+    s, rest = 1 / (1 + torch.exp(-v)), 1 / (1 + torch.exp(v))
+    gate, slope, size = (v * s, s * (1 + v * rest), s * (1 + v.abs() * rest)) if act == "silu" else (s, s * rest, s * rest)
+    for got, want, big, fine, coarse in ((y, gate, gate.abs(), 2.0 ** -20, 2.0 ** -17), (dz, slope, size, 2.0 ** -19, 2.0 ** -16)):
+        bound = fine * big if dtype == F32 else coarse * big + 2.0 ** -8 * want.abs()
+        over = float(((got.to(F64) - x * want).abs() / bound.clamp_min(1e-300)).max())
+        assert over <= 1, over
+
+
+def test_gates_beyond_the_exponentials_range():
+    """Behind 87 the exponential leaves fp32's range: the gate goes to 0 or z all the same, NaN stays NaN."""
+    z = torch.tensor([-89.0, -150.0, -3e38, -float("inf"), 89.0, 150.0, 3e38, float("nan")], device=DEV).view(1, 1, 8)
+    x, y = torch.ones_like(z), torch.empty_like(z)
+    dx, dz = torch.empty_like(z), torch.empty_like(z)
+    layer = Q.GatedNorm(1, 8, act="sigmoid", eps=0.0, dtype=F32)
+    layer.forward(x, z, None, y)
+    layer.backward(x, z, None, torch.ones_like(z), dx, dz)
+    for v in (y, dz):
+        assert (v[0, 0, :4].abs() < 1e-37).all() and torch.isnan(v[0, 0, 7])
+    assert (y[0, 0, 4:7] == 1).all() and (dz[0, 0, 4:7].abs() < 1e-37).all()
+    z[0, 0, 3] = -88.0
+    z[0, 0, 7] = 88.0
+    Q.GatedNorm(1, 8, eps=0.0, dtype=F32).forward(x, z, None, y)
+    assert (y[0, 0, :4].abs() < 1e-35).all() and torch.equal(y[0, 0, 4:], z[0, 0, 4:])
