@@ -90,7 +90,7 @@ template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv
                 float p = bias[e];
 #pragma unroll
                 for (int k = 0; k < W; ++k) p = fmaf(w[W - 1 - k][e], x[(i - k) & 3][e], p);
-                y[e] = a.silu ? gate_of(SQ_ACT_SILU, p) : p;
+                y[e] = a.silu ? gate_of<F32>(SQ_ACT_SILU, p) : p;
             }
             if (t0 + i < last) store_n<F32, VEC, N>(a.y, (int64_t)(b.t0 + t0 + i) * a.channels + c0, y, left);
         }
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvArgs a, int64_t 
                     float p = bias[e], value, slope = 1.f;
 #pragma unroll
                     for (int k = 0; k < W; ++k) p = fmaf(w[W - 1 - k][e], x[(i - k) & 3][e], p);
-                    if (a.silu) gate_and_slope(SQ_ACT_SILU, p, value, slope);
+                    if (a.silu) gate_and_slope<F32>(SQ_ACT_SILU, p, value, slope);
                     d[i][e] = inside ? dy[e] * slope : 0.f;
                     if (mine) {
 #pragma unroll
@@ -264,7 +264,7 @@ template <bool F32, bool VEC, int W> __global__ __launch_bounds__(256) void conv
         }
         if (a.silu)
 #pragma unroll
-            for (int e = 0; e < N; ++e) p[e] = gate_of(SQ_ACT_SILU, p[e]);
+            for (int e = 0; e < N; ++e) p[e] = gate_of<F32>(SQ_ACT_SILU, p[e]);
         store_n<F32, VEC, N>(a.y, (int64_t)r * a.channels + c0, p, left);
     }
 }

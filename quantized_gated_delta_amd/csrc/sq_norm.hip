@@ -181,7 +181,7 @@ __global__ __launch_bounds__(T) void gate_forward_kernel(GateArgs a, uint32_t ro
         widen_row<F32, K>(row.z, z);
         if (a.z)
 #pragma unroll
-            for (int e = 0; e < 8 * K; ++e) z[e] = gate_of(a.act, z[e]);
+            for (int e = 0; e < 8 * K; ++e) z[e] = gate_of<F32>(a.act, z[e]);
         float s[1] = {0.f};
 #pragma unroll
         for (int e = 0; e < 8 * K; ++e) {
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(T) void gate_backward_kernel(GateArgs a, uint32_t r
 #pragma unroll
         for (int e = 0; e < 8 * K; ++e) {
             act[e] = 1.f, slope[e] = 0.f;
-            if (a.z) gate_and_slope(a.act, z[e], act[e], slope[e]);
+            if (a.z) gate_and_slope<F32>(a.act, z[e], act[e], slope[e]);
             const float u = FIRST ? x[e] * act[e] : x[e], t = FIRST ? dy[e] * w[e] : dy[e] * w[e] * act[e];
             s[0] = fmaf(u, u, s[0]);
             s[1] = fmaf(t, u, s[1]);

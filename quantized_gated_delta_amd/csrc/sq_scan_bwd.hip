@@ -248,7 +248,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(ScanArgs a, int64_t slot
                 const double rs = wave_scan((double)ri, l), zs = wave_scan((double)z, l);
                 const float dg = (float)((double)pairs + (__shfl(rs, 63, 64) - rs + (double)ri) + (zs - (double)z) + (double)s.g[w].in[63] * e), dt = s.g[w].dt[l];
                 float draw = fmaf(A, dg, u);
-                if (a.softplus) draw *= sigmoid_of(raw + bias);
+                if (a.softplus) draw *= sigmoid_of<F32>(raw + bias);
                 if (l >= rows) draw = 0.f;
                 else st_elem<F32>(a.draw, (t0 + l) * a.ddt_stride + pt.head, draw);
                 float sums[3] = {dt * dg, draw, dyx};

@@ -249,7 +249,7 @@ def test_gradients_against_differences():
 
 
 # ------------------------------------------------------------------ gates far from 0
-@pytest.mark.parametrize("dtype", [BF], ids=["bf16"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("act", ["silu", "sigmoid"])
 def test_gates_are_accurate_relative_to_themselves(act, dtype):
     """Gates and slopes of any size, not against the largest.  Rows of +1 and -1 and no eps, so that y and dz are the gate and its

@@ -165,6 +165,22 @@ def test_graph_replays():
             assert torch.equal(out[k], want[k]), (seed, k)
 
 
+def test_activation_far_from_zero():
+    """SiLU and its slope relative to themselves: one tap of 1, so that p is the input.  Tolerances as derived for the gated norm's
+    gates: 2^-20 of SiLU, 2^-19 of its slope's terms."""
+    b = batch(lens=(501,), C=64, dtype=F32, bias=False, start=False, dS=False)
+    b["x"].copy_(torch.linspace(-80, 80, 501 * 64, device=DEV).view(501, 64))
+    b["dy"].fill_(1.0)
+    b["weight"].zero_()
+    b["weight"][:, 3] = 1.0
+    out, v = run(b), b["x"].to(F64)
+    s, rest = 1 / (1 + torch.exp(-v)), 1 / (1 + torch.exp(v))
+    off = float(((out["y"].to(F64) - v * s).abs() / (v * s).abs().clamp_min(1e-300)).max())
+    assert off <= 2.0 ** -20, off
+    off = float(((out["dx"].to(F64) - s * (1 + v * rest)).abs() / (s * (1 + v.abs() * rest))).max())
+    assert off <= 2.0 ** -19, off
+
+
 # ------------------------------------------------------------------ one token
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("n,C,W,act,wide", [(1, 1, 2, "silu", 0), (5, 64, 4, "silu", 8), (130, 40, 3, None, 0), (3, 1001, 4, "silu", 1)], ids=str)
