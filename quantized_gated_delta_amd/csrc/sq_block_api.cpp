@@ -89,11 +89,8 @@ sq_status check_batch(int32_t n_seq, int64_t n_tokens) {
     if (n_tokens >= kMaxTokens) return fail(SQ_EUNSUPPORTED, "n_tokens exceeds 2^31 - 2^16");
     return SQ_OK;
 }
-sq_status check_cu(const int32_t *cu) {
-    if (!cu) return fail(SQ_EINVAL, "cu is NULL");
-    if (!aligned(cu, 4)) return fail(SQ_EINVAL, "cu is not 4-byte aligned");
-    return SQ_OK;
-}
+// cu, which the kernels read all along.
+Arg list_of(const int32_t *cu, int32_t n_seq) { return dense("cu", cu, true, false, 4 * ((int64_t)n_seq + 1), 4); }
 sq_status check_step(const void *pool, int32_t n_slots, const int32_t *slot_idx, int32_t n) {
     if (n_slots < 1) return fail(SQ_EINVAL, "n_slots must be >= 1 (got %d)", n_slots);
     if (n < 0) return fail(SQ_EINVAL, "n must be >= 0 (got %d)", n);
@@ -250,10 +247,10 @@ sq_status sq_conv_forward(const sq_conv_desc *desc, const int32_t *cu, const voi
     if (desc->n_seq == 0) return SQ_OK;
     const int e = size_of(desc->dtype);
     const int64_t c = desc->n_channels, n = desc->n_tokens, xs = stride_or(desc->x_stride, c), state = desc->n_seq * (int64_t)(desc->width - 1) * c * e;
-    const Arg args[] = {{kx, x, true, false, n, c * e, xs * e, (uintptr_t)e}, dense("weight", weight, true, false, c * desc->width * 4, 4),
+    const Arg args[] = {list_of(cu, desc->n_seq), {kx, x, true, false, n, c * e, xs * e, (uintptr_t)e}, dense("weight", weight, true, false, c * desc->width * 4, 4),
                         dense("bias", bias, false, false, c * 4, 4), dense(kS0, S0, false, false, state, e),
                         dense(ky, y, true, true, n * c * e, e), dense(kS_out, S_out, false, true, state, e)};
-    if ((st = check_cu(cu)) || (st = check_args(args, kNone))) return st;
+    if ((st = check_args(args, kNone))) return st;
     if (debug_slots() && (st = check_sequences(desc->n_seq, desc->n_tokens, cu, stream))) return st;
     sqk::ConvArgs a = conv_args(desc, cu, x, weight, bias);
     a.S0 = S0; a.y = y; a.S_out = S_out;
@@ -277,13 +274,13 @@ sq_status sq_conv_backward(const sq_conv_desc *desc, const int32_t *cu, const vo
     }
     const int e = size_of(desc->dtype);
     const int64_t c = desc->n_channels, n = desc->n_tokens, xs = stride_or(desc->x_stride, c), state = desc->n_seq * (int64_t)(desc->width - 1) * c * e;
-    const Arg args[] = {{kx, x, true, false, n, c * e, xs * e, (uintptr_t)e}, dense("weight", weight, true, false, c * desc->width * 4, 4),
+    const Arg args[] = {list_of(cu, desc->n_seq), {kx, x, true, false, n, c * e, xs * e, (uintptr_t)e}, dense("weight", weight, true, false, c * desc->width * 4, 4),
                         dense("bias", bias, false, false, c * 4, 4), dense(kS0, S0, false, false, state, e),
                         dense(kdy, dy, true, false, n * c * e, e), dense(kdS_out, dS_out, false, false, state, e),
                         dense(kdx, dx, true, true, n * c * e, e), dense("dweight", dweight, true, true, c * desc->width * 4, 4),
                         dense("dbias", dbias, false, true, c * 4, 4), dense(kdS0, dS0, false, true, state, e),
                         dense("work", work, false, true, (int64_t)need, 1)};
-    if ((st = check_cu(cu)) || (st = check_work("work", work, work_bytes, need)) || (st = check_args(args, kNone))) return st;
+    if ((st = check_work("work", work, work_bytes, need)) || (st = check_args(args, kNone))) return st;
     if (debug_slots() && (st = check_sequences(desc->n_seq, desc->n_tokens, cu, stream))) return st;
     sqk::ConvArgs a = conv_args(desc, cu, x, weight, bias);
     a.S0 = S0; a.dy = dy; a.dS_out = dS_out; a.dx = dx; a.dweight = dweight; a.dbias = dbias; a.dS0 = dS0;
@@ -333,13 +330,13 @@ sq_status sq_scan_forward(const sq_scan_desc *desc, const int32_t *cu, const voi
     const int e = size_of(desc->in_dtype), ey = size_of(desc->y_dtype);
     const int64_t n = desc->n_tokens, h = desc->n_heads, wide = h * desc->d_head, keys = (int64_t)desc->n_groups * desc->d_state;
     const int64_t state = desc->n_seq * h * desc->d_state * desc->d_head * 4;
-    const Arg args[] = {{kx, x, true, false, n, wide * e, stride_or(desc->x_stride, wide) * e, 16}, {"raw", raw, true, false, n, h * e, stride_or(desc->dt_stride, h) * e, (uintptr_t)e},
+    const Arg args[] = {list_of(cu, desc->n_seq), {kx, x, true, false, n, wide * e, stride_or(desc->x_stride, wide) * e, 16}, {"raw", raw, true, false, n, h * e, stride_or(desc->dt_stride, h) * e, (uintptr_t)e},
                         dense("A", A, true, false, h * 4, 4), {"B", B, true, false, n, keys * e, stride_or(desc->b_stride, keys) * e, 16},
                         {"C", C, true, false, n, keys * e, stride_or(desc->c_stride, keys) * e, 16}, dense("D", D, false, false, h * 4, 4),
                         dense("dt_bias", dt_bias, false, false, h * 4, 4), dense(kS0, S0, false, false, state, 16), dense(ky, y, true, true, n * wide * ey, 16),
                         dense(kS_out, S_out, false, true, state, 16), dense("save", save, false, true, (int64_t)keep, 1), dense("work", work, false, true, (int64_t)need, 1)};
     const Same same[] = {{kS0, kS_out}};
-    if ((st = check_cu(cu)) || (st = check_work("work", work, work_bytes, need)) || (save && (st = check_work("save", save, save_bytes, keep))) ||
+    if ((st = check_work("work", work, work_bytes, need)) || (save && (st = check_work("save", save, save_bytes, keep))) ||
         (st = check_args(args, same)))
         return st;
     if (debug_slots() && (st = check_sequences(desc->n_seq, desc->n_tokens, cu, stream))) return st;
@@ -366,7 +363,7 @@ sq_status sq_scan_backward(const sq_scan_desc *desc, const int32_t *cu, const vo
     const int e = size_of(desc->in_dtype);
     const int64_t n = desc->n_tokens, h = desc->n_heads, wide = h * desc->d_head, keys = (int64_t)desc->n_groups * desc->d_state;
     const int64_t state = desc->n_seq * h * desc->d_state * desc->d_head * 4;
-    const Arg args[] = {{kx, x, true, false, n, wide * e, stride_or(desc->x_stride, wide) * e, 16}, {"raw", raw, true, false, n, h * e, stride_or(desc->dt_stride, h) * e, (uintptr_t)e},
+    const Arg args[] = {list_of(cu, desc->n_seq), {kx, x, true, false, n, wide * e, stride_or(desc->x_stride, wide) * e, 16}, {"raw", raw, true, false, n, h * e, stride_or(desc->dt_stride, h) * e, (uintptr_t)e},
                         dense("A", A, true, false, h * 4, 4), {"B", B, true, false, n, keys * e, stride_or(desc->b_stride, keys) * e, 16},
                         {"C", C, true, false, n, keys * e, stride_or(desc->c_stride, keys) * e, 16}, dense("D", D, false, false, h * 4, 4),
                         dense("dt_bias", dt_bias, false, false, h * 4, 4), dense(kdy, dy, true, false, n * wide * e, 16),
@@ -377,7 +374,7 @@ sq_status sq_scan_backward(const sq_scan_desc *desc, const int32_t *cu, const vo
                         dense("dD", dD, false, true, h * 4, 4), dense("ddt_bias", ddt_bias, false, true, h * 4, 4), dense(kdS0, dS0, false, true, state, 16),
                         dense("work", work, false, true, (int64_t)need, 1)};
     const Same same[] = {{kdS0, kdS_out}};
-    if ((st = check_cu(cu)) || (st = check_work("work", work, work_bytes, need)) || (st = check_work("save", save, save_bytes, keep)) ||
+    if ((st = check_work("work", work, work_bytes, need)) || (st = check_work("save", save, save_bytes, keep)) ||
         (st = check_args(args, same)))
         return st;
     if (debug_slots() && (st = check_sequences(desc->n_seq, desc->n_tokens, cu, stream))) return st;

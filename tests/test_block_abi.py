@@ -203,6 +203,19 @@ def test_scan_no_ops():
     scan_step(n=0, state_pool=None, slot_idx=None, x=None, y=None)
 
 
+def test_outputs_over_the_list_of_sequences():
+    """A kernel that still reads cu while another workgroup writes over it would see a wrong list."""
+    for out in ("y", "S_out"):
+        refused(Q.SQ_EINVAL, "cu and %s overlap" % out, conv_forward, **{out: at(0)})
+        refused(Q.SQ_EINVAL, "cu and %s overlap" % out, scan_forward, **{out: at(0)})
+    for out in ("dx", "dweight", "dbias", "dS0", "work"):
+        refused(Q.SQ_EINVAL, "cu and %s overlap" % out, conv_backward, cu=at(40) + 8, **{out: at(40)})
+    for out in ("dx", "draw", "dA", "dB", "dC", "dD", "ddt_bias", "dS0", "work"):
+        refused(Q.SQ_EINVAL, "cu and %s overlap" % out, scan_backward, cu=at(40) + 12, **{out: at(40)})
+    for out in ("save", "work"):
+        refused(Q.SQ_EINVAL, "cu and %s overlap" % out, scan_forward, cu=at(40) + 252, **{out: at(40)})
+
+
 # ------------------------------------------------------------------ norms
 def gate_desc(**kw):
     return Q.gated_norm_desc(**{**dict(n_tokens=10, n_groups=2, d=64), **kw})
