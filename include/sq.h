@@ -634,8 +634,8 @@ sq_status sq_gated_norm_bytes(const sq_gated_norm_desc *desc, size_t *work);
 /* weight: fp32, or NULL for ones. */
 sq_status sq_gated_norm_forward(const sq_gated_norm_desc *desc, const void *x, const void *z,
                                 const float *weight, void *y, hipStream_t stream);
-/* Gradients for the same inputs.  dweight: fp32, written, or NULL.  dx may be dy itself where both
- * are dense. */
+/* Gradients for the same inputs.  dweight: fp32, written, or NULL (then work is not used).  dx may
+ * be dy itself where both are dense. */
 sq_status sq_gated_norm_backward(const sq_gated_norm_desc *desc, const void *x, const void *z,
                                  const float *weight, const void *dy, void *dx, void *dz,
                                  float *dweight, void *work, size_t work_bytes,
@@ -663,7 +663,8 @@ sq_status sq_residual_norm_forward(const sq_residual_norm_desc *desc, const void
                                    const float *weight, void *r_out, void *h, hipStream_t stream);
 /* Gradients, from o and r as the forward pass had them.
  *   dh: gradient of h, or NULL where there is none;  dr_out: of r_out, or NULL for zeros;
- *   d_o: required;  dr: or NULL;  dpost_weight, dscale, dweight: fp32 [d], written, or NULL;
+ *   d_o: required;  dr: or NULL;  dpost_weight, dscale, dweight: fp32 [d], written, or NULL (all
+ *   three: work is not used);
  *   dr may be dr_out itself, d_o may be dh itself. */
 sq_status sq_residual_norm_backward(const sq_residual_norm_desc *desc, const void *o, const void *r,
                                     const float *post_weight, const float *scale,

@@ -449,9 +449,9 @@ sq_status sq_gated_norm_backward(const sq_gated_norm_desc *desc, const void *x, 
     const Arg args[] = {{kx, x, true, false, n, wide * e, xs * e, (uintptr_t)e}, {"z", z, gate, false, n, wide * e, zs * e, (uintptr_t)e},
                         dense("weight", weight, false, false, (desc->shared_weight ? desc->d : wide) * 4, 4), {kdy, dy, true, false, n, wide * e, wide * e, (uintptr_t)e},
                         {kdx, dx, true, true, n, wide * e, dxs * e, (uintptr_t)e}, {"dz", dz, gate, true, n, wide * e, dzs * e, (uintptr_t)e},
-                        dense("dweight", dweight, false, true, (desc->shared_weight ? desc->d : wide) * 4, 4), dense("work", work, false, true, (int64_t)need, 1)};
+                        dense("dweight", dweight, false, true, (desc->shared_weight ? desc->d : wide) * 4, 4), dense("work", dweight ? work : nullptr, false, true, (int64_t)need, 1)};
     const Same same[] = {{kdy, kdx}};
-    if ((st = check_args(args, same)) || (dweight && (st = check_work("work", work, work_bytes, need)))) return st;
+    if ((dweight && (st = check_work("work", work, work_bytes, need))) || (st = check_args(args, same))) return st;
     sqk::GateArgs a = gate_args(desc, x, z, weight);
     a.dy = dy; a.dx = dx; a.dz = dz; a.dweight = dweight; a.partial = static_cast<float *>(work);
     const void *const p[] = {x, z, dy, dx, dz, weight};
@@ -496,6 +496,7 @@ sq_status sq_residual_norm_backward(const sq_residual_norm_desc *desc, const voi
     sq_status st = sq_residual_norm_bytes(desc, &need);
     if (st) return st;
     if (dpost_weight && !post_weight) return fail(SQ_EINVAL, "dpost_weight is given, but post_weight is NULL");
+    const bool sums = dpost_weight || dscale || dweight;  // over the rows, in the workspace
     const int e = size_of(desc->dtype), er = size_of(desc->res_dtype);
     const int64_t n = desc->n_rows, d = desc->d;
     const Arg args[] = {dense("o", o, true, false, n * d * e, e), dense(kr, r, false, false, n * d * er, er),
@@ -504,9 +505,9 @@ sq_status sq_residual_norm_backward(const sq_residual_norm_desc *desc, const voi
                         dense(kdr_out, dr_out, false, false, n * d * er, er), dense(kd_o, d_o, true, true, n * d * e, e),
                         dense(kdr, dr, false, true, n * d * er, er), dense("dpost_weight", dpost_weight, false, true, d * 4, 4),
                         dense("dscale", dscale, false, true, d * 4, 4), dense("dweight", dweight, false, true, d * 4, 4),
-                        dense("work", work, false, true, (int64_t)need, 1)};
+                        dense("work", sums ? work : nullptr, false, true, (int64_t)need, 1)};
     const Same same[] = {{kdr, kdr_out}, {kdh, kd_o}};
-    if ((st = check_args(args, same)) || ((dpost_weight || dscale || dweight) && (st = check_work("work", work, work_bytes, need)))) return st;
+    if ((sums && (st = check_work("work", work, work_bytes, need))) || (st = check_args(args, same))) return st;
     sqk::ResidualArgs a{};
     a.o = o; a.r = r; a.post = post_weight; a.scale = scale; a.weight = weight; a.dh = dh; a.dr_out = dr_out;
     a.d_o = d_o; a.dr = dr; a.dpost = dpost_weight; a.dscale = dscale; a.dweight = dweight; a.partial = static_cast<float *>(work);

@@ -298,6 +298,19 @@ def test_residual_pointers():
     res_forward(Q.residual_norm_desc(0, 64), o=None, r_out=None)
 
 
+def test_a_workspace_that_no_call_uses_is_not_held_against_it():
+    """Without gradients of parameters the norms' backward pass writes no workspace: one of another size, which other tensors
+    lie right behind, is no overlap.  Each call is refused for a later pair of arguments alone."""
+    rows = 4000  # with gradients of parameters: 512 rows of partial sums
+    behind = dict(work=at(20), work_bytes=256)
+    refused(Q.SQ_EINVAL, "dy and dz overlap", gate_backward, gate_desc(n_tokens=rows), dweight=None, x=at(20) + 256, dz=at(3), **behind)
+    refused(Q.SQ_EINVAL, "dr_out and d_o overlap", res_backward, Q.residual_norm_desc(rows, 64), dweight=None, dscale=None, dpost_weight=None, o=at(20) + 256,
+            d_o=at(6), **behind)
+    # with them it has to be large enough, which is said first
+    refused(Q.SQ_ENOMEM, "work", gate_backward, gate_desc(n_tokens=rows), dy=at(20) + 256, **behind)
+    refused(Q.SQ_ENOMEM, "work", res_backward, Q.residual_norm_desc(rows, 64), dh=at(20) + 256, **behind)
+
+
 def test_null_descriptors():
     L = B._lib()
     for name in ("sq_conv_bytes", "sq_gated_norm_bytes", "sq_residual_norm_bytes"):
