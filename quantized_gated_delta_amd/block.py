@@ -254,8 +254,13 @@ def _room(nbytes, device):
     return _torch.empty(max(256, nbytes), dtype=_torch.uint8, device=device)
 
 
-def _span(buf):
-    return (None, 0) if buf is None else (buf.data_ptr(), buf.numel())
+def _span(buf, dev):
+    """Address and size of an object's workspace, which has to be on the device of the call's tensors."""
+    if buf is None:
+        return None, 0
+    if buf.get_device() != dev:
+        raise ValueError("the object's workspace is on %s, not on the device of the tensors" % buf.device)
+    return buf.data_ptr(), buf.numel()
 
 
 def _copy(desc):
@@ -305,7 +310,7 @@ class ShortConv:
         c, f32, dt = self.n_channels, _torch.float32, self.dtype
         sq_conv_backward(*args, _tensor("dy", dy, tokens, dt, dev), _maybe("dS_out", dS_out, state, dt, dev), _tensor("dx", dx, tokens, dt, dev),
                          _tensor("dweight", dweight, (c, self.width), f32, dev), _maybe("dbias", dbias, (c,), f32, dev),
-                         _maybe("dS0", dS0, state, dt, dev), *_span(self.work), stream)
+                         _maybe("dS0", dS0, state, dt, dev), *_span(self.work, dev), stream)
 
 
 def conv_step(pool, slot_idx, x, weight, y, bias=None, act="silu", stream=None) -> None:
@@ -368,8 +373,8 @@ class SelectiveScan:
         tokens at which the sequences begin and end.  Returns the call's number, for backward."""
         args, start, dev, n, state = self._inputs(x, dt, A, B, C, cu, D, dt_bias, S0)
         py = _tensor("y", y, (n, self.n_heads, self.d_head), self.y_dtype, dev)
-        save, save_bytes = _span(self.save)
-        work, work_bytes = _span(self.work)
+        save, save_bytes = _span(self.save, dev)
+        work, work_bytes = _span(self.work, dev)
         sq_scan_forward(*args, start, py, _maybe("S_out", S_out, state, _torch.float32, dev), save, work, save_bytes, work_bytes, stream)
         self.calls, self._sizes = self.calls + 1, (state[0], n)
         return self.calls
@@ -393,8 +398,8 @@ class SelectiveScan:
         pdt, desc.ddt_stride = _tokens("ddt", ddt, (n, h), to, dev)
         pdb, desc.db_stride = _tokens("dB", dB, keys, to, dev)
         pdc, desc.dc_stride = _tokens("dC", dC, keys, to, dev)
-        save, save_bytes = _span(self.save)
-        work, work_bytes = _span(self.work)
+        save, save_bytes = _span(self.save, dev)
+        work, work_bytes = _span(self.work, dev)
         sq_scan_backward(*args, _tensor("dy", dy, wide, to, dev), _maybe("dS_out", dS_out, state, f32, dev), save, pdx, pdt,
                          _tensor("dA", dA, (h,), f32, dev), pdb, pdc, _maybe("dD", dD, (h,), f32, dev), _maybe("ddt_bias", ddt_bias, (h,), f32, dev),
                          _maybe("dS0", dS0, state, f32, dev), work, save_bytes, work_bytes, stream)
@@ -466,7 +471,7 @@ class GatedNorm:
         pdw = _maybe("dweight", dweight, self._wide, _torch.float32, dev)
         if pdw is not None and self.work is None:
             raise ValueError("dweight needs train=True")
-        sq_gated_norm_backward(desc, px, pz, pw, pdy, pdx, pdz, pdw, *_span(self.work), stream)
+        sq_gated_norm_backward(desc, px, pz, pw, pdy, pdx, pdz, pdw, *_span(None if pdw is None else self.work, dev), stream)
 
 
 class ResidualNorm:
@@ -505,7 +510,8 @@ class ResidualNorm:
         row, f32 = (self.d,), _torch.float32
         pdo = _tensor("do", do, shape, self.dtype, dev)
         grads = [_maybe(name, t, row, f32, dev) for name, t in (("dpost_weight", dpost_weight), ("dscale", dscale), ("dweight", dweight))]
-        if self.work is None and any(g is not None for g in grads):
+        sums = any(g is not None for g in grads)
+        if sums and self.work is None:
             raise ValueError("gradients of parameters need train=True")
         sq_residual_norm_backward(*args, _maybe("dh", dh, shape, self.dtype, dev), _maybe("dr_out", dr_out, shape, self.res_dtype, dev), pdo,
-                                  _maybe("dr", dr, shape, self.res_dtype, dev), *grads, *_span(self.work), stream)
+                                  _maybe("dr", dr, shape, self.res_dtype, dev), *grads, *_span(self.work if sums else None, dev), stream)

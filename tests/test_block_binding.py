@@ -114,3 +114,36 @@ def test_residual_norm():
     check(lambda **k: layer.backward(stream=0, **k), back, "o", optional)
     with pytest.raises(ValueError, match="train"):
         Q.ResidualNorm(40, res_dtype=F32, device="cpu").backward(stream=0, **back)
+
+
+class Elsewhere(OnDevice):
+    """A device tensor that says that it is on another device than the call's."""
+    get_device = lambda self: 1  # noqa: E731
+
+
+def test_workspaces_of_another_device():
+    """An object's workspaces lie where it was made: a call with tensors of another device would hand their addresses to that one."""
+    conv, back, scan, gate, res = (Q.ShortConv(2, 20, 24, 4, device="cpu", train=True), Q.SelectiveScan(2, 20, 4, 64, 64, 2, device="cpu", train=True),
+                                   Q.SelectiveScan(2, 20, 4, 64, 64, 2, device="cpu"), Q.GatedNorm(2, 40, device="cpu", train=True), Q.ResidualNorm(40, device="cpu", train=True))
+    for layer in (conv, back, scan, gate, res):
+        layer.work = layer.work.as_subclass(Elsewhere)
+    there = pytest.raises(ValueError, match="workspace")
+    tokens, taps = (lambda: device(20, 24)), device(24, 4, dtype=F32)
+    with there:
+        conv.backward(tokens(), taps, device(3, dtype=I32), tokens(), tokens(), device(24, 4, dtype=F32), stream=0)
+    args, out = scan_tensors(), dict(dy=device(20, 4, 64), dx=device(20, 4, 64), ddt=device(20, 4), dA=device(4, dtype=F32), dB=device(20, 2, 64), dC=device(20, 2, 64))
+    with there:
+        scan.forward(y=device(20, 4, 64), stream=0, **args)
+    back.calls, back._sizes = 1, (2, 20)
+    for name in ("work", "save"):
+        with there:
+            back.forward(y=device(20, 4, 64), stream=0, **args)
+        with there:
+            back.backward(stream=0, **args, **out)
+        back.work, back.save = back.work.as_subclass(OnDevice), back.save.as_subclass(Elsewhere)
+    rows, w = (lambda: device(6, 2, 40)), lambda: device(40, dtype=F32)  # noqa: E731
+    with there:
+        gate.backward(rows(), rows(), w(), rows(), rows(), rows(), w(), stream=0)
+    row = lambda: device(6, 40)  # noqa: E731
+    with there:
+        res.backward(row(), row(), row(), row(), row(), row(), weight=w(), dweight=w(), stream=0)
