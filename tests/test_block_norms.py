@@ -289,3 +289,21 @@ def test_gates_beyond_the_exponentials_range():
     z[0, 0, 7] = 88.0
     Q.GatedNorm(1, 8, eps=0.0, dtype=F32).forward(x, z, None, y)
     assert (y[0, 0, :4].abs() < 1e-35).all() and torch.equal(y[0, 0, 4:], z[0, 0, 4:])
+
+
+# ------------------------------------------------------------------ rows in several turns
+# A forward pass has up to 2048 workgroups of 256 threads (one row of 2048 each), 1024 of 512 or 512 of 1024, a pass back 512: more
+# rows, and a workgroup walks over several, the last one's fewer.
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("first,shared", [(False, True), (True, False)], ids=["after", "first"])
+@pytest.mark.parametrize("T,G,d", [(2100, 1, 2048), (1100, 2, 2047), (1090, 1, 4104), (1030, 1, 8192), (530, 1, 9001), (520, 1, 16384)], ids=str)
+def test_gated_rows_in_several_turns(T, G, d, first, shared, dtype):
+    b = gate_batch(T=T, G=G, d=d, first=first, shared=shared, dtype=dtype)
+    near(gate_run(b), gate_plain(b), gate_plain(b, size=True), T * G)
+
+
+@pytest.mark.parametrize("types", [(BF, BF), (BF, F32), (F32, F32)], ids=["bf16", "mixed", "f32"])
+@pytest.mark.parametrize("T,d", [(2100, 2048), (2077, 2043), (1090, 4104), (1030, 8192), (1025, 5001), (530, 9001), (520, 16384)], ids=str)
+def test_residual_rows_in_several_turns(T, d, types):
+    b = res_batch(T=T, d=d, dtype=types[0], res=types[1])
+    near(res_run(b), res_plain(b), res_plain(b, size=True), T)

@@ -229,6 +229,42 @@ def test_long_sequences_in_long_segments():
         check(b, run(b, train=False))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", [dict(H=10), dict(H=9, P=128), dict(H=34, G=2)], ids=["ten", "halves", "groups"])
+def test_gradients_of_many_heads_in_one_workgroup(case, dtype):
+    """1024 chunks and more leave a workgroup all heads of a group: 10, 18 and 17 parts of heads, of which it takes eight at once,
+    in whole chunks and in chunks of a few tokens."""
+    b = batch(lens=[130, 64, 0, 90] + [1 + i % 2 for i in range(1030)], N=64, dtype=dtype, **case)
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_gradients_in_long_segments(dtype):
+    """130 heads make segments of 512 tokens: three of one sequence, one of another."""
+    b = batch(lens=(1030, 70), H=130, N=64, dtype=dtype)
+    check(b, run(b))
+
+
+def test_more_sequences_than_one_search_tells_apart():
+    """4200 sequences: the search for a chunk's sequence goes through two steps of 64 lanes.  A token's results do not depend on how
+    many sequences there are, so they equal to the bit those of the same sequences in calls of 600, which the tests above hold to
+    the recurrence."""
+    lens = [i % 3 for i in range(4200)]
+    b = batch(lens=lens, H=1, N=64)
+    whole, at = run(b), 0
+    for s in range(0, 4200, 600):
+        n = sum(lens[s:s + 600])
+        part = dict(b, case=dict(b["case"], lens=lens[s:s + 600]), cu=(b["cu"][s:s + 601] - at).contiguous(),
+                    **{k: b[k][at:at + n].contiguous() for k in ("x", "dt", "B", "C", "dy")}, **{k: b[k][s:s + 600].clone() for k in ("S0", "dS")})
+        out = run(part)
+        for k, v in out.items():
+            if k in ("S", "dS0"):
+                assert torch.equal(v, whole[k][s:s + 600]), (s, k)
+            elif k in ("y", "dx", "ddt", "dB", "dC"):
+                assert torch.equal(v, whole[k][at:at + n]), (s, k)
+        at += n
+
+
 def test_steps_of_time_as_a_part_of_a_projection():
     b = batch(lens=(70, 30), H=3)
     want = run(b)
