@@ -615,7 +615,8 @@ sq_status sq_scan_step(const sq_scan_desc *desc, float *state_pool, int32_t n_sl
 
 /* The norm behind a layer, with its gate, over rows of d (each group of a token):
  *   y = rms(x) * weight * act(z),  or, with gate_first, y = rms(x * act(z)) * weight,
- *   rms(x) = x / sqrt(mean(x^2) + eps), the squares summed in fp32 (so |x| under 1e19 / sqrt(d)).
+ *   rms(x) = x / sqrt(mean(x^2) + eps), the squares summed in fp32 (so |x| under 1e19 / sqrt(d), and
+ *   with eps = 0 the largest of a row above 1e-18 sqrt(d)).
  * x, z, y: [n_tokens, n_groups, d]; y may be x itself where x is dense. */
 typedef struct {
     int64_t n_tokens;     /* >= 0; n_tokens * n_groups < 2^31 */

@@ -6,8 +6,8 @@
 //   db = sum_t dp[t];  dS0 is dx at the W - 1 places before the sequence.
 //
 // Bound by memory: one input and one output per element and a handful of operations.  A lane has 8
-// neighbouring channels (16 bytes of bf16; backwards 4, whose sums and windows leave room for four waves per SIMD) and walks a
-// run of tokens with the last W - 1 inputs in registers, so an input is read (W - 1 + run) / run times, and
+// neighbouring channels (16 bytes of bf16; backwards 4, whose sums and windows then leave room for three waves per SIMD: four at
+// width 2 in bf16, two at width 4 in fp32) and walks a run of tokens with the last W - 1 inputs in registers, so an input is read (W - 1 + run) / run times, and
 // that by a lane of the same L2.
 #include "sq_block.h"
 

@@ -447,7 +447,10 @@ template <typename F> void pick(bool b, F f) {
 } // namespace
 
 // Vectors of a thread and most threads of a workgroup: rows of up to 4096 columns are one vector of 8 to each of up to 512
-// threads, longer ones two (which above 8192, with 1024 threads and so 128 registers, spills in the backward passes).
+// threads, longer ones two.  What spills, in bytes a lane: above 8192 columns, with 1024 threads and so 128 registers, all passes
+// back (gated 136 to 372, residual 544 to 700) and the residual forward with o and r in fp32 (28); the residual pass back at
+// up to 4096 columns, held to four waves per SIMD, in all types but bf16 with an fp32 residual (40 to 64; without 16-byte loads
+// all, 72 to 128) and from there to 8192 in all but bf16 throughout (32 to 108).
 template <int KK, int TT> struct RowShape { static constexpr int K = KK, T = TT; };
 template <typename F> void pick_row(int d, F f) {
     if (d <= 4096) f(RowShape<1, 512>{});

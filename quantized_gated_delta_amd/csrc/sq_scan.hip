@@ -29,7 +29,7 @@ constexpr int kGates = 4;  // chunks whose gates are formed at once, one by each
 // The main passes, forwards and (in brackets) backwards.  The state takes up the keys K = B [C] with the
 // columns X = x [dy], and is read by the queries Q = C [B]; a query meets the keys of its own
 // chunk up to [from] its own place in `pairs`.  NT: terms that the results are accurate to.
-// What bounds it: two workgroups to a CU by registers and LDS, which hold LDS (0.44 of the cycles) and vector instructions
+// What bounds it: two workgroups to a CU by registers and LDS (fp32 with d_state 128: one, of 107 KB), which hold LDS (0.44 of the cycles) and vector instructions
 // (0.39) busy with the matrix units at 0.21; a chunk takes 8000 cycles alone.  8192 tokens x 64 heads, d_state 128, d_head
 // 64, bf16: own pass 44 us, main pass 100 to 105; x 32 heads in training, with the states saved: 28, 74 to 81, back 27 and 91
 // to 100.
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void s
     __shared__ Gates gates[kGates];
     __shared__ float dots[2][PASS == kMainBack ? 4 : 1][64];
 
-    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4, g8 = (l >> 4) * 8;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, r = l & 15, g4 = (l >> 4) * 4;
     // the heads of a group read the same B and C: workgroups go to the 8 XCDs in turn, and each
     // XCD gets neighbouring heads
     const int parts = a.n_heads * (a.d_head / kHeadPart), each = (parts + 7) / 8;
